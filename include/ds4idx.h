@@ -280,6 +280,154 @@ int ds4idx_sparse_attention(const void* q, const void* kv, int64_t kv_rows, cons
  * synchronisation failed, else OK. */
 int ds4idx_sparse_attention_status(void* stream);
 
+/* ---- Rotary positions of queries and keys: the step before the cache writer, the indexer and the
+ * attention. Every pair (a, b) of the rotated slice of a head of token t becomes
+ *     scale * (a cos(x) - b sin(x), a sin(x) + b cos(x)),   x = positions[t] * inv_freq[pair],
+ * where pair i is elements (2i, 2i + 1) (interleaved) or (i, i + rot_dim / 2) (halves). With
+ * inverse != 0 the angle is negated (same scale): the transpose, which maps the gradient of the
+ * output to the gradient of the input. The angle is off by at most |position| * (2^-65 turn + 2^-53
+ * of the frequency) at any position; the rotation is fp32, rounded once to the tensor's type. */
+
+typedef enum {
+  DS4IDX_ROTARY_PLAIN = 0,  /* inv_freq[i] = base^(-2 i / rot_dim) */
+  DS4IDX_ROTARY_LINEAR = 1, /* divided by factor */
+  DS4IDX_ROTARY_YARN = 2    /* YaRN: pairs that turn more than beta_fast times within the original
+                               context keep their frequency, those that turn less than beta_slow
+                               times are divided by factor, a ramp joins them; scale is
+                               0.1 ln(factor) + 1 */
+} ds4idx_rotary_scaling;
+
+/* One tensor of a rotary call. x and out point at the first rotated element of token 0, head 0
+ * (DEVICE, aligned to an element); element (t, h, i) lies t * stride_t + h * stride_h + i elements
+ * further (strides in elements; rotated elements adjacent). out may equal x with equal strides
+ * (in place); otherwise the two must not overlap. Elements outside the slice are not touched.
+ * 16-byte aligned pointers and strides move 16 bytes a thread; others 2 or 4. */
+typedef struct {
+  const void* x;
+  void* out;
+  int32_t dtype;       /* DS4IDX_BF16 or DS4IDX_F32 */
+  int32_t interleaved; /* else halves */
+  int32_t n_heads;     /* 1..65536 */
+  int32_t reserved;
+  int64_t x_stride_t, x_stride_h, out_stride_t, out_stride_h;
+} ds4idx_rotary_tensor;
+
+/* Host computation, no device access: fills freqs[rot_dim / 2] with the frequencies as 64-bit
+ * fractions of a turn per position (inv_freq / 2 pi * 2^64) and *scale. rot_dim even, 2..256;
+ * base > 1; factor >= 1; original_max_position >= 1 and 0 < beta_slow <= beta_fast for YaRN. */
+int ds4idx_rotary_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
+                        int64_t original_max_position, double beta_fast, double beta_slow,
+                        uint64_t* freqs, float* scale);
+
+/* Rotates 1..4 tensors of the same T tokens in one launch. tensors and freqs are HOST arrays (read
+ * before the call returns); positions DEVICE int64 [T] (any sign). Asynchronous on `stream`,
+ * allocates nothing. Errors: INVALID_ARG, LAUNCH. T = 0 is a no-op. */
+int ds4idx_rotary(int32_t n_tensors, const ds4idx_rotary_tensor* tensors, int64_t T,
+                  int32_t rot_dim, const int64_t* positions, const uint64_t* freqs, float scale,
+                  int32_t inverse, void* stream);
+
+/* ---- The 4-bit latent cache: the latent rows of sparse attention (576 = 512 value dims + 64
+ * rotary dims) in 416 bytes instead of 1152. One row:
+ *   bytes   0..255  512 integers n in -7..7, stored as n + 8 in four bits: of each eight dims (one
+ *                   little-endian 32-bit word) dim 2p stands in bits 4p..4p+3 and dim 2p + 1 in
+ *                   bits 16+4p..16+4p+3;
+ *   bytes 256..287  32 scale codes, one for each 16 dims: code c = 2^(c / 8 - 20) * (1 + (c % 8) / 8)
+ *                   (integer division; 1e-6 .. 3840);
+ *   bytes 288..415  the 64 rotary dims as bf16.
+ * Dim i of the first 512 is n * scale, exact in bf16. A scale is the code nearest to absmax / 7 of
+ * its 16 dims (ties to the even code, clamped to 0..255), n is x / scale rounded to nearest, ties
+ * to even, clamped to -7..7: both are exact decisions, so the bytes are a function of the inputs.
+ * Inputs must be finite. The cache pointer is 32-byte aligned. */
+
+/* Writes n rows x [n, 576] (in_dtype DS4IDX_F32 or DS4IDX_BF16, 16-byte aligned) into cache rows
+ * slots[i] (DEVICE int64 [n]; rows outside the cache, e.g. -1, are skipped) or dst_offset + i
+ * (slots NULL). Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH. n = 0 is a no-op. */
+int ds4idx_quantize_latents(const void* x, int32_t in_dtype, int64_t n, const int64_t* slots,
+                            int64_t dst_offset, uint8_t* cache, int64_t cache_rows, void* stream);
+
+/* Reads n rows back as values: out [n, 576] (out_dtype DS4IDX_F32 or DS4IDX_BF16, both exact;
+ * 16-byte aligned) from cache rows rows[i] (DEVICE int64 [n]; rows outside the cache read as zeros)
+ * or start + i (rows NULL, start + n <= cache_rows). Errors as above. */
+int ds4idx_read_latents(const uint8_t* cache, int64_t cache_rows, const int64_t* rows,
+                        int64_t start, int64_t n, void* out, int32_t out_dtype, void* stream);
+
+/* Where the tokens of a call find position s of their sequence in a pool of rows: pool row
+ * kv_row0[t] + s (kv_row0 DEVICE int64 [T]; NULL = 0), or through a page table. */
+typedef struct {
+  const int64_t* kv_row0;    /* DEVICE int64 [T] or NULL; must be NULL with a page table */
+  const int32_t* page_table; /* DEVICE int32 [n_seqs, pages_per_seq] or NULL */
+  const int32_t* token_seq;  /* DEVICE int32 [T]: the table row of token t; NULL = row t */
+  int32_t page_size;         /* positions per page (>= 1, any size) */
+  int32_t pages_per_seq;
+  int64_t n_seqs;
+} ds4idx_placement;
+/* A position past its table row, a table row outside 0..n_seqs-1, or a pool row outside the pool
+ * makes the list entry empty: nothing out of range is read. */
+
+/* Attention of q over the selected rows of a 4-bit latent cache. For token t, head h, over the
+ * non-empty entries j of its list:
+ *     s_j = sm_scale * q[t,h,:] . row_j,    out[t,h,:] = sum_j softmax(s)_j * row_j[0:512],
+ *     lse[t,h] = log sum_j exp(s_j) (natural; -inf and out = 0 if the list is empty),
+ *     weights[t,j] = sum_h softmax(s)_j (0 in empty entries).
+ *  q        [T, n_heads, 576] bf16, 16-byte aligned; n_heads 1..128 (128 uses the tensor cores
+ *           fully; fewer heads cost the same time).
+ *  cache    [kv_rows, 416], 32-byte aligned, 1 <= kv_rows < 2^31.
+ *  idx      [T, n_sel] int32 positions, 1 <= n_sel <= 512; negative = empty, anywhere in the list
+ *           (the indexer's lists: n_sel = 512). Positions of a list must be distinct.
+ *  where    HOST, may be NULL (row = position).
+ *  out      [T, n_heads, 512] bf16, 32-byte aligned; lse [T, n_heads] fp32 or NULL; weights
+ *           [T, n_sel] fp32 or NULL (summed in a fixed order).
+ * Cache values are exact in bf16; products accumulate in fp32, softmax and sums are fp32, the
+ * probabilities are rounded to bf16 for the value product. Rows of empty entries are never read.
+ * T <= 76 runs a cluster of CTAs per token. Asynchronous on `stream`, allocates nothing. Bounded
+ * device waits that run out are recorded for ds4idx_sparse_attention_status.
+ * Errors: INVALID_ARG, UNSUPPORTED (d_qk != 576, d_v != 512), LAUNCH, CUDA. T = 0 is a no-op. */
+int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, int64_t kv_rows,
+                               const int32_t* idx, const ds4idx_placement* where, int64_t T,
+                               int32_t n_heads, int32_t d_qk, int32_t d_v, int32_t n_sel,
+                               float sm_scale, void* out, float* lse, float* weights,
+                               void* stream);
+
+/* ---- Eviction by accumulated attention weight. Each pool row has a total, int64 in units of
+ * 2^-32 (fixed point: integer adds commute, so the order of atomics does not change a result). */
+
+/* total[row of (t, idx[t,j])] += round(weights[t,j] * 2^32) for every non-empty entry; weights
+ * [T, n_sel] fp32 below 2^30 in size (others add nothing). n_sel >= 1. Asynchronous, allocates
+ * nothing. Errors: INVALID_ARG, LAUNCH. T = 0 is a no-op. */
+int ds4idx_evict_accumulate(int64_t* total, int64_t pool_rows, const float* weights,
+                            const int32_t* idx, const ds4idx_placement* where, int64_t T,
+                            int32_t n_sel, void* stream);
+
+/* Chooses the rows that B sequences keep. Sequence b has seq_lens[b] >= 0 rows from pool row
+ * starts[b] and keeps min(keep[b], seq_lens[b]) of them: all if keep[b] >= seq_lens[b], else its
+ * first n_sink, its last n_recent and, of the others, those with the largest totals (ties to the
+ * lower position). kept [B, width] int32 (DEVICE): the kept positions ascending, then -1; width >=
+ * every count. starts, seq_lens, keep: HOST int64 [B]; 1 <= B <= 64; seq_lens <= 2^30;
+ * 0 <= n_sink + n_recent <= keep[b]. Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH,
+ * CUDA. */
+int ds4idx_evict_select(const int64_t* total, int64_t pool_rows, int32_t B, const int64_t* starts,
+                        const int64_t* seq_lens, const int64_t* keep, int64_t n_sink,
+                        int64_t n_recent, int32_t* kept, int64_t width, void* stream);
+
+/* One per-row array of a pool (latent rows, index keys, key scales, totals, ...). */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t src_rows, dst_rows;
+  int32_t row_bytes; /* 1..65536 */
+  int32_t reserved;
+} ds4idx_row_array;
+
+/* Moves the kept rows of B sequences together: for every array, dst row dst_starts[b] + i = src row
+ * src_starts[b] + kept[b][i], i < counts[b] (kept as written by ds4idx_evict_select, counts[b] =
+ * min(keep[b], seq_lens[b])). 1 <= n_arrays <= 8. The written rows of an array must not overlap the
+ * source range of any sequence in it (checked against src_starts[b] .. + src_lens[b]). HOST: arrays,
+ * src_starts, src_lens, dst_starts, counts; DEVICE: kept [B, width] (an entry outside 0..src_lens-1
+ * leaves its row unwritten). Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH. */
+int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t B, const int64_t* src_starts,
+                         const int64_t* src_lens, const int64_t* dst_starts, const int64_t* counts,
+                         int32_t n_arrays, const ds4idx_row_array* arrays, void* stream);
+
 /* Test support for the bounded device waits (the pages have no counterpart). Every mbarrier
  * wait in the kernels gives up after a limit (2 s by default), records DS4IDX_ERR_DEVICE_TIMEOUT
  * for ds4idx_sync_status, waits for its own copies and tensor-core work to finish, frees its

@@ -78,6 +78,16 @@ constexpr uint32_t kVStrideK = 1024;
 
 __device__ uint32_t g_err;  // bounded-wait timeouts, read by ds4idx_sparse_attention_status
 
+// Its device address on the current device, for the other attention kernel of the library.
+uint32_t* sparse_attention_error_word() {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_err) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  return static_cast<uint32_t*>(p);
+}
+
 struct SAParams {
   const int32_t* idx;      // [T, 512]
   const int64_t* row0;     // [T] kv row of key 0 (or null)

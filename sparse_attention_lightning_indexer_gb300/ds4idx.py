@@ -36,7 +36,10 @@ EXPORTS = ("ds4idx_create", "ds4idx_score_topk", "ds4idx_score_topk_batched",
            "ds4idx_status_string", "ds4idx_version", "ds4idx_score_topk_batched_noalloc",
            "ds4idx_kernels_launched", "ds4idx_debug_wait_test", "ds4idx_plan_query",
            "ds4idx_quantize_keys", "ds4idx_quantize_queries", "ds4idx_score_topk_varlen",
-           "ds4idx_merge_topk", "ds4idx_sparse_attention", "ds4idx_sparse_attention_status")
+           "ds4idx_merge_topk", "ds4idx_sparse_attention", "ds4idx_sparse_attention_status",
+           "ds4idx_rotary_freqs", "ds4idx_rotary", "ds4idx_quantize_latents",
+           "ds4idx_read_latents", "ds4idx_sparse_attention_q4", "ds4idx_evict_accumulate",
+           "ds4idx_evict_select", "ds4idx_evict_compact")
 
 _lock = threading.Lock()
 _lib = None
@@ -53,6 +56,26 @@ class Config(ctypes.Structure):
                 ("topk", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("max_T", ctypes.c_int64), ("max_S", ctypes.c_int64),
                 ("max_batch", ctypes.c_int64)]
+
+
+class RotaryTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_stride_t", ctypes.c_int64),
+                ("x_stride_h", ctypes.c_int64), ("out_stride_t", ctypes.c_int64),
+                ("out_stride_h", ctypes.c_int64)]
+
+
+class Placement(ctypes.Structure):
+    _fields_ = [("kv_row0", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("token_seq", ctypes.c_void_p), ("page_size", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("n_seqs", ctypes.c_int64)]
+
+
+class RowArray(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_rows", ctypes.c_int64),
+                ("dst_rows", ctypes.c_int64), ("row_bytes", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -110,6 +133,19 @@ def load(path: str | None = None):
         lib.ds4idx_quantize_keys.restype = ctypes.c_int
         lib.ds4idx_quantize_queries.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp]
         lib.ds4idx_quantize_queries.restype = ctypes.c_int
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        lib.ds4idx_rotary_freqs.argtypes = [i32, f64, i32, f64, i64, f64, f64, vp, vp]
+        lib.ds4idx_rotary.argtypes = [i32, vp, i64, i32, vp, vp, f32, i32, vp]
+        lib.ds4idx_quantize_latents.argtypes = [vp, i32, i64, vp, i64, vp, i64, vp]
+        lib.ds4idx_read_latents.argtypes = [vp, i64, vp, i64, i64, vp, i32, vp]
+        lib.ds4idx_sparse_attention_q4.argtypes = [vp, vp, i64, vp, vp, i64, i32, i32, i32, i32,
+                                                   f32, vp, vp, vp, vp]
+        lib.ds4idx_evict_accumulate.argtypes = [vp, i64, vp, vp, vp, i64, i32, vp]
+        lib.ds4idx_evict_select.argtypes = [vp, i64, i32, vp, vp, vp, i64, i64, vp, i64, vp]
+        lib.ds4idx_evict_compact.argtypes = [vp, i64, i32, vp, vp, vp, vp, i32, vp, vp]
+        for name in ("rotary_freqs", "rotary", "quantize_latents", "read_latents",
+                     "sparse_attention_q4", "evict_accumulate", "evict_select", "evict_compact"):
+            getattr(lib, "ds4idx_" + name).restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -235,6 +271,294 @@ def sparse_attention(q, kv, idx, sm_scale: float, kv_row0=None, out=None, lse=No
 
 def sparse_attention_status(stream=None):
     _check(load().ds4idx_sparse_attention_status(_stream_ptr(stream)), "ds4idx_sparse_attention")
+
+
+# ---- rotary positions
+
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
+
+
+class RotaryFreqs:
+    """Frequencies of a rotary embedding: 64-bit fractions of a turn per position, and the scale of
+    the cosines and sines. Made on the host by ``rotary_freqs``."""
+
+    def __init__(self, rot_dim: int, freqs, scale: float):
+        self.rot_dim = rot_dim
+        self.freqs = freqs          # ctypes uint64 [rot_dim / 2]
+        self.scale = scale
+
+
+def rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_max_position: int = 4096, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0) -> RotaryFreqs:
+    """Plain, linearly scaled or YaRN frequencies (see include/ds4idx.h)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
+    f = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))()
+    scale = ctypes.c_float()
+    _check(load().ds4idx_rotary_freqs(int(rot_dim), float(base), ROTARY_SCALINGS[scaling],
+                                      float(factor), int(original_max_position), float(beta_fast),
+                                      float(beta_slow), ctypes.cast(f, ctypes.c_void_p),
+                                      ctypes.cast(ctypes.byref(scale), ctypes.c_void_p)),
+           "ds4idx_rotary_freqs")
+    return RotaryFreqs(int(rot_dim), f, scale.value)
+
+
+def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = False, outs=None,
+           stream=None):
+    """Rotates one tensor or up to four (of the same tokens) in one launch.
+
+    Each is the rotated slice of a projection, [T, H, rot_dim] or [T, rot_dim] (bf16 or fp32, any
+    strides, the last dim adjacent). positions [T] int64. interleaved: one bool, or one for each
+    tensor (False = halves). inverse: the transposed rotation, which is the gradient. outs: tensors
+    of the same shapes to write (may be the inputs themselves); None allocates dense ones.
+    """
+    single = isinstance(xs, torch.Tensor)
+    xs = [xs] if single else list(xs)
+    n = len(xs)
+    if not 1 <= n <= 4:
+        raise ValueError("rotary takes 1 to 4 tensors")
+    layouts = [interleaved] * n if isinstance(interleaved, bool) else list(interleaved)
+    if outs is None:
+        outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+    else:
+        outs = [outs] if isinstance(outs, torch.Tensor) else list(outs)
+    if len(layouts) != n or len(outs) != n:
+        raise ValueError("interleaved and outs need one entry per tensor")
+    T = xs[0].shape[0]
+    _need(positions, (T,), "positions", torch.int64)
+    d = (RotaryTensor * n)()
+    for k, (x, o, il) in enumerate(zip(xs, outs, layouts)):
+        if x.dim() not in (2, 3) or x.shape[0] != T or x.shape[-1] != freqs.rot_dim:
+            raise ValueError(f"tensor {k} has shape {tuple(x.shape)}, expected "
+                             f"[{T}, H, {freqs.rot_dim}] or [{T}, {freqs.rot_dim}]")
+        if o.shape != x.shape or o.dtype != x.dtype:
+            raise ValueError(f"out {k} must have the shape and dtype of tensor {k}")
+        for t in (x, o):
+            if not t.is_cuda:
+                raise ValueError(f"tensor {k} must be a CUDA tensor")
+            if t.stride(-1) != 1:
+                raise ValueError(f"the rotated dim of tensor {k} must be adjacent")
+        if _in_dtype(x, f"tensor {k}") == F32:
+            d[k].dtype = F32
+        else:
+            d[k].dtype = BF16
+        heads = x.dim() == 3
+        if heads and x.shape[1] < 1:
+            raise ValueError(f"tensor {k} has no head")
+        d[k].x, d[k].out = x.data_ptr(), o.data_ptr()
+        d[k].interleaved = 1 if il else 0
+        d[k].n_heads = x.shape[1] if heads else 1
+        d[k].x_stride_t, d[k].out_stride_t = x.stride(0), o.stride(0)
+        if heads:
+            d[k].x_stride_h, d[k].out_stride_h = x.stride(1), o.stride(1)
+    vp = ctypes.c_void_p
+    _check(load().ds4idx_rotary(n, ctypes.cast(d, vp), T, freqs.rot_dim, _ptr(positions),
+                                ctypes.cast(freqs.freqs, vp), freqs.scale, 1 if inverse else 0,
+                                _stream_ptr(stream)), "ds4idx_rotary")
+    return outs[0] if single else outs
+
+
+class _RotaryFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, positions, freqs, layouts, inverse, *xs):
+        ctx.save_for_backward(positions)
+        ctx.args = (freqs, layouts, inverse)
+        return tuple(rotary(list(xs), positions, freqs, layouts, inverse))
+
+    @staticmethod
+    def backward(ctx, *grads):
+        freqs, layouts, inverse = ctx.args
+        grads = [g if g.stride(-1) == 1 else g.contiguous() for g in grads]
+        back = _RotaryFunction.apply(ctx.saved_tensors[0], freqs, layouts, not inverse, *grads)
+        return (None, None, None, None, *back)
+
+
+def rotary_autograd(xs, positions, freqs: RotaryFreqs, interleaved=True):
+    """``rotary`` for training: new tensors whose gradients are the inverse rotation."""
+    single = isinstance(xs, torch.Tensor)
+    xs = [xs] if single else list(xs)
+    layouts = [interleaved] * len(xs) if isinstance(interleaved, bool) else list(interleaved)
+    ys = _RotaryFunction.apply(positions, freqs, layouts, False, *xs)
+    return ys[0] if single else list(ys)
+
+
+# ---- the 4-bit latent cache
+
+Q4_ROW_BYTES = 416
+
+
+def _cache_rows(cache) -> int:
+    _need(cache, (cache.shape[0], Q4_ROW_BYTES), "cache", torch.uint8)
+    return cache.shape[0]
+
+
+def quantize_latents(x, cache, dst_offset: int = 0, slots=None, stream=None):
+    """Writes latent rows x [n, 576] (fp32/bf16) in 4 bits into cache [R, 416] uint8, at rows
+    dst_offset.. or at slots [n] (int64, -1 skips a row)."""
+    n = x.shape[0]
+    _need(x, (n, SA_DQK), "x")
+    R = _cache_rows(cache)
+    if slots is not None:
+        _need(slots, (n,), "slots", torch.int64)
+    _check(load().ds4idx_quantize_latents(_ptr(x), _in_dtype(x, "x"), n, _ptr(slots),
+                                          int(dst_offset), _ptr(cache), R, _stream_ptr(stream)),
+           "ds4idx_quantize_latents")
+    return cache
+
+
+def read_latents(cache, rows=None, start: int = 0, n: int | None = None, out=None,
+                 dtype=torch.bfloat16, stream=None):
+    """The values of cache rows ``rows`` [n] (int64; rows outside the cache give zeros) or of rows
+    start .. start + n - 1 (n None: to the end), as [n, 576] bf16 or fp32."""
+    R = _cache_rows(cache)
+    if rows is not None:
+        n = rows.shape[0]
+        _need(rows, (n,), "rows", torch.int64)
+    elif n is None:
+        n = R - int(start)
+    if out is None:
+        out = torch.empty((n, SA_DQK), dtype=dtype, device=cache.device)
+    _need(out, (n, SA_DQK), "out")
+    _check(load().ds4idx_read_latents(_ptr(cache), R, _ptr(rows), int(start), n, _ptr(out),
+                                      _in_dtype(out, "out"), _stream_ptr(stream)),
+           "ds4idx_read_latents")
+    return out
+
+
+def _placement(T, kv_row0, page_table, page_size, token_seq):
+    """The ds4idx_placement of a call, or None (row = position)."""
+    if kv_row0 is None and page_table is None:
+        if token_seq is not None:
+            raise ValueError("token_seq needs a page_table")
+        return None
+    w = Placement()
+    if kv_row0 is not None:
+        if page_table is not None or token_seq is not None:
+            raise ValueError("kv_row0 and page_table exclude each other")
+        _need(kv_row0, (T,), "kv_row0", torch.int64)
+        w.kv_row0 = kv_row0.data_ptr()
+        return w
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seqs, pages_per_seq]")
+    _need(page_table, tuple(page_table.shape), "page_table", torch.int32)
+    w.page_table = page_table.data_ptr()
+    w.n_seqs, w.pages_per_seq, w.page_size = page_table.shape[0], page_table.shape[1], int(page_size)
+    if token_seq is not None:
+        _need(token_seq, (T,), "token_seq", torch.int32)
+        w.token_seq = token_seq.data_ptr()
+    return w
+
+
+def _ref(w):
+    return None if w is None else ctypes.cast(ctypes.byref(w), ctypes.c_void_p)
+
+
+def sparse_attention_q4(q, cache, idx, sm_scale: float, kv_row0=None, page_table=None,
+                        page_size: int = 0, token_seq=None, out=None, lse=None, weights=None,
+                        want_weights: bool = False, stream=None):
+    """Attention of q [T, H, 576] (bf16, 1 <= H <= 128) over the selected rows of a 4-bit latent
+    cache [R, 416]: idx [T, n_sel] int32 positions (negative = empty, n_sel <= 512). Position s of
+    token t is cache row kv_row0[t] + s, or is found through page_table [n_seqs, pages] int32 with
+    page_size positions a page and token_seq [T] int32 (None: row t).
+    Returns (out [T, H, 512] bf16, lse [T, H] fp32, weights [T, n_sel] fp32 or None): weights is
+    each entry's probability summed over the heads."""
+    T, H, n_sel = q.shape[0], q.shape[1], idx.shape[1]
+    R = _cache_rows(cache)
+    _need(q, (T, H, SA_DQK), "q", torch.bfloat16)
+    _need(idx, (T, n_sel), "idx", torch.int32)
+    where = _placement(T, kv_row0, page_table, page_size, token_seq)
+    dev = q.device
+    if out is None:
+        out = torch.empty((T, H, SA_DV), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    if weights is None and want_weights:
+        weights = torch.empty((T, n_sel), dtype=torch.float32, device=dev)
+    _need(out, (T, H, SA_DV), "out", torch.bfloat16)
+    _need(lse, (T, H), "lse", torch.float32)
+    if weights is not None:
+        _need(weights, (T, n_sel), "weights", torch.float32)
+    _check(load().ds4idx_sparse_attention_q4(_ptr(q), _ptr(cache), R, _ptr(idx), _ref(where), T, H,
+                                             SA_DQK, SA_DV, n_sel, float(sm_scale), _ptr(out),
+                                             _ptr(lse), _ptr(weights), _stream_ptr(stream)),
+           "ds4idx_sparse_attention_q4")
+    return out, lse, weights
+
+
+# ---- eviction by accumulated attention weight
+
+def evict_accumulate(total, weights, idx, kv_row0=None, page_table=None, page_size: int = 0,
+                     token_seq=None, stream=None):
+    """total [R] int64 (units of 2^-32) += weights [T, n_sel] of the rows of idx [T, n_sel]; the
+    placement as in ``sparse_attention_q4``."""
+    T, n_sel = idx.shape[0], idx.shape[1]
+    R = total.shape[0]
+    _need(total, (R,), "total", torch.int64)
+    _need(weights, (T, n_sel), "weights", torch.float32)
+    _need(idx, (T, n_sel), "idx", torch.int32)
+    where = _placement(T, kv_row0, page_table, page_size, token_seq)
+    _check(load().ds4idx_evict_accumulate(_ptr(total), R, _ptr(weights), _ptr(idx), _ref(where), T,
+                                          n_sel, _stream_ptr(stream)), "ds4idx_evict_accumulate")
+    return total
+
+
+def _i64(values):
+    return (ctypes.c_int64 * max(1, len(values)))(*[int(v) for v in values])
+
+
+def evict_select(total, starts, seq_lens, keep, n_sink: int = 0, n_recent: int = 0, kept=None,
+                 stream=None):
+    """The positions that sequences keep (see include/ds4idx.h): starts, seq_lens, keep: B host ints
+    each. Returns kept [B, max count] int32, ascending, then -1."""
+    B = len(seq_lens)
+    if len(starts) != B or len(keep) != B:
+        raise ValueError("starts, seq_lens and keep need one entry per sequence")
+    R = total.shape[0]
+    _need(total, (R,), "total", torch.int64)
+    if kept is None:
+        width = max([min(int(k), int(s)) for k, s in zip(keep, seq_lens)], default=0)
+        kept = torch.empty((B, max(width, 0)), dtype=torch.int32, device=total.device)
+    _need(kept, (B, kept.shape[1]), "kept", torch.int32)
+    vp = ctypes.c_void_p
+    _check(load().ds4idx_evict_select(_ptr(total), R, B, ctypes.cast(_i64(starts), vp),
+                                      ctypes.cast(_i64(seq_lens), vp), ctypes.cast(_i64(keep), vp),
+                                      int(n_sink), int(n_recent), _ptr(kept), kept.shape[1],
+                                      _stream_ptr(stream)), "ds4idx_evict_select")
+    return kept
+
+
+def evict_compact(kept, seq_lens, keep, src_starts, dst_starts, srcs, dsts, stream=None):
+    """Moves the kept rows (``evict_select`` of the same seq_lens and keep) of up to 8 per-row
+    arrays: dsts[k][dst_starts[b] + i] = srcs[k][src_starts[b] + kept[b, i]]. A written region must
+    not overlap a sequence's source rows."""
+    B = len(seq_lens)
+    if any(len(v) != B for v in (keep, src_starts, dst_starts)):
+        raise ValueError("keep, src_starts and dst_starts need one entry per sequence")
+    if len(srcs) != len(dsts):
+        raise ValueError("srcs and dsts need the same number of arrays")
+    _need(kept, (B, kept.shape[1]), "kept", torch.int32)
+    a = (RowArray * max(1, len(srcs)))()
+    if len(srcs) > 8:
+        raise ValueError("at most 8 arrays")
+    for k, (s, d) in enumerate(zip(srcs, dsts)):
+        _need(s, tuple(s.shape), f"srcs[{k}]")
+        _need(d, (d.shape[0], *s.shape[1:]), f"dsts[{k}]", s.dtype)
+        row = s.element_size()
+        for n in s.shape[1:]:
+            row *= n
+        a[k].src, a[k].dst = s.data_ptr(), d.data_ptr()
+        a[k].src_rows, a[k].dst_rows, a[k].row_bytes = s.shape[0], d.shape[0], row
+    counts = [min(int(k), int(n)) for k, n in zip(keep, seq_lens)]
+    vp = ctypes.c_void_p
+    _check(load().ds4idx_evict_compact(_ptr(kept), kept.shape[1], B,
+                                       ctypes.cast(_i64(src_starts), vp),
+                                       ctypes.cast(_i64(seq_lens), vp),
+                                       ctypes.cast(_i64(dst_starts), vp),
+                                       ctypes.cast(_i64(counts), vp), len(srcs),
+                                       ctypes.cast(a, vp), _stream_ptr(stream)),
+           "ds4idx_evict_compact")
+    return dsts
 
 
 def status_string(status: int) -> str:
