@@ -54,24 +54,34 @@ constexpr float kNegInf = -__builtin_inff();
 template <int C>
 struct Cfg {
   static constexpr int NK = kK / C;                     // slots of a CTA
-  static constexpr int KBytes = NK * 128;               // one key chunk
-  static constexpr int NKS = C == 1 ? 2 : C == 2 ? 3 : C == 4 ? 5 : 9;
-  static constexpr int NQS = C == 1 ? 4 : C == 2 ? 6 : C == 4 ? 7 : 8;
-  static constexpr int OffQ = NKS * KBytes;
+  // One latent stage: KS keys x CW chunks of 64 dims, one (key, chunk) a worker thread, 64 KB.
+  static constexpr int KS = NK < 256 ? NK : 256;
+  static constexpr int CW = kWorkers / KS;              // 2, 2, 4, 8
+  static constexpr int Stages = 8 / CW;                 // per key part
+  static constexpr int KeyParts = NK / KS;              // 2 at C = 1
+  // Two slots: the rotary chunk and the odd latent stages in slot 1, the even ones in slot 0.
+  static constexpr int Slot1 = KS * CW * 128;
+  static constexpr int OffQ = Slot1 + (C == 8 ? NK * 128 : KS * CW * 128);
+  static constexpr int NQS = C == 8 ? 8 : 4;
   static constexpr int RingBytes = OffQ + NQS * kQBytes;
   static constexpr int Region = RingBytes > kOffV + kVBytes ? RingBytes : kOffV + kVBytes;
-  static constexpr int G = C;                           // worker groups: key chunks in the making
-  static constexpr int CPT = 8 / G;                     // latent chunks of a thread
+  // Lanes that share a row: 2 (64 bytes of codes) where a stage has two chunks of 256 keys.
+  static constexpr int RowLanes = C <= 2 ? 2 : 1;
   static constexpr int DV = kLatent / C;                // value dims of a CTA
   static constexpr int NB = DV / 64 < 4 ? DV / 64 : 4;  // 64-dim pieces of a V block
   static constexpr int Halves = DV / 64 / NB;           // passes over the keys (2 at C = 1)
   static constexpr int GV = 8 / NB;                     // V blocks in the making = V stages
   static constexpr int VStage = NB * 64 * 128;
+  static constexpr int VLanes = NB == 4 ? 4 : 1;        // lanes that share a row of a V block
   static constexpr int OCol = C == 1 ? 0 : 256;         // first TMEM column of O
   static constexpr int CP = NK / 4;                     // S columns of a thread
   static constexpr int W = CP < 32 ? CP : 32;
-  static constexpr int OP = NB * 64 / 4;                // O columns of a thread per half
+  static constexpr int OP = DV / 4;                     // O columns of a thread
   static constexpr int OW = OP < 32 ? OP : 32;
+  // The output is staged over P at C = 1. In a cluster this CTA's copies of P may still be read, so
+  // it goes over the V blocks, which hold it (512 / C dims).
+  static constexpr int OffO = C == 1 ? 0 : kOffV;
+  static_assert(C == 1 || DV / 64 * kPBlock <= kVBytes, "output staging");
 
   static constexpr int OffRows = Region;
   static constexpr int OffMask = OffRows + kK * 4;
@@ -79,7 +89,7 @@ struct Cfg {
   static constexpr int OffX = OffRed + 2 * 4 * kH * 4;            // [2][C][128] of the cluster
   static constexpr int OffW = OffX + (C > 1 ? 2 * C * kH * 4 : 0);  // [4][NK] key weights
   static constexpr int OffBars = OffW + 4 * NK * 4;
-  static constexpr int NumBars = 2 * NQS + 2 * NKS + 2 * GV + 6;
+  static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 5;
   static constexpr int OffMisc = OffBars + NumBars * 8;
   static constexpr int Smem = OffMisc + 16 + 1024;
   static_assert(GV * VStage == kVBytes && Smem <= 232448, "shared memory");
@@ -88,7 +98,6 @@ struct Cfg {
 struct Params {
   const uint8_t* cache;
   const int32_t* idx;
-  uint16_t* out;
   float* lse;
   float* weights;
   uint32_t* err;
@@ -97,16 +106,13 @@ struct Params {
   float scale_log2;
 };
 
+// One 32-byte sector. Without allocation in L1: every row is another line, and the few lines that
+// the shared memory leaves to L1 would bound the loads in flight (chunk of 4096: 988 -> 838 us).
 __device__ __forceinline__ void ld32(const void* p, uint32_t (&r)[8]) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
                  "=r"(r[7])
                : "l"(p));
-}
-__device__ __forceinline__ void st32(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar,
                                             int32_t x, int32_t y) {
@@ -115,6 +121,17 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const void* src, const CUtensorMap* m, int32_t x,
+                                             int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+// Commits this thread's bulk stores and waits until they have read shared memory.
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout: blocks of 64 N
 // (64 keys x 128 bytes apart), atoms of 8 keys along K.
@@ -187,17 +204,50 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity,
   }
 }
 
-// One 64-dim chunk of a latent row to the 128 swizzled bytes of row `r` at `base`.
-__device__ __forceinline__ void store_chunk(uint8_t* base, int r, const uint32_t (&codes)[8],
-                                            uint32_t scales) {
+// One 64-dim chunk of a latent row to the 128 swizzled bytes of row `r` at `base`. Where several
+// lanes share a row (each its own chunk, chunks a multiple of 1 KB apart), lane x of them writes
+// its 16-byte pieces in the order u ^ x * 8 / kLanes, so that the eight lanes of a store
+// wavefront hit eight different banks.
+template <int kLanes>
+__device__ __forceinline__ void store_chunk(uint8_t* base, int r, uint32_t (&codes)[8],
+                                            uint32_t scales, int x) {
+  int ord = 0;
+  if constexpr (kLanes == 2) {
+    ord = 4 * x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = codes[j], b = codes[j + 4];
+      codes[j] = x ? b : a;
+      codes[j + 4] = x ? a : b;
+    }
+    scales = x ? __funnelshift_l(scales, scales, 16) : scales;  // groups g ^ 2
+  } else if constexpr (kLanes == 4) {
+    ord = 2 * x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = codes[j], b = codes[j + 4];
+      codes[j] = x & 2 ? b : a;
+      codes[j + 4] = x & 2 ? a : b;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 4)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t a = codes[j + k], b = codes[j + k + 2];
+        codes[j + k] = x & 1 ? b : a;
+        codes[j + k + 2] = x & 1 ? a : b;
+      }
+    scales = __byte_perm(scales, 0, 0x3210u ^ (0x1111u * x));  // groups g ^ x
+  }
   uint8_t* row = base + r * 128;
+  const int sw = (r & 7) ^ ord;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const uint32_t s2 = scale_bf16x2((scales >> (8 * g)) & 0xFFu), c2 = offset_bf16x2(s2);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int u = 2 * g + h;
-      *reinterpret_cast<uint4*>(row + ((u ^ (r & 7)) * 16)) = word_to_bf16(codes[u], s2, c2);
+      *reinterpret_cast<uint4*>(row + ((u ^ sw) * 16)) = word_to_bf16(codes[u], s2, c2);
     }
   }
 }
@@ -231,6 +281,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[W]) {
 template <int C>
 __global__ void __launch_bounds__(kThreads, 1)
     sparse_attn_q4_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                          const __grid_constant__ CUtensorMap tmap_o,
                           const __grid_constant__ Params p) {
   using F = Cfg<C>;
   extern __shared__ uint8_t smem_raw[];
@@ -246,14 +297,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = bars;
   uint64_t* q_empty = q_full + F::NQS;
   uint64_t* k_full = q_empty + F::NQS;
-  uint64_t* k_empty = k_full + F::NKS;
-  uint64_t* v_full = k_empty + F::NKS;
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;
   uint64_t* v_empty = v_full + F::GV;
   uint64_t* s_ready = v_empty + F::GV;
   uint64_t* m_full = s_ready + 1;
   uint64_t* l_full = s_ready + 2;
   uint64_t* p_full = s_ready + 3;
-  uint64_t* o_ready = s_ready + 4;  // [2]
+  uint64_t* o_ready = s_ready + 4;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + F::OffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + F::OffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -266,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
-    for (int i = 0; i < F::NKS; ++i) {
-      mbar_init(&k_full[i], 16 / F::G);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 16);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < F::GV; ++i) {
@@ -278,8 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(m_full, 4 * C);
     mbar_init(l_full, 4 * C);
     mbar_init(p_full, 16 + (C > 1 ? 1 : 0));
-    mbar_init(&o_ready[0], 1);
-    mbar_init(&o_ready[1], 1);
+    mbar_init(o_ready, 1);
     *s_abort = 0u;
     fence_mbar_init();
   }
@@ -313,59 +363,96 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kMmaWarp) {
     bool ok = true;
-    // ---------------- A: key chunks
+    // ---------------- A: key chunks. Stage 0 is the rotary chunk of all keys, then the latent
+    // stages; stage i sits in slot (i + 1) % 2.
+    const int parts = (nc + F::KS - 1) / F::KS;
+    int stage = 0;
+    auto stage_begin = [&] {
+      if (ok) ok = mbar_wait_warp(&k_empty[(stage + 1) & 1], ((stage >> 1) & 1) ^ 1u, s_abort, err);
+    };
+    auto stage_end = [&] {
+      if (ok) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[(stage + 1) & 1]);
+      }
+      ++stage;
+    };
     if (nc > 0) {
-      const int kk = tid % F::NK, grp = tid / F::NK;
-      const int32_t row_id = kk < nc ? s_rows[slot0 + kk] : -1;
-      const bool live = row_id >= 0;
-      const uint8_t* row = p.cache + static_cast<int64_t>(live ? row_id : 0) * kRowBytes;
-      constexpr int PF = F::CPT < 3 ? F::CPT : 3;  // chunks in flight
-      uint32_t codes[PF][8], scales[F::CPT];
+      const int ch = F::RowLanes == 2 ? tid & 1 : tid / F::KS;
+      const int kk = F::RowLanes == 2 ? tid >> 1 : tid % F::KS;
+      constexpr int Units = F::Stages * F::KeyParts;
+      constexpr int PF = Units < 3 ? Units : 3;  // codes in flight
+      const uint8_t* row[F::KeyParts];           // null: an empty slot
+      uint32_t codes[PF][8], scales[F::KeyParts][F::Stages];
 #pragma unroll
-      for (int i = 0; i < PF; ++i) {
+      for (int k = 0; k < F::KeyParts; ++k) {
+        const int key = k * F::KS + kk;
+        const int32_t r = key < nc ? s_rows[slot0 + key] : -1;
+        row[k] = r >= 0 ? p.cache + static_cast<int64_t>(r) * kRowBytes : nullptr;
+      }
+      // unit u: chunk (u / KeyParts) * CW + ch of key part u % KeyParts
+      auto load = [&](int u, uint32_t (&c)[8]) {
+        const uint8_t* src = row[u % F::KeyParts];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) codes[i][j] = kEmptyWord;
-        if (live) ld32(row + (grp + F::G * i) * 32, codes[i]);
+        for (int j = 0; j < 8; ++j) c[j] = kEmptyWord;
+        if (src) ld32(src + ((u / F::KeyParts) * F::CW + ch) * 32, c);
+      };
+      // the rotary dims: four lanes a row, 32 bytes each
+      constexpr int RU = F::NK * 4 > kWorkers ? F::NK * 4 / kWorkers : 1;
+      uint32_t rope[RU][8];
+#pragma unroll
+      for (int i = 0; i < RU; ++i) {
+        const int key = (tid + i * kWorkers) >> 2;
+        const int32_t r = key < nc ? s_rows[slot0 + key] : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rope[i][j] = 0u;
+        if (r >= 0)
+          ld32(p.cache + static_cast<int64_t>(r) * kRowBytes + kOffRope + (tid & 3) * 32, rope[i]);
       }
 #pragma unroll
-      for (int i = 0; i < F::CPT; ++i)
-        scales[i] = live ? *reinterpret_cast<const uint32_t*>(row + kOffScale + 4 * (grp + F::G * i))
-                         : 0u;
+      for (int k = 0; k < F::KeyParts; ++k) {
+        if constexpr (F::RowLanes == 2) {
+          uint32_t all[8] = {};
+          if (row[k]) ld32(row[k] + kOffScale, all);
 #pragma unroll
-      for (int i = 0; i < F::CPT; ++i) {
-        const int c = grp + F::G * i, st = c % F::NKS;
-        if (ok) ok = mbar_wait_warp(&k_empty[st], ((c / F::NKS) & 1) ^ 1u, s_abort, err);
-        if (ok) {
-          if (kk < nc) store_chunk(smem + st * F::KBytes, kk, codes[i % PF], scales[i]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[st]);
+          for (int i = 0; i < F::Stages; ++i) scales[k][i] = ch ? all[2 * i + 1] : all[2 * i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < F::Stages; ++i)
+            scales[k][i] = row[k] ? *reinterpret_cast<const uint32_t*>(row[k] + kOffScale +
+                                                                       4 * (i * F::CW + ch))
+                                  : 0u;
         }
-        if (i + PF < F::CPT && live) ld32(row + (grp + F::G * (i + PF)) * 32, codes[i % PF]);
       }
-      if (grp == 0 && ok) {  // the rotary chunk, bf16 as it is
-        uint32_t r[4][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+      for (int u = 0; u < PF; ++u) load(u, codes[u]);
+      stage_begin();
+      if (ok) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) r[j][k] = 0u;
-          if (live) ld32(row + kOffRope + 32 * j, r[j]);
-        }
-        constexpr int c = kChunks - 1, st = c % F::NKS;
-        ok = mbar_wait_warp(&k_empty[st], ((c / F::NKS) & 1) ^ 1u, s_abort, err);
-        if (ok) {
-          uint8_t* dst = smem + st * F::KBytes + kk * 128;
-          if (kk < nc) {
+        for (int i = 0; i < RU; ++i) {
+          const int key = (tid + i * kWorkers) >> 2;
+          uint8_t* dst = smem + F::Slot1 + key * 128;
+          if (key < nc) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<uint4*>(dst + ((u ^ (kk & 7)) * 16)) =
-                  make_uint4(r[u / 2][4 * (u & 1)], r[u / 2][4 * (u & 1) + 1],
-                             r[u / 2][4 * (u & 1) + 2], r[u / 2][4 * (u & 1) + 3]);
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<uint4*>(dst + (((2 * (tid & 3) + h) ^ (key & 7)) * 16)) = make_uint4(
+                  rope[i][4 * h], rope[i][4 * h + 1], rope[i][4 * h + 2], rope[i][4 * h + 3]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[st]);
         }
+      }
+      stage_end();
+#pragma unroll
+      for (int u = 0; u < Units; ++u) {
+        const int part = u % F::KeyParts;
+        if (part < parts) {
+          stage_begin();
+          if (ok && part * F::KS + kk < nc)
+            store_chunk<F::RowLanes>(smem + ((stage + 1) & 1) * F::Slot1 + ch * (F::KS * 128), kk,
+                                     codes[u % PF], scales[part][u / F::KeyParts], ch);
+          stage_end();
+        }
+        if (u + PF < Units) load(u + PF, codes[u % PF]);
       }
     }
     // ---------------- B: softmax
@@ -381,6 +468,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     constexpr uint32_t kAll = F::W == 32 ? 0xFFFFFFFFu : 0xFFFFu;
     auto worker_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory"); };
+    // Value blocks of this thread's group: its codes are read one block ahead.
+    const int gv = tid / (64 * F::NB), vtid = tid % (64 * F::NB);
+    const int vnb = F::VLanes == 4 ? vtid & 3 : vtid / 64, vr = F::VLanes == 4 ? vtid >> 2 : vtid % 64;
+    const int vblocks = gv < nblk ? (nblk - gv + F::GV - 1) / F::GV : 0;  // per half
+    uint32_t vc[2][8], vs[2];
+    auto v_load = [&](int n, uint32_t (&codes)[8], uint32_t& sc) {  // n: this group's n-th block
+      if (n >= vblocks * F::Halves) return;
+      const int half = n >= vblocks ? 1 : 0;
+      const int32_t r = s_rows[(gv + F::GV * (n - half * vblocks)) * 64 + vr];
+      const int chunk = rank * (F::DV / 64) + half * F::NB + vnb;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) codes[j] = kEmptyWord;
+      sc = 0u;
+      if (r >= 0) {
+        const uint8_t* row = p.cache + static_cast<int64_t>(r) * kRowBytes;
+        ld32(row + chunk * 32, codes);
+        sc = *reinterpret_cast<const uint32_t*>(row + kOffScale + 4 * chunk);
+      }
+    };
+    auto v_store = [&](int n, uint32_t (&codes)[8], uint32_t sc) {
+      if (n >= vblocks * F::Halves) return;
+      if (ok) ok = mbar_wait_warp(&v_empty[gv], (n & 1) ^ 1u, s_abort, err);
+      if (!ok) return;
+      store_chunk<F::VLanes>(smem + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc, vnb);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[gv]);
+    };
+    v_load(0, vc[0], vs[0]);
+    v_load(1, vc[1], vs[1]);
     ok = mbar_wait_warp(s_ready, 0u, s_abort, err) && ok;
     tc_fence_after();
     float mx = kNegInf;
@@ -411,35 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < C) arrive_peer(peer(smem_u32(m_full), lane));
       }
     }
-    // The V blocks this group makes first, while the maxima travel (the rings are done with).
-    const int gv = tid / (64 * F::NB), vr = tid % 64, vnb = (tid / 64) % F::NB;
-    int vuse = 0;
-    auto v_load = [&](int half, int kb, uint32_t (&codes)[8], uint32_t& sc) {
-      const int32_t r = s_rows[kb * 64 + vr];
-      const int chunk = rank * (F::DV / 64) + half * F::NB + vnb;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) codes[j] = kEmptyWord;
-      sc = 0u;
-      if (r >= 0) {
-        const uint8_t* row = p.cache + static_cast<int64_t>(r) * kRowBytes;
-        ld32(row + chunk * 32, codes);
-        sc = *reinterpret_cast<const uint32_t*>(row + kOffScale + 4 * chunk);
-      }
-    };
-    auto v_store = [&](const uint32_t (&codes)[8], uint32_t sc) {
-      if (ok) ok = mbar_wait_warp(&v_empty[gv], (vuse & 1) ^ 1u, s_abort, err);
-      ++vuse;
-      if (!ok) return;
-      store_chunk(smem + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[gv]);
-    };
-    uint32_t vc[8], vs;
-    if (gv < nblk) {
-      v_load(0, gv, vc, vs);
-      v_store(vc, vs);
-    }
+    // its first block while the maxima travel (the rings are done with)
+    v_store(0, vc[0], vs[0]);
     if constexpr (C > 1) {
       ok = __all_sync(0xffffffffu, wait_cluster(m_full, 0u, s_abort, err)) && ok;
 #pragma unroll
@@ -532,27 +622,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (p.lse && rank == 0 && part == 0 && h < p.n_heads)
       p.lse[t * p.n_heads + h] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
-    // ---------------- C: value blocks, then the output
+    // ---------------- C: value blocks, then the output through shared memory
 #pragma unroll 1
-    for (int n = (gv < nblk ? 1 : 0), half = 0; half < F::Halves; ++half, n = 0) {
-#pragma unroll 1
-      for (int kb = gv + F::GV * n; kb < nblk; kb += F::GV) {
-        v_load(half, kb, vc, vs);
-        v_store(vc, vs);
-      }
+    for (int n = 1; n < vblocks * F::Halves; n += 2) {
+      v_load(n + 1, vc[0], vs[0]);
+      v_store(n, vc[1], vs[1]);
+      v_load(n + 2, vc[1], vs[1]);
+      v_store(n + 1, vc[0], vs[0]);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* orow = p.out + (t * p.n_heads + h) * kLatent + rank * F::DV;
-#pragma unroll 1
-    for (int half = 0; half < F::Halves; ++half) {
-      if (nblk > 0 && ok) {
-        ok = mbar_wait_warp(&o_ready[half], 0u, s_abort, err);
-        tc_fence_after();
-      }
-      if (!ok) break;
+    if (nblk > 0) {
+      if (ok) ok = mbar_wait_warp(o_ready, 0u, s_abort, err);
+      tc_fence_after();
+    }
+    if (ok) {
 #pragma unroll 1
       for (int i = 0; i < F::OP / F::OW; ++i) {
-        const int col = half * F::NB * 64 + part * F::OP + i * F::OW;
+        const int col = part * F::OP + i * F::OW;
         uint32_t r[F::OW], pk[F::OW / 2];
         if (nblk > 0) {
           tmem_ld<F::OW>(tmem + lane_base + F::OCol + col, r);
@@ -562,34 +648,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < F::OW; j += 2)
           pk[j / 2] = nblk > 0 ? pack_bf16x2(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv)
                                : 0u;
-        if (h < p.n_heads) {
+        uint8_t* row = smem + F::OffO + (col >> 6) * kPBlock + h * 128;
 #pragma unroll
-          for (int u = 0; u < F::OW / 16; ++u) st32(orow + col + 16 * u, pk + 8 * u);
+        for (int u = 0; u < F::OW / 8; ++u) {
+          const int cc = ((col & 63) >> 3) + u;
+          *reinterpret_cast<uint4*>(row + ((cc ^ (h & 7)) * 16)) =
+              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         }
       }
+    }
+    fence_proxy_async_smem();
+    worker_sync();
+    if (ok && tid == 0) {
+#pragma unroll 1
+      for (int i = 0; i < F::DV / 64; ++i)
+        tma_store_2d(smem + F::OffO + i * kPBlock, &tmap_o, rank * F::DV + i * 64,
+                     static_cast<int32_t>(t * p.n_heads));
+      bulk_store_wait();
     }
   } else if (warp == kMmaWarp) {
     // ---------------- MMA issue (one thread)
     if (lane == 0) {
       bool ok = true;
       if (nc > 0) {
-        for (int c = 0; c < kChunks; ++c) {
-          const int qs = c % F::NQS, ks = c % F::NKS;
-          ok = mbar_wait(&q_full[qs], (c / F::NQS) & 1, s_abort, err) &&
-               mbar_wait(&k_full[ks], (c / F::NKS) & 1, s_abort, err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t qa = smem_u32(smem + F::OffQ + qs * kQBytes);
-          const uint32_t kb = smem_u32(smem + ks * F::KBytes);
-          for (int k0 = 0; k0 < nc; k0 += 256) {
-            const uint32_t idesc = instr_desc(1u, 1u, 128, min(256, nc - k0));
+        // Q chunk i of the order rotary, 0 .. 7; key stage i as the workers make them
+        const uint64_t q0 = smem_desc_sw128(smem_u32(smem + F::OffQ));
+        const uint64_t k0 = smem_desc_sw128(smem_u32(smem));
+        int stage = 0;
+        auto q_ready = [&](int i) {
+          return mbar_wait(&q_full[i % F::NQS], (i / F::NQS) & 1, s_abort, err);
+        };
+        auto k_ready = [&] {
+          return mbar_wait(&k_full[(stage + 1) & 1], (stage >> 1) & 1, s_abort, err);
+        };
+        // S columns col .. col + n - 1 += Q chunk i x the n keys at byte `at` of the rings
+        auto product = [&](int i, int at, int col, int n, bool first) {
+          const uint32_t idesc = instr_desc(1u, 1u, 128, n);
+          const uint64_t qd = q0 + (i % F::NQS) * (kQBytes >> 4), kd = k0 + (at >> 4);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_bf16(tmem + k0, smem_desc_sw128(qa + s * 32),
-                       smem_desc_sw128(kb + k0 * 128 + s * 32), idesc, (c | s) ? 1u : 0u);
+          for (int s = 0; s < 4; ++s)
+            mma_bf16(tmem + col, qd + 2 * s, kd + 2 * s, idesc, first && s == 0 ? 0u : 1u);
+        };
+        const int parts = (nc + F::KS - 1) / F::KS;
+        ok = q_ready(0) && k_ready();
+        if (ok) {
+          tc_fence_after();
+          for (int k = 0; k < parts; ++k)
+            product(0, F::Slot1 + k * F::KS * 128, k * F::KS, min(F::KS, nc - k * F::KS), true);
+          mma_commit(&q_empty[0]);
+          mma_commit(&k_empty[1]);
+          ++stage;
+        }
+        for (int c0 = 0; ok && c0 < 8; c0 += F::CW) {
+          for (int k = 0; ok && k < parts; ++k) {
+            ok = k_ready();
+#pragma unroll
+            for (int c = 0; c < F::CW; ++c) {
+              if (!ok || (k == 0 && !(ok = q_ready(1 + c0 + c)))) break;
+              tc_fence_after();
+              product(1 + c0 + c, ((stage + 1) & 1) * F::Slot1 + c * F::KS * 128, k * F::KS,
+                      min(F::KS, nc - k * F::KS), false);
+              if (k == parts - 1) mma_commit(&q_empty[(1 + c0 + c) % F::NQS]);
+            }
+            mma_commit(&k_empty[(stage + 1) & 1]);
+            ++stage;
           }
-          mma_commit(&q_empty[qs]);
-          mma_commit(&k_empty[ks]);
         }
       }
       mma_commit(s_ready);
@@ -600,24 +723,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           else ok = mbar_wait(p_full, 0u, s_abort, err);
         }
         tc_fence_after();
-        const uint32_t pa = smem_u32(smem);
+        const uint64_t p0 = smem_desc_sw128(smem_u32(smem));
+        const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV));
         for (int half = 0; half < F::Halves; ++half) {
           for (int kb = 0; ok && kb < nblk; ++kb) {
             const int st = kb % F::GV;
             const int use = half * ((nblk - st + F::GV - 1) / F::GV) + kb / F::GV;
             if (!(ok = mbar_wait(&v_full[st], use & 1, s_abort, err))) break;
             tc_fence_after();
-            const uint32_t vb = smem_u32(smem + kOffV + st * F::VStage);
+            const uint64_t pd = p0 + kb * (kPBlock >> 4), vd = v0 + st * (F::VStage >> 4);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              mma_bf16(tmem + F::OCol + half * 256, smem_desc_sw128(pa + kb * kPBlock + s * 32),
-                       smem_desc_mn_sw128(vb + s * 16 * 128), idesc, (kb | s) ? 1u : 0u);
+              mma_bf16(tmem + F::OCol + half * 256, pd + 2 * s, vd + s * (16 * 128 >> 4), idesc,
+                       (kb | s) ? 1u : 0u);
             mma_commit(&v_empty[st]);
           }
-          mma_commit(&o_ready[half]);
         }
+        mma_commit(o_ready);
         // every MMA has completed before TMEM is released (bounded, also after an abort)
-        mbar_drain(&o_ready[F::Halves - 1], 0u);
+        mbar_drain(o_ready, 0u);
         // copies of other CTAs into this one's P have landed (bounded)
         if (C > 1 && !ok) mbar_drain(p_full, 0u);
       }
@@ -633,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qs = c % F::NQS;
         if (!mbar_wait(&q_empty[qs], ((c / F::NQS) & 1) ^ 1u, s_abort, err)) break;
         mbar_arrive_expect_tx(&q_full[qs], bytes);
-        tma_load_2d(smem + F::OffQ + qs * kQBytes, &tmap_q, &q_full[qs], c * 64,
+        tma_load_2d(smem + F::OffQ + qs * kQBytes, &tmap_q, &q_full[qs], c == 0 ? kLatent : (c - 1) * 64,
                     static_cast<int32_t>(t * p.n_heads));
         issued = c + 1;
       }
@@ -655,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 PFN_cuTensorMapEncodeTiled_v12000 g_enc = nullptr;
 std::once_flag g_enc_once;
 
-bool encode_q(CUtensorMap* m, const void* q, int64_t rows, int32_t box_rows) {
+// A [rows, width] bf16 tensor in boxes of box_rows x 64, 128-byte swizzle.
+bool encode(CUtensorMap* m, const void* base, int32_t width, int64_t rows, int32_t box_rows) {
   std::call_once(g_enc_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult r{};
@@ -665,24 +790,24 @@ bool encode_q(CUtensorMap* m, const void* q, int64_t rows, int32_t box_rows) {
       g_enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!g_enc) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(kRowDims), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(kRowDims) * 2};
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * 2};
   cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t es[2] = {1u, 1u};
-  return g_enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims, strides, box, es,
+  return g_enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int C>
-int launch(const CUtensorMap& tq, const Params& p, int64_t T, void* stream) {
+int launch(const CUtensorMap& tq, const CUtensorMap& to, const Params& p, int64_t T, void* stream) {
   if (cudaFuncSetAttribute(sparse_attn_q4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Cfg<C>::Smem) != cudaSuccess) {
     cudaGetLastError();
     return DS4IDX_ERR_CUDA;
   }
   return launch_dependent(sparse_attn_q4_kernel<C>, static_cast<unsigned>(T * C), kThreads,
-                          Cfg<C>::Smem, C, stream, tq, p);
+                          Cfg<C>::Smem, C, stream, tq, to, p);
 }
 
 }  // namespace ds4qa
@@ -703,11 +828,12 @@ extern "C" int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, i
       !aligned_to(idx, 4) || !aligned_to(out, 32) || !aligned_to(lse, 4) ||
       !aligned_to(weights, 4) || !make_placement(where, kv_rows, T, &p.place))
     return DS4IDX_ERR_INVALID_ARG;
-  CUtensorMap tq;
-  if (!encode_q(&tq, q, T * n_heads, n_heads)) return DS4IDX_ERR_CUDA;
+  CUtensorMap tq, to;
+  if (!encode(&tq, q, kRowDims, T * n_heads, n_heads) ||
+      !encode(&to, out, kLatent, T * n_heads, n_heads))
+    return DS4IDX_ERR_CUDA;
   p.cache = cache;
   p.idx = idx;
-  p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.weights = weights;
   p.err = ds4a::sparse_attention_error_word();
@@ -716,8 +842,8 @@ extern "C" int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, i
   p.n_sel = n_sel;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   // The widest cluster whose CTAs still fit the 152 SMs at once (clusters of 8 pack two to a GPC).
-  if (T <= 16) return launch<8>(tq, p, T, stream);
-  if (T <= 32) return launch<4>(tq, p, T, stream);
-  if (T <= 76) return launch<2>(tq, p, T, stream);
-  return launch<1>(tq, p, T, stream);
+  if (T <= 16) return launch<8>(tq, to, p, T, stream);
+  if (T <= 32) return launch<4>(tq, to, p, T, stream);
+  if (T <= 76) return launch<2>(tq, to, p, T, stream);
+  return launch<1>(tq, to, p, T, stream);
 }
