@@ -80,10 +80,16 @@ __device__ uint32_t g_err;  // bounded-wait timeouts, read by ds4idx_sparse_atte
 
 // Its device address on the current device, for the other attention kernel of the library.
 uint32_t* sparse_attention_error_word() {
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_err) != cudaSuccess) {
-    cudaGetLastError();
-    return nullptr;
+  static std::atomic<void*> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  void* p = dev < 64 ? known[dev].load(std::memory_order_relaxed) : nullptr;
+  if (!p) {
+    if (cudaGetSymbolAddress(&p, g_err) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    if (dev < 64) known[dev].store(p, std::memory_order_relaxed);
   }
   return static_cast<uint32_t*>(p);
 }

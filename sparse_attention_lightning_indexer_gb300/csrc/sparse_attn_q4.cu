@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -801,10 +802,17 @@ bool encode(CUtensorMap* m, const void* base, int32_t width, int64_t rows, int32
 
 template <int C>
 int launch(const CUtensorMap& tq, const CUtensorMap& to, const Params& p, int64_t T, void* stream) {
-  if (cudaFuncSetAttribute(sparse_attn_q4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Cfg<C>::Smem) != cudaSuccess) {
-    cudaGetLastError();
-    return DS4IDX_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};  // devices on which the attribute is set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DS4IDX_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(done.load(std::memory_order_relaxed) & bit) || !bit) {
+    if (cudaFuncSetAttribute(sparse_attn_q4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<C>::Smem) != cudaSuccess) {
+      cudaGetLastError();
+      return DS4IDX_ERR_CUDA;
+    }
+    done.fetch_or(bit, std::memory_order_relaxed);
   }
   return launch_dependent(sparse_attn_q4_kernel<C>, static_cast<unsigned>(T * C), kThreads,
                           Cfg<C>::Smem, C, stream, tq, to, p);

@@ -7,8 +7,11 @@ CPU fallback: if the library is missing or the device is not sm_103, calls raise
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import math
 import os
+import struct
 import threading
 
 import torch
@@ -85,6 +88,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Loads libds4idx.so (built in-tree by ``build.build()``). Raises if it is absent."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -275,6 +280,7 @@ def sparse_attention_status(stream=None):
 
 # ---- rotary positions
 
+_ROTARY_TENSOR = struct.Struct("=QQiiiiqqqq")   # RotaryTensor, without its field-by-field cost
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
 
 
@@ -285,6 +291,7 @@ class RotaryFreqs:
     def __init__(self, rot_dim: int, freqs, scale: float):
         self.rot_dim = rot_dim
         self.freqs = freqs          # ctypes uint64 [rot_dim / 2]
+        self.address = ctypes.addressof(freqs)
         self.scale = scale
 
 
@@ -298,9 +305,8 @@ def rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", fac
     scale = ctypes.c_float()
     _check(load().ds4idx_rotary_freqs(int(rot_dim), float(base), ROTARY_SCALINGS[scaling],
                                       float(factor), int(original_max_position), float(beta_fast),
-                                      float(beta_slow), ctypes.cast(f, ctypes.c_void_p),
-                                      ctypes.cast(ctypes.byref(scale), ctypes.c_void_p)),
-           "ds4idx_rotary_freqs")
+                                      float(beta_slow), ctypes.addressof(f),
+                                      ctypes.addressof(scale)), "ds4idx_rotary_freqs")
     return RotaryFreqs(int(rot_dim), f, scale.value)
 
 
@@ -327,35 +333,29 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
         raise ValueError("interleaved and outs need one entry per tensor")
     T = xs[0].shape[0]
     _need(positions, (T,), "positions", torch.int64)
-    d = (RotaryTensor * n)()
+    rot = freqs.rot_dim
+    d = ctypes.create_string_buffer(n * _ROTARY_TENSOR.size)
     for k, (x, o, il) in enumerate(zip(xs, outs, layouts)):
-        if x.dim() not in (2, 3) or x.shape[0] != T or x.shape[-1] != freqs.rot_dim:
-            raise ValueError(f"tensor {k} has shape {tuple(x.shape)}, expected "
-                             f"[{T}, H, {freqs.rot_dim}] or [{T}, {freqs.rot_dim}]")
-        if o.shape != x.shape or o.dtype != x.dtype:
+        shape, st, so = x.shape, x.stride(), o.stride()
+        dims = len(shape)
+        if dims not in (2, 3) or shape[0] != T or shape[-1] != rot:
+            raise ValueError(f"tensor {k} has shape {tuple(shape)}, expected [{T}, H, {rot}] or "
+                             f"[{T}, {rot}]")
+        if o.shape != shape or o.dtype != x.dtype:
             raise ValueError(f"out {k} must have the shape and dtype of tensor {k}")
-        for t in (x, o):
-            if not t.is_cuda:
-                raise ValueError(f"tensor {k} must be a CUDA tensor")
-            if t.stride(-1) != 1:
-                raise ValueError(f"the rotated dim of tensor {k} must be adjacent")
-        if _in_dtype(x, f"tensor {k}") == F32:
-            d[k].dtype = F32
-        else:
-            d[k].dtype = BF16
-        heads = x.dim() == 3
-        if heads and x.shape[1] < 1:
+        if not (x.is_cuda and o.is_cuda):
+            raise ValueError(f"tensor {k} must be a CUDA tensor")
+        if st[-1] != 1 or so[-1] != 1:
+            raise ValueError(f"the rotated dim of tensor {k} must be adjacent")
+        heads, xh, oh = (shape[1], st[1], so[1]) if dims == 3 else (1, 0, 0)
+        if heads < 1:
             raise ValueError(f"tensor {k} has no head")
-        d[k].x, d[k].out = x.data_ptr(), o.data_ptr()
-        d[k].interleaved = 1 if il else 0
-        d[k].n_heads = x.shape[1] if heads else 1
-        d[k].x_stride_t, d[k].out_stride_t = x.stride(0), o.stride(0)
-        if heads:
-            d[k].x_stride_h, d[k].out_stride_h = x.stride(1), o.stride(1)
-    vp = ctypes.c_void_p
-    _check(load().ds4idx_rotary(n, ctypes.cast(d, vp), T, freqs.rot_dim, _ptr(positions),
-                                ctypes.cast(freqs.freqs, vp), freqs.scale, 1 if inverse else 0,
-                                _stream_ptr(stream)), "ds4idx_rotary")
+        _ROTARY_TENSOR.pack_into(d, k * _ROTARY_TENSOR.size, x.data_ptr(), o.data_ptr(),
+                                 _in_dtype(x, "a rotary tensor"), 1 if il else 0, heads, 0, st[0],
+                                 xh, so[0], oh)
+    _check(load().ds4idx_rotary(n, ctypes.addressof(d), T, rot, positions.data_ptr(), freqs.address,
+                                freqs.scale, 1 if inverse else 0, _stream_ptr(stream)),
+           "ds4idx_rotary")
     return outs[0] if single else outs
 
 
@@ -451,7 +451,7 @@ def _placement(T, kv_row0, page_table, page_size, token_seq):
 
 
 def _ref(w):
-    return None if w is None else ctypes.cast(ctypes.byref(w), ctypes.c_void_p)
+    return None if w is None else ctypes.addressof(w)
 
 
 def sparse_attention_q4(q, cache, idx, sm_scale: float, kv_row0=None, page_table=None,
@@ -488,6 +488,9 @@ def sparse_attention_q4(q, cache, idx, sm_scale: float, kv_row0=None, page_table
 
 # ---- eviction by accumulated attention weight
 
+_ROW_ARRAY = struct.Struct("=QQqqii")            # RowArray
+
+
 def evict_accumulate(total, weights, idx, kv_row0=None, page_table=None, page_size: int = 0,
                      token_seq=None, stream=None):
     """total [R] int64 (units of 2^-32) += weights [T, n_sel] of the rows of idx [T, n_sel]; the
@@ -504,7 +507,11 @@ def evict_accumulate(total, weights, idx, kv_row0=None, page_table=None, page_si
 
 
 def _i64(values):
-    return (ctypes.c_int64 * max(1, len(values)))(*[int(v) for v in values])
+    return array.array("q", [int(v) for v in values])
+
+
+def _i64_address(a):
+    return a.buffer_info()[0]
 
 
 def evict_select(total, starts, seq_lens, keep, n_sink: int = 0, n_recent: int = 0, kept=None,
@@ -520,10 +527,10 @@ def evict_select(total, starts, seq_lens, keep, n_sink: int = 0, n_recent: int =
         width = max([min(int(k), int(s)) for k, s in zip(keep, seq_lens)], default=0)
         kept = torch.empty((B, max(width, 0)), dtype=torch.int32, device=total.device)
     _need(kept, (B, kept.shape[1]), "kept", torch.int32)
-    vp = ctypes.c_void_p
-    _check(load().ds4idx_evict_select(_ptr(total), R, B, ctypes.cast(_i64(starts), vp),
-                                      ctypes.cast(_i64(seq_lens), vp), ctypes.cast(_i64(keep), vp),
-                                      int(n_sink), int(n_recent), _ptr(kept), kept.shape[1],
+    host = _i64([*starts, *seq_lens, *keep])
+    at = _i64_address(host)
+    _check(load().ds4idx_evict_select(_ptr(total), R, B, at, at + 8 * B, at + 16 * B, int(n_sink),
+                                      int(n_recent), _ptr(kept), kept.shape[1],
                                       _stream_ptr(stream)), "ds4idx_evict_select")
     return kept
 
@@ -538,25 +545,21 @@ def evict_compact(kept, seq_lens, keep, src_starts, dst_starts, srcs, dsts, stre
     if len(srcs) != len(dsts):
         raise ValueError("srcs and dsts need the same number of arrays")
     _need(kept, (B, kept.shape[1]), "kept", torch.int32)
-    a = (RowArray * max(1, len(srcs)))()
-    if len(srcs) > 8:
+    n = len(srcs)
+    if n > 8:
         raise ValueError("at most 8 arrays")
-    for k, (s, d) in enumerate(zip(srcs, dsts)):
-        _need(s, tuple(s.shape), f"srcs[{k}]")
-        _need(d, (d.shape[0], *s.shape[1:]), f"dsts[{k}]", s.dtype)
-        row = s.element_size()
-        for n in s.shape[1:]:
-            row *= n
-        a[k].src, a[k].dst = s.data_ptr(), d.data_ptr()
-        a[k].src_rows, a[k].dst_rows, a[k].row_bytes = s.shape[0], d.shape[0], row
-    counts = [min(int(k), int(n)) for k, n in zip(keep, seq_lens)]
-    vp = ctypes.c_void_p
-    _check(load().ds4idx_evict_compact(_ptr(kept), kept.shape[1], B,
-                                       ctypes.cast(_i64(src_starts), vp),
-                                       ctypes.cast(_i64(seq_lens), vp),
-                                       ctypes.cast(_i64(dst_starts), vp),
-                                       ctypes.cast(_i64(counts), vp), len(srcs),
-                                       ctypes.cast(a, vp), _stream_ptr(stream)),
+    d = ctypes.create_string_buffer(max(1, n) * _ROW_ARRAY.size)
+    for k, (src, dst) in enumerate(zip(srcs, dsts)):
+        shape = src.shape
+        _need(src, tuple(shape), f"srcs[{k}]")
+        _need(dst, (dst.shape[0], *shape[1:]), f"dsts[{k}]", src.dtype)
+        _ROW_ARRAY.pack_into(d, k * _ROW_ARRAY.size, src.data_ptr(), dst.data_ptr(), shape[0],
+                             dst.shape[0], src.element_size() * math.prod(shape[1:]), 0)
+    counts = [min(int(k), int(m)) for k, m in zip(keep, seq_lens)]
+    host = _i64([*src_starts, *seq_lens, *dst_starts, *counts])
+    at = _i64_address(host)
+    _check(load().ds4idx_evict_compact(_ptr(kept), kept.shape[1], B, at, at + 8 * B, at + 16 * B,
+                                       at + 24 * B, n, ctypes.addressof(d), _stream_ptr(stream)),
            "ds4idx_evict_compact")
     return dsts
 
@@ -574,12 +577,19 @@ def _check(status: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current device's raw stream handle without building a Stream object (about 1 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_ptr(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _codes(t: torch.Tensor, dtype: int, name: str) -> torch.Tensor:
@@ -597,6 +607,8 @@ def _codes(t: torch.Tensor, dtype: int, name: str) -> torch.Tensor:
 def _need(t: torch.Tensor, shape, name: str, dtype=None):
     if t is None:
         raise ValueError(f"{name} is required")
+    if t.is_cuda and t.shape == shape and t.is_contiguous() and (dtype is None or t.dtype == dtype):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
