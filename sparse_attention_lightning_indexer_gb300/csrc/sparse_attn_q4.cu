@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <mutex>
@@ -46,6 +47,7 @@ constexpr int kK = 512;        // list slots
 constexpr int kChunks = 9;     // 64-dim chunks of a key: 8 latent, 1 rotary
 constexpr int kWorkers = 512, kMmaWarp = 16;  // warp 17 loads Q
 constexpr int kThreads = 18 * 32;
+constexpr int kSms = 152;
 constexpr int kQBytes = kH * 128;
 constexpr int kPBlock = kH * 128;            // 64 keys of P
 constexpr int kOffV = (kK / 64) * kPBlock;   // P first, then the V blocks
@@ -85,12 +87,13 @@ struct Cfg {
   static_assert(C == 1 || DV / 64 * kPBlock <= kVBytes, "output staging");
 
   static constexpr int OffRows = Region;
-  static constexpr int OffMask = OffRows + kK * 4;
-  static constexpr int OffRed = OffMask + 64;                     // [2][4][128] max, sum
+  static constexpr int Bufs = C == 1 ? 2 : 1;           // row lists: this token's and the next's
+  static constexpr int OffMask = OffRows + Bufs * kK * 4;
+  static constexpr int OffRed = OffMask + Bufs * 64;                     // [2][4][128] max, sum
   static constexpr int OffX = OffRed + 2 * 4 * kH * 4;            // [2][C][128] of the cluster
   static constexpr int OffW = OffX + (C > 1 ? 2 * C * kH * 4 : 0);  // [4][NK] key weights
   static constexpr int OffBars = OffW + 4 * NK * 4;
-  static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 5;
+  static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 9;
   static constexpr int OffMisc = OffBars + NumBars * 8;
   static constexpr int Smem = OffMisc + 16 + 1024;
   static_assert(GV * VStage == kVBytes && Smem <= 232448, "shared memory");
@@ -103,7 +106,7 @@ struct Params {
   float* weights;
   uint32_t* err;
   Placement place;
-  int32_t n_heads, n_sel;
+  int32_t T, n_heads, n_sel;
   float scale_log2;
 };
 
@@ -130,9 +133,14 @@ __device__ __forceinline__ void tma_store_2d(const void* src, const CUtensorMap*
                "r"(x), "r"(y), "r"(smem_u32(src))
                : "memory");
 }
-// Commits this thread's bulk stores and waits until they have read shared memory.
+// Closes this thread's group of bulk stores; waits until all but the last N groups have read
+// shared memory.
+__device__ __forceinline__ void bulk_store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
 __device__ __forceinline__ void bulk_store_wait() {
-  asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout: blocks of 64 N
 // (64 keys x 128 bytes apart), atoms of 8 keys along K.
@@ -289,8 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every CTA of a cluster has the same dynamic shared-memory base, so the offsets agree
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  int32_t* s_rows = reinterpret_cast<int32_t*>(smem + F::OffRows);
-  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + F::OffMask);
   float* s_red = reinterpret_cast<float*>(smem + F::OffRed);
   float* s_x = reinterpret_cast<float*>(smem + F::OffX);
   float* s_w = reinterpret_cast<float*>(smem + F::OffW);
@@ -306,10 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* l_full = s_ready + 2;
   uint64_t* p_full = s_ready + 3;
   uint64_t* o_ready = s_ready + 4;
+  uint64_t* o_free = s_ready + 5;     // O is read, S may be written again
+  uint64_t* rows_full = s_ready + 6;  // [2] a later token's row list is in place
+  uint64_t* done = s_ready + 8;       // every MMA has completed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + F::OffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + F::OffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t t = blockIdx.x / C;
+  // C = 1: CTAs that stay, taking tokens blockIdx.x, blockIdx.x + gridDim.x, ...
+  const int t_first = blockIdx.x / C, t_step = gridDim.x;
   const int rank = blockIdx.x % C;
   uint32_t* err = p.err;
 
@@ -331,6 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(l_full, 4 * C);
     mbar_init(p_full, 16 + (C > 1 ? 1 : 0));
     mbar_init(o_ready, 1);
+    mbar_init(o_free, 17);
+    mbar_init(&rows_full[0], 1);
+    mbar_init(&rows_full[1], 1);
+    mbar_init(done, 1);
     *s_abort = 0u;
     fence_mbar_init();
   }
@@ -340,35 +354,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   griddep_wait();
   griddep_launch_dependents();
-  if (tid < kK) {
+  // The row list of a token: slots j = base + (0 .. 31) by one warp.
+  auto load_rows = [&](int t, int buf, int base) {
+    const int j = base + lane;
     int64_t r = -1;
-    if (tid < p.n_sel) {
-      const TokenPlace tp = place_token(p.place, t);
-      r = place_row(p.place, tp, p.idx[t * p.n_sel + tid]);
-    }
-    s_rows[tid] = static_cast<int32_t>(r);
+    if (j < p.n_sel) r = place_row(p.place, place_token(p.place, t), p.idx[static_cast<int64_t>(t) * p.n_sel + j]);
+    reinterpret_cast<int32_t*>(smem + F::OffRows)[buf * kK + j] = static_cast<int32_t>(r);
     const uint32_t m = __ballot_sync(0xffffffffu, r >= 0);
-    if (lane == 0) s_mask[warp] = m;
-  }
+    if (lane == 0) reinterpret_cast<uint32_t*>(smem + F::OffMask)[buf * 16 + base / 32] = m;
+  };
+  if (warp < 16) load_rows(t_first, 0, warp * 32);
   tc_fence_before();
   __syncthreads();
   if constexpr (C > 1) cluster_sync();  // every CTA's barriers are set up
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  int nblk = 0;  // blocks of 64 slots up to the last used one
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (s_mask[i]) nblk = i / 2 + 1;
   const int slot0 = rank * F::NK;
-  const int nc = min(F::NK, max(0, nblk * 64 - slot0));  // this CTA's used slots (by 64)
+  // Blocks of 64 slots up to the last used one of a row list.
+  auto used_blocks = [&](int buf) {
+    const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + F::OffMask) + buf * 16;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (mask[i]) n = i / 2 + 1;
+    return n;
+  };
+  // This CTA's used slots (by 64).
+  auto used_slots = [&](int blocks) { return min(F::NK, max(0, blocks * 64 - slot0)); };
 
   if (warp < kMmaWarp) {
     bool ok = true;
-    // ---------------- A: key chunks. Stage 0 is the rotary chunk of all keys, then the latent
-    // stages; stage i sits in slot (i + 1) % 2.
+    auto worker_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory"); };
+    const int quad = warp & 3, part = warp >> 2;
+    const int h = quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t scol = tmem + lane_base + part * F::CP;
+    int stage = 0;       // key stages made so far; stage i sits in slot (i + 1) % 2
+    uint32_t vuse = 0;   // V blocks this group has made so far
+    uint32_t it = 0;     // tokens done
+#pragma unroll 1
+    for (int t = t_first; t < p.T; t += t_step, ++it) {
+    const int buf = F::Bufs == 2 ? it & 1 : 0;
+    if (it > 0 && ok) ok = mbar_wait_warp(&rows_full[buf], ((it - 1) >> 1) & 1, s_abort, err);
+    const int32_t* s_rows = reinterpret_cast<const int32_t*>(smem + F::OffRows) + buf * kK;
+    const uint32_t* s_mask = reinterpret_cast<const uint32_t*>(smem + F::OffMask) + buf * 16;
+    const int nblk = used_blocks(buf), nc = used_slots(nblk);
+    // ---------------- A: key chunks, first the rotary chunk of all keys, then the latent stages
     const int parts = (nc + F::KS - 1) / F::KS;
-    int stage = 0;
+    // The last token's output may still be read from the slots: its half in the slot that comes
+    // first was sent first, so that half is waited for before a stage is made, the rest after it.
+    int pending = it > 0 ? 2 : 0;
     auto stage_begin = [&] {
+      if (C == 1 && pending > 0) {
+        --pending;
+        if (tid == 0) {
+          if (pending) bulk_store_wait<1>(); else bulk_store_wait<0>();
+        }
+        worker_sync();
+      }
       if (ok) ok = mbar_wait_warp(&k_empty[(stage + 1) & 1], ((stage >> 1) & 1) ^ 1u, s_abort, err);
     };
     auto stage_end = [&] {
@@ -433,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < RU; ++i) {
           const int key = (tid + i * kWorkers) >> 2;
-          uint8_t* dst = smem + F::Slot1 + key * 128;
+          uint8_t* dst = smem + ((stage + 1) & 1) * F::Slot1 + key * 128;
           if (key < nc) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -445,30 +488,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       stage_end();
 #pragma unroll
       for (int u = 0; u < Units; ++u) {
-        const int part = u % F::KeyParts;
-        if (part < parts) {
+        const int kp = u % F::KeyParts;
+        if (kp < parts) {
           stage_begin();
-          if (ok && part * F::KS + kk < nc)
+          if (ok && kp * F::KS + kk < nc)
             store_chunk<F::RowLanes>(smem + ((stage + 1) & 1) * F::Slot1 + ch * (F::KS * 128), kk,
-                                     codes[u % PF], scales[part][u / F::KeyParts], ch);
+                                     codes[u % PF], scales[kp][u / F::KeyParts], ch);
           stage_end();
         }
         if (u + PF < Units) load(u + PF, codes[u % PF]);
       }
     }
+    if (C == 1 && pending > 0) {  // an empty list made no stage
+      if (tid == 0) bulk_store_wait<0>();
+      worker_sync();
+    }
     // ---------------- B: softmax
-    const int quad = warp & 3, part = warp >> 2;
-    const int h = quad * 32 + lane;
-    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const int nch = min(F::CP, max(0, nc - part * F::CP)) / F::W;  // chunks of W columns
-    const uint32_t scol = tmem + lane_base + part * F::CP;
     auto mask_of = [&](int i) -> uint32_t {
       const int s = slot0 + part * F::CP + i * F::W;
       const uint32_t m = s_mask[s >> 5];
       return F::W == 32 ? m : (m >> (s & 16)) & 0xFFFFu;
     };
     constexpr uint32_t kAll = F::W == 32 ? 0xFFFFFFFFu : 0xFFFFu;
-    auto worker_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory"); };
     // Value blocks of this thread's group: its codes are read one block ahead.
     const int gv = tid / (64 * F::NB), vtid = tid % (64 * F::NB);
     const int vnb = F::VLanes == 4 ? vtid & 3 : vtid / 64, vr = F::VLanes == 4 ? vtid >> 2 : vtid % 64;
@@ -490,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto v_store = [&](int n, uint32_t (&codes)[8], uint32_t sc) {
       if (n >= vblocks * F::Halves) return;
-      if (ok) ok = mbar_wait_warp(&v_empty[gv], (n & 1) ^ 1u, s_abort, err);
+      if (ok) ok = mbar_wait_warp(&v_empty[gv], (vuse & 1) ^ 1u, s_abort, err);
+      ++vuse;
       if (!ok) return;
       store_chunk<F::VLanes>(smem + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc, vnb);
       fence_proxy_async_smem();
@@ -499,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     v_load(0, vc[0], vs[0]);
     v_load(1, vc[1], vs[1]);
-    ok = mbar_wait_warp(s_ready, 0u, s_abort, err) && ok;
+    if (ok) ok = mbar_wait_warp(s_ready, it & 1, s_abort, err);
     tc_fence_after();
     float mx = kNegInf;
     if (ok) {
@@ -615,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       worker_sync();
       if (tid < F::NK && slot0 + tid < p.n_sel)
-        p.weights[t * p.n_sel + slot0 + tid] =
+        p.weights[static_cast<int64_t>(t) * p.n_sel + slot0 + tid] =
             (s_w[tid] + s_w[F::NK + tid]) + (s_w[2 * F::NK + tid] + s_w[3 * F::NK + tid]);
     }
     if constexpr (C == 1) {
@@ -632,139 +675,192 @@ __global__ void __launch_bounds__(kThreads, 1)
       v_store(n + 1, vc[0], vs[0]);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (nblk > 0) {
-      if (ok) ok = mbar_wait_warp(o_ready, 0u, s_abort, err);
-      tc_fence_after();
-    }
-    if (ok) {
+    if (ok) ok = mbar_wait_warp(o_ready, it & 1, s_abort, err);
+    tc_fence_after();
+    // Output columns of 64 dims each, in F::Halves runs; at C = 1 a run fills one key slot, and the
+    // run in the slot that the next token's first stage takes goes first.
+    constexpr int RunCols = F::DV / F::Halves, PartCols = RunCols / 4;
 #pragma unroll 1
-      for (int i = 0; i < F::OP / F::OW; ++i) {
-        const int col = part * F::OP + i * F::OW;
-        uint32_t r[F::OW], pk[F::OW / 2];
-        if (nblk > 0) {
-          tmem_ld<F::OW>(tmem + lane_base + F::OCol + col, r);
-          tmem_wait_ld();
-        }
+    for (int run = 0; run < F::Halves; ++run) {
+      const int half = C == 1 ? ((stage + 1) & 1) ^ run : run;
+      if (ok) {
+#pragma unroll 1
+        for (int i = 0; i < PartCols / F::OW; ++i) {
+          const int col = half * RunCols + part * PartCols + i * F::OW;
+          uint32_t r[F::OW], pk[F::OW / 2];
+          if (nblk > 0) {
+            tmem_ld<F::OW>(tmem + lane_base + F::OCol + col, r);
+            tmem_wait_ld();
+          }
 #pragma unroll
-        for (int j = 0; j < F::OW; j += 2)
-          pk[j / 2] = nblk > 0 ? pack_bf16x2(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv)
-                               : 0u;
-        uint8_t* row = smem + F::OffO + (col >> 6) * kPBlock + h * 128;
+          for (int j = 0; j < F::OW; j += 2)
+            pk[j / 2] = nblk > 0 ? pack_bf16x2(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv)
+                                 : 0u;
+          uint8_t* row = smem + F::OffO + (col >> 6) * kPBlock + h * 128;
 #pragma unroll
-        for (int u = 0; u < F::OW / 8; ++u) {
-          const int cc = ((col & 63) >> 3) + u;
-          *reinterpret_cast<uint4*>(row + ((cc ^ (h & 7)) * 16)) =
-              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+          for (int u = 0; u < F::OW / 8; ++u) {
+            const int cc = ((col & 63) >> 3) + u;
+            *reinterpret_cast<uint4*>(row + ((cc ^ (h & 7)) * 16)) =
+                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+          }
         }
       }
-    }
-    fence_proxy_async_smem();
-    worker_sync();
-    if (ok && tid == 0) {
+      fence_proxy_async_smem();
+      if (run == F::Halves - 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+      }
+      worker_sync();
+      if (tid == 0) {
+        if (ok) {
 #pragma unroll 1
-      for (int i = 0; i < F::DV / 64; ++i)
-        tma_store_2d(smem + F::OffO + i * kPBlock, &tmap_o, rank * F::DV + i * 64,
-                     static_cast<int32_t>(t * p.n_heads));
-      bulk_store_wait();
+          for (int i = 0; i < RunCols / 64; ++i)
+            tma_store_2d(smem + F::OffO + (half * (RunCols / 64) + i) * kPBlock, &tmap_o,
+                         rank * F::DV + half * RunCols + i * 64,
+                         t * p.n_heads);
+        }
+        bulk_store_commit();
+      }
     }
+    if constexpr (C > 1) break;
+    }
+    if (tid == 0) bulk_store_wait<0>();
   } else if (warp == kMmaWarp) {
     // ---------------- MMA issue (one thread)
     if (lane == 0) {
       bool ok = true;
-      if (nc > 0) {
-        // Q chunk i of the order rotary, 0 .. 7; key stage i as the workers make them
-        const uint64_t q0 = smem_desc_sw128(smem_u32(smem + F::OffQ));
-        const uint64_t k0 = smem_desc_sw128(smem_u32(smem));
-        int stage = 0;
-        auto q_ready = [&](int i) {
-          return mbar_wait(&q_full[i % F::NQS], (i / F::NQS) & 1, s_abort, err);
-        };
-        auto k_ready = [&] {
-          return mbar_wait(&k_full[(stage + 1) & 1], (stage >> 1) & 1, s_abort, err);
-        };
-        // S columns col .. col + n - 1 += Q chunk i x the n keys at byte `at` of the rings
-        auto product = [&](int i, int at, int col, int n, bool first) {
-          const uint32_t idesc = instr_desc(1u, 1u, 128, n);
-          const uint64_t qd = q0 + (i % F::NQS) * (kQBytes >> 4), kd = k0 + (at >> 4);
+      const uint64_t q0 = smem_desc_sw128(smem_u32(smem + F::OffQ));
+      const uint64_t k0 = smem_desc_sw128(smem_u32(smem));
+      const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV));
+      constexpr uint32_t o_idesc = instr_desc(1u, 1u, 128, F::NB * 64) | (1u << 16);  // B MN-major
+      uint32_t qn = 0, it = 0;  // Q chunks taken before this token, tokens done
+      int stage = 0;            // key stages taken
+      uint32_t vn[F::GV] = {};  // blocks taken from each V stage
+      auto q_ready = [&](uint32_t i) {
+        return mbar_wait(&q_full[i % F::NQS], (i / F::NQS) & 1, s_abort, err);
+      };
+      auto k_ready = [&] {
+        return mbar_wait(&k_full[(stage + 1) & 1], (stage >> 1) & 1, s_abort, err);
+      };
+      // S columns col .. col + n - 1 += Q chunk i x the n keys at byte `at` of the slots
+      auto product = [&](uint32_t i, int at, int col, int n, bool first) {
+        const uint32_t idesc = instr_desc(1u, 1u, 128, n);
+        const uint64_t qd = q0 + (i % F::NQS) * (kQBytes >> 4), kd = k0 + (at >> 4);
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma_bf16(tmem + col, qd + 2 * s, kd + 2 * s, idesc, first && s == 0 ? 0u : 1u);
-        };
-        const int parts = (nc + F::KS - 1) / F::KS;
-        ok = q_ready(0) && k_ready();
-        if (ok) {
-          tc_fence_after();
-          for (int k = 0; k < parts; ++k)
-            product(0, F::Slot1 + k * F::KS * 128, k * F::KS, min(F::KS, nc - k * F::KS), true);
-          mma_commit(&q_empty[0]);
-          mma_commit(&k_empty[1]);
-          ++stage;
-        }
-        for (int c0 = 0; ok && c0 < 8; c0 += F::CW) {
-          for (int k = 0; ok && k < parts; ++k) {
-            ok = k_ready();
-#pragma unroll
-            for (int c = 0; c < F::CW; ++c) {
-              if (!ok || (k == 0 && !(ok = q_ready(1 + c0 + c)))) break;
-              tc_fence_after();
-              product(1 + c0 + c, ((stage + 1) & 1) * F::Slot1 + c * F::KS * 128, k * F::KS,
-                      min(F::KS, nc - k * F::KS), false);
-              if (k == parts - 1) mma_commit(&q_empty[(1 + c0 + c) % F::NQS]);
-            }
+        for (int s = 0; s < 4; ++s)
+          mma_bf16(tmem + col, qd + 2 * s, kd + 2 * s, idesc, first && s == 0 ? 0u : 1u);
+      };
+#pragma unroll 1
+      for (int t = t_first; ok && t < p.T; t += t_step, ++it) {
+        const int buf = F::Bufs == 2 ? it & 1 : 0;
+        if (it > 0)
+          ok = mbar_wait(&rows_full[buf], ((it - 1) >> 1) & 1, s_abort, err) &&
+               mbar_wait(o_free, (it - 1) & 1, s_abort, err);
+        if (!ok) break;
+        tc_fence_after();
+        const int nblk = used_blocks(buf), nc = used_slots(nblk);
+        if (nc > 0) {
+          // Q chunks in the order rotary, 0 .. 7; key stages as the workers make them
+          const int parts = (nc + F::KS - 1) / F::KS;
+          ok = q_ready(qn) && k_ready();
+          if (ok) {
+            tc_fence_after();
+            for (int k = 0; k < parts; ++k)
+              product(qn, ((stage + 1) & 1) * F::Slot1 + k * F::KS * 128, k * F::KS,
+                      min(F::KS, nc - k * F::KS), true);
+            mma_commit(&q_empty[qn % F::NQS]);
             mma_commit(&k_empty[(stage + 1) & 1]);
             ++stage;
           }
+          for (int c0 = 0; ok && c0 < 8; c0 += F::CW) {
+            for (int k = 0; ok && k < parts; ++k) {
+              ok = k_ready();
+#pragma unroll
+              for (int c = 0; c < F::CW; ++c) {
+                const uint32_t i = qn + 1 + c0 + c;
+                if (!ok || (k == 0 && !(ok = q_ready(i)))) break;
+                tc_fence_after();
+                product(i, ((stage + 1) & 1) * F::Slot1 + c * F::KS * 128, k * F::KS,
+                        min(F::KS, nc - k * F::KS), false);
+                if (k == parts - 1) mma_commit(&q_empty[i % F::NQS]);
+              }
+              mma_commit(&k_empty[(stage + 1) & 1]);
+              ++stage;
+            }
+          }
+          qn += kChunks;
         }
-      }
-      mma_commit(s_ready);
-      if (nblk > 0) {
-        constexpr uint32_t idesc = instr_desc(1u, 1u, 128, F::NB * 64) | (1u << 16);  // B MN-major
+        mma_commit(s_ready);
         if (ok) {
-          if constexpr (C > 1) ok = wait_cluster(p_full, 0u, s_abort, err);
-          else ok = mbar_wait(p_full, 0u, s_abort, err);
+          if constexpr (C > 1) ok = wait_cluster(p_full, it & 1, s_abort, err);
+          else ok = mbar_wait(p_full, it & 1, s_abort, err);
         }
         tc_fence_after();
-        const uint64_t p0 = smem_desc_sw128(smem_u32(smem));
-        const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV));
         for (int half = 0; half < F::Halves; ++half) {
-          for (int kb = 0; ok && kb < nblk; ++kb) {
-            const int st = kb % F::GV;
-            const int use = half * ((nblk - st + F::GV - 1) / F::GV) + kb / F::GV;
-            if (!(ok = mbar_wait(&v_full[st], use & 1, s_abort, err))) break;
-            tc_fence_after();
-            const uint64_t pd = p0 + kb * (kPBlock >> 4), vd = v0 + st * (F::VStage >> 4);
+#pragma unroll 1
+          for (int kb0 = 0; ok && kb0 < nblk; kb0 += F::GV) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_bf16(tmem + F::OCol + half * 256, pd + 2 * s, vd + s * (16 * 128 >> 4), idesc,
-                       (kb | s) ? 1u : 0u);
-            mma_commit(&v_empty[st]);
+            for (int st = 0; st < F::GV; ++st) {
+              const int kb = kb0 + st;
+              if (!ok || kb >= nblk) break;
+              if (!(ok = mbar_wait(&v_full[st], vn[st] & 1, s_abort, err))) break;
+              ++vn[st];
+              tc_fence_after();
+              const uint64_t pd = k0 + kb * (kPBlock >> 4), vd = v0 + st * (F::VStage >> 4);
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                mma_bf16(tmem + F::OCol + half * 256, pd + 2 * s, vd + s * (16 * 128 >> 4), o_idesc,
+                         (kb | s) ? 1u : 0u);
+              mma_commit(&v_empty[st]);
+            }
           }
         }
         mma_commit(o_ready);
-        // every MMA has completed before TMEM is released (bounded, also after an abort)
-        mbar_drain(o_ready, 0u);
-        // copies of other CTAs into this one's P have landed (bounded)
-        if (C > 1 && !ok) mbar_drain(p_full, 0u);
+        if constexpr (C > 1) break;
       }
-      mbar_drain(s_ready, 0u);
+      // every MMA has completed before TMEM is released (bounded, also after an abort)
+      mma_commit(done);
+      mbar_drain(done, 0u);
+      // copies of other CTAs into this one's P have landed (bounded)
+      if (C > 1 && !ok) mbar_drain(p_full, 0u);
     }
     __syncwarp();
   } else {
-    // ---------------- Q chunks (one thread)
-    if (lane == 0 && nc > 0) {
-      const uint32_t bytes = static_cast<uint32_t>(p.n_heads) * 128u;
-      int issued = 0;
-      for (int c = 0; c < kChunks; ++c) {
-        const int qs = c % F::NQS;
-        if (!mbar_wait(&q_empty[qs], ((c / F::NQS) & 1) ^ 1u, s_abort, err)) break;
-        mbar_arrive_expect_tx(&q_full[qs], bytes);
-        tma_load_2d(smem + F::OffQ + qs * kQBytes, &tmap_q, &q_full[qs], c == 0 ? kLatent : (c - 1) * 64,
-                    static_cast<int32_t>(t * p.n_heads));
-        issued = c + 1;
+    // ---------------- Q chunks and the next token's row list (one warp)
+    const uint32_t bytes = static_cast<uint32_t>(p.n_heads) * 128u;
+    uint32_t qn = 0, it = 0;  // Q chunks asked for so far, tokens done
+    bool ok = true;
+#pragma unroll 1
+    for (int t = t_first; ok && t < p.T; t += t_step, ++it) {
+      const int buf = F::Bufs == 2 ? it & 1 : 0;
+      if (used_slots(used_blocks(buf)) > 0) {
+        for (int c = 0; ok && c < kChunks; ++c, ++qn) {
+          const uint32_t qs = qn % F::NQS;
+          if (!(ok = mbar_wait_warp(&q_empty[qs], ((qn / F::NQS) & 1) ^ 1u, s_abort, err))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[qs], bytes);
+            tma_load_2d(smem + F::OffQ + qs * kQBytes, &tmap_q, &q_full[qs],
+                        c == 0 ? kLatent : (c - 1) * 64, t * p.n_heads);
+          }
+        }
       }
-      for (int c = max(0, issued - F::NQS); c < issued; ++c)  // never exit with loads in flight
-        mbar_drain(&q_full[c % F::NQS], (c / F::NQS) & 1);
+      if (C > 1 || !ok) break;
+      if (t + t_step < p.T) {  // that list's last readers arrived when they were done with O
+        if (it > 0) ok = mbar_wait_warp(o_free, (it - 1) & 1, s_abort, err);
+        if (!ok) break;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) load_rows(t + t_step, buf ^ 1, i * 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rows_full[buf ^ 1]);
+      }
+      // the Q ring lies over the V blocks: no load before P V is done
+      ok = mbar_wait_warp(o_ready, it & 1, s_abort, err);
+      if (ok && lane == 0) mbar_arrive(o_free);
     }
+    if (lane == 0)  // never exit with loads in flight
+      for (uint32_t i = qn > F::NQS ? qn - F::NQS : 0; i < qn; ++i)
+        mbar_drain(&q_full[i % F::NQS], (i / F::NQS) & 1);
     __syncwarp();
   }
   __syncwarp();
@@ -814,7 +910,9 @@ int launch(const CUtensorMap& tq, const CUtensorMap& to, const Params& p, int64_
     }
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_dependent(sparse_attn_q4_kernel<C>, static_cast<unsigned>(T * C), kThreads,
+  // One CTA an SM fits. More tokens than SMs: the CTAs stay and take the tokens in turn.
+  const int64_t grid = C == 1 ? std::min<int64_t>(T, kSms) : T * C;
+  return launch_dependent(sparse_attn_q4_kernel<C>, static_cast<unsigned>(grid), kThreads,
                           Cfg<C>::Smem, C, stream, tq, to, p);
 }
 
@@ -846,6 +944,7 @@ extern "C" int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, i
   p.weights = weights;
   p.err = ds4a::sparse_attention_error_word();
   if (!p.err) return DS4IDX_ERR_CUDA;
+  p.T = static_cast<int32_t>(T);
   p.n_heads = n_heads;
   p.n_sel = n_sel;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
