@@ -93,7 +93,7 @@ struct Cfg {
   static constexpr int OffX = OffRed + 2 * 4 * kH * 4;            // [2][C][128] of the cluster
   static constexpr int OffW = OffX + (C > 1 ? 2 * C * kH * 4 : 0);  // [4][NK] key weights
   static constexpr int OffBars = OffW + 4 * NK * 4;
-  static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 9;
+  static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 9 + C;
   static constexpr int OffMisc = OffBars + NumBars * 8;
   static constexpr int Smem = OffMisc + 16 + 1024;
   static_assert(GV * VStage == kVBytes && Smem <= 232448, "shared memory");
@@ -162,6 +162,15 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 // ---- other CTAs of the cluster
@@ -310,11 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_ready = v_empty + F::GV;
   uint64_t* m_full = s_ready + 1;
   uint64_t* l_full = s_ready + 2;
-  uint64_t* p_full = s_ready + 3;
   uint64_t* o_ready = s_ready + 4;
   uint64_t* o_free = s_ready + 5;     // O is read, S may be written again
   uint64_t* rows_full = s_ready + 6;  // [2] a later token's row list is in place
   uint64_t* done = s_ready + 8;       // every MMA has completed
+  uint64_t* p_full = s_ready + 9;     // [C] P of each CTA's slots is in place here
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + F::OffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + F::OffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -339,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(s_ready, 1);
     mbar_init(m_full, 4 * C);
     mbar_init(l_full, 4 * C);
-    mbar_init(p_full, 16 + (C > 1 ? 1 : 0));
+    for (int i = 0; i < C; ++i) mbar_init(&p_full[i], i == rank ? 16 : 1);
     mbar_init(o_ready, 1);
     mbar_init(o_free, 17);
     mbar_init(&rows_full[0], 1);
@@ -378,6 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 16; ++i)
       if (mask[i]) n = i / 2 + 1;
     return n;
+  };
+  // The order in which P V takes its blocks: this CTA's own first, then as the others' shares come.
+  auto block_at = [&](int i) {
+    constexpr int per = 8 / C;
+    return C == 1 ? i : ((rank - i / per) & (C - 1)) * per + i % per;
   };
   // This CTA's used slots (by 64).
   auto used_slots = [&](int blocks) { return min(F::NK, max(0, blocks * 64 - slot0)); };
@@ -519,7 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto v_load = [&](int n, uint32_t (&codes)[8], uint32_t& sc) {  // n: this group's n-th block
       if (n >= vblocks * F::Halves) return;
       const int half = n >= vblocks ? 1 : 0;
-      const int32_t r = s_rows[(gv + F::GV * (n - half * vblocks)) * 64 + vr];
+      int kb = gv + F::GV * (n - half * vblocks);
+      if constexpr (C > 1) {
+#pragma unroll
+        for (int i = 0, k = n; i < 8; ++i) {
+          const int b = block_at(i);
+          if (b % F::GV == gv && b < nblk && k-- == 0) kb = b;
+        }
+      }
+      const int32_t r = s_rows[kb * 64 + vr];
       const int chunk = rank * (F::DV / 64) + half * F::NB + vnb;
 #pragma unroll
       for (int j = 0; j < 8; ++j) codes[j] = kEmptyWord;
@@ -615,19 +637,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     worker_sync();
     l = (s_red[4 * kH + h] + s_red[5 * kH + h]) + (s_red[6 * kH + h] + s_red[7 * kH + h]);
     if constexpr (C > 1) {
-      if (tid < C && tid != rank && ok && nc > 0) {
-        copy_to_peer(peer(smem_u32(smem + (slot0 / 64) * kPBlock), tid),
-                     smem_u32(smem + (slot0 / 64) * kPBlock), (nc / 64) * kPBlock,
-                     peer(smem_u32(p_full), tid));
-      }
-      if (tid == 0) mbar_arrive_expect_tx(p_full, (nblk - nc / 64) * kPBlock);
-      if (lane == 0) mbar_arrive(p_full);
       if (part == 0) {
 #pragma unroll
         for (int r = 0; r < C; ++r) st_peer(peer(smem_u32(s_x + (C + rank) * kH + h), r), l);
         __syncwarp();
         if (lane < C) arrive_peer(peer(smem_u32(l_full), lane));
       }
+      if (lane == 0) mbar_arrive(&p_full[rank]);
+      if (warp == 15 && lane > 0 && lane < C) {
+        const int to = (rank + lane) & (C - 1);
+        if (ok && nc > 0)
+          copy_to_peer(peer(smem_u32(smem + (slot0 / 64) * kPBlock), to),
+                       smem_u32(smem + (slot0 / 64) * kPBlock), (nc / 64) * kPBlock,
+                       peer(smem_u32(&p_full[rank]), to));
+        // what the CTA `to` sends here
+        mbar_arrive_expect_tx(&p_full[to],
+                              min(8 / C, max(0, nblk - to * (8 / C))) * kPBlock);
+      }
+      __syncwarp();
       ok = __all_sync(0xffffffffu, wait_cluster(l_full, 0u, s_abort, err)) && ok;
       l = 0.f;
 #pragma unroll
@@ -662,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             (s_w[tid] + s_w[F::NK + tid]) + (s_w[2 * F::NK + tid] + s_w[3 * F::NK + tid]);
     }
     if constexpr (C == 1) {
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(&p_full[0]);
     }
     if (p.lse && rank == 0 && part == 0 && h < p.n_heads)
       p.lse[t * p.n_heads + h] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
@@ -727,103 +754,119 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) bulk_store_wait<0>();
   } else if (warp == kMmaWarp) {
-    // ---------------- MMA issue (one thread)
-    if (lane == 0) {
-      bool ok = true;
-      const uint64_t q0 = smem_desc_sw128(smem_u32(smem + F::OffQ));
-      const uint64_t k0 = smem_desc_sw128(smem_u32(smem));
-      const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV));
-      constexpr uint32_t o_idesc = instr_desc(1u, 1u, 128, F::NB * 64) | (1u << 16);  // B MN-major
-      uint32_t qn = 0, it = 0;  // Q chunks taken before this token, tokens done
-      int stage = 0;            // key stages taken
-      uint32_t vn[F::GV] = {};  // blocks taken from each V stage
-      auto q_ready = [&](uint32_t i) {
-        return mbar_wait(&q_full[i % F::NQS], (i / F::NQS) & 1, s_abort, err);
-      };
-      auto k_ready = [&] {
-        return mbar_wait(&k_full[(stage + 1) & 1], (stage >> 1) & 1, s_abort, err);
-      };
-      // S columns col .. col + n - 1 += Q chunk i x the n keys at byte `at` of the slots
-      auto product = [&](uint32_t i, int at, int col, int n, bool first) {
-        const uint32_t idesc = instr_desc(1u, 1u, 128, n);
-        const uint64_t qd = q0 + (i % F::NQS) * (kQBytes >> 4), kd = k0 + (at >> 4);
+    // ---------------- MMA issue: the warp waits together and one elected lane issues. Descriptors
+    // stay warp-uniform; formed in one thread's registers each MMA would wait for their moves to
+    // uniform registers, about 100 clocks, more than an MMA of N = 64 takes.
+    const bool lead = elect_one();
+    bool ok = true;
+    const uint64_t q0 = smem_desc_sw128(smem_u32(smem + F::OffQ));
+    const uint64_t k0 = smem_desc_sw128(smem_u32(smem));
+    const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV));
+    constexpr uint32_t o_idesc = instr_desc(1u, 1u, 128, F::NB * 64) | (1u << 16);  // B MN-major
+    uint32_t qn = 0, it = 0;  // Q chunks taken before this token, tokens done
+    uint32_t stage = 0;       // key stages taken
+    uint32_t vn[F::GV] = {};  // blocks taken from each V stage
+    auto q_ready = [&](uint32_t i) {
+      return mbar_wait_warp(&q_full[i % F::NQS], (i / F::NQS) & 1, s_abort, err);
+    };
+    auto k_ready = [&] {
+      return mbar_wait_warp(&k_full[(stage + 1) & 1], (stage >> 1) & 1, s_abort, err);
+    };
+    // S columns col .. col + n - 1 += Q chunk i x the n keys at byte `at` of the slots
+    auto product = [&](uint32_t i, int at, int col, int n, bool first) {
+      const uint32_t idesc = instr_desc(1u, 1u, 128, n);
+      const uint64_t qd = q0 + (i % F::NQS) * (kQBytes >> 4), kd = k0 + (at >> 4);
+      if (lead) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
           mma_bf16(tmem + col, qd + 2 * s, kd + 2 * s, idesc, first && s == 0 ? 0u : 1u);
-      };
+      }
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (lead) mma_commit(bar);
+    };
 #pragma unroll 1
-      for (int t = t_first; ok && t < p.T; t += t_step, ++it) {
-        const int buf = F::Bufs == 2 ? it & 1 : 0;
-        if (it > 0)
-          ok = mbar_wait(&rows_full[buf], ((it - 1) >> 1) & 1, s_abort, err) &&
-               mbar_wait(o_free, (it - 1) & 1, s_abort, err);
-        if (!ok) break;
-        tc_fence_after();
-        const int nblk = used_blocks(buf), nc = used_slots(nblk);
-        if (nc > 0) {
-          // Q chunks in the order rotary, 0 .. 7; key stages as the workers make them
-          const int parts = (nc + F::KS - 1) / F::KS;
-          ok = q_ready(qn) && k_ready();
-          if (ok) {
-            tc_fence_after();
-            for (int k = 0; k < parts; ++k)
-              product(qn, ((stage + 1) & 1) * F::Slot1 + k * F::KS * 128, k * F::KS,
-                      min(F::KS, nc - k * F::KS), true);
-            mma_commit(&q_empty[qn % F::NQS]);
-            mma_commit(&k_empty[(stage + 1) & 1]);
+    for (int t = t_first; ok && t < p.T; t += t_step, ++it) {
+      const int buf = F::Bufs == 2 ? it & 1 : 0;
+      if (it > 0)
+        ok = mbar_wait_warp(&rows_full[buf], ((it - 1) >> 1) & 1, s_abort, err) &&
+             mbar_wait_warp(o_free, (it - 1) & 1, s_abort, err);
+      if (!ok) break;
+      tc_fence_after();
+      const int nblk = used_blocks(buf), nc = used_slots(nblk);
+      if (nc > 0) {
+        // Q chunks in the order rotary, 0 .. 7; key stages as the workers make them
+        const int parts = (nc + F::KS - 1) / F::KS;
+        ok = q_ready(qn) && k_ready();
+        if (ok) {
+          tc_fence_after();
+          for (int k = 0; k < parts; ++k)
+            product(qn, ((stage + 1) & 1) * F::Slot1 + k * F::KS * 128, k * F::KS,
+                    min(F::KS, nc - k * F::KS), true);
+          commit(&q_empty[qn % F::NQS]);
+          commit(&k_empty[(stage + 1) & 1]);
+          ++stage;
+        }
+#pragma unroll 1
+        for (int c0 = 0; ok && c0 < 8; c0 += F::CW) {
+#pragma unroll 1
+          for (int k = 0; ok && k < parts; ++k) {
+            ok = k_ready();
+#pragma unroll
+            for (int c = 0; c < F::CW; ++c) {
+              const uint32_t i = qn + 1 + c0 + c;
+              if (!ok || (k == 0 && !(ok = q_ready(i)))) break;
+              tc_fence_after();
+              product(i, ((stage + 1) & 1) * F::Slot1 + c * F::KS * 128, k * F::KS,
+                      min(F::KS, nc - k * F::KS), false);
+              if (k == parts - 1) commit(&q_empty[i % F::NQS]);
+            }
+            commit(&k_empty[(stage + 1) & 1]);
             ++stage;
           }
-          for (int c0 = 0; ok && c0 < 8; c0 += F::CW) {
-            for (int k = 0; ok && k < parts; ++k) {
-              ok = k_ready();
-#pragma unroll
-              for (int c = 0; c < F::CW; ++c) {
-                const uint32_t i = qn + 1 + c0 + c;
-                if (!ok || (k == 0 && !(ok = q_ready(i)))) break;
-                tc_fence_after();
-                product(i, ((stage + 1) & 1) * F::Slot1 + c * F::KS * 128, k * F::KS,
-                        min(F::KS, nc - k * F::KS), false);
-                if (k == parts - 1) mma_commit(&q_empty[i % F::NQS]);
-              }
-              mma_commit(&k_empty[(stage + 1) & 1]);
-              ++stage;
-            }
-          }
-          qn += kChunks;
         }
-        mma_commit(s_ready);
-        if (ok) {
-          if constexpr (C > 1) ok = wait_cluster(p_full, it & 1, s_abort, err);
-          else ok = mbar_wait(p_full, it & 1, s_abort, err);
-        }
-        tc_fence_after();
-        for (int half = 0; half < F::Halves; ++half) {
+        qn += kChunks;
+      }
+      commit(s_ready);
+      if (C == 1 && ok) ok = mbar_wait_warp(&p_full[0], it & 1, s_abort, err);
+      for (int half = 0; half < F::Halves; ++half) {
 #pragma unroll 1
-          for (int kb0 = 0; ok && kb0 < nblk; kb0 += F::GV) {
+        for (int i0 = 0, taken = 0; ok && i0 < 8; i0 += F::GV) {
 #pragma unroll
-            for (int st = 0; st < F::GV; ++st) {
-              const int kb = kb0 + st;
-              if (!ok || kb >= nblk) break;
-              if (!(ok = mbar_wait(&v_full[st], vn[st] & 1, s_abort, err))) break;
-              ++vn[st];
-              tc_fence_after();
-              const uint64_t pd = k0 + kb * (kPBlock >> 4), vd = v0 + st * (F::VStage >> 4);
+          for (int j = 0; j < F::GV; ++j) {
+            const int kb = block_at(i0 + j);
+            if (!ok || kb >= nblk) continue;
+            const int st = C == 1 ? j : kb % F::GV;
+            if (C > 1 && !(ok = mbar_wait_warp(&p_full[kb / (8 / C)], 0u, s_abort, err))) break;
+            uint32_t use = 0;
+#pragma unroll
+            for (int v = 0; v < F::GV; ++v)
+              if (v == st) use = vn[v]++;
+            if (!(ok = mbar_wait_warp(&v_full[st], use & 1, s_abort, err))) break;
+            tc_fence_after();
+            const uint64_t pd = k0 + kb * (kPBlock >> 4), vd = v0 + st * (F::VStage >> 4);
+            if (lead) {
 #pragma unroll
               for (int s = 0; s < 4; ++s)
                 mma_bf16(tmem + F::OCol + half * 256, pd + 2 * s, vd + s * (16 * 128 >> 4), o_idesc,
-                         (kb | s) ? 1u : 0u);
-              mma_commit(&v_empty[st]);
+                         (taken | s) ? 1u : 0u);
             }
+            ++taken;
+            commit(&v_empty[st]);
           }
         }
-        mma_commit(o_ready);
-        if constexpr (C > 1) break;
       }
-      // every MMA has completed before TMEM is released (bounded, also after an abort)
-      mma_commit(done);
+      commit(o_ready);
+      if constexpr (C > 1) break;
+    }
+    // every MMA has completed before TMEM is released (bounded, also after an abort)
+    commit(done);
+    if (lead) {
       mbar_drain(done, 0u);
-      // copies of other CTAs into this one's P have landed (bounded)
-      if (C > 1 && !ok) mbar_drain(p_full, 0u);
+      // shares of P from other CTAs have landed (bounded)
+      if (C > 1 && !ok)
+        for (int i = 0; i < C; ++i)
+          if (i != rank) mbar_drain(&p_full[i], 0u);
     }
     __syncwarp();
   } else {
