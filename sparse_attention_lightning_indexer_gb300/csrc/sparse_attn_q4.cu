@@ -62,10 +62,12 @@ struct Cfg {
   static constexpr int CW = kWorkers / KS;              // 2, 2, 4, 8
   static constexpr int Stages = 8 / CW;                 // per key part
   static constexpr int KeyParts = NK / KS;              // 2 at C = 1
-  // Two slots: the rotary chunk and the odd latent stages in slot 1, the even ones in slot 0.
-  static constexpr int Slot1 = KS * CW * 128;
-  static constexpr int OffQ = Slot1 + (C == 8 ? NK * 128 : KS * CW * 128);
-  static constexpr int NQS = C == 8 ? 8 : 4;
+  static constexpr int KSlots = C == 8 ? 1 : 2;
+  static constexpr int KSlot = KS * CW * 128;           // 64 KB
+  static constexpr int OffQ = KSlots * KSlot;
+  // The ring of 16 KB items: a token's rotary key pieces, its rotary Q chunk, its other Q chunks.
+  static constexpr int NQS = C == 8 ? 9 : 5;
+  static constexpr int RP = NK < 128 ? NK : 128;        // keys of a rotary piece
   static constexpr int RingBytes = OffQ + NQS * kQBytes;
   static constexpr int Region = RingBytes > kOffV + kVBytes ? RingBytes : kOffV + kVBytes;
   // Lanes that share a row: 2 (64 bytes of codes) where a stage has two chunks of 256 keys.
@@ -93,7 +95,7 @@ struct Cfg {
   static constexpr int OffX = OffRed + 2 * 4 * kH * 4;            // [2][C][128] of the cluster
   static constexpr int OffW = OffX + (C > 1 ? 2 * C * kH * 4 : 0);  // [4][NK] key weights
   static constexpr int OffBars = OffW + 4 * NK * 4;
-  static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 9 + C;
+  static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 10 + C;
   static constexpr int OffMisc = OffBars + NumBars * 8;
   static constexpr int Smem = OffMisc + 16 + 1024;
   static_assert(GV * VStage == kVBytes && Smem <= 232448, "shared memory");
@@ -141,6 +143,13 @@ __device__ __forceinline__ void bulk_store_commit() {
 template <int N>
 __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout: blocks of 64 N
 // (64 keys x 128 bytes apart), atoms of 8 keys along K.
@@ -323,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_free = s_ready + 5;     // O is read, S may be written again
   uint64_t* rows_full = s_ready + 6;  // [2] a later token's row list is in place
   uint64_t* done = s_ready + 8;       // every MMA has completed
-  uint64_t* p_full = s_ready + 9;     // [C] P of each CTA's slots is in place here
+  uint64_t* rope_full = s_ready + 9;  // the rotary pieces are in place
+  uint64_t* p_full = s_ready + 10;    // [C] P of each CTA's slots is in place here
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + F::OffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + F::OffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -354,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&rows_full[0], 1);
     mbar_init(&rows_full[1], 1);
     mbar_init(done, 1);
+    mbar_init(rope_full, 16);
     *s_abort = 0u;
     fence_mbar_init();
   }
@@ -403,112 +414,111 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t scol = tmem + lane_base + part * F::CP;
-    int stage = 0;       // key stages made so far; stage i sits in slot (i + 1) % 2
+    int stage = 0;       // latent key stages made so far; stage i sits in slot i % 2
     uint32_t vuse = 0;   // V blocks this group has made so far
     uint32_t it = 0;     // tokens done
+    const int ch = F::RowLanes == 2 ? tid & 1 : tid / F::KS;  // this thread's (key, chunk)
+    const int kk = F::RowLanes == 2 ? tid >> 1 : tid % F::KS;
+    constexpr int Units = F::Stages * F::KeyParts;
+    constexpr int PF = Units < 2 ? Units : 2;  // codes in flight
+    // Scale words: a whole sector (both lanes of a row read it, each uses every other word) where a
+    // thread needs four of them, single words otherwise.
+    constexpr int SW = F::RowLanes == 2 ? 8 : F::Stages;
+    const uint8_t* krow[F::KeyParts] = {};     // null: an empty slot
+    uint32_t codes[PF][8], scales[F::KeyParts][SW] = {};
+    // unit u: chunk (u / KeyParts) * CW + ch of key part u % KeyParts
+    auto load = [&](int u, uint32_t (&c)[8]) {
+      const uint8_t* src = krow[u % F::KeyParts];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = kEmptyWord;
+      if (src) ld32(src + ((u / F::KeyParts) * F::CW + ch) * 32, c);
+    };
+    auto scale_of = [&](int k, int i) -> uint32_t {
+      if constexpr (SW == 8) return ch ? scales[k][2 * i + 1] : scales[k][2 * i];
+      else return scales[k][i];
+    };
+    // The rows, scales and first codes of a token whose list is in place.
+    auto fetch = [&](int buf) {
+      const int32_t* rows = reinterpret_cast<const int32_t*>(smem + F::OffRows) + buf * kK;
+#pragma unroll
+      for (int k = 0; k < F::KeyParts; ++k) {
+        const int32_t r = rows[slot0 + k * F::KS + kk];
+        krow[k] = r >= 0 ? p.cache + static_cast<int64_t>(r) * kRowBytes : nullptr;
+      }
+#pragma unroll
+      for (int u = 0; u < PF; ++u) load(u, codes[u]);
+#pragma unroll
+      for (int k = 0; k < F::KeyParts; ++k) {
+#pragma unroll
+        for (int i = 0; i < SW; ++i) scales[k][i] = 0u;
+        if (krow[k]) {
+          if constexpr (SW == 8) {
+            ld32(krow[k] + kOffScale, scales[k]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < SW; ++i)
+              scales[k][i] =
+                  *reinterpret_cast<const uint32_t*>(krow[k] + kOffScale + 4 * (i * F::CW + ch));
+          }
+        }
+      }
+    };
+    // The rotary dims of a token's keys, copied into the ring behind everything else: eight lanes a
+    // row, any row for an empty slot (its scores are masked). All warps share it: one warp's copies
+    // of 512 rows take about 11 K clocks, TMA gathers of four rows 13 K.
+    uint32_t qn = 0;     // ring items of the tokens before
+    auto fetch_rope = [&](int buf) {
+      const int32_t* rows = reinterpret_cast<const int32_t*>(smem + F::OffRows) + buf * kK + slot0;
+      const int used = used_slots(used_blocks(buf));
+#pragma unroll 4
+      for (int j = tid >> 3; j < used; j += kWorkers / 8)
+        cp_async16(smem + F::OffQ + (qn + j / F::RP) % F::NQS * kQBytes + (j % F::RP) * 128 +
+                       (((lane & 7) ^ (j & 7)) * 16),
+                   p.cache + static_cast<int64_t>(max(rows[j], 0)) * kRowBytes + kOffRope +
+                       (lane & 7) * 16);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch_rope(0);
+    fetch(0);
 #pragma unroll 1
     for (int t = t_first; t < p.T; t += t_step, ++it) {
     const int buf = F::Bufs == 2 ? it & 1 : 0;
-    if (it > 0 && ok) ok = mbar_wait_warp(&rows_full[buf], ((it - 1) >> 1) & 1, s_abort, err);
     const int32_t* s_rows = reinterpret_cast<const int32_t*>(smem + F::OffRows) + buf * kK;
     const uint32_t* s_mask = reinterpret_cast<const uint32_t*>(smem + F::OffMask) + buf * 16;
     const int nblk = used_blocks(buf), nc = used_slots(nblk);
-    // ---------------- A: key chunks, first the rotary chunk of all keys, then the latent stages
+    // ---------------- A: latent key stages
     const int parts = (nc + F::KS - 1) / F::KS;
     // The last token's output may still be read from the slots: its half in the slot that comes
     // first was sent first, so that half is waited for before a stage is made, the rest after it.
     int pending = it > 0 ? 2 : 0;
-    auto stage_begin = [&] {
-      if (C == 1 && pending > 0) {
-        --pending;
-        if (tid == 0) {
-          if (pending) bulk_store_wait<1>(); else bulk_store_wait<0>();
-        }
-        worker_sync();
-      }
-      if (ok) ok = mbar_wait_warp(&k_empty[(stage + 1) & 1], ((stage >> 1) & 1) ^ 1u, s_abort, err);
-    };
-    auto stage_end = [&] {
-      if (ok) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[(stage + 1) & 1]);
-      }
-      ++stage;
-    };
+    cp_async_wait<0>();
     if (nc > 0) {
-      const int ch = F::RowLanes == 2 ? tid & 1 : tid / F::KS;
-      const int kk = F::RowLanes == 2 ? tid >> 1 : tid % F::KS;
-      constexpr int Units = F::Stages * F::KeyParts;
-      constexpr int PF = Units < 3 ? Units : 3;  // codes in flight
-      const uint8_t* row[F::KeyParts];           // null: an empty slot
-      uint32_t codes[PF][8], scales[F::KeyParts][F::Stages];
-#pragma unroll
-      for (int k = 0; k < F::KeyParts; ++k) {
-        const int key = k * F::KS + kk;
-        const int32_t r = key < nc ? s_rows[slot0 + key] : -1;
-        row[k] = r >= 0 ? p.cache + static_cast<int64_t>(r) * kRowBytes : nullptr;
-      }
-      // unit u: chunk (u / KeyParts) * CW + ch of key part u % KeyParts
-      auto load = [&](int u, uint32_t (&c)[8]) {
-        const uint8_t* src = row[u % F::KeyParts];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = kEmptyWord;
-        if (src) ld32(src + ((u / F::KeyParts) * F::CW + ch) * 32, c);
-      };
-      // the rotary dims: four lanes a row, 32 bytes each
-      constexpr int RU = F::NK * 4 > kWorkers ? F::NK * 4 / kWorkers : 1;
-      uint32_t rope[RU][8];
-#pragma unroll
-      for (int i = 0; i < RU; ++i) {
-        const int key = (tid + i * kWorkers) >> 2;
-        const int32_t r = key < nc ? s_rows[slot0 + key] : -1;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) rope[i][j] = 0u;
-        if (r >= 0)
-          ld32(p.cache + static_cast<int64_t>(r) * kRowBytes + kOffRope + (tid & 3) * 32, rope[i]);
-      }
-#pragma unroll
-      for (int k = 0; k < F::KeyParts; ++k) {
-        if constexpr (F::RowLanes == 2) {
-          uint32_t all[8] = {};
-          if (row[k]) ld32(row[k] + kOffScale, all);
-#pragma unroll
-          for (int i = 0; i < F::Stages; ++i) scales[k][i] = ch ? all[2 * i + 1] : all[2 * i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < F::Stages; ++i)
-            scales[k][i] = row[k] ? *reinterpret_cast<const uint32_t*>(row[k] + kOffScale +
-                                                                       4 * (i * F::CW + ch))
-                                  : 0u;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < PF; ++u) load(u, codes[u]);
-      stage_begin();
-      if (ok) {
-#pragma unroll
-        for (int i = 0; i < RU; ++i) {
-          const int key = (tid + i * kWorkers) >> 2;
-          uint8_t* dst = smem + ((stage + 1) & 1) * F::Slot1 + key * 128;
-          if (key < nc) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<uint4*>(dst + (((2 * (tid & 3) + h) ^ (key & 7)) * 16)) = make_uint4(
-                  rope[i][4 * h], rope[i][4 * h + 1], rope[i][4 * h + 2], rope[i][4 * h + 3]);
-          }
-        }
-      }
-      stage_end();
+      qn += kChunks + (nc + F::RP - 1) / F::RP;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rope_full);
 #pragma unroll
       for (int u = 0; u < Units; ++u) {
         const int kp = u % F::KeyParts;
         if (kp < parts) {
-          stage_begin();
-          if (ok && kp * F::KS + kk < nc)
-            store_chunk<F::RowLanes>(smem + ((stage + 1) & 1) * F::Slot1 + ch * (F::KS * 128), kk,
-                                     codes[u % PF], scales[kp][u / F::KeyParts], ch);
-          stage_end();
+          if (C == 1 && pending > 0) {
+            --pending;
+            if (tid == 0) {
+              if (pending) bulk_store_wait<1>(); else bulk_store_wait<0>();
+            }
+            worker_sync();
+          }
+          const int slot = stage & (F::KSlots - 1);
+          if (ok) ok = mbar_wait_warp(&k_empty[slot], ((stage >> 1) & 1) ^ 1u, s_abort, err);
+          if (ok) {
+            if (kp * F::KS + kk < nc)
+              store_chunk<F::RowLanes>(smem + slot * F::KSlot + ch * (F::KS * 128), kk,
+                                       codes[u % PF], scale_of(kp, u / F::KeyParts), ch);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[slot]);
+          }
+          ++stage;
         }
         if (u + PF < Units) load(u + PF, codes[u % PF]);
       }
@@ -660,8 +670,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < C; ++r) l += s_x[(C + r) * kH + h];
     }
-    if (p.weights) {
-      // w_j = sum over heads of exp2(s - m) / l, once more from S (intact until P V starts)
+    // w_j = sum over heads of exp2(s - m) / l, once more from S: at C = 1 before P V may write there,
+    // in a cluster (S and O apart) while P V runs.
+    auto key_weights = [&] {
       const float off = l > 0.f && h < p.n_heads ? mm + __log2f(l) : __int_as_float(0x7f800000);
       for (int i = 0; i < F::CP / F::W; ++i) {
         float v[F::W];
@@ -687,7 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid < F::NK && slot0 + tid < p.n_sel)
         p.weights[static_cast<int64_t>(t) * p.n_sel + slot0 + tid] =
             (s_w[tid] + s_w[F::NK + tid]) + (s_w[2 * F::NK + tid] + s_w[3 * F::NK + tid]);
-    }
+    };
+    if (C == 1 && p.weights) key_weights();
     if constexpr (C == 1) {
       if (lane == 0) mbar_arrive(&p_full[0]);
     }
@@ -701,15 +713,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       v_load(n + 2, vc[1], vs[1]);
       v_store(n + 1, vc[0], vs[0]);
     }
+    if (C > 1 && p.weights) key_weights();
+    if constexpr (C == 1) {  // the next token's first reads, behind P V and the output
+      if (t + t_step < p.T) {
+        if (ok) ok = mbar_wait_warp(&rows_full[buf ^ 1], (it >> 1) & 1, s_abort, err);
+        if (ok) fetch(buf ^ 1);
+      }
+    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     if (ok) ok = mbar_wait_warp(o_ready, it & 1, s_abort, err);
     tc_fence_after();
+    if (C == 1 && ok && t + t_step < p.T) fetch_rope(buf ^ 1);  // (the ring lies over the V blocks)
     // Output columns of 64 dims each, in F::Halves runs; at C = 1 a run fills one key slot, and the
     // run in the slot that the next token's first stage takes goes first.
     constexpr int RunCols = F::DV / F::Halves, PartCols = RunCols / 4;
 #pragma unroll 1
     for (int run = 0; run < F::Halves; ++run) {
-      const int half = C == 1 ? ((stage + 1) & 1) ^ run : run;
+      const int half = C == 1 ? (stage & 1) ^ run : run;
       if (ok) {
 #pragma unroll 1
         for (int i = 0; i < PartCols / F::OW; ++i) {
@@ -763,16 +783,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k0 = smem_desc_sw128(smem_u32(smem));
     const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV));
     constexpr uint32_t o_idesc = instr_desc(1u, 1u, 128, F::NB * 64) | (1u << 16);  // B MN-major
-    uint32_t qn = 0, it = 0;  // Q chunks taken before this token, tokens done
-    uint32_t stage = 0;       // key stages taken
+    uint32_t qn = 0, it = 0;  // ring items taken, tokens done
+    uint32_t stage = 0;       // latent key stages taken
     uint32_t vn[F::GV] = {};  // blocks taken from each V stage
+    uint32_t q_phase = 0;     // bit: the parity of the next Q chunk in a ring place
+    uint32_t ropes = 0;       // rotary pieces taken (tokens)
     auto q_ready = [&](uint32_t i) {
-      return mbar_wait_warp(&q_full[i % F::NQS], (i / F::NQS) & 1, s_abort, err);
+      const uint32_t at = i % F::NQS, parity = q_phase >> at & 1u;
+      q_phase ^= 1u << at;
+      return mbar_wait_warp(&q_full[at], parity, s_abort, err);
     };
     auto k_ready = [&] {
-      return mbar_wait_warp(&k_full[(stage + 1) & 1], (stage >> 1) & 1, s_abort, err);
+      return mbar_wait_warp(&k_full[stage & (F::KSlots - 1)], (stage >> 1) & 1, s_abort, err);
     };
-    // S columns col .. col + n - 1 += Q chunk i x the n keys at byte `at` of the slots
+    // S columns col .. col + n - 1 += ring item i (a Q chunk) x the n keys at byte `at`
     auto product = [&](uint32_t i, int at, int col, int n, bool first) {
       const uint32_t idesc = instr_desc(1u, 1u, 128, n);
       const uint64_t qd = q0 + (i % F::NQS) * (kQBytes >> 4), kd = k0 + (at >> 4);
@@ -795,37 +819,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int nblk = used_blocks(buf), nc = used_slots(nblk);
       if (nc > 0) {
-        // Q chunks in the order rotary, 0 .. 7; key stages as the workers make them
-        const int parts = (nc + F::KS - 1) / F::KS;
-        ok = q_ready(qn) && k_ready();
-        if (ok) {
-          tc_fence_after();
-          for (int k = 0; k < parts; ++k)
-            product(qn, ((stage + 1) & 1) * F::Slot1 + k * F::KS * 128, k * F::KS,
-                    min(F::KS, nc - k * F::KS), true);
+        // the rotary chunk, keys in pieces from the ring
+        const uint32_t rope = qn + (nc + F::RP - 1) / F::RP;
+        ok = mbar_wait_warp(rope_full, ropes++ & 1, s_abort, err) && q_ready(rope);
+        tc_fence_after();
+        for (int k = 0; ok && k < nc; k += F::RP, ++qn) {
+          product(rope, F::OffQ + (qn % F::NQS) * kQBytes, k, min(F::RP, nc - k), true);
           commit(&q_empty[qn % F::NQS]);
-          commit(&k_empty[(stage + 1) & 1]);
-          ++stage;
         }
+        commit(&q_empty[rope % F::NQS]);
+        qn = rope + 1;
+        // the latent chunks, key stages as the workers make them
+        const int parts = (nc + F::KS - 1) / F::KS;
 #pragma unroll 1
         for (int c0 = 0; ok && c0 < 8; c0 += F::CW) {
 #pragma unroll 1
           for (int k = 0; ok && k < parts; ++k) {
             ok = k_ready();
+            const int slot = stage & (F::KSlots - 1);
 #pragma unroll
             for (int c = 0; c < F::CW; ++c) {
-              const uint32_t i = qn + 1 + c0 + c;
+              const uint32_t i = qn + c0 + c;
               if (!ok || (k == 0 && !(ok = q_ready(i)))) break;
               tc_fence_after();
-              product(i, ((stage + 1) & 1) * F::Slot1 + c * F::KS * 128, k * F::KS,
-                      min(F::KS, nc - k * F::KS), false);
+              product(i, slot * F::KSlot + c * F::KS * 128, k * F::KS, min(F::KS, nc - k * F::KS),
+                      false);
               if (k == parts - 1) commit(&q_empty[i % F::NQS]);
             }
-            commit(&k_empty[(stage + 1) & 1]);
+            commit(&k_empty[slot]);
             ++stage;
           }
         }
-        qn += kChunks;
+        qn += kChunks - 1;
       }
       commit(s_ready);
       if (C == 1 && ok) ok = mbar_wait_warp(&p_full[0], it & 1, s_abort, err);
@@ -872,19 +897,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- Q chunks and the next token's row list (one warp)
     const uint32_t bytes = static_cast<uint32_t>(p.n_heads) * 128u;
-    uint32_t qn = 0, it = 0;  // Q chunks asked for so far, tokens done
+    uint32_t qn = 0, it = 0;  // ring items so far, tokens done
+    uint32_t q_phase = 0, q_used = 0;  // bits: parity of the next Q chunk in a place, places used
     bool ok = true;
 #pragma unroll 1
     for (int t = t_first; ok && t < p.T; t += t_step, ++it) {
       const int buf = F::Bufs == 2 ? it & 1 : 0;
-      if (used_slots(used_blocks(buf)) > 0) {
-        for (int c = 0; ok && c < kChunks; ++c, ++qn) {
+      const int nc = used_slots(used_blocks(buf));
+      const int pieces = (nc + F::RP - 1) / F::RP;
+      if (nc > 0) {
+        qn += pieces;  // made by the workers
+        for (int i = 0; i < kChunks; ++i, ++qn) {
           const uint32_t qs = qn % F::NQS;
           if (!(ok = mbar_wait_warp(&q_empty[qs], ((qn / F::NQS) & 1) ^ 1u, s_abort, err))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&q_full[qs], bytes);
             tma_load_2d(smem + F::OffQ + qs * kQBytes, &tmap_q, &q_full[qs],
-                        c == 0 ? kLatent : (c - 1) * 64, t * p.n_heads);
+                        i == 0 ? kLatent : (i - 1) * 64, t * p.n_heads);
+            q_phase ^= 1u << qs;
+            q_used |= 1u << qs;
           }
         }
       }
@@ -902,8 +933,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && lane == 0) mbar_arrive(o_free);
     }
     if (lane == 0)  // never exit with loads in flight
-      for (uint32_t i = qn > F::NQS ? qn - F::NQS : 0; i < qn; ++i)
-        mbar_drain(&q_full[i % F::NQS], (i / F::NQS) & 1);
+      for (int i = 0; i < F::NQS; ++i)
+        if (q_used >> i & 1u) mbar_drain(&q_full[i], (q_phase >> i & 1u) ^ 1u);
     __syncwarp();
   }
   __syncwarp();
