@@ -231,12 +231,18 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity,
   }
 }
 
+// 16 bytes to a shared-memory address.
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
 // One 64-dim chunk of a latent row to the 128 swizzled bytes of row `r` at `base`. Where several
 // lanes share a row (each its own chunk, chunks a multiple of 1 KB apart), lane x of them writes
 // its 16-byte pieces in the order u ^ x * 8 / kLanes, so that the eight lanes of a store
 // wavefront hit eight different banks.
 template <int kLanes>
-__device__ __forceinline__ void store_chunk(uint8_t* base, int r, uint32_t (&codes)[8],
+__device__ __forceinline__ void store_chunk(uint32_t base, int r, uint32_t (&codes)[8],
                                             uint32_t scales, int x) {
   int ord = 0;
   if constexpr (kLanes == 2) {
@@ -266,16 +272,14 @@ __device__ __forceinline__ void store_chunk(uint8_t* base, int r, uint32_t (&cod
       }
     scales = __byte_perm(scales, 0, 0x3210u ^ (0x1111u * x));  // groups g ^ x
   }
-  uint8_t* row = base + r * 128;
-  const int sw = (r & 7) ^ ord;
+  const uint32_t at = base + r * 128 + (((r & 7) ^ ord) * 16);  // rows are 128-byte aligned
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const uint32_t s2 = scale_bf16x2((scales >> (8 * g)) & 0xFFu), c2 = offset_bf16x2(s2);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int u = 2 * g + h;
-      *reinterpret_cast<uint4*>(row + ((u ^ sw) * 16)) = word_to_bf16(codes[u], s2, c2);
-    }
+    // the scale byte in both halves, to bf16 (q4_format.cuh)
+    const uint32_t s2 = __byte_perm(scales, 0, 0x4040u | (g << 8) | g) * 16u + 0x35803580u;
+    const uint32_t c2 = offset_bf16x2(s2);
+    st_shared16(at ^ (32 * g), word_to_bf16(codes[2 * g], s2, c2));
+    st_shared16(at ^ (32 * g + 16), word_to_bf16(codes[2 * g + 1], s2, c2));
   }
 }
 
@@ -315,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every CTA of a cluster has the same dynamic shared-memory base, so the offsets agree
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t smem0 = smem_u32(smem);
   float* s_red = reinterpret_cast<float*>(smem + F::OffRed);
   float* s_x = reinterpret_cast<float*>(smem + F::OffX);
   float* s_w = reinterpret_cast<float*>(smem + F::OffW);
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) ok = mbar_wait_warp(&k_empty[slot], ((stage >> 1) & 1) ^ 1u, s_abort, err);
           if (ok) {
             if (kp * F::KS + kk < nc)
-              store_chunk<F::RowLanes>(smem + slot * F::KSlot + ch * (F::KS * 128), kk,
+              store_chunk<F::RowLanes>(smem0 + slot * F::KSlot + ch * (F::KS * 128), kk,
                                        codes[u % PF], scale_of(kp, u / F::KeyParts), ch);
             fence_proxy_async_smem();
             __syncwarp();
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = mbar_wait_warp(&v_empty[gv], (vuse & 1) ^ 1u, s_abort, err);
       ++vuse;
       if (!ok) return;
-      store_chunk<F::VLanes>(smem + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc, vnb);
+      store_chunk<F::VLanes>(smem0 + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc, vnb);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[gv]);
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     v_load(1, vc[1], vs[1]);
     if (ok) ok = mbar_wait_warp(s_ready, it & 1, s_abort, err);
     tc_fence_after();
-    float mx = kNegInf;
+    float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
     if (ok) {
       for (int i = 0; i < nch; ++i) {
         uint32_t r[F::W];
@@ -585,14 +590,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t vm = mask_of(i);
         if (vm == kAll) {
 #pragma unroll
-          for (int j = 0; j < F::W; ++j) mx = fmaxf(mx, __uint_as_float(r[j]));
+          for (int j = 0; j < F::W; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
         } else {
 #pragma unroll
           for (int j = 0; j < F::W; ++j)
-            mx = fmaxf(mx, ((vm >> j) & 1u) ? __uint_as_float(r[j]) : kNegInf);
+            mx4[j & 3] = fmaxf(mx4[j & 3], ((vm >> j) & 1u) ? __uint_as_float(r[j]) : kNegInf);
         }
       }
     }
+    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
     s_red[part * kH + h] = mx * p.scale_log2;  // scale > 0: the maximum of the scaled scores
     worker_sync();
     float m = fmaxf(fmaxf(s_red[h], s_red[kH + h]), fmaxf(s_red[2 * kH + h], s_red[3 * kH + h]));
@@ -632,13 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[j / 2] = pack_bf16x2(p0, p1);
         }
         const int s = slot0 + part * F::CP + i * F::W;
-        uint8_t* row = smem + (s >> 6) * kPBlock + h * 128;
+        const uint32_t at = smem0 + (s >> 6) * kPBlock + h * 128 + ((h & 7) ^ ((s & 63) >> 3)) * 16;
 #pragma unroll
-        for (int u = 0; u < F::W / 8; ++u) {
-          const int cc = ((s & 63) >> 3) + u;
-          *reinterpret_cast<uint4*>(row + ((cc ^ (h & 7)) * 16)) =
-              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-        }
+        for (int u = 0; u < F::W / 8; ++u)
+          st_shared16(at ^ (16 * u), make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]));
       }
     }
     s_red[4 * kH + part * kH + h] = l;
@@ -743,13 +746,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < F::OW; j += 2)
             pk[j / 2] = nblk > 0 ? pack_bf16x2(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv)
                                  : 0u;
-          uint8_t* row = smem + F::OffO + (col >> 6) * kPBlock + h * 128;
+          const uint32_t at =
+              smem0 + F::OffO + (col >> 6) * kPBlock + h * 128 + ((h & 7) ^ ((col & 63) >> 3)) * 16;
 #pragma unroll
-          for (int u = 0; u < F::OW / 8; ++u) {
-            const int cc = ((col & 63) >> 3) + u;
-            *reinterpret_cast<uint4*>(row + ((cc ^ (h & 7)) * 16)) =
-                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-          }
+          for (int u = 0; u < F::OW / 8; ++u)
+            st_shared16(at ^ (16 * u),
+                        make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]));
         }
       }
       fence_proxy_async_smem();
