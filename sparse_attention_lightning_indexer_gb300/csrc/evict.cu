@@ -5,12 +5,13 @@
 // in which the atomics of a chunk's tokens arrive; fp32 atomics would not give that.
 //
 // Choice. Of a sequence's rows between its sinks and its recent ones the need largest totals are
-// kept, ties to the lower position. A cluster of CTAs owns a sequence, each CTA a contiguous part
-// and each of its warps a contiguous segment. A radix select from the highest bit in which any two
-// totals differ, 11 bits a pass: counts per digit in shared memory, summed over the cluster's
-// shared memories, give the digit that holds the cut; a pass ends the search early when the
-// whole digit is kept. Then one pass counts kept rows per segment and one writes them in order.
-// Few bytes (8 per row, read from L2 after the first pass): bound by the latency of the passes.
+// kept, ties to the lower position. One CTA or a cluster of 8 owns a sequence, each CTA a contiguous
+// part, each warp a contiguous segment, kept on chip up to 196608 totals. A radix select of 11 bits
+// a pass: counts per digit in shared memory, each CTA sums a slice of the bins over the cluster, all
+// scan the slice that holds the cut. The first digit is the leading bit's place and the five bits
+// behind it, so the pass separates totals of any size; a pass ends the search when the whole digit
+// is kept. Then one pass counts the kept rows per segment and one writes them in order. The bytes
+// are few (8 a row, read once); bound by the instructions of the passes and the cluster's barriers.
 //
 // Move. Bound by HBM: each kept row is read and written once, in the widest units its size and
 // addresses allow, by CTAs that take about 16 KB of one array each.
@@ -72,27 +73,33 @@ __device__ __forceinline__ uint32_t ld_peer32(const void* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_u32(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ uint64_t ld_peer64(const void* p, uint32_t rank) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer_u32(p, rank)) : "memory");
-  return v;
-}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// The bits of a key above the undecided ones.
-__device__ __forceinline__ uint64_t above(uint64_t key, int undecided) {
-  return undecided >= 64 ? 0ull : key >> undecided;
+// First digit of a total: 0 for negative ones, 1 for zero, else 32 bins per power of two by the five
+// bits behind the leading one (of the truncating conversion to fp32, which keeps 23). Totals
+// spread over many powers of two, so equal widths would put most of them into a few bins.
+__device__ __forceinline__ uint32_t first_digit(uint64_t key) {
+  const uint64_t t = key & ~(1ull << 63);
+  const uint32_t f = __float_as_uint(__ull2float_rz(t)) >> 18;
+  const uint32_t digit = t ? f - (127 * 32 - 2) : 1u;
+  return key >> 63 ? digit : 0u;
 }
 
+constexpr int kOnChip = 24;  // keys of a thread in shared memory
+
+// K = 4: a thread's keys (at most four) are in registers. K = 0: the first kOnChip are in shared
+// memory, the rest (sequences past 24576 totals a CTA) are read again by every pass.
+template <int K>
 __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ uint32_t s_hist[2][kBins];
-  __shared__ uint64_t s_diff;
+  __shared__ uint32_t s_sums[2][kBins / 2];  // this CTA's slice, summed over the cluster
   __shared__ uint32_t s_warp[kWarps];
   __shared__ uint32_t s_gt[kWarps], s_eq[kWarps];
-  __shared__ uint32_t s_cut[3];   // digit, rows above it, rows in it
-  __shared__ uint32_t s_tot[2];   // this CTA's kept-for-sure and tied rows
+  __shared__ uint32_t s_cut[3];       // digit, rows above it, rows in it
+  __shared__ uint32_t s_slice[2];     // rows in this CTA's slice of the bins
+  __shared__ uint32_t s_tot[2];       // this CTA's kept-for-sure and tied rows
   griddep_wait();
   griddep_launch_dependents();
   const int C = p.cluster;
@@ -118,101 +125,167 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
 
   const int64_t* mid = p.total + p.start[b] + sink;
   const int32_t m = static_cast<int32_t>(n - sink - recent);  // > need
-  const int32_t per = static_cast<int32_t>((m + C - 1) / C);
-  const int32_t c0 = static_cast<int32_t>(
-      min(static_cast<int64_t>(m), static_cast<int64_t>(rank) * per));
-  const int32_t c1 = static_cast<int32_t>(min(static_cast<int64_t>(m), static_cast<int64_t>(c0) + per));
-  auto key_at = [&](int32_t i) { return static_cast<uint64_t>(mid[i]) ^ (1ull << 63); };
-
-  const uint64_t key0 = key_at(0);
-  if (tid == 0) s_diff = 0;
-  for (int i = tid; i < 2 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0;
-  __syncthreads();
-  uint64_t diff = 0;
+  const int32_t per = (m + C - 1) / C;
+  const int32_t c0 = min(m, static_cast<int32_t>(rank) * per), c1 = min(m, c0 + per);
+  const int32_t seg = ((c1 - c0 + kWarps - 1) / kWarps + 31) & ~31;
+  const int32_t w0 = min(c1, c0 + warp * seg), w1 = min(c1, w0 + seg);
+  extern __shared__ uint64_t s_keys[];  // [kOnChip][kThreads]
+  uint64_t keys[4];
+  auto read = [&](int32_t i) { return i < w1 ? static_cast<uint64_t>(mid[i]) ^ (1ull << 63) : 0; };
+  if constexpr (K == 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) keys[u] = read(w0 + u * 32 + lane);
+  } else {
+    // (asynchronous copies, all in flight together; the sign is turned when a key is used)
+    for (int u = 0; u < kOnChip; ++u) {
+      const int32_t i = w0 + u * 32 + lane;
+      if (i < w1)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                         smem_u32(s_keys + u * kThreads + tid)),
+                     "l"(mid + i)
+                     : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // each thread reads only its own copies
+  }
+  // f(key, position, in): every key of this warp's segment, all lanes together
+  auto each = [&](auto&& f) {
+    if constexpr (K == 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (w0 + u * 32 >= w1) break;
+        f(keys[u], w0 + u * 32 + lane, w0 + u * 32 + lane < w1);
+      }
+    } else {
+      int32_t i0 = w0;
 #pragma unroll 4
-  for (int32_t i = c0 + tid; i < c1; i += kThreads) diff |= key_at(i) ^ key0;
-  for (int o = 16; o; o >>= 1) diff |= __shfl_xor_sync(0xffffffffu, diff, o);
-  if (lane == 0 && diff) atomicOr(reinterpret_cast<unsigned long long*>(&s_diff), diff);
-  cluster_sync();
-  diff = 0;
-  for (int r = 0; r < C; ++r) diff |= ld_peer64(&s_diff, r);
+      for (int u = 0; u < kOnChip; ++u, i0 += 32) {
+        if (i0 >= w1) break;
+        f(s_keys[u * kThreads + tid] ^ (1ull << 63), i0 + lane, i0 + lane < w1);
+      }
+#pragma unroll 8
+      for (; i0 < w1; i0 += 32) f(read(i0 + lane), i0 + lane, i0 + lane < w1);
+    }
+  };
 
-  int top = diff ? 64 - __clzll(diff) : 0;  // undecided low bits
-  uint64_t prefix = above(key0, top);
+  for (int i = tid; i < 2 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0;
+  for (int i = tid; i < kBins; i += kThreads) (&s_sums[0][0])[i] = 0;
+  __syncthreads();
+  int top = 64;          // undecided low bits of a key; 64: no pass done yet
+  uint64_t lo = 0, hi = ~0ull;  // the keys that share the decided bits
   int buf = 0;
   bool whole = false;
   while (top > 0 && !whole) {
+    const bool first = top == 64;
     const int d = min(kDigit, top), shift = top - d;
     uint32_t* hist = s_hist[buf];
-    for (int32_t i0 = c0; i0 < c1; i0 += kThreads * 4) {
-      uint64_t k[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int32_t i = i0 + u * kThreads + tid;
-        k[u] = i < c1 ? key_at(i) : 0;
+    each([&](uint64_t key, int32_t, bool in) {
+      in = in && key >= lo && key <= hi;
+      const uint32_t act = __ballot_sync(0xffffffffu, in);
+      if (!act) return;
+      const uint32_t digit =
+          first ? first_digit(key) : static_cast<uint32_t>(key >> shift) & ((1u << d) - 1);
+      // many rows share one total (rows never attended): one add if the whole warp does
+      const uint32_t d0 = __shfl_sync(0xffffffffu, digit, __ffs(act) - 1);
+      if (__all_sync(0xffffffffu, !in || digit == d0)) {
+        if (lane == 0) atomicAdd(hist + d0, __popc(act));
+      } else if (in) {
+        atomicAdd(hist + digit, 1u);
       }
+    });
+    // Sums over the cluster: CTA r adds up a slice of the bins (a peer's count a thread, so that
+    // the loads' latencies overlap) and publishes the slice's total; then every CTA finds the slice
+    // that holds the cut, and the digit in it.
+    const int slice = kBins / C;
+    uint32_t* sums = s_sums[buf];
+    uint32_t base = 0;      // rows in the slices above the one that holds the cut
+    int owner = 0;
+    if (C == 1) {
+      __syncthreads();
+    } else {
+      cluster_sync();
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int32_t i = i0 + u * kThreads + tid;
-        const bool in = i < c1 && above(k[u], top) == prefix;
-        const uint32_t digit = static_cast<uint32_t>(k[u] >> shift) & ((1u << d) - 1);
-        // many rows share one total (rows never attended): one add for the first lane's digit
-        const uint32_t act = __ballot_sync(0xffffffffu, in);
-        if (act) {
-          const int lead = __ffs(act) - 1;
-          const uint32_t dl = __shfl_sync(0xffffffffu, digit, lead);
-          const uint32_t same = __ballot_sync(0xffffffffu, in && digit == dl);
-          if (lane == lead) atomicAdd(hist + dl, __popc(same));
-          if (in && digit != dl) atomicAdd(hist + digit, 1u);
-        }
+      for (int q = tid; q < kBins; q += kThreads) {
+        const uint32_t v = ld_peer32(hist + rank * slice + q % slice, q / slice);
+        if (v) atomicAdd(sums + q % slice, v);
       }
+      __syncthreads();
+      uint32_t sum = tid < slice ? sums[tid] : 0;  // slice <= 1024 = threads
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0) s_warp[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        sum = __reduce_add_sync(0xffffffffu, s_warp[lane]);
+        if (lane == 0) s_slice[buf] = sum;
+      }
+      cluster_sync();
+      // lane l: the slice C - 1 - l, so that a running sum counts the rows above
+      const uint32_t t = lane < C ? ld_peer32(&s_slice[buf], C - 1 - lane) : 0;
+      uint32_t inc = t;
+      for (int o = 1; o < 16; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const int at = __ffs(__ballot_sync(0xffffffffu, lane < C && inc >= need)) - 1;
+      base = __shfl_sync(0xffffffffu, inc - t, at);
+      owner = C - 1 - at;
     }
-    cluster_sync();
-    // bins in falling order, two a thread: their sums over the cluster, then a scan
-    const int b0 = kBins - 1 - 2 * tid, b1 = b0 - 1;
+    // the other buffers were last read before this pass's first barrier
+    for (int i = tid; i < kBins; i += kThreads) s_hist[buf ^ 1][i] = 0;
+    for (int i = tid; i < kBins / 2; i += kThreads) s_sums[buf ^ 1][i] = 0;
+    // that slice's bins in falling order, two a thread at C = 1, else at most one or two
+    const int per_thread = (slice + kThreads - 1) / kThreads;
+    const int bin0 = owner * slice + slice - 1 - per_thread * tid;  // this thread's first bin
     uint32_t h0 = 0, h1 = 0;
-    for (int r = 0; r < C; ++r) {
-      h0 += ld_peer32(hist + b0, r);
-      h1 += ld_peer32(hist + b1, r);
+    if (per_thread * tid < slice) {
+      h0 = C > 1 ? ld_peer32(sums + bin0 - owner * slice, owner) : hist[bin0];
+      if (per_thread == 2) h1 = hist[bin0 - 1];  // (C = 1)
     }
     uint32_t inc = h0 + h1;
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
+    __syncthreads();  // (s_warp is free again)
     if (lane == 31) s_warp[warp] = inc;
-    // the other buffer was last read before this pass's cluster barrier
-    for (int i = tid; i < kBins; i += kThreads) s_hist[buf ^ 1][i] = 0;
     __syncthreads();
-    uint32_t base = 0;
-    for (int w = 0; w < warp; ++w) base += s_warp[w];
-    const uint32_t ex = base + inc - h0 - h1;
+    const uint32_t below = lane < warp ? s_warp[lane] : 0;
+    const uint32_t ex = base + __reduce_add_sync(0xffffffffu, below) + inc - h0 - h1;
     if (ex < need && need <= ex + h0) {
-      s_cut[0] = b0;
+      s_cut[0] = bin0;
       s_cut[1] = ex;
       s_cut[2] = h0;
     } else if (ex + h0 < need && need <= ex + h0 + h1) {
-      s_cut[0] = b1;
+      s_cut[0] = bin0 - 1;
       s_cut[1] = ex + h0;
       s_cut[2] = h1;
     }
     __syncthreads();
-    prefix = (prefix << d) | s_cut[0];
+    const uint32_t digit = s_cut[0];
     need -= s_cut[1];
     whole = need == s_cut[2];
-    top = shift;
+    if (!first) {
+      lo += static_cast<uint64_t>(digit) << shift;
+      top = shift;
+    } else if (digit == 0) {         // negative totals: bit 63 is decided
+      top = 63;
+    } else if (digit == 1) {         // zero
+      lo = 1ull << 63;
+      top = 0;
+    } else {                         // leading bit e, then five bits (all of them if e < 5)
+      const int e = (digit - 2) / 32;
+      const uint32_t lead = 32 + (digit - 2) % 32;
+      top = max(e - 5, 0);
+      lo = (1ull << 63) | (e >= 5 ? static_cast<uint64_t>(lead) << top : lead >> (5 - e));
+    }
+    hi = lo + ((1ull << top) - 1);
     buf ^= 1;
   }
   // kept: above the cut, and of those at it the first `need` in position order
-  const int32_t seg = ((c1 - c0 + kWarps - 1) / kWarps + 31) & ~31;
-  const int32_t w0 = min(c1, c0 + warp * seg), w1 = min(c1, w0 + seg);
   uint32_t ng = 0, ne = 0;
-#pragma unroll 4
-  for (int32_t i = w0 + lane; i < w1; i += 32) {
-    const uint64_t a = above(key_at(i), top);
-    ng += a > prefix;
-    ne += a == prefix;
-  }
+  each([&](uint64_t key, int32_t, bool in) {
+    ng += in && key > hi;
+    ne += in && key >= lo && key <= hi;
+  });
   ng = __reduce_add_sync(0xffffffffu, ng);
   ne = __reduce_add_sync(0xffffffffu, ne);
   if (lane == 0) {
@@ -220,38 +293,35 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const __grid_consta
     s_eq[warp] = ne;
   }
   __syncthreads();
-  if (tid == 0) {
-    uint32_t g = 0, e = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      g += s_gt[w];
-      e += s_eq[w];
+  if (warp == 0) {
+    const uint32_t g = __reduce_add_sync(0xffffffffu, s_gt[lane]);
+    const uint32_t e = __reduce_add_sync(0xffffffffu, s_eq[lane]);
+    if (lane == 0) {
+      s_tot[0] = g;
+      s_tot[1] = e;
     }
-    s_tot[0] = g;
-    s_tot[1] = e;
   }
-  cluster_sync();
+  if (C > 1) cluster_sync();
   uint32_t g = 0, e = 0;
-  for (uint32_t r = 0; r < rank; ++r) {
-    g += ld_peer32(&s_tot[0], r);
-    e += ld_peer32(&s_tot[1], r);
+  if (lane < rank) {
+    g = ld_peer32(&s_tot[0], lane);
+    e = ld_peer32(&s_tot[1], lane);
   }
-  for (int w = 0; w < warp; ++w) {
-    g += s_gt[w];
-    e += s_eq[w];
-  }
+  g += lane < warp ? s_gt[lane] : 0;
+  e += lane < warp ? s_eq[lane] : 0;
+  g = __reduce_add_sync(0xffffffffu, g);
+  e = __reduce_add_sync(0xffffffffu, e);
   const uint32_t lt = (1u << lane) - 1;
-  for (int32_t i0 = w0; i0 < w1; i0 += 32) {
-    const int32_t i = i0 + lane;
-    const uint64_t a = i < w1 ? above(key_at(i), top) : 0;
-    const bool is_g = i < w1 && a > prefix, is_e = i < w1 && a == prefix;
+  each([&](uint64_t key, int32_t i, bool in) {
+    const bool is_g = in && key > hi, is_e = in && key >= lo && key <= hi;
     const uint32_t bg = __ballot_sync(0xffffffffu, is_g), be = __ballot_sync(0xffffffffu, is_e);
     const uint32_t eb = e + __popc(be & lt);
     if (is_g || (is_e && eb < need))
       out[sink + g + __popc(bg & lt) + min(eb, need)] = static_cast<int32_t>(sink + i);
     g += __popc(bg);
     e += __popc(be);
-  }
-  cluster_sync();  // no CTA leaves while another may still read its totals
+  });
+  if (C > 1) cluster_sync();  // no CTA leaves while another may still read its counts
 }
 
 // ------------------------------------------------------------------------------ move
@@ -382,10 +452,22 @@ extern "C" int ds4idx_evict_select(const int64_t* total, int64_t pool_rows, int3
   p.width = width;
   p.sink = n_sink;
   p.recent = n_recent;
-  // One CTA reads 4096 totals in four loads a thread; longer sequences are shared by a cluster.
-  p.cluster = longest <= 4096 ? 1 : 8;
-  return launch_dependent(select_kernel, static_cast<unsigned>(B * p.cluster), kThreads, 0,
-                          p.cluster, stream, p);
+  // One CTA up to four totals a thread (in registers: 9 us at 4096, of which a cluster would spend
+  // more on its barriers); else a cluster of 8, the largest portable size. (Clusters of 16 hold
+  // 262144 totals on chip, but only four of them run at once.)
+  if (longest <= 4 * kThreads) {
+    p.cluster = 1;
+    return launch_dependent(select_kernel<4>, static_cast<unsigned>(B), kThreads, 0, 1, stream, p);
+  }
+  constexpr size_t kKeyBytes = kOnChip * kThreads * sizeof(uint64_t);
+  if (cudaFuncSetAttribute(select_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kKeyBytes) != cudaSuccess) {
+    cudaGetLastError();
+    return DS4IDX_ERR_CUDA;
+  }
+  p.cluster = 8;
+  return launch_dependent(select_kernel<0>, static_cast<unsigned>(B * 8), kThreads, kKeyBytes, 8,
+                          stream, p);
 }
 
 extern "C" int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t B,

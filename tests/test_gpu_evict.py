@@ -73,6 +73,9 @@ def _totals(kind, R, rng):
     ([10], [3], 0, 0), ([10], [1], 1, 0), ([10], [9], 4, 5), ([5, 0, 7], [5, 2, 9], 1, 1),
     ([300, 4096, 1], [150, 4095, 1], 0, 1), ([4097, 100], [2000, 99], 4, 60),
     ([40001, 9000, 20000], [31000, 100, 20000], 3, 77),
+    # every cluster size, and past what stays on chip
+    ([16384], [16383], 0, 0), ([16385, 17], [9000, 16], 0, 3), ([70000], [1], 0, 0),
+    ([140001, 5], [70000, 13], 4, 9), ([262150], [131000], 4, 64),
 ])
 def test_select_matches_definition(lens, keep, sink, recent, kind):
     rng = np.random.default_rng(len(lens) + lens[0])
