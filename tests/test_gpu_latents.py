@@ -66,6 +66,19 @@ def test_fp32_values_next_to_ties():
     assert np.array_equal(cache.cpu().numpy(), _bytes(x))
 
 
+def test_past_the_largest_scale():
+    # the largest scale is 3840: 7.5 of it is a tie that must clamp to 7, far values saturate
+    x = torch.zeros(3, 576)
+    for k in range(32):
+        v = 3840.0 * torch.tensor([7.5, 7.25, 7.4375, 6.5, 5.5, 100.0, 3e38, 1.0])
+        x[0, 16 * k:16 * k + 8] = v * (1 if k % 2 else -1)
+        x[1, 16 * k:16 * k + 5] = v[:5]
+        x[2, 16 * k] = v[0]
+    cache = torch.zeros(3, 416, dtype=torch.uint8, device="cuda")
+    ds4idx.quantize_latents(x.cuda(), cache)
+    assert np.array_equal(cache.cpu().numpy(), _bytes(x))
+
+
 def test_slots_and_reading_by_rows():
     n, R = 200, 333
     x = _rows(n, torch.bfloat16, 7)
