@@ -460,11 +460,8 @@ extern "C" int ds4idx_evict_select(const int64_t* total, int64_t pool_rows, int3
     return launch_dependent(select_kernel<4>, static_cast<unsigned>(B), kThreads, 0, 1, stream, p);
   }
   constexpr size_t kKeyBytes = kOnChip * kThreads * sizeof(uint64_t);
-  if (cudaFuncSetAttribute(select_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kKeyBytes) != cudaSuccess) {
-    cudaGetLastError();
-    return DS4IDX_ERR_CUDA;
-  }
+  static std::atomic<uint64_t> done{0};
+  if (!allow_shared(select_kernel<0>, kKeyBytes, done)) return DS4IDX_ERR_CUDA;
   p.cluster = 8;
   return launch_dependent(select_kernel<0>, static_cast<unsigned>(B * 8), kThreads, kKeyBytes, 8,
                           stream, p);

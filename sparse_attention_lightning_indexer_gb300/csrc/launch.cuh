@@ -18,6 +18,23 @@ inline bool aligned_to(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// Lets `kernel` use `bytes` of dynamic shared memory; one call per device and kernel (`done`: a bit for
+// each device on which it was made).
+template <typename Kernel>
+bool allow_shared(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 template <typename... Params, typename... Args>
 int launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
                      unsigned cluster, void* stream, Args&&... args) {

@@ -983,18 +983,8 @@ bool encode(CUtensorMap* m, const void* base, int32_t width, int64_t rows, int32
 
 template <int C>
 int launch(const CUtensorMap& tq, const CUtensorMap& to, const Params& p, int64_t T, void* stream) {
-  static std::atomic<uint64_t> done{0};  // devices on which the attribute is set
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DS4IDX_ERR_CUDA;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(done.load(std::memory_order_relaxed) & bit) || !bit) {
-    if (cudaFuncSetAttribute(sparse_attn_q4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<C>::Smem) != cudaSuccess) {
-      cudaGetLastError();
-      return DS4IDX_ERR_CUDA;
-    }
-    done.fetch_or(bit, std::memory_order_relaxed);
-  }
+  static std::atomic<uint64_t> done{0};
+  if (!allow_shared(sparse_attn_q4_kernel<C>, Cfg<C>::Smem, done)) return DS4IDX_ERR_CUDA;
   // One CTA an SM fits. More tokens than SMs: the CTAs stay and take the tokens in turn.
   const int64_t grid = C == 1 ? std::min<int64_t>(T, kSms) : T * C;
   return launch_dependent(sparse_attn_q4_kernel<C>, static_cast<unsigned>(grid), kThreads,

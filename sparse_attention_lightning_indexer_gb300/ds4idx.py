@@ -354,7 +354,7 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
                                  _in_dtype(x, "a rotary tensor"), 1 if il else 0, heads, 0, st[0],
                                  xh, so[0], oh)
     _check(load().ds4idx_rotary(n, ctypes.addressof(d), T, rot, positions.data_ptr(), freqs.address,
-                                freqs.scale, 1 if inverse else 0, _stream_ptr(stream)),
+                                freqs.scale, 1 if inverse else 0, _stream_ptr(stream, positions)),
            "ds4idx_rotary")
     return outs[0] if single else outs
 
@@ -389,8 +389,9 @@ Q4_ROW_BYTES = 416
 
 
 def _cache_rows(cache) -> int:
-    _need(cache, (cache.shape[0], Q4_ROW_BYTES), "cache", torch.uint8)
-    return cache.shape[0]
+    rows = cache.shape[0]
+    _need(cache, (rows, Q4_ROW_BYTES), "cache", torch.uint8)
+    return rows
 
 
 def quantize_latents(x, cache, dst_offset: int = 0, slots=None, stream=None):
@@ -402,7 +403,8 @@ def quantize_latents(x, cache, dst_offset: int = 0, slots=None, stream=None):
     if slots is not None:
         _need(slots, (n,), "slots", torch.int64)
     _check(load().ds4idx_quantize_latents(_ptr(x), _in_dtype(x, "x"), n, _ptr(slots),
-                                          int(dst_offset), _ptr(cache), R, _stream_ptr(stream)),
+                                          int(dst_offset), _ptr(cache), R,
+                                          _stream_ptr(stream, cache)),
            "ds4idx_quantize_latents")
     return cache
 
@@ -421,7 +423,7 @@ def read_latents(cache, rows=None, start: int = 0, n: int | None = None, out=Non
         out = torch.empty((n, SA_DQK), dtype=dtype, device=cache.device)
     _need(out, (n, SA_DQK), "out")
     _check(load().ds4idx_read_latents(_ptr(cache), R, _ptr(rows), int(start), n, _ptr(out),
-                                      _in_dtype(out, "out"), _stream_ptr(stream)),
+                                      _in_dtype(out, "out"), _stream_ptr(stream, cache)),
            "ds4idx_read_latents")
     return out
 
@@ -481,7 +483,7 @@ def sparse_attention_q4(q, cache, idx, sm_scale: float, kv_row0=None, page_table
         _need(weights, (T, n_sel), "weights", torch.float32)
     _check(load().ds4idx_sparse_attention_q4(_ptr(q), _ptr(cache), R, _ptr(idx), _ref(where), T, H,
                                              SA_DQK, SA_DV, n_sel, float(sm_scale), _ptr(out),
-                                             _ptr(lse), _ptr(weights), _stream_ptr(stream)),
+                                             _ptr(lse), _ptr(weights), _stream_ptr(stream, q)),
            "ds4idx_sparse_attention_q4")
     return out, lse, weights
 
@@ -502,12 +504,12 @@ def evict_accumulate(total, weights, idx, kv_row0=None, page_table=None, page_si
     _need(idx, (T, n_sel), "idx", torch.int32)
     where = _placement(T, kv_row0, page_table, page_size, token_seq)
     _check(load().ds4idx_evict_accumulate(_ptr(total), R, _ptr(weights), _ptr(idx), _ref(where), T,
-                                          n_sel, _stream_ptr(stream)), "ds4idx_evict_accumulate")
+                                          n_sel, _stream_ptr(stream, total)), "ds4idx_evict_accumulate")
     return total
 
 
 def _i64(values):
-    return array.array("q", [int(v) for v in values])
+    return array.array("q", values)
 
 
 def _i64_address(a):
@@ -524,14 +526,14 @@ def evict_select(total, starts, seq_lens, keep, n_sink: int = 0, n_recent: int =
     R = total.shape[0]
     _need(total, (R,), "total", torch.int64)
     if kept is None:
-        width = max([min(int(k), int(s)) for k, s in zip(keep, seq_lens)], default=0)
+        width = max(map(min, keep, seq_lens), default=0)
         kept = torch.empty((B, max(width, 0)), dtype=torch.int32, device=total.device)
     _need(kept, (B, kept.shape[1]), "kept", torch.int32)
     host = _i64([*starts, *seq_lens, *keep])
     at = _i64_address(host)
     _check(load().ds4idx_evict_select(_ptr(total), R, B, at, at + 8 * B, at + 16 * B, int(n_sink),
                                       int(n_recent), _ptr(kept), kept.shape[1],
-                                      _stream_ptr(stream)), "ds4idx_evict_select")
+                                      _stream_ptr(stream, total)), "ds4idx_evict_select")
     return kept
 
 
@@ -550,16 +552,21 @@ def evict_compact(kept, seq_lens, keep, src_starts, dst_starts, srcs, dsts, stre
         raise ValueError("at most 8 arrays")
     d = ctypes.create_string_buffer(max(1, n) * _ROW_ARRAY.size)
     for k, (src, dst) in enumerate(zip(srcs, dsts)):
-        shape = src.shape
-        _need(src, tuple(shape), f"srcs[{k}]")
-        _need(dst, (dst.shape[0], *shape[1:]), f"dsts[{k}]", src.dtype)
-        _ROW_ARRAY.pack_into(d, k * _ROW_ARRAY.size, src.data_ptr(), dst.data_ptr(), shape[0],
-                             dst.shape[0], src.element_size() * math.prod(shape[1:]), 0)
-    counts = [min(int(k), int(m)) for k, m in zip(keep, seq_lens)]
+        shape, dshape = src.shape, dst.shape
+        if not (src.is_cuda and dst.is_cuda and src.is_contiguous() and dst.is_contiguous()
+                and src.dtype == dst.dtype and shape[1:] == dshape[1:]):
+            _need(src, tuple(shape), f"srcs[{k}]")
+            _need(dst, (dshape[0], *shape[1:]), f"dsts[{k}]", src.dtype)
+        rows = shape[0]
+        row = src.nbytes // rows if rows else src.element_size() * math.prod(shape[1:])
+        _ROW_ARRAY.pack_into(d, k * _ROW_ARRAY.size, src.data_ptr(), dst.data_ptr(), rows,
+                             dshape[0], row, 0)
+    counts = list(map(min, keep, seq_lens))
     host = _i64([*src_starts, *seq_lens, *dst_starts, *counts])
     at = _i64_address(host)
     _check(load().ds4idx_evict_compact(_ptr(kept), kept.shape[1], B, at, at + 8 * B, at + 16 * B,
-                                       at + 24 * B, n, ctypes.addressof(d), _stream_ptr(stream)),
+                                       at + 24 * B, n, ctypes.addressof(d),
+                                       _stream_ptr(stream, kept)),
            "ds4idx_evict_compact")
     return dsts
 
@@ -584,11 +591,16 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_ptr(stream):
+def _stream_ptr(stream, tensor=None):
+    """The stream of a call: the one given, else the current one (of the device of ``tensor``, which
+    saves asking for the current device)."""
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None and torch.cuda.is_initialized():
-        return _raw_stream(torch.cuda.current_device())
+    if _raw_stream is not None:
+        if tensor is not None:
+            return _raw_stream(tensor.get_device())
+        if torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
