@@ -378,9 +378,10 @@ typedef struct {
  *  out      [T, n_heads, 512] bf16, 32-byte aligned; lse [T, n_heads] fp32 or NULL; weights
  *           [T, n_sel] fp32 or NULL (summed in a fixed order).
  * Cache values are exact in bf16; products accumulate in fp32, softmax and sums are fp32, the
- * probabilities are rounded to bf16 for the value product. Rows of empty entries are never read.
- * T <= 76 runs a cluster of CTAs per token. Asynchronous on `stream`, allocates nothing. Bounded
- * device waits that run out are recorded for ds4idx_sparse_attention_status.
+ * probabilities are rounded to bf16 for the value product. What a row of no entry holds (NaN
+ * included) does not reach the results. Few tokens (up to about half the SMs) run a cluster of CTAs
+ * each. Asynchronous on `stream`, allocates nothing. Bounded device waits that run out are recorded
+ * for ds4idx_sparse_attention_status.
  * Errors: INVALID_ARG, UNSUPPORTED (d_qk != 576, d_v != 512), LAUNCH, CUDA. T = 0 is a no-op. */
 int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, int64_t kv_rows,
                                const int32_t* idx, const ds4idx_placement* where, int64_t T,

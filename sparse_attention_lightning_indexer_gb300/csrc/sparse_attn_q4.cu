@@ -981,6 +981,35 @@ bool encode(CUtensorMap* m, const void* base, int32_t width, int64_t rows, int32
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How many clusters of C CTAs run at once on the current device (asked once per device; 0: an error).
+template <int C>
+int64_t clusters_at_once() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_shared(sparse_attn_q4_kernel<C>, Cfg<C>::Smem, done)) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<C>::Smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, sparse_attn_q4_kernel<C>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 template <int C>
 int launch(const CUtensorMap& tq, const CUtensorMap& to, const Params& p, int64_t T, void* stream) {
   static std::atomic<uint64_t> done{0};
@@ -1023,9 +1052,11 @@ extern "C" int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, i
   p.n_heads = n_heads;
   p.n_sel = n_sel;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
-  // The widest cluster whose CTAs still fit the 152 SMs at once (clusters of 8 pack two to a GPC).
-  if (T <= 16) return launch<8>(tq, to, p, T, stream);
-  if (T <= 32) return launch<4>(tq, to, p, T, stream);
-  if (T <= 76) return launch<2>(tq, to, p, T, stream);
+  // The widest cluster of which all tokens run at once. 512 rows, 128 heads, us for 8 / 4 / 2 / 1 CTAs
+  // a token: 12.9 / 13.3 / 17.3 / 26.1 at 12 tokens, 17.3 / 13.6 / 17.3 / 26.2 at 16 (15 clusters of 8
+  // run at once), 37 / 26 / 17.6 / 26.5 at 37 (36 of 4), 64 / 32 / 22.6 / 26.6 at 77 (76 of 2).
+  if (T <= clusters_at_once<8>()) return launch<8>(tq, to, p, T, stream);
+  if (T <= clusters_at_once<4>()) return launch<4>(tq, to, p, T, stream);
+  if (T <= clusters_at_once<2>()) return launch<2>(tq, to, p, T, stream);
   return launch<1>(tq, to, p, T, stream);
 }

@@ -67,6 +67,7 @@ def _check(q, rows_bytes, pool, scale, out, lse, w):
     (16, 128, 512, [512, 0, 1, 63, 64, 65, 300, 511]), (17, 16, 512, [512, 130, 0, 7]),
     (32, 128, 200, [200, 128, 129, 1]), (33, 128, 512, [512, 256, 257, 0, 31]),
     (76, 64, 512, [512, 100]), (77, 128, 512, [512, 255, 1, 0, 257]),
+    (15, 128, 512, [512, 449]), (36, 128, 300, [300, 0, 200]), (37, 128, 512, [512, 9]),
     (160, 128, 512, [512, 500, 32]), (90, 5, 33, [33, 0, 9]),
     # several tokens a CTA, empty ones first, last and in a row
     (470, 16, 512, [0, 0, 512, 3, 0, 300, 257]), (460, 128, 512, [512, 511, 64, 1, 129]),
