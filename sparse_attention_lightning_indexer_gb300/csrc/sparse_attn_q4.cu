@@ -3,22 +3,27 @@
 //
 // A cluster of C = 1, 2, 4 or 8 CTAs owns one token. Both products are split without partial sums:
 //   A  S[128 heads x 512/C keys] = Q K^T: a CTA takes its share of the list's slots (TMEM columns
-//      0 .. 512/C - 1). 9 chunks of 64 dims pass through two rings in shared memory: the Q chunk by
-//      TMA, the key chunk by the worker threads, which read a row's 32 bytes of codes, turn them
-//      into bf16 (exact) and write the 128-byte-swizzled operand.
+//      0 .. 512/C - 1). First the rotary chunk of 64 dims, whose keys are copied as they are, then
+//      the 8 latent chunks: worker threads read codes, turn them into bf16 (exact) and write the
+//      128-byte-swizzled operand in stages of 64 KB. Q chunks come by TMA.
 //   B  softmax: the row maxima and sums of the CTAs meet in each other's shared memory, so every
 //      probability is final relative to the list's maximum; P goes as bf16 into shared memory in
 //      the layout of an MMA A operand, each CTA's share copied to the others by bulk copies.
 //   C  O[128 heads x 512/C dims] = P V over all slots: blocks of 64 keys of the CTA's value dims are
 //      turned into bf16 again, as an MN-major B operand. Nothing is joined afterwards.
-// C = 1 fills the GPU for many tokens; a cluster shortens the chain of phases for few.
+// C = 1 fills the GPU for many tokens: its CTAs stay and take tokens in turn, reading the next
+// token's first rows behind this one's products. A cluster shortens the chain of phases for few.
 //
 // Warps 0..15 are the workers (unpacking, softmax, output: TMEM lane quadrant warp % 4, column
-// quarter warp / 4), warp 16 issues tcgen05.mma, warp 17 loads Q.
+// quarter warp / 4), warp 16 issues tcgen05.mma, warp 17 loads Q and the next token's row list.
 //
 // The unpacked tile serves as K (K-major) and as V (MN-major) in the same layout; it is made
 // twice because O takes all 512 TMEM columns at C = 1, so P V starts only after the whole of S is
 // read, and 512 unpacked rows (576 KB) do not fit shared memory.
+//
+// 128 heads, 512 rows: 11.3 us for one token (C = 8; the latency of the phases), 703 us for 4096
+// tokens of a 65536-row cache, 831 TFLOP/s, 0.43 of the measured tensor peak: bound by the unpacking
+// on the half-rate integer pipe and by shared memory, of which the MMAs read 96 bytes a clock.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -383,7 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto load_rows = [&](int t, int buf, int base) {
     const int j = base + lane;
     int64_t r = -1;
-    if (j < p.n_sel) r = place_row(p.place, place_token(p.place, t), p.idx[static_cast<int64_t>(t) * p.n_sel + j]);
+    if (j < p.n_sel)
+      r = place_row(p.place, place_token(p.place, t),
+                    p.idx[static_cast<int64_t>(t) * p.n_sel + j]);
     reinterpret_cast<int32_t*>(smem + F::OffRows)[buf * kK + j] = static_cast<int32_t>(r);
     const uint32_t m = __ballot_sync(0xffffffffu, r >= 0);
     if (lane == 0) reinterpret_cast<uint32_t*>(smem + F::OffMask)[buf * 16 + base / 32] = m;
@@ -487,301 +494,301 @@ __global__ void __launch_bounds__(kThreads, 1)
     fetch(0);
 #pragma unroll 1
     for (int t = t_first; t < p.T; t += t_step, ++it) {
-    const int buf = F::Bufs == 2 ? it & 1 : 0;
-    const int32_t* s_rows = reinterpret_cast<const int32_t*>(smem + F::OffRows) + buf * kK;
-    const uint32_t* s_mask = reinterpret_cast<const uint32_t*>(smem + F::OffMask) + buf * 16;
-    const int nblk = used_blocks(buf), nc = used_slots(nblk);
-    // ---------------- A: latent key stages
-    const int parts = (nc + F::KS - 1) / F::KS;
-    // The last token's output may still be read from the slots: its half in the slot that comes
-    // first was sent first, so that half is waited for before a stage is made, the rest after it.
-    int pending = it > 0 ? 2 : 0;
-    cp_async_wait<0>();
-    if (nc > 0) {
-      qn += kChunks + (nc + F::RP - 1) / F::RP;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(rope_full);
+      const int buf = F::Bufs == 2 ? it & 1 : 0;
+      const int32_t* s_rows = reinterpret_cast<const int32_t*>(smem + F::OffRows) + buf * kK;
+      const uint32_t* s_mask = reinterpret_cast<const uint32_t*>(smem + F::OffMask) + buf * 16;
+      const int nblk = used_blocks(buf), nc = used_slots(nblk);
+      // ---------------- A: latent key stages
+      const int parts = (nc + F::KS - 1) / F::KS;
+      // The last token's output may still be read from the slots: its half in the slot that comes
+      // first was sent first, so that half is waited for before a stage is made, the rest after it.
+      int pending = it > 0 ? 2 : 0;
+      cp_async_wait<0>();
+      if (nc > 0) {
+        qn += kChunks + (nc + F::RP - 1) / F::RP;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rope_full);
 #pragma unroll
-      for (int u = 0; u < Units; ++u) {
-        const int kp = u % F::KeyParts;
-        if (kp < parts) {
-          if (C == 1 && pending > 0) {
-            --pending;
-            if (tid == 0) {
-              if (pending) bulk_store_wait<1>(); else bulk_store_wait<0>();
+        for (int u = 0; u < Units; ++u) {
+          const int kp = u % F::KeyParts;
+          if (kp < parts) {
+            if (C == 1 && pending > 0) {
+              --pending;
+              if (tid == 0) {
+                if (pending) bulk_store_wait<1>(); else bulk_store_wait<0>();
+              }
+              worker_sync();
             }
-            worker_sync();
+            const int slot = stage & (F::KSlots - 1);
+            if (ok) ok = mbar_wait_warp(&k_empty[slot], ((stage >> 1) & 1) ^ 1u, s_abort, err);
+            if (ok) {
+              if (kp * F::KS + kk < nc)
+                store_chunk<F::RowLanes>(smem0 + slot * F::KSlot + ch * (F::KS * 128), kk,
+                                         codes[u % PF], scale_of(kp, u / F::KeyParts), ch);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&k_full[slot]);
+            }
+            ++stage;
           }
-          const int slot = stage & (F::KSlots - 1);
-          if (ok) ok = mbar_wait_warp(&k_empty[slot], ((stage >> 1) & 1) ^ 1u, s_abort, err);
-          if (ok) {
-            if (kp * F::KS + kk < nc)
-              store_chunk<F::RowLanes>(smem0 + slot * F::KSlot + ch * (F::KS * 128), kk,
-                                       codes[u % PF], scale_of(kp, u / F::KeyParts), ch);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&k_full[slot]);
-          }
-          ++stage;
-        }
-        if (u + PF < Units) load(u + PF, codes[u % PF]);
-      }
-    }
-    if (C == 1 && pending > 0) {  // an empty list made no stage
-      if (tid == 0) bulk_store_wait<0>();
-      worker_sync();
-    }
-    // ---------------- B: softmax
-    const int nch = min(F::CP, max(0, nc - part * F::CP)) / F::W;  // chunks of W columns
-    auto mask_of = [&](int i) -> uint32_t {
-      const int s = slot0 + part * F::CP + i * F::W;
-      const uint32_t m = s_mask[s >> 5];
-      return F::W == 32 ? m : (m >> (s & 16)) & 0xFFFFu;
-    };
-    constexpr uint32_t kAll = F::W == 32 ? 0xFFFFFFFFu : 0xFFFFu;
-    // Value blocks of this thread's group: its codes are read one block ahead.
-    const int gv = tid / (64 * F::NB), vtid = tid % (64 * F::NB);
-    const int vnb = F::VLanes == 4 ? vtid & 3 : vtid / 64, vr = F::VLanes == 4 ? vtid >> 2 : vtid % 64;
-    const int vblocks = gv < nblk ? (nblk - gv + F::GV - 1) / F::GV : 0;  // per half
-    uint32_t vc[2][8], vs[2];
-    auto v_load = [&](int n, uint32_t (&codes)[8], uint32_t& sc) {  // n: this group's n-th block
-      if (n >= vblocks * F::Halves) return;
-      const int half = n >= vblocks ? 1 : 0;
-      int kb = gv + F::GV * (n - half * vblocks);
-      if constexpr (C > 1) {
-#pragma unroll
-        for (int i = 0, k = n; i < 8; ++i) {
-          const int b = block_at(i);
-          if (b % F::GV == gv && b < nblk && k-- == 0) kb = b;
+          if (u + PF < Units) load(u + PF, codes[u % PF]);
         }
       }
-      const int32_t r = s_rows[kb * 64 + vr];
-      const int chunk = rank * (F::DV / 64) + half * F::NB + vnb;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) codes[j] = kEmptyWord;
-      sc = 0u;
-      if (r >= 0) {
-        const uint8_t* row = p.cache + static_cast<int64_t>(r) * kRowBytes;
-        ld32(row + chunk * 32, codes);
-        sc = *reinterpret_cast<const uint32_t*>(row + kOffScale + 4 * chunk);
+      if (C == 1 && pending > 0) {  // an empty list made no stage
+        if (tid == 0) bulk_store_wait<0>();
+        worker_sync();
       }
-    };
-    auto v_store = [&](int n, uint32_t (&codes)[8], uint32_t sc) {
-      if (n >= vblocks * F::Halves) return;
-      if (ok) ok = mbar_wait_warp(&v_empty[gv], (vuse & 1) ^ 1u, s_abort, err);
-      ++vuse;
-      if (!ok) return;
-      store_chunk<F::VLanes>(smem0 + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc, vnb);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[gv]);
-    };
-    v_load(0, vc[0], vs[0]);
-    v_load(1, vc[1], vs[1]);
-    if (ok) ok = mbar_wait_warp(s_ready, it & 1, s_abort, err);
-    tc_fence_after();
-    float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-    if (ok) {
-      for (int i = 0; i < nch; ++i) {
-        uint32_t r[F::W];
-        tmem_ld<F::W>(scol + i * F::W, r);
-        tmem_wait_ld();
-        const uint32_t vm = mask_of(i);
-        if (vm == kAll) {
-#pragma unroll
-          for (int j = 0; j < F::W; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
-        } else {
-#pragma unroll
-          for (int j = 0; j < F::W; ++j)
-            mx4[j & 3] = fmaxf(mx4[j & 3], ((vm >> j) & 1u) ? __uint_as_float(r[j]) : kNegInf);
-        }
-      }
-    }
-    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-    s_red[part * kH + h] = mx * p.scale_log2;  // scale > 0: the maximum of the scaled scores
-    worker_sync();
-    float m = fmaxf(fmaxf(s_red[h], s_red[kH + h]), fmaxf(s_red[2 * kH + h], s_red[3 * kH + h]));
-    if constexpr (C > 1) {
-      if (part == 0) {
-#pragma unroll
-        for (int r = 0; r < C; ++r) st_peer(peer(smem_u32(s_x + rank * kH + h), r), m);
-        __syncwarp();
-        if (lane < C) arrive_peer(peer(smem_u32(m_full), lane));
-      }
-    }
-    // its first block while the maxima travel (the rings are done with)
-    v_store(0, vc[0], vs[0]);
-    if constexpr (C > 1) {
-      ok = __all_sync(0xffffffffu, wait_cluster(m_full, 0u, s_abort, err)) && ok;
-#pragma unroll
-      for (int r = 0; r < C; ++r) m = fmaxf(m, s_x[r * kH + h]);
-    }
-    const float mm = m == kNegInf ? 0.f : m;
-    float l = 0.f;
-    if (ok) {
-      for (int i = 0; i < nch; ++i) {
-        uint32_t r[F::W];
-        tmem_ld<F::W>(scol + i * F::W, r);
-        tmem_wait_ld();
-        const uint32_t vm = mask_of(i);
-        uint32_t pk[F::W / 2];
-        // (the branch outside: with a select per element the pass takes twice as long)
-        if (vm == kAll) {
-#pragma unroll
-          for (int j = 0; j < F::W; j += 2) {
-            const float p0 = exp2_approx(fmaf(__uint_as_float(r[j]), p.scale_log2, -mm));
-            const float p1 = exp2_approx(fmaf(__uint_as_float(r[j + 1]), p.scale_log2, -mm));
-            l += p0 + p1;
-            pk[j / 2] = pack_bf16x2(p0, p1);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < F::W; j += 2) {
-            float p0 = exp2_approx(fmaf(__uint_as_float(r[j]), p.scale_log2, -mm));
-            float p1 = exp2_approx(fmaf(__uint_as_float(r[j + 1]), p.scale_log2, -mm));
-            p0 = ((vm >> j) & 1u) ? p0 : 0.f;
-            p1 = ((vm >> (j + 1)) & 1u) ? p1 : 0.f;
-            l += p0 + p1;
-            pk[j / 2] = pack_bf16x2(p0, p1);
-          }
-        }
+      // ---------------- B: softmax
+      const int nch = min(F::CP, max(0, nc - part * F::CP)) / F::W;  // chunks of W columns
+      auto mask_of = [&](int i) -> uint32_t {
         const int s = slot0 + part * F::CP + i * F::W;
-        const uint32_t at = smem0 + (s >> 6) * kPBlock + h * 128 + ((h & 7) ^ ((s & 63) >> 3)) * 16;
+        const uint32_t m = s_mask[s >> 5];
+        return F::W == 32 ? m : (m >> (s & 16)) & 0xFFFFu;
+      };
+      constexpr uint32_t kAll = F::W == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+      // Value blocks of this thread's group: its codes are read one block ahead.
+      const int gv = tid / (64 * F::NB), vtid = tid % (64 * F::NB);
+      const int vnb = F::VLanes == 4 ? vtid & 3 : vtid / 64, vr = F::VLanes == 4 ? vtid >> 2 : vtid % 64;
+      const int vblocks = gv < nblk ? (nblk - gv + F::GV - 1) / F::GV : 0;  // per half
+      uint32_t vc[2][8], vs[2];
+      auto v_load = [&](int n, uint32_t (&codes)[8], uint32_t& sc) {  // n: this group's n-th block
+        if (n >= vblocks * F::Halves) return;
+        const int half = n >= vblocks ? 1 : 0;
+        int kb = gv + F::GV * (n - half * vblocks);
+        if constexpr (C > 1) {
 #pragma unroll
-        for (int u = 0; u < F::W / 8; ++u)
-          st_shared16(at ^ (16 * u), make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]));
-      }
-    }
-    s_red[4 * kH + part * kH + h] = l;
-    fence_proxy_async_smem();  // P (generic writes) before the MMAs and copies that read it
-    tc_fence_before();
-    worker_sync();
-    l = (s_red[4 * kH + h] + s_red[5 * kH + h]) + (s_red[6 * kH + h] + s_red[7 * kH + h]);
-    if constexpr (C > 1) {
-      if (part == 0) {
+          for (int i = 0, k = n; i < 8; ++i) {
+            const int b = block_at(i);
+            if (b % F::GV == gv && b < nblk && k-- == 0) kb = b;
+          }
+        }
+        const int32_t r = s_rows[kb * 64 + vr];
+        const int chunk = rank * (F::DV / 64) + half * F::NB + vnb;
 #pragma unroll
-        for (int r = 0; r < C; ++r) st_peer(peer(smem_u32(s_x + (C + rank) * kH + h), r), l);
+        for (int j = 0; j < 8; ++j) codes[j] = kEmptyWord;
+        sc = 0u;
+        if (r >= 0) {
+          const uint8_t* row = p.cache + static_cast<int64_t>(r) * kRowBytes;
+          ld32(row + chunk * 32, codes);
+          sc = *reinterpret_cast<const uint32_t*>(row + kOffScale + 4 * chunk);
+        }
+      };
+      auto v_store = [&](int n, uint32_t (&codes)[8], uint32_t sc) {
+        if (n >= vblocks * F::Halves) return;
+        if (ok) ok = mbar_wait_warp(&v_empty[gv], (vuse & 1) ^ 1u, s_abort, err);
+        ++vuse;
+        if (!ok) return;
+        store_chunk<F::VLanes>(smem0 + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc, vnb);
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane < C) arrive_peer(peer(smem_u32(l_full), lane));
-      }
-      if (lane == 0) mbar_arrive(&p_full[rank]);
-      if (warp == 15 && lane > 0 && lane < C) {
-        const int to = (rank + lane) & (C - 1);
-        if (ok && nc > 0)
-          copy_to_peer(peer(smem_u32(smem + (slot0 / 64) * kPBlock), to),
-                       smem_u32(smem + (slot0 / 64) * kPBlock), (nc / 64) * kPBlock,
-                       peer(smem_u32(&p_full[rank]), to));
-        // what the CTA `to` sends here
-        mbar_arrive_expect_tx(&p_full[to],
-                              min(8 / C, max(0, nblk - to * (8 / C))) * kPBlock);
-      }
-      __syncwarp();
-      ok = __all_sync(0xffffffffu, wait_cluster(l_full, 0u, s_abort, err)) && ok;
-      l = 0.f;
-#pragma unroll
-      for (int r = 0; r < C; ++r) l += s_x[(C + r) * kH + h];
-    }
-    // w_j = sum over heads of exp2(s - m) / l, once more from S: at C = 1 before P V may write there,
-    // in a cluster (S and O apart) while P V runs.
-    auto key_weights = [&] {
-      const float off = l > 0.f && h < p.n_heads ? mm + __log2f(l) : __int_as_float(0x7f800000);
-      for (int i = 0; i < F::CP / F::W; ++i) {
-        float v[F::W];
-        if (ok && i < nch) {
+        if (lane == 0) mbar_arrive(&v_full[gv]);
+      };
+      v_load(0, vc[0], vs[0]);
+      v_load(1, vc[1], vs[1]);
+      if (ok) ok = mbar_wait_warp(s_ready, it & 1, s_abort, err);
+      tc_fence_after();
+      float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+      if (ok) {
+        for (int i = 0; i < nch; ++i) {
           uint32_t r[F::W];
           tmem_ld<F::W>(scol + i * F::W, r);
           tmem_wait_ld();
           const uint32_t vm = mask_of(i);
+          if (vm == kAll) {
 #pragma unroll
-          for (int j = 0; j < F::W; ++j)
-            v[j] = ((vm >> j) & 1u) && h < p.n_heads
-                       ? exp2_approx(fmaf(__uint_as_float(r[j]), p.scale_log2, -off))
-                       : 0.f;
-        } else {
+            for (int j = 0; j < F::W; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
+          } else {
 #pragma unroll
-          for (int j = 0; j < F::W; ++j) v[j] = 0.f;
+            for (int j = 0; j < F::W; ++j)
+              mx4[j & 3] = fmaxf(mx4[j & 3], ((vm >> j) & 1u) ? __uint_as_float(r[j]) : kNegInf);
+          }
         }
-        const float sum = column_sums<F::W>(v, lane);
-        if (lane < F::W) s_w[quad * F::NK + part * F::CP + i * F::W + lane] = sum;
       }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      s_red[part * kH + h] = mx * p.scale_log2;  // scale > 0: the maximum of the scaled scores
+      worker_sync();
+      float m = fmaxf(fmaxf(s_red[h], s_red[kH + h]), fmaxf(s_red[2 * kH + h], s_red[3 * kH + h]));
+      if constexpr (C > 1) {
+        if (part == 0) {
+#pragma unroll
+          for (int r = 0; r < C; ++r) st_peer(peer(smem_u32(s_x + rank * kH + h), r), m);
+          __syncwarp();
+          if (lane < C) arrive_peer(peer(smem_u32(m_full), lane));
+        }
+      }
+      // its first block while the maxima travel (the rings are done with)
+      v_store(0, vc[0], vs[0]);
+      if constexpr (C > 1) {
+        ok = __all_sync(0xffffffffu, wait_cluster(m_full, 0u, s_abort, err)) && ok;
+#pragma unroll
+        for (int r = 0; r < C; ++r) m = fmaxf(m, s_x[r * kH + h]);
+      }
+      const float mm = m == kNegInf ? 0.f : m;
+      float l = 0.f;
+      if (ok) {
+        for (int i = 0; i < nch; ++i) {
+          uint32_t r[F::W];
+          tmem_ld<F::W>(scol + i * F::W, r);
+          tmem_wait_ld();
+          const uint32_t vm = mask_of(i);
+          uint32_t pk[F::W / 2];
+          // (the branch outside: with a select per element the pass takes twice as long)
+          if (vm == kAll) {
+#pragma unroll
+            for (int j = 0; j < F::W; j += 2) {
+              const float p0 = exp2_approx(fmaf(__uint_as_float(r[j]), p.scale_log2, -mm));
+              const float p1 = exp2_approx(fmaf(__uint_as_float(r[j + 1]), p.scale_log2, -mm));
+              l += p0 + p1;
+              pk[j / 2] = pack_bf16x2(p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < F::W; j += 2) {
+              float p0 = exp2_approx(fmaf(__uint_as_float(r[j]), p.scale_log2, -mm));
+              float p1 = exp2_approx(fmaf(__uint_as_float(r[j + 1]), p.scale_log2, -mm));
+              p0 = ((vm >> j) & 1u) ? p0 : 0.f;
+              p1 = ((vm >> (j + 1)) & 1u) ? p1 : 0.f;
+              l += p0 + p1;
+              pk[j / 2] = pack_bf16x2(p0, p1);
+            }
+          }
+          const int s = slot0 + part * F::CP + i * F::W;
+          const uint32_t at = smem0 + (s >> 6) * kPBlock + h * 128 + ((h & 7) ^ ((s & 63) >> 3)) * 16;
+#pragma unroll
+          for (int u = 0; u < F::W / 8; ++u)
+            st_shared16(at ^ (16 * u), make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]));
+        }
+      }
+      s_red[4 * kH + part * kH + h] = l;
+      fence_proxy_async_smem();  // P (generic writes) before the MMAs and copies that read it
       tc_fence_before();
       worker_sync();
-      if (tid < F::NK && slot0 + tid < p.n_sel)
-        p.weights[static_cast<int64_t>(t) * p.n_sel + slot0 + tid] =
-            (s_w[tid] + s_w[F::NK + tid]) + (s_w[2 * F::NK + tid] + s_w[3 * F::NK + tid]);
-    };
-    if (C == 1 && p.weights) key_weights();
-    if constexpr (C == 1) {
-      if (lane == 0) mbar_arrive(&p_full[0]);
-    }
-    if (p.lse && rank == 0 && part == 0 && h < p.n_heads)
-      p.lse[t * p.n_heads + h] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
-    // ---------------- C: value blocks, then the output through shared memory
-#pragma unroll 1
-    for (int n = 1; n < vblocks * F::Halves; n += 2) {
-      v_load(n + 1, vc[0], vs[0]);
-      v_store(n, vc[1], vs[1]);
-      v_load(n + 2, vc[1], vs[1]);
-      v_store(n + 1, vc[0], vs[0]);
-    }
-    if (C > 1 && p.weights) key_weights();
-    if constexpr (C == 1) {  // the next token's first reads, behind P V and the output
-      if (t + t_step < p.T) {
-        if (ok) ok = mbar_wait_warp(&rows_full[buf ^ 1], (it >> 1) & 1, s_abort, err);
-        if (ok) fetch(buf ^ 1);
+      l = (s_red[4 * kH + h] + s_red[5 * kH + h]) + (s_red[6 * kH + h] + s_red[7 * kH + h]);
+      if constexpr (C > 1) {
+        if (part == 0) {
+#pragma unroll
+          for (int r = 0; r < C; ++r) st_peer(peer(smem_u32(s_x + (C + rank) * kH + h), r), l);
+          __syncwarp();
+          if (lane < C) arrive_peer(peer(smem_u32(l_full), lane));
+        }
+        if (lane == 0) mbar_arrive(&p_full[rank]);
+        if (warp == 15 && lane > 0 && lane < C) {
+          const int to = (rank + lane) & (C - 1);
+          if (ok && nc > 0)
+            copy_to_peer(peer(smem_u32(smem + (slot0 / 64) * kPBlock), to),
+                         smem_u32(smem + (slot0 / 64) * kPBlock), (nc / 64) * kPBlock,
+                         peer(smem_u32(&p_full[rank]), to));
+          // what the CTA `to` sends here
+          mbar_arrive_expect_tx(&p_full[to],
+                                min(8 / C, max(0, nblk - to * (8 / C))) * kPBlock);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, wait_cluster(l_full, 0u, s_abort, err)) && ok;
+        l = 0.f;
+#pragma unroll
+        for (int r = 0; r < C; ++r) l += s_x[(C + r) * kH + h];
       }
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (ok) ok = mbar_wait_warp(o_ready, it & 1, s_abort, err);
-    tc_fence_after();
-    if (C == 1 && ok && t + t_step < p.T) fetch_rope(buf ^ 1);  // (the ring lies over the V blocks)
-    // Output columns of 64 dims each, in F::Halves runs; at C = 1 a run fills one key slot, and the
-    // run in the slot that the next token's first stage takes goes first.
-    constexpr int RunCols = F::DV / F::Halves, PartCols = RunCols / 4;
-#pragma unroll 1
-    for (int run = 0; run < F::Halves; ++run) {
-      const int half = C == 1 ? (stage & 1) ^ run : run;
-      if (ok) {
-#pragma unroll 1
-        for (int i = 0; i < PartCols / F::OW; ++i) {
-          const int col = half * RunCols + part * PartCols + i * F::OW;
-          uint32_t r[F::OW], pk[F::OW / 2];
-          if (nblk > 0) {
-            tmem_ld<F::OW>(tmem + lane_base + F::OCol + col, r);
+      // w_j = sum over heads of exp2(s - m) / l, once more from S: at C = 1 before P V may write there,
+      // in a cluster (S and O apart) while P V runs.
+      auto key_weights = [&] {
+        const float off = l > 0.f && h < p.n_heads ? mm + __log2f(l) : __int_as_float(0x7f800000);
+        for (int i = 0; i < F::CP / F::W; ++i) {
+          float v[F::W];
+          if (ok && i < nch) {
+            uint32_t r[F::W];
+            tmem_ld<F::W>(scol + i * F::W, r);
             tmem_wait_ld();
+            const uint32_t vm = mask_of(i);
+#pragma unroll
+            for (int j = 0; j < F::W; ++j)
+              v[j] = ((vm >> j) & 1u) && h < p.n_heads
+                         ? exp2_approx(fmaf(__uint_as_float(r[j]), p.scale_log2, -off))
+                         : 0.f;
+          } else {
+#pragma unroll
+            for (int j = 0; j < F::W; ++j) v[j] = 0.f;
           }
-#pragma unroll
-          for (int j = 0; j < F::OW; j += 2)
-            pk[j / 2] = nblk > 0 ? pack_bf16x2(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv)
-                                 : 0u;
-          const uint32_t at =
-              smem0 + F::OffO + (col >> 6) * kPBlock + h * 128 + ((h & 7) ^ ((col & 63) >> 3)) * 16;
-#pragma unroll
-          for (int u = 0; u < F::OW / 8; ++u)
-            st_shared16(at ^ (16 * u),
-                        make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]));
+          const float sum = column_sums<F::W>(v, lane);
+          if (lane < F::W) s_w[quad * F::NK + part * F::CP + i * F::W + lane] = sum;
+        }
+        tc_fence_before();
+        worker_sync();
+        if (tid < F::NK && slot0 + tid < p.n_sel)
+          p.weights[static_cast<int64_t>(t) * p.n_sel + slot0 + tid] =
+              (s_w[tid] + s_w[F::NK + tid]) + (s_w[2 * F::NK + tid] + s_w[3 * F::NK + tid]);
+      };
+      if (C == 1 && p.weights) key_weights();
+      if constexpr (C == 1) {
+        if (lane == 0) mbar_arrive(&p_full[0]);
+      }
+      if (p.lse && rank == 0 && part == 0 && h < p.n_heads)
+        p.lse[t * p.n_heads + h] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
+      // ---------------- C: value blocks, then the output through shared memory
+#pragma unroll 1
+      for (int n = 1; n < vblocks * F::Halves; n += 2) {
+        v_load(n + 1, vc[0], vs[0]);
+        v_store(n, vc[1], vs[1]);
+        v_load(n + 2, vc[1], vs[1]);
+        v_store(n + 1, vc[0], vs[0]);
+      }
+      if (C > 1 && p.weights) key_weights();
+      if constexpr (C == 1) {  // the next token's first reads, behind P V and the output
+        if (t + t_step < p.T) {
+          if (ok) ok = mbar_wait_warp(&rows_full[buf ^ 1], (it >> 1) & 1, s_abort, err);
+          if (ok) fetch(buf ^ 1);
         }
       }
-      fence_proxy_async_smem();
-      if (run == F::Halves - 1) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
-      }
-      worker_sync();
-      if (tid == 0) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (ok) ok = mbar_wait_warp(o_ready, it & 1, s_abort, err);
+      tc_fence_after();
+      if (C == 1 && ok && t + t_step < p.T) fetch_rope(buf ^ 1);  // (the ring lies over the V blocks)
+      // Output columns of 64 dims each, in F::Halves runs; at C = 1 a run fills one key slot, and the
+      // run in the slot that the next token's first stage takes goes first.
+      constexpr int RunCols = F::DV / F::Halves, PartCols = RunCols / 4;
+#pragma unroll 1
+      for (int run = 0; run < F::Halves; ++run) {
+        const int half = C == 1 ? (stage & 1) ^ run : run;
         if (ok) {
 #pragma unroll 1
-          for (int i = 0; i < RunCols / 64; ++i)
-            tma_store_2d(smem + F::OffO + (half * (RunCols / 64) + i) * kPBlock, &tmap_o,
-                         rank * F::DV + half * RunCols + i * 64,
-                         t * p.n_heads);
+          for (int i = 0; i < PartCols / F::OW; ++i) {
+            const int col = half * RunCols + part * PartCols + i * F::OW;
+            uint32_t r[F::OW], pk[F::OW / 2];
+            if (nblk > 0) {
+              tmem_ld<F::OW>(tmem + lane_base + F::OCol + col, r);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int j = 0; j < F::OW; j += 2)
+              pk[j / 2] = nblk > 0 ? pack_bf16x2(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv)
+                                   : 0u;
+            const uint32_t at =
+                smem0 + F::OffO + (col >> 6) * kPBlock + h * 128 + ((h & 7) ^ ((col & 63) >> 3)) * 16;
+#pragma unroll
+            for (int u = 0; u < F::OW / 8; ++u)
+              st_shared16(at ^ (16 * u),
+                          make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]));
+          }
         }
-        bulk_store_commit();
+        fence_proxy_async_smem();
+        if (run == F::Halves - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+        }
+        worker_sync();
+        if (tid == 0) {
+          if (ok) {
+#pragma unroll 1
+            for (int i = 0; i < RunCols / 64; ++i)
+              tma_store_2d(smem + F::OffO + (half * (RunCols / 64) + i) * kPBlock, &tmap_o,
+                           rank * F::DV + half * RunCols + i * 64,
+                           t * p.n_heads);
+          }
+          bulk_store_commit();
+        }
       }
-    }
-    if constexpr (C > 1) break;
+      if constexpr (C > 1) break;
     }
     if (tid == 0) bulk_store_wait<0>();
   } else if (warp == kMmaWarp) {
