@@ -9,7 +9,7 @@
 //   B  softmax: the row maxima and sums of the CTAs meet in each other's shared memory, so every
 //      probability is final relative to the list's maximum; P goes as bf16 into shared memory in
 //      the layout of an MMA A operand, each CTA's share copied to the others by bulk copies.
-//   C  O[128 heads x 512/C dims] = P V over all slots: blocks of 64 keys of the CTA's value dims are
+//   C  O[128 heads x 512/C dims] = P V over all slots: blocks of 32 or 64 keys of the CTA's value dims are
 //      turned into bf16 again, as an MN-major B operand. Nothing is joined afterwards.
 // C = 1 fills the GPU for many tokens: its CTAs stay and take tokens in turn, reading the next
 // token's first rows behind this one's products. A cluster shortens the chain of phases for few.
@@ -80,8 +80,10 @@ struct Cfg {
   static constexpr int DV = kLatent / C;                // value dims of a CTA
   static constexpr int NB = DV / 64 < 4 ? DV / 64 : 4;  // 64-dim pieces of a V block
   static constexpr int Halves = DV / 64 / NB;           // passes over the keys (2 at C = 1)
-  static constexpr int GV = 8 / NB;                     // V blocks in the making = V stages
-  static constexpr int VStage = NB * 64 * 128;
+  static constexpr int VK = NB == 4 ? 32 : 64;          // keys of a V block
+  static constexpr int VBlocks = kK / VK;               // at most, per pass
+  static constexpr int VStage = NB * VK * 128;
+  static constexpr int GV = kVBytes / VStage;           // V blocks in the making = V stages
   static constexpr int VLanes = NB == 4 ? 4 : 1;        // lanes that share a row of a V block
   static constexpr int OCol = C == 1 ? 0 : 256;         // first TMEM column of O
   static constexpr int CP = NK / 4;                     // S columns of a thread
@@ -103,7 +105,7 @@ struct Cfg {
   static constexpr int NumBars = 2 * NQS + 2 * 2 + 2 * GV + 10 + C;
   static constexpr int OffMisc = OffBars + NumBars * 8;
   static constexpr int Smem = OffMisc + 16 + 1024;
-  static_assert(GV * VStage == kVBytes && Smem <= 232448, "shared memory");
+  static_assert(GV * VK * NB == kWorkers && Smem <= 232448, "one (key, chunk) a worker thread");
 };
 
 struct Params {
@@ -157,11 +159,11 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout: blocks of 64 N
-// (64 keys x 128 bytes apart), atoms of 8 keys along K.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+// `stride` bytes apart, atoms of 8 keys (1 KB) along K.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t stride) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((64u * 128u) >> 4) << 16;
+  d |= static_cast<uint64_t>(stride >> 4) << 16;
   d |= static_cast<uint64_t>(1024u >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < F::GV; ++i) {
-      mbar_init(&v_full[i], 2 * F::NB);
+      mbar_init(&v_full[i], F::VK * F::NB / 32);
       mbar_init(&v_empty[i], 1);
     }
     mbar_init(s_ready, 1);
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // The order in which P V takes its blocks: this CTA's own first, then as the others' shares come.
   auto block_at = [&](int i) {
-    constexpr int per = 8 / C;
+    constexpr int per = F::VBlocks / C;
     return C == 1 ? i : ((rank - i / per) & (C - 1)) * per + i % per;
   };
   // This CTA's used slots (by 64).
@@ -548,9 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       constexpr uint32_t kAll = F::W == 32 ? 0xFFFFFFFFu : 0xFFFFu;
       // Value blocks of this thread's group: its codes are read one block ahead.
-      const int gv = tid / (64 * F::NB), vtid = tid % (64 * F::NB);
-      const int vnb = F::VLanes == 4 ? vtid & 3 : vtid / 64, vr = F::VLanes == 4 ? vtid >> 2 : vtid % 64;
-      const int vblocks = gv < nblk ? (nblk - gv + F::GV - 1) / F::GV : 0;  // per half
+      const int gv = tid / (F::VK * F::NB), vtid = tid % (F::VK * F::NB);
+      const int vnb = F::VLanes == 4 ? vtid & 3 : vtid / F::VK;
+      const int vr = F::VLanes == 4 ? vtid >> 2 : vtid % F::VK;
+      const int nvb = nblk * (64 / F::VK);                                  // used V blocks
+      const int vblocks = gv < nvb ? (nvb - gv + F::GV - 1) / F::GV : 0;    // this group's, per half
       uint32_t vc[2][8], vs[2];
       auto v_load = [&](int n, uint32_t (&codes)[8], uint32_t& sc) {  // n: this group's n-th block
         if (n >= vblocks * F::Halves) return;
@@ -558,12 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kb = gv + F::GV * (n - half * vblocks);
         if constexpr (C > 1) {
 #pragma unroll
-          for (int i = 0, k = n; i < 8; ++i) {
+          for (int i = 0, k = n; i < F::VBlocks; ++i) {
             const int b = block_at(i);
-            if (b % F::GV == gv && b < nblk && k-- == 0) kb = b;
+            if (b % F::GV == gv && b < nvb && k-- == 0) kb = b;
           }
         }
-        const int32_t r = s_rows[kb * 64 + vr];
+        const int32_t r = s_rows[kb * F::VK + vr];
         const int chunk = rank * (F::DV / 64) + half * F::NB + vnb;
 #pragma unroll
         for (int j = 0; j < 8; ++j) codes[j] = kEmptyWord;
@@ -579,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = mbar_wait_warp(&v_empty[gv], (vuse & 1) ^ 1u, s_abort, err);
         ++vuse;
         if (!ok) return;
-        store_chunk<F::VLanes>(smem0 + kOffV + gv * F::VStage + vnb * (64 * 128), vr, codes, sc, vnb);
+        store_chunk<F::VLanes>(smem0 + kOffV + gv * F::VStage + vnb * (F::VK * 128), vr, codes, sc,
+                               vnb);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[gv]);
@@ -799,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const uint64_t q0 = smem_desc_sw128(smem_u32(smem + F::OffQ));
     const uint64_t k0 = smem_desc_sw128(smem_u32(smem));
-    const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV));
+    const uint64_t v0 = smem_desc_mn_sw128(smem_u32(smem + kOffV), F::VK * 128);
     constexpr uint32_t o_idesc = instr_desc(1u, 1u, 128, F::NB * 64) | (1u << 16);  // B MN-major
     uint32_t qn = 0, it = 0;  // ring items taken, tokens done
     uint32_t stage = 0;       // latent key stages taken
@@ -874,23 +879,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (C == 1 && ok) ok = mbar_wait_warp(&p_full[0], it & 1, s_abort, err);
       for (int half = 0; half < F::Halves; ++half) {
 #pragma unroll 1
-        for (int i0 = 0, taken = 0; ok && i0 < 8; i0 += F::GV) {
+        for (int i0 = 0, taken = 0; ok && i0 < F::VBlocks; i0 += F::GV) {
 #pragma unroll
           for (int j = 0; j < F::GV; ++j) {
             const int kb = block_at(i0 + j);
-            if (!ok || kb >= nblk) continue;
+            if (!ok || kb >= nblk * (64 / F::VK)) continue;
             const int st = C == 1 ? j : kb % F::GV;
-            if (C > 1 && !(ok = mbar_wait_warp(&p_full[kb / (8 / C)], 0u, s_abort, err))) break;
+            if (C > 1 && !(ok = mbar_wait_warp(&p_full[kb / (F::VBlocks / C)], 0u, s_abort, err)))
+              break;
             uint32_t use = 0;
 #pragma unroll
             for (int v = 0; v < F::GV; ++v)
               if (v == st) use = vn[v]++;
             if (!(ok = mbar_wait_warp(&v_full[st], use & 1, s_abort, err))) break;
             tc_fence_after();
-            const uint64_t pd = k0 + kb * (kPBlock >> 4), vd = v0 + st * (F::VStage >> 4);
+            const int key = kb * F::VK;
+            const uint64_t pd = k0 + (key >> 6) * (kPBlock >> 4) + (key & 63) * 2 / 16;
+            const uint64_t vd = v0 + st * (F::VStage >> 4);
             if (lead) {
 #pragma unroll
-              for (int s = 0; s < 4; ++s)
+              for (int s = 0; s < F::VK / 16; ++s)
                 mma_bf16(tmem + F::OCol + half * 256, pd + 2 * s, vd + s * (16 * 128 >> 4), o_idesc,
                          (taken | s) ? 1u : 0u);
             }
