@@ -80,7 +80,11 @@ struct Cfg {
   static constexpr int DV = kLatent / C;                // value dims of a CTA
   static constexpr int NB = DV / 64 < 4 ? DV / 64 : 4;  // 64-dim pieces of a V block
   static constexpr int Halves = DV / 64 / NB;           // passes over the keys (2 at C = 1)
-  static constexpr int VK = NB == 4 ? 32 : 64;          // keys of a V block
+  // Keys of a V block. At C = 1 blocks of 32 in four stages: one group's hand-over to the products
+  // hides behind three others (4096 tokens 677 us, blocks of 64 in two stages 703). A pair of CTAs
+  // gains nothing by that, as its products also wait for P, and pays for twice the hand-overs (37
+  // tokens 21.4 us, with 64 keys 20.8).
+  static constexpr int VK = C == 1 ? 32 : 64;
   static constexpr int VBlocks = kK / VK;               // at most, per pass
   static constexpr int VStage = NB * VK * 128;
   static constexpr int GV = kVBytes / VStage;           // V blocks in the making = V stages
