@@ -9,8 +9,8 @@
 //   B  softmax: the row maxima and sums of the CTAs meet in each other's shared memory, so every
 //      probability is final relative to the list's maximum; P goes as bf16 into shared memory in
 //      the layout of an MMA A operand, each CTA's share copied to the others by bulk copies.
-//   C  O[128 heads x 512/C dims] = P V over all slots: blocks of 32 or 64 keys of the CTA's value dims are
-//      turned into bf16 again, as an MN-major B operand. Nothing is joined afterwards.
+//   C  O[128 heads x 512/C dims] = P V over all slots: blocks of 32 or 64 keys of the CTA's value
+//      dims are turned into bf16 again, as an MN-major B operand. Nothing is joined afterwards.
 // C = 1 fills the GPU for many tokens: its CTAs stay and take tokens in turn, reading the next
 // token's first rows behind this one's products. A cluster shortens the chain of phases for few.
 //
@@ -21,8 +21,8 @@
 // twice because O takes all 512 TMEM columns at C = 1, so P V starts only after the whole of S is
 // read, and 512 unpacked rows (576 KB) do not fit shared memory.
 //
-// 128 heads, 512 rows: 11.3 us for one token (C = 8; the latency of the phases), 703 us for 4096
-// tokens of a 65536-row cache, 831 TFLOP/s, 0.43 of the measured tensor peak: bound by the unpacking
+// 128 heads, 512 rows: 11.7 us for one token (C = 8; the latency of the phases), 677 us for 4096
+// tokens of a 65536-row cache, 863 TFLOP/s, 0.44 of the measured tensor peak: bound by the unpacking
 // on the half-rate integer pipe and by shared memory, of which the MMAs read 96 bytes a clock.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -1071,9 +1071,10 @@ extern "C" int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, i
   p.n_heads = n_heads;
   p.n_sel = n_sel;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
-  // The widest cluster of which all tokens run at once. 512 rows, 128 heads, us for 8 / 4 / 2 / 1 CTAs
-  // a token: 12.9 / 13.3 / 17.3 / 26.1 at 12 tokens, 17.3 / 13.6 / 17.3 / 26.2 at 16 (15 clusters of 8
-  // run at once), 37 / 26 / 17.6 / 26.5 at 37 (36 of 4), 64 / 32 / 22.6 / 26.6 at 77 (76 of 2).
+  // The widest cluster of which all tokens run at once (15 of 8, 36 of 4 and 76 of 2 on the GPU asked
+  // first; it depends on which SMs a part has). 512 rows, 128 heads, us for 8 / 4 / 2 / 1 CTAs a token:
+  // 12.9 / 13.4 / 17.4 / 25.8 at 12 tokens, 23 / 13.4 / 17.3 / 25.8 at 16, 35 / 18.2 / 17.6 / 25.8 at 37
+  // (26 instead of 18.2 where a second round is needed), 71 / 39 / 34 / 26.5 at 77.
   if (T <= clusters_at_once<8>()) return launch<8>(tq, to, p, T, stream);
   if (T <= clusters_at_once<4>()) return launch<4>(tq, to, p, T, stream);
   if (T <= clusters_at_once<2>()) return launch<2>(tq, to, p, T, stream);
