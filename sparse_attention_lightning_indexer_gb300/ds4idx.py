@@ -332,7 +332,8 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
     if len(layouts) != n or len(outs) != n:
         raise ValueError("interleaved and outs need one entry per tensor")
     T = xs[0].shape[0]
-    _need(positions, (T,), "positions", torch.int64)
+    dev = _device(positions, "positions")
+    _need(positions, (T,), "positions", torch.int64, dev)
     rot = freqs.rot_dim
     d = ctypes.create_string_buffer(n * _ROTARY_TENSOR.size)
     for k, (x, o, il) in enumerate(zip(xs, outs, layouts)):
@@ -343,8 +344,8 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
                              f"[{T}, {rot}]")
         if o.shape != shape or o.dtype != x.dtype:
             raise ValueError(f"out {k} must have the shape and dtype of tensor {k}")
-        if not (x.is_cuda and o.is_cuda):
-            raise ValueError(f"tensor {k} must be a CUDA tensor")
+        if x.get_device() != dev or o.get_device() != dev:
+            raise ValueError(f"tensor {k} and its out must be on the device of positions, cuda:{dev}")
         if st[-1] != 1 or so[-1] != 1:
             raise ValueError(f"the rotated dim of tensor {k} must be adjacent")
         heads, xh, oh = (shape[1], st[1], so[1]) if dims == 3 else (1, 0, 0)
@@ -354,7 +355,7 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
                                  _in_dtype(x, "a rotary tensor"), 1 if il else 0, heads, 0, st[0],
                                  xh, so[0], oh)
     _check(load().ds4idx_rotary(n, ctypes.addressof(d), T, rot, positions.data_ptr(), freqs.address,
-                                freqs.scale, 1 if inverse else 0, _stream_ptr(stream, positions)),
+                                freqs.scale, 1 if inverse else 0, _stream_ptr(stream, dev)),
            "ds4idx_rotary")
     return outs[0] if single else outs
 
@@ -388,9 +389,9 @@ def rotary_autograd(xs, positions, freqs: RotaryFreqs, interleaved=True):
 Q4_ROW_BYTES = 416
 
 
-def _cache_rows(cache) -> int:
+def _cache_rows(cache, dev) -> int:
     rows = cache.shape[0]
-    _need(cache, (rows, Q4_ROW_BYTES), "cache", torch.uint8)
+    _need(cache, (rows, Q4_ROW_BYTES), "cache", torch.uint8, dev)
     return rows
 
 
@@ -398,13 +399,14 @@ def quantize_latents(x, cache, dst_offset: int = 0, slots=None, stream=None):
     """Writes latent rows x [n, 576] (fp32/bf16) in 4 bits into cache [R, 416] uint8, at rows
     dst_offset.. or at slots [n] (int64, -1 skips a row)."""
     n = x.shape[0]
-    _need(x, (n, SA_DQK), "x")
-    R = _cache_rows(cache)
+    dev = _device(cache, "cache")
+    _need(x, (n, SA_DQK), "x", None, dev)
+    R = _cache_rows(cache, dev)
     if slots is not None:
-        _need(slots, (n,), "slots", torch.int64)
+        _need(slots, (n,), "slots", torch.int64, dev)
     _check(load().ds4idx_quantize_latents(_ptr(x), _in_dtype(x, "x"), n, _ptr(slots),
                                           int(dst_offset), _ptr(cache), R,
-                                          _stream_ptr(stream, cache)),
+                                          _stream_ptr(stream, dev)),
            "ds4idx_quantize_latents")
     return cache
 
@@ -413,22 +415,23 @@ def read_latents(cache, rows=None, start: int = 0, n: int | None = None, out=Non
                  dtype=torch.bfloat16, stream=None):
     """The values of cache rows ``rows`` [n] (int64; rows outside the cache give zeros) or of rows
     start .. start + n - 1 (n None: to the end), as [n, 576] bf16 or fp32."""
-    R = _cache_rows(cache)
+    dev = _device(cache, "cache")
+    R = _cache_rows(cache, dev)
     if rows is not None:
         n = rows.shape[0]
-        _need(rows, (n,), "rows", torch.int64)
+        _need(rows, (n,), "rows", torch.int64, dev)
     elif n is None:
         n = R - int(start)
     if out is None:
         out = torch.empty((n, SA_DQK), dtype=dtype, device=cache.device)
-    _need(out, (n, SA_DQK), "out")
+    _need(out, (n, SA_DQK), "out", None, dev)
     _check(load().ds4idx_read_latents(_ptr(cache), R, _ptr(rows), int(start), n, _ptr(out),
-                                      _in_dtype(out, "out"), _stream_ptr(stream, cache)),
+                                      _in_dtype(out, "out"), _stream_ptr(stream, dev)),
            "ds4idx_read_latents")
     return out
 
 
-def _placement(T, kv_row0, page_table, page_size, token_seq):
+def _placement(T, kv_row0, page_table, page_size, token_seq, dev):
     """The ds4idx_placement of a call, or None (row = position)."""
     if kv_row0 is None and page_table is None:
         if token_seq is not None:
@@ -438,16 +441,16 @@ def _placement(T, kv_row0, page_table, page_size, token_seq):
     if kv_row0 is not None:
         if page_table is not None or token_seq is not None:
             raise ValueError("kv_row0 and page_table exclude each other")
-        _need(kv_row0, (T,), "kv_row0", torch.int64)
+        _need(kv_row0, (T,), "kv_row0", torch.int64, dev)
         w.kv_row0 = kv_row0.data_ptr()
         return w
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n_seqs, pages_per_seq]")
-    _need(page_table, tuple(page_table.shape), "page_table", torch.int32)
+    _need(page_table, tuple(page_table.shape), "page_table", torch.int32, dev)
     w.page_table = page_table.data_ptr()
     w.n_seqs, w.pages_per_seq, w.page_size = page_table.shape[0], page_table.shape[1], int(page_size)
     if token_seq is not None:
-        _need(token_seq, (T,), "token_seq", torch.int32)
+        _need(token_seq, (T,), "token_seq", torch.int32, dev)
         w.token_seq = token_seq.data_ptr()
     return w
 
@@ -466,24 +469,24 @@ def sparse_attention_q4(q, cache, idx, sm_scale: float, kv_row0=None, page_table
     Returns (out [T, H, 512] bf16, lse [T, H] fp32, weights [T, n_sel] fp32 or None): weights is
     each entry's probability summed over the heads."""
     T, H, n_sel = q.shape[0], q.shape[1], idx.shape[1]
-    R = _cache_rows(cache)
-    _need(q, (T, H, SA_DQK), "q", torch.bfloat16)
-    _need(idx, (T, n_sel), "idx", torch.int32)
-    where = _placement(T, kv_row0, page_table, page_size, token_seq)
-    dev = q.device
+    dev = _device(q, "q")
+    R = _cache_rows(cache, dev)
+    _need(q, (T, H, SA_DQK), "q", torch.bfloat16, dev)
+    _need(idx, (T, n_sel), "idx", torch.int32, dev)
+    where = _placement(T, kv_row0, page_table, page_size, token_seq, dev)
     if out is None:
-        out = torch.empty((T, H, SA_DV), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, H, SA_DV), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     if weights is None and want_weights:
-        weights = torch.empty((T, n_sel), dtype=torch.float32, device=dev)
-    _need(out, (T, H, SA_DV), "out", torch.bfloat16)
-    _need(lse, (T, H), "lse", torch.float32)
+        weights = torch.empty((T, n_sel), dtype=torch.float32, device=q.device)
+    _need(out, (T, H, SA_DV), "out", torch.bfloat16, dev)
+    _need(lse, (T, H), "lse", torch.float32, dev)
     if weights is not None:
-        _need(weights, (T, n_sel), "weights", torch.float32)
+        _need(weights, (T, n_sel), "weights", torch.float32, dev)
     _check(load().ds4idx_sparse_attention_q4(_ptr(q), _ptr(cache), R, _ptr(idx), _ref(where), T, H,
                                              SA_DQK, SA_DV, n_sel, float(sm_scale), _ptr(out),
-                                             _ptr(lse), _ptr(weights), _stream_ptr(stream, q)),
+                                             _ptr(lse), _ptr(weights), _stream_ptr(stream, dev)),
            "ds4idx_sparse_attention_q4")
     return out, lse, weights
 
@@ -499,12 +502,13 @@ def evict_accumulate(total, weights, idx, kv_row0=None, page_table=None, page_si
     placement as in ``sparse_attention_q4``."""
     T, n_sel = idx.shape[0], idx.shape[1]
     R = total.shape[0]
-    _need(total, (R,), "total", torch.int64)
-    _need(weights, (T, n_sel), "weights", torch.float32)
-    _need(idx, (T, n_sel), "idx", torch.int32)
-    where = _placement(T, kv_row0, page_table, page_size, token_seq)
+    dev = _device(total, "total")
+    _need(total, (R,), "total", torch.int64, dev)
+    _need(weights, (T, n_sel), "weights", torch.float32, dev)
+    _need(idx, (T, n_sel), "idx", torch.int32, dev)
+    where = _placement(T, kv_row0, page_table, page_size, token_seq, dev)
     _check(load().ds4idx_evict_accumulate(_ptr(total), R, _ptr(weights), _ptr(idx), _ref(where), T,
-                                          n_sel, _stream_ptr(stream, total)), "ds4idx_evict_accumulate")
+                                          n_sel, _stream_ptr(stream, dev)), "ds4idx_evict_accumulate")
     return total
 
 
@@ -524,16 +528,17 @@ def evict_select(total, starts, seq_lens, keep, n_sink: int = 0, n_recent: int =
     if len(starts) != B or len(keep) != B:
         raise ValueError("starts, seq_lens and keep need one entry per sequence")
     R = total.shape[0]
-    _need(total, (R,), "total", torch.int64)
+    dev = _device(total, "total")
+    _need(total, (R,), "total", torch.int64, dev)
     if kept is None:
         width = max(map(min, keep, seq_lens), default=0)
         kept = torch.empty((B, max(width, 0)), dtype=torch.int32, device=total.device)
-    _need(kept, (B, kept.shape[1]), "kept", torch.int32)
+    _need(kept, (B, kept.shape[1]), "kept", torch.int32, dev)
     host = _i64([*starts, *seq_lens, *keep])
     at = _i64_address(host)
     _check(load().ds4idx_evict_select(_ptr(total), R, B, at, at + 8 * B, at + 16 * B, int(n_sink),
                                       int(n_recent), _ptr(kept), kept.shape[1],
-                                      _stream_ptr(stream, total)), "ds4idx_evict_select")
+                                      _stream_ptr(stream, dev)), "ds4idx_evict_select")
     return kept
 
 
@@ -546,17 +551,18 @@ def evict_compact(kept, seq_lens, keep, src_starts, dst_starts, srcs, dsts, stre
         raise ValueError("keep, src_starts and dst_starts need one entry per sequence")
     if len(srcs) != len(dsts):
         raise ValueError("srcs and dsts need the same number of arrays")
-    _need(kept, (B, kept.shape[1]), "kept", torch.int32)
+    dev = _device(kept, "kept")
+    _need(kept, (B, kept.shape[1]), "kept", torch.int32, dev)
     n = len(srcs)
     if n > 8:
         raise ValueError("at most 8 arrays")
     d = ctypes.create_string_buffer(max(1, n) * _ROW_ARRAY.size)
     for k, (src, dst) in enumerate(zip(srcs, dsts)):
         shape, dshape = src.shape, dst.shape
-        if not (src.is_cuda and dst.is_cuda and src.is_contiguous() and dst.is_contiguous()
-                and src.dtype == dst.dtype and shape[1:] == dshape[1:]):
-            _need(src, tuple(shape), f"srcs[{k}]")
-            _need(dst, (dshape[0], *shape[1:]), f"dsts[{k}]", src.dtype)
+        if not (src.get_device() == dev and dst.get_device() == dev and src.is_contiguous()
+                and dst.is_contiguous() and src.dtype == dst.dtype and shape[1:] == dshape[1:]):
+            _need(src, tuple(shape), f"srcs[{k}]", None, dev)
+            _need(dst, (dshape[0], *shape[1:]), f"dsts[{k}]", src.dtype, dev)
         rows = shape[0]
         row = src.nbytes // rows if rows else src.element_size() * math.prod(shape[1:])
         _ROW_ARRAY.pack_into(d, k * _ROW_ARRAY.size, src.data_ptr(), dst.data_ptr(), rows,
@@ -566,7 +572,7 @@ def evict_compact(kept, seq_lens, keep, src_starts, dst_starts, srcs, dsts, stre
     at = _i64_address(host)
     _check(load().ds4idx_evict_compact(_ptr(kept), kept.shape[1], B, at, at + 8 * B, at + 16 * B,
                                        at + 24 * B, n, ctypes.addressof(d),
-                                       _stream_ptr(stream, kept)),
+                                       _stream_ptr(stream, dev)),
            "ds4idx_evict_compact")
     return dsts
 
@@ -591,14 +597,29 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_ptr(stream, tensor=None):
-    """The stream of a call: the one given, else the current one (of the device of ``tensor``, which
-    saves asking for the current device)."""
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _device(t, name: str) -> int:
+    """The device of a call: that of its first tensor. It has to be the current one, where the
+    kernel is launched; ``_need`` holds the call's other tensors to it."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _stream_ptr(stream, dev=None):
+    """The stream of a call: the one given (it has to be of device ``dev``), else the current one."""
     if stream is not None:
+        if dev is not None and getattr(stream, "device_index", dev) != dev:
+            raise ValueError(f"stream is of cuda:{stream.device_index}, the tensors of cuda:{dev}")
         return stream.cuda_stream
     if _raw_stream is not None:
-        if tensor is not None:
-            return _raw_stream(tensor.get_device())
+        if dev is not None:
+            return _raw_stream(dev)
         if torch.cuda.is_initialized():
             return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
@@ -616,13 +637,17 @@ def _codes(t: torch.Tensor, dtype: int, name: str) -> torch.Tensor:
     return t
 
 
-def _need(t: torch.Tensor, shape, name: str, dtype=None):
+def _need(t: torch.Tensor, shape, name: str, dtype=None, dev=None):
+    """Raises unless t is a contiguous CUDA tensor of this shape (and dtype, and on device dev)."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.is_cuda and t.shape == shape and t.is_contiguous() and (dtype is None or t.dtype == dtype):
+    if ((t.is_cuda if dev is None else t.get_device() == dev) and t.shape == shape
+            and t.is_contiguous() and (dtype is None or t.dtype == dtype)):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's other tensors on cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if tuple(t.shape) != tuple(shape):
