@@ -379,7 +379,9 @@ typedef struct {
  *           [T, n_sel] fp32 or NULL (summed in a fixed order).
  * Cache values are exact in bf16; products accumulate in fp32, softmax and sums are fp32, the
  * probabilities are rounded to bf16 for the value product. What a row of no entry holds (NaN
- * included) does not reach the results. Few tokens (up to about half the SMs) run a cluster of CTAs
+ * included) does not reach the results. Scores that are not finite follow the formulas: NaN among
+ * them gives lse, out and the head's weights NaN; +infinity lse +infinity and out NaN; a list of
+ * -infinity alone lse -infinity and out NaN, unlike an empty one. Few tokens (up to about half the SMs) run a cluster of CTAs
  * each. Asynchronous on `stream`, allocates nothing. Bounded device waits that run out are recorded
  * for ds4idx_sparse_attention_status.
  * Errors: INVALID_ARG, UNSUPPORTED (d_qk != 576, d_v != 512), LAUNCH, CUDA. T = 0 is a no-op. */

@@ -57,7 +57,7 @@ constexpr int kQBytes = kH * 128;
 constexpr int kPBlock = kH * 128;            // 64 keys of P
 constexpr int kOffV = (kK / 64) * kPBlock;   // P first, then the V blocks
 constexpr int kVBytes = 64 * 1024;
-constexpr float kNegInf = -__builtin_inff();
+constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
 
 template <int C>
 struct Cfg {
@@ -633,7 +633,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int r = 0; r < C; ++r) m = fmaxf(m, s_x[r * kH + h]);
       }
-      const float mm = m == kNegInf ? 0.f : m;
+      // Finite, so that a score of +-infinity keeps its meaning in s - mm. A sum l that is NaN, infinite
+      // or (scores of -infinity alone) zero then gives lse and out by the formulas; only an empty list
+      // is set apart, by its mask.
+      const float mm = fminf(fmaxf(m, -kMax), kMax);
       float l = 0.f;
       if (ok) {
         for (int i = 0; i < nch; ++i) {
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the rounding of m + log2 l, 2^-24 of the scores' size, would be left in the weights. (The
       // branch outside, as above: chunk of 4096 with weights 777 us, a select per element 834.)
       auto key_weights = [&] {
-        const float part_of = l > 0.f ? 1.f / l : 0.f;
+        const float part_of = nblk > 0 ? 1.f / l : 0.f;
         for (int i = 0; i < F::CP / F::W; ++i) {
           float v[F::W];
           if (ok && i < nch) {
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[0]);
       }
       if (p.lse && rank == 0 && part == 0 && h < p.n_heads)
-        p.lse[t * p.n_heads + h] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
+        p.lse[t * p.n_heads + h] = nblk > 0 ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
       // ---------------- C: value blocks, then the output through shared memory
 #pragma unroll 1
       for (int n = 1; n < vblocks * F::Halves; n += 2) {
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) fetch(buf ^ 1);
         }
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = nblk > 0 ? 1.f / l : 0.f;
       if (ok) ok = mbar_wait_warp(o_ready, it & 1, s_abort, err);
       tc_fence_after();
       if (C == 1 && ok && t + t_step < p.T) fetch_rope(buf ^ 1);  // (the ring lies over the V blocks)
