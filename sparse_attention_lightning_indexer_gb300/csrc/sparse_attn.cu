@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       uint32_t rb[2][32];
       m = fmaxf(red[h], red[kH + h]);
-      const float mm = m == -__int_as_float(0x7f800000) ? 0.f : m;
+      const float mm = fminf(fmaxf(m, -__FLT_MAX__), __FLT_MAX__);  // finite: s - mm keeps infinities
       tmem_ld32(tmem + lane_base + 32 * i0, rb[0]);
       tmem_wait_ld();
       float ls = 0.f;
@@ -392,9 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(p_ready);
     softmax_sync();  // both halves' sums are in shared memory
     if (ok) l = red[2 * kH + h] + red[3 * kH + h];
+    // Only an empty list is set apart, by its mask: a sum l that is NaN (or zero, at scores of
+    // -infinity alone) gives lse and out by the formulas.
+    uint32_t used = 0u;
+    for (int i = 0; i < kK / 32; ++i) used |= s_mask[i];
     if (p.lse && g == 0)
-      p.lse[t * kH + h] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -__int_as_float(0x7f800000);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+      p.lse[t * kH + h] = used ? (m + __log2f(l)) * 0.69314718055994531f : -__int_as_float(0x7f800000);
+    const float inv = used ? 1.f / l : 0.f;
     uint16_t* orow = p.out + (t * kH + h) * kDv;
     const uint64_t pass = policy_evict_first();
     for (int half = 0; ok && half < 2; ++half) {
