@@ -423,9 +423,10 @@ typedef struct {
 
 /* Moves the kept rows of B sequences together: for every array, dst row dst_starts[b] + i = src row
  * src_starts[b] + kept[b][i], i < counts[b] (kept as written by ds4idx_evict_select, counts[b] =
- * min(keep[b], seq_lens[b])). 1 <= n_arrays <= 8. The written rows of an array must not overlap the
- * source range of any sequence in it (checked against src_starts[b] .. + src_lens[b]). HOST: arrays,
- * src_starts, src_lens, dst_starts, counts; DEVICE: kept [B, width] (an entry outside 0..src_lens-1
+ * min(keep[b], seq_lens[b])). 1 <= n_arrays <= 8. The rows written for a sequence in an array must not
+ * overlap those of another sequence or array, nor a source range (src_starts[b] .. + src_lens[b]) of
+ * any sequence in any array: refused, as their order is not defined. Source ranges may overlap. HOST:
+ * arrays, src_starts, src_lens, dst_starts, counts; DEVICE: kept [B, width] (an entry outside 0..src_lens-1
  * leaves its row unwritten). Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH. */
 int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t B, const int64_t* src_starts,
                          const int64_t* src_lens, const int64_t* dst_starts, const int64_t* counts,

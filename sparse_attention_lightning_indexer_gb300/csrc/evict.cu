@@ -399,9 +399,22 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   }
 }
 
-bool overlap(const uint8_t* a, int64_t na, const uint8_t* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && x < y + nb && y < x + na;
+// A range of bytes that a move reads (a sequence's source rows) or writes.
+struct Range {
+  uintptr_t at, end;
+  bool written;
+};
+// Whether a written range meets any other: sorted by their starts, a range that begins before the end
+// of an earlier one meets it. Reads may share rows.
+bool written_meets_another(Range* r, int n) {
+  std::sort(r, r + n, [](const Range& a, const Range& b) { return a.at < b.at; });
+  uintptr_t any_end = 0, written_end = 0;
+  for (int i = 0; i < n; ++i) {
+    if (r[i].at < (r[i].written ? any_end : written_end)) return true;
+    any_end = std::max(any_end, r[i].end);
+    if (r[i].written) written_end = std::max(written_end, r[i].end);
+  }
+  return false;
 }
 
 }  // namespace ds4e
@@ -492,6 +505,8 @@ extern "C" int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t 
   }
   p.rows = p.first[B];
   int64_t ctas = 0;
+  Range ranges[kMaxArrays * 2 * kMaxB];
+  int n_ranges = 0;
   for (int k = 0; k < n_arrays; ++k) {
     const ds4idx_row_array& d = arrays[k];
     if (d.row_bytes < 1 || d.row_bytes > 65536) return DS4IDX_ERR_INVALID_ARG;
@@ -501,10 +516,12 @@ extern "C" int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t 
     for (int b = 0; b < B; ++b) {
       if (src_starts[b] > d.src_rows - src_lens[b] || dst_starts[b] > d.dst_rows - counts[b])
         return DS4IDX_ERR_INVALID_ARG;
-      for (int c = 0; c < B; ++c)
-        if (overlap(dst + dst_starts[b] * d.row_bytes, counts[b] * d.row_bytes,
-                    src + src_starts[c] * d.row_bytes, src_lens[c] * d.row_bytes))
-          return DS4IDX_ERR_INVALID_ARG;
+      auto range = [&](const uint8_t* base, int64_t row, int64_t rows, bool written) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(base) + row * d.row_bytes;
+        if (rows > 0) ranges[n_ranges++] = {at, at + rows * d.row_bytes, written};
+      };
+      range(src, src_starts[b], src_lens[b], false);
+      range(dst, dst_starts[b], counts[b], true);
     }
     const uintptr_t bits = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
                            static_cast<uintptr_t>(d.row_bytes);
@@ -519,6 +536,7 @@ extern "C" int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t 
     ctas += (p.rows + a.rows - 1) / a.rows;
   }
   if (p.rows == 0) return DS4IDX_OK;
+  if (written_meets_another(ranges, n_ranges)) return DS4IDX_ERR_INVALID_ARG;
   if (!kept || !aligned_to(kept, 4) || ctas > 0x7FFFFFFF) return DS4IDX_ERR_INVALID_ARG;
   return launch_dependent(move_kernel, static_cast<unsigned>(ctas), kMoveThreads, 0, 1, stream, p);
 }

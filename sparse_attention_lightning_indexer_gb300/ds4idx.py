@@ -544,8 +544,8 @@ def evict_select(total, starts, seq_lens, keep, n_sink: int = 0, n_recent: int =
 
 def evict_compact(kept, seq_lens, keep, src_starts, dst_starts, srcs, dsts, stream=None):
     """Moves the kept rows (``evict_select`` of the same seq_lens and keep) of up to 8 per-row
-    arrays: dsts[k][dst_starts[b] + i] = srcs[k][src_starts[b] + kept[b, i]]. A written region must
-    not overlap a sequence's source rows."""
+    arrays: dsts[k][dst_starts[b] + i] = srcs[k][src_starts[b] + kept[b, i]]. Written rows must not
+    overlap other written rows or any sequence's source rows, in any of the arrays."""
     B = len(seq_lens)
     if any(len(v) != B for v in (keep, src_starts, dst_starts)):
         raise ValueError("keep, src_starts and dst_starts need one entry per sequence")
