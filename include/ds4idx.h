@@ -300,7 +300,9 @@ typedef enum {
 /* One tensor of a rotary call. x and out point at the first rotated element of token 0, head 0
  * (DEVICE, aligned to an element); element (t, h, i) lies t * stride_t + h * stride_h + i elements
  * further (strides in elements; rotated elements adjacent). out may equal x with equal strides
- * (in place); otherwise the two must not overlap. Elements outside the slice are not touched.
+ * (in place). Otherwise no out of a call may overlap itself (a stride of 0), another out or any x:
+ * refused, as are an out and another tensor whose spans of memory interleave at different token
+ * strides. Elements outside the slice are not touched.
  * 16-byte aligned pointers and strides move 16 bytes a thread; others 2 or 4. */
 typedef struct {
   const void* x;

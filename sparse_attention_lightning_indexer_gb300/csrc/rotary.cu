@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "launch.cuh"
+#include "overlap.h"
 #include "ptx.cuh"
 
 namespace ds4r {
@@ -284,6 +285,22 @@ extern "C" int ds4idx_rotary(int32_t n_tensors, const ds4idx_rotary_tensor* tens
   }
   if (T == 0) return DS4IDX_OK;
   if (!positions || !aligned_to(positions, 8) || total > (1 << 24)) return DS4IDX_ERR_INVALID_ARG;
+  // A CTA reads some items before and some after another writes its own: outputs that share bytes
+  // with each other or with an input (other than in place) would depend on that order.
+  Pieces x[kMaxTensors], out[kMaxTensors];
+  for (int k = 0; k < n_tensors; ++k) {
+    const ds4idx_rotary_tensor& d = tensors[k];
+    const int64_t width = static_cast<int64_t>(rot_dim) * (d.dtype == DS4IDX_F32 ? 4 : 2);
+    x[k] = Pieces(d.x, T, p.t[k].xt, d.n_heads, p.t[k].xh, width);
+    out[k] = Pieces(d.out, T, p.t[k].ot, d.n_heads, p.t[k].oh, width);
+  }
+  for (int k = 0; k < n_tensors; ++k) {
+    if (overlaps_itself(out[k])) return DS4IDX_ERR_INVALID_ARG;
+    for (int j = 0; j < n_tensors; ++j)
+      if ((j > k && overlap(out[k], out[j])) ||
+          (!(j == k && same(out[k], x[k])) && overlap(out[k], x[j])))
+        return DS4IDX_ERR_INVALID_ARG;
+  }
   p.total = static_cast<int32_t>(total);
   // Few tokens: split a token's items over CTAs until about two CTAs an SM are busy, each with at
   // least a load a thread. Many tokens: as few CTAs a token as keep kBatch loads a thread.

@@ -317,7 +317,8 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
     Each is the rotated slice of a projection, [T, H, rot_dim] or [T, rot_dim] (bf16 or fp32, any
     strides, the last dim adjacent). positions [T] int64. interleaved: one bool, or one for each
     tensor (False = halves). inverse: the transposed rotation, which is the gradient. outs: tensors
-    of the same shapes to write (may be the inputs themselves); None allocates dense ones.
+    of the same shapes to write, which may be the inputs themselves but not overlap otherwise; None
+    allocates dense ones.
     """
     single = isinstance(xs, torch.Tensor)
     xs = [xs] if single else list(xs)
