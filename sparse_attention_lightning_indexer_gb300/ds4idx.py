@@ -207,11 +207,11 @@ def quantize_queries(q, w, q_codes=None, w_out=None, qscale=None, stream=None):
     _need(w, (T, H_I), "w", torch.float32)
     dev = q.device
     if q_codes is None:
-        q_codes = torch.empty((T, H_I, D_I), dtype=torch.uint8, device=dev)
+        q_codes = _new((T, H_I, D_I), torch.uint8, dev, stream)
     if w_out is None:
-        w_out = torch.empty((T, H_I), dtype=torch.float32, device=dev)
+        w_out = _new((T, H_I), torch.float32, dev, stream)
     if qscale is None:
-        qscale = torch.empty((T,), dtype=torch.float32, device=dev)
+        qscale = _new((T,), torch.float32, dev, stream)
     _need(q_codes, (T, H_I, D_I), "q_codes", torch.uint8)
     _need(w_out, (T, H_I), "w_out", torch.float32)
     _need(qscale, (T,), "qscale", torch.float32)
@@ -231,9 +231,9 @@ def merge_topk(in_idx, in_score, idx_offsets, row0=None, out_idx=None, out_score
     _need(in_score, (L, rows, TOPK), "in_score", torch.float32)
     dev = in_idx.device
     if out_idx is None:
-        out_idx = torch.empty((rows, TOPK), dtype=torch.int32, device=dev)
+        out_idx = _new((rows, TOPK), torch.int32, dev, stream)
     if out_score is None:
-        out_score = torch.empty((rows, TOPK), dtype=torch.float32, device=dev)
+        out_score = _new((rows, TOPK), torch.float32, dev, stream)
     _need(out_idx, (rows, TOPK), "out_idx", torch.int32)
     _need(out_score, (rows, TOPK), "out_score", torch.float32)
     if len(idx_offsets) != L or (row0 is not None and len(row0) != L):
@@ -262,9 +262,9 @@ def sparse_attention(q, kv, idx, sm_scale: float, kv_row0=None, out=None, lse=No
     if kv_row0 is not None:
         _need(kv_row0, (T,), "kv_row0", torch.int64)
     if out is None:
-        out = torch.empty((T, SA_HEADS, SA_DV), dtype=torch.bfloat16, device=q.device)
+        out = _new((T, SA_HEADS, SA_DV), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, SA_HEADS), dtype=torch.float32, device=q.device)
+        lse = _new((T, SA_HEADS), torch.float32, q.device, stream)
     _need(out, (T, SA_HEADS, SA_DV), "out", torch.bfloat16)
     _need(lse, (T, SA_HEADS), "lse", torch.float32)
     _check(load().ds4idx_sparse_attention(_ptr(q), _ptr(kv), R, _ptr(idx), _ptr(kv_row0), T,
@@ -327,7 +327,7 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
         raise ValueError("rotary takes 1 to 4 tensors")
     layouts = [interleaved] * n if isinstance(interleaved, bool) else list(interleaved)
     if outs is None:
-        outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+        outs = [_new(x.shape, x.dtype, x.device, stream) for x in xs]
     else:
         outs = [outs] if isinstance(outs, torch.Tensor) else list(outs)
     if len(layouts) != n or len(outs) != n:
@@ -424,7 +424,7 @@ def read_latents(cache, rows=None, start: int = 0, n: int | None = None, out=Non
     elif n is None:
         n = R - int(start)
     if out is None:
-        out = torch.empty((n, SA_DQK), dtype=dtype, device=cache.device)
+        out = _new((n, SA_DQK), dtype, cache.device, stream)
     _need(out, (n, SA_DQK), "out", None, dev)
     _check(load().ds4idx_read_latents(_ptr(cache), R, _ptr(rows), int(start), n, _ptr(out),
                                       _in_dtype(out, "out"), _stream_ptr(stream, dev)),
@@ -476,11 +476,11 @@ def sparse_attention_q4(q, cache, idx, sm_scale: float, kv_row0=None, page_table
     _need(idx, (T, n_sel), "idx", torch.int32, dev)
     where = _placement(T, kv_row0, page_table, page_size, token_seq, dev)
     if out is None:
-        out = torch.empty((T, H, SA_DV), dtype=torch.bfloat16, device=q.device)
+        out = _new((T, H, SA_DV), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _new((T, H), torch.float32, q.device, stream)
     if weights is None and want_weights:
-        weights = torch.empty((T, n_sel), dtype=torch.float32, device=q.device)
+        weights = _new((T, n_sel), torch.float32, q.device, stream)
     _need(out, (T, H, SA_DV), "out", torch.bfloat16, dev)
     _need(lse, (T, H), "lse", torch.float32, dev)
     if weights is not None:
@@ -533,7 +533,7 @@ def evict_select(total, starts, seq_lens, keep, n_sink: int = 0, n_recent: int =
     _need(total, (R,), "total", torch.int64, dev)
     if kept is None:
         width = max(map(min, keep, seq_lens), default=0)
-        kept = torch.empty((B, max(width, 0)), dtype=torch.int32, device=total.device)
+        kept = _new((B, max(width, 0)), torch.int32, total.device, stream)
     _need(kept, (B, kept.shape[1]), "kept", torch.int32, dev)
     host = _i64([*starts, *seq_lens, *keep])
     at = _i64_address(host)
@@ -638,6 +638,22 @@ def _codes(t: torch.Tensor, dtype: int, name: str) -> torch.Tensor:
     return t
 
 
+def _new(shape, dtype, device, stream):
+    """An output of a call on ``stream`` (None: the current one), from that stream's memory: what the
+    current stream gave back may still be in use by its queued work. The current stream, on which
+    the caller may go on with the output, is recorded as its user."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(t.device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
 def _need(t: torch.Tensor, shape, name: str, dtype=None, dev=None):
     """Raises unless t is a contiguous CUDA tensor of this shape (and dtype, and on device dev)."""
     if t is None:
@@ -704,9 +720,9 @@ class Indexer:
             _need(kscale, (S,), "kscale", torch.float32)
         dev = q.device
         if out_idx is None:
-            out_idx = torch.empty((T, self.topk), dtype=torch.int32, device=dev)
+            out_idx = _new((T, self.topk), torch.int32, dev, stream)
         if out_score is None and want_score:
-            out_score = torch.empty((T, self.topk), dtype=torch.float32, device=dev)
+            out_score = _new((T, self.topk), torch.float32, dev, stream)
         _need(out_idx, (T, self.topk), "out_idx", torch.int32)
         if out_score is not None:
             _need(out_score, (T, self.topk), "out_score", torch.float32)
@@ -729,9 +745,9 @@ class Indexer:
             _need(kscale, (B, S), "kscale", torch.float32)
         dev = q.device
         if out_idx is None:
-            out_idx = torch.empty((B, T, self.topk), dtype=torch.int32, device=dev)
+            out_idx = _new((B, T, self.topk), torch.int32, dev, stream)
         if out_score is None:
-            out_score = torch.empty((B, T, self.topk), dtype=torch.float32, device=dev)
+            out_score = _new((B, T, self.topk), torch.float32, dev, stream)
         _need(out_idx, (B, T, self.topk), "out_idx", torch.int32)
         _need(out_score, (B, T, self.topk), "out_score", torch.float32)
         pos = (ctypes.c_int64 * B)(*[int(x) for x in pos_offsets])
@@ -770,9 +786,9 @@ class Indexer:
                 raise ValueError("page_table must be [B, pages_per_seq]")
         dev = q.device
         if out_idx is None:
-            out_idx = torch.empty((Q, self.topk), dtype=torch.int32, device=dev)
+            out_idx = _new((Q, self.topk), torch.int32, dev, stream)
         if out_score is None:
-            out_score = torch.empty((Q, self.topk), dtype=torch.float32, device=dev)
+            out_score = _new((Q, self.topk), torch.float32, dev, stream)
         _need(out_idx, (Q, self.topk), "out_idx", torch.int32)
         _need(out_score, (Q, self.topk), "out_score", torch.float32)
         I64 = ctypes.c_int64
@@ -801,7 +817,7 @@ class Indexer:
         if kscale is not None:
             _need(kscale, (S,), "kscale", torch.float32)
         if out is None:
-            out = torch.empty((T, S), dtype=torch.float32, device=q.device)
+            out = _new((T, S), torch.float32, q.device, stream)
         _need(out, (T, S), "out", torch.float32)
         st = self._lib.ds4idx_score_dense_debug(self._h, _ptr(q), _ptr(w), _ptr(kcache),
                                                 _ptr(kscale), T, S, int(pos_offset), _ptr(out),
