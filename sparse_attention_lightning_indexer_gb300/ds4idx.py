@@ -318,7 +318,8 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
     strides, the last dim adjacent). positions [T] int64. interleaved: one bool, or one for each
     tensor (False = halves). inverse: the transposed rotation, which is the gradient. outs: tensors
     of the same shapes to write, which may be the inputs themselves but not overlap otherwise; None
-    allocates dense ones.
+    allocates dense ones. Where gradients are recorded for an input, the results carry them (the inverse
+    rotation); outs cannot, and are refused then.
     """
     single = isinstance(xs, torch.Tensor)
     xs = [xs] if single else list(xs)
@@ -326,6 +327,11 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
     if not 1 <= n <= 4:
         raise ValueError("rotary takes 1 to 4 tensors")
     layouts = [interleaved] * n if isinstance(interleaved, bool) else list(interleaved)
+    if torch.is_grad_enabled() and any(x.requires_grad for x in xs):
+        if outs is not None:
+            raise ValueError("outs carry no gradient: leave them out, or call under torch.no_grad()")
+        ys = _rotary_recorded(xs, positions, freqs, layouts, inverse, stream)
+        return ys[0] if single else list(ys)
     if outs is None:
         outs = [_new(x.shape, x.dtype, x.device, stream) for x in xs]
     else:
@@ -376,13 +382,21 @@ class _RotaryFunction(torch.autograd.Function):
         return (None, None, None, None, *back)
 
 
+def _rotary_recorded(xs, positions, freqs, layouts, inverse, stream):
+    """The rotation in the autograd graph. The backward pass runs on the stream that is current here."""
+    if stream is None:
+        return _RotaryFunction.apply(positions, freqs, layouts, inverse, *xs)
+    current = torch.cuda.current_stream(positions.device)
+    with torch.cuda.stream(stream):
+        ys = _RotaryFunction.apply(positions, freqs, layouts, inverse, *xs)
+    for y in ys:
+        y.record_stream(current)
+    return ys
+
+
 def rotary_autograd(xs, positions, freqs: RotaryFreqs, interleaved=True):
     """``rotary`` for training: new tensors whose gradients are the inverse rotation."""
-    single = isinstance(xs, torch.Tensor)
-    xs = [xs] if single else list(xs)
-    layouts = [interleaved] * len(xs) if isinstance(interleaved, bool) else list(interleaved)
-    ys = _RotaryFunction.apply(positions, freqs, layouts, False, *xs)
-    return ys[0] if single else list(ys)
+    return rotary(xs, positions, freqs, interleaved)
 
 
 # ---- the 4-bit latent cache

@@ -14,7 +14,7 @@ BF16, F32, I64, I32, U8 = torch.bfloat16, torch.float32, torch.int64, torch.int3
 class Tensor:
     def __init__(self, shape, dtype, dev=0):
         self.shape, self.dtype, self.dev = torch.Size(shape), dtype, dev
-        self.is_cuda, self.device = dev >= 0, "meta"
+        self.is_cuda, self.device, self.requires_grad = dev >= 0, "meta", False
         self.nbytes = self.shape.numel() * dtype.itemsize
 
     def get_device(self):
