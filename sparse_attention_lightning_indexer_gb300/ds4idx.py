@@ -175,12 +175,14 @@ def plan_query(num_sms: int, B: int, T: int, S: int, pos_offsets, fixed_scratch:
     return dict(zip(PLAN_FIELDS, list(out)))
 
 
+_IN_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 def _in_dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"{name} must be float32 or bfloat16")
+    code = _IN_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return code
 
 
 def quantize_keys(k, kcache, kscale, dst_offset: int = 0, slots=None, stream=None):
@@ -280,7 +282,8 @@ def sparse_attention_status(stream=None):
 
 # ---- rotary positions
 
-_ROTARY_TENSOR = struct.Struct("=QQiiiiqqqq")   # RotaryTensor, without its field-by-field cost
+# RotaryTensor, 1 to 4 of them, without its field-by-field cost
+_ROTARY_TENSORS = [struct.Struct("=" + "QQiiiiqqqq" * n) for n in range(5)]
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
 
 
@@ -327,11 +330,12 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
     if not 1 <= n <= 4:
         raise ValueError("rotary takes 1 to 4 tensors")
     layouts = [interleaved] * n if isinstance(interleaved, bool) else list(interleaved)
-    if torch.is_grad_enabled() and any(x.requires_grad for x in xs):
-        if outs is not None:
-            raise ValueError("outs carry no gradient: leave them out, or call under torch.no_grad()")
-        ys = _rotary_recorded(xs, positions, freqs, layouts, inverse, stream)
-        return ys[0] if single else list(ys)
+    for x in xs:
+        if x.requires_grad and torch.is_grad_enabled():
+            if outs is not None:
+                raise ValueError("outs carry no gradient: leave them out, or call under torch.no_grad()")
+            ys = _rotary_recorded(xs, positions, freqs, layouts, inverse, stream)
+            return ys[0] if single else list(ys)
     if outs is None:
         outs = [_new(x.shape, x.dtype, x.device, stream) for x in xs]
     else:
@@ -342,14 +346,15 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
     dev = _device(positions, "positions")
     _need(positions, (T,), "positions", torch.int64, dev)
     rot = freqs.rot_dim
-    d = ctypes.create_string_buffer(n * _ROTARY_TENSOR.size)
+    fields = []
     for k, (x, o, il) in enumerate(zip(xs, outs, layouts)):
         shape, st, so = x.shape, x.stride(), o.stride()
         dims = len(shape)
         if dims not in (2, 3) or shape[0] != T or shape[-1] != rot:
             raise ValueError(f"tensor {k} has shape {tuple(shape)}, expected [{T}, H, {rot}] or "
                              f"[{T}, {rot}]")
-        if o.shape != shape or o.dtype != x.dtype:
+        dtype = x.dtype
+        if o.shape != shape or o.dtype != dtype:
             raise ValueError(f"out {k} must have the shape and dtype of tensor {k}")
         if x.get_device() != dev or o.get_device() != dev:
             raise ValueError(f"tensor {k} and its out must be on the device of positions, cuda:{dev}")
@@ -358,12 +363,13 @@ def rotary(xs, positions, freqs: RotaryFreqs, interleaved=True, inverse: bool = 
         heads, xh, oh = (shape[1], st[1], so[1]) if dims == 3 else (1, 0, 0)
         if heads < 1:
             raise ValueError(f"tensor {k} has no head")
-        _ROTARY_TENSOR.pack_into(d, k * _ROTARY_TENSOR.size, x.data_ptr(), o.data_ptr(),
-                                 _in_dtype(x, "a rotary tensor"), 1 if il else 0, heads, 0, st[0],
-                                 xh, so[0], oh)
-    _check(load().ds4idx_rotary(n, ctypes.addressof(d), T, rot, positions.data_ptr(), freqs.address,
-                                freqs.scale, 1 if inverse else 0, _stream_ptr(stream, dev)),
-           "ds4idx_rotary")
+        code = _IN_DTYPES.get(dtype)
+        if code is None:
+            raise TypeError(f"tensor {k} must be float32 or bfloat16")
+        fields += (x.data_ptr(), o.data_ptr(), code, 1 if il else 0, heads, 0, st[0], xh, so[0], oh)
+    _check(load().ds4idx_rotary(n, _ROTARY_TENSORS[n].pack(*fields), T, rot, positions.data_ptr(),
+                                freqs.address, freqs.scale, 1 if inverse else 0,
+                                _stream_ptr(stream, dev)), "ds4idx_rotary")
     return outs[0] if single else outs
 
 
