@@ -285,8 +285,9 @@ int ds4idx_sparse_attention_status(void* stream);
  *     scale * (a cos(x) - b sin(x), a sin(x) + b cos(x)),   x = positions[t] * inv_freq[pair],
  * where pair i is elements (2i, 2i + 1) (interleaved) or (i, i + rot_dim / 2) (halves). With
  * inverse != 0 the angle is negated (same scale): the transpose, which maps the gradient of the
- * output to the gradient of the input. The angle is off by at most |position| * (2^-65 turn + 2^-53
- * of the frequency) at any position; the rotation is fp32, rounded once to the tensor's type. */
+ * output to the gradient of the input. The product with the frequencies that ds4idx_rotary_freqs
+ * makes is exact modulo one turn at any position, so the angle is off by |position| times what the
+ * frequency is; the rotation is fp32, rounded once to the tensor's type. */
 
 typedef enum {
   DS4IDX_ROTARY_PLAIN = 0,  /* inv_freq[i] = base^(-2 i / rot_dim) */
@@ -316,7 +317,9 @@ typedef struct {
 
 /* Host computation, no device access: fills freqs[rot_dim / 2] with the frequencies as 64-bit
  * fractions of a turn per position (inv_freq / 2 pi * 2^64) and *scale. rot_dim even, 2..256;
- * base > 1; factor >= 1; original_max_position >= 1 and 0 < beta_slow <= beta_fast for YaRN. */
+ * base > 1; factor >= 1; original_max_position >= 1 and 0 < beta_slow <= beta_fast for YaRN. A
+ * frequency is off by at most (5 + ln base) * 2^-53 of it, (9 + ln base + min(factor, 256)) * 2^-53
+ * with YaRN (double arithmetic), and 2^-65 turn. */
 int ds4idx_rotary_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
                         int64_t original_max_position, double beta_fast, double beta_slow,
                         uint64_t* freqs, float* scale);

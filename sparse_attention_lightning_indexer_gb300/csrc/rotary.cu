@@ -7,9 +7,10 @@
 //
 // Angles. A frequency is kept as a 64-bit fraction of a turn, f = round(inv_freq / 2pi * 2^64), so
 // the angle modulo one turn is the low 64 bits of position * f: one integer product, exact in the
-// wrap, off by at most |position| * 2^-65 turns from the rounding of f (and position * 2^-53
-// relative from the double it came from). The two top bits give the quadrant; the rest, within
-// an eighth of a turn, is converted to fp32 (relative error 2^-24) for sincospi.
+// wrap. What is left is |position| times the error of f: 2^-65 turn from its rounding, and that of the
+// double formula, a few 2^-53 of it (5.9 measured; the header has the bound). The two top bits give
+// the quadrant; the rest, within an eighth of a turn, is converted to fp32 (relative error 2^-24) for
+// sincospi.
 //
 // Bound by HBM (each rotated element read and written once) for chunks and by latency for decode.
 // A CTA takes one token and a share of its 16-byte items: the first loads are in flight while 32
