@@ -326,7 +326,7 @@ int ds4idx_rotary_freqs(int32_t rot_dim, double base, int32_t scaling, double fa
 
 /* Rotates 1..4 tensors of the same T tokens in one launch. tensors and freqs are HOST arrays (read
  * before the call returns); positions DEVICE int64 [T] (any sign). Asynchronous on `stream`,
- * allocates nothing. Errors: INVALID_ARG, LAUNCH. T = 0 is a no-op. */
+ * allocates nothing. Errors: INVALID_ARG, LAUNCH, CUDA. T = 0 is a no-op. */
 int ds4idx_rotary(int32_t n_tensors, const ds4idx_rotary_tensor* tensors, int64_t T,
                   int32_t rot_dim, const int64_t* positions, const uint64_t* freqs, float scale,
                   int32_t inverse, void* stream);

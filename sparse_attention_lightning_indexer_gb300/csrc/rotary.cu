@@ -306,7 +306,9 @@ extern "C" int ds4idx_rotary(int32_t n_tensors, const ds4idx_rotary_tensor* tens
   // Few tokens: split a token's items over CTAs until about two CTAs an SM are busy, each with at
   // least a load a thread. Many tokens: as few CTAs a token as keep kBatch loads a thread.
   const int64_t most = std::max<int64_t>(1, (total + kThreads - 1) / kThreads);
-  const int64_t fill = std::min<int64_t>(most, std::max<int64_t>(1, 304 / T));
+  const int64_t sms = sm_count();
+  if (sms == 0) return DS4IDX_ERR_CUDA;
+  const int64_t fill = std::min<int64_t>(most, std::max<int64_t>(1, 2 * sms / T));
   const int64_t least = (total + kBatch * kThreads - 1) / (kBatch * kThreads);
   const int64_t shares = std::max<int64_t>(1, std::max(fill, least));
   if (shares * T > 0x7FFFFFFF) return DS4IDX_ERR_INVALID_ARG;

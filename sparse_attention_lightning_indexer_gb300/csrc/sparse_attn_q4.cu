@@ -52,7 +52,6 @@ constexpr int kK = 512;        // list slots
 constexpr int kChunks = 9;     // 64-dim chunks of a key: 8 latent, 1 rotary
 constexpr int kWorkers = 512, kMmaWarp = 16;  // warp 17 loads Q
 constexpr int kThreads = 18 * 32;
-constexpr int kSms = 152;
 constexpr int kQBytes = kH * 128;
 constexpr int kPBlock = kH * 128;            // 64 keys of P
 constexpr int kOffV = (kK / 64) * kPBlock;   // P first, then the V blocks
@@ -1046,7 +1045,8 @@ int launch(const CUtensorMap& tq, const CUtensorMap& to, const Params& p, int64_
   static std::atomic<uint64_t> done{0};
   if (!allow_shared(sparse_attn_q4_kernel<C>, Cfg<C>::Smem, done)) return DS4IDX_ERR_CUDA;
   // One CTA an SM fits. More tokens than SMs: the CTAs stay and take the tokens in turn.
-  const int64_t grid = C == 1 ? std::min<int64_t>(T, kSms) : T * C;
+  const int64_t grid = C == 1 ? std::min<int64_t>(T, sm_count()) : T * C;
+  if (grid == 0) return DS4IDX_ERR_CUDA;
   return launch_dependent(sparse_attn_q4_kernel<C>, static_cast<unsigned>(grid), kThreads,
                           Cfg<C>::Smem, C, stream, tq, to, p);
 }
