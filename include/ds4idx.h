@@ -345,8 +345,8 @@ int ds4idx_rotary(int32_t n_tensors, const ds4idx_rotary_tensor* tensors, int64_
  * Inputs must be finite. The cache pointer is 32-byte aligned. */
 
 /* Writes n rows x [n, 576] (in_dtype DS4IDX_F32 or DS4IDX_BF16, 16-byte aligned) into cache rows
- * slots[i] (DEVICE int64 [n]; rows outside the cache, e.g. -1, are skipped) or dst_offset + i
- * (slots NULL). Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH. n = 0 is a no-op. */
+ * slots[i] (DEVICE int64 [n], distinct: of two rows for one slot each byte may come from either; rows
+ * outside the cache, e.g. -1, are skipped) or dst_offset + i (slots NULL). Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH. n = 0 is a no-op. */
 int ds4idx_quantize_latents(const void* x, int32_t in_dtype, int64_t n, const int64_t* slots,
                             int64_t dst_offset, uint8_t* cache, int64_t cache_rows, void* stream);
 
@@ -386,9 +386,9 @@ typedef struct {
  * probabilities are rounded to bf16 for the value product. What a row of no entry holds (NaN
  * included) does not reach the results. Scores that are not finite follow the formulas: NaN among
  * them gives lse, out and the head's weights NaN; +infinity lse +infinity and out NaN; a list of
- * -infinity alone lse -infinity and out NaN, unlike an empty one. Few tokens (up to about half the SMs) run a cluster of CTAs
- * each. Asynchronous on `stream`, allocates nothing. Bounded device waits that run out are recorded
- * for ds4idx_sparse_attention_status.
+ * -infinity alone lse -infinity and out NaN, unlike an empty one. Few tokens (up to about half the
+ * SMs) run a cluster of CTAs each. Asynchronous on `stream`, allocates nothing. Bounded device waits
+ * that run out are recorded for ds4idx_sparse_attention_status.
  * Errors: INVALID_ARG, UNSUPPORTED (d_qk != 576, d_v != 512), LAUNCH, CUDA. T = 0 is a no-op. */
 int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, int64_t kv_rows,
                                const int32_t* idx, const ds4idx_placement* where, int64_t T,
@@ -400,8 +400,8 @@ int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, int64_t kv_r
  * 2^-32 (fixed point: integer adds commute, so the order of atomics does not change a result). */
 
 /* total[row of (t, idx[t,j])] += round(weights[t,j] * 2^32) for every non-empty entry; weights
- * [T, n_sel] fp32 below 2^30 in size (others add nothing). n_sel >= 1. Asynchronous, allocates
- * nothing. Errors: INVALID_ARG, LAUNCH. T = 0 is a no-op. */
+ * [T, n_sel] fp32 below 2^30 in size (others add nothing). n_sel >= 1, 1 <= pool_rows < 2^31.
+ * Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH. T = 0 is a no-op. */
 int ds4idx_evict_accumulate(int64_t* total, int64_t pool_rows, const float* weights,
                             const int32_t* idx, const ds4idx_placement* where, int64_t T,
                             int32_t n_sel, void* stream);

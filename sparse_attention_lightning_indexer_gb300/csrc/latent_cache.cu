@@ -1,5 +1,8 @@
-// The 4-bit latent cache's writer and reader (format: q4_format.cuh). Both are HBM streams: a row
-// is one warp, a lane one group of 16 dims (its absmax needs no other lane) and two rotary dims.
+// The 4-bit latent cache's writer and reader (format: q4_format.cuh): a row is one warp, a lane one
+// group of 16 dims (its absmax needs no other lane) and two rotary dims. 65536 rows: read back as bf16
+// in 16.4 us, an HBM stream (floor 15.4, part of the rows come from L2), as fp32 in 38 (floor 26.7);
+// written from bf16 in 24.6 us (floor 15.4), bound by the half-rate integer pipe (71% busy, DRAM 37%),
+// from fp32 in 34.8 (floor 26.7).
 //
 // Rounding. The scale is the code nearest to absmax / 7 and an integer the one nearest to
 // x / scale, ties to even, both decided exactly: the fp32 quotient only proposes, and where it

@@ -21,9 +21,10 @@
 // twice because O takes all 512 TMEM columns at C = 1, so P V starts only after the whole of S is
 // read, and 512 unpacked rows (576 KB) do not fit shared memory.
 //
-// 128 heads, 512 rows: 11.7 us for one token (C = 8; the latency of the phases), 677 us for 4096
-// tokens of a 65536-row cache, 863 TFLOP/s, 0.44 of the measured tensor peak: bound by the unpacking
-// on the half-rate integer pipe and by shared memory, of which the MMAs read 96 bytes a clock.
+// 128 heads, 512 rows: 11.4 us for one token (C = 8; the latency of the phases), 680 us for 4096
+// tokens of a 65536-row cache (780 with key weights), 859 TFLOP/s, 0.44 of the measured tensor peak:
+// bound by the unpacking on the half-rate integer pipe and by shared memory, of which the MMAs read
+// 96 bytes a clock.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
