@@ -301,7 +301,8 @@ class RotaryFreqs:
 def rotary_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                  original_max_position: int = 4096, beta_fast: float = 32.0,
                  beta_slow: float = 1.0) -> RotaryFreqs:
-    """Plain, linearly scaled or YaRN frequencies (see include/ds4idx.h)."""
+    """Plain, linearly scaled or YaRN frequencies (see include/ds4idx.h). The scale of the cosines and
+    sines is 1, with YaRN 0.1 ln(factor) + 1; ``scale`` of the result may be set to a model's own."""
     if scaling not in ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
     f = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))()
@@ -624,6 +625,8 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 def _device(t, name: str) -> int:
     """The device of a call: that of its first tensor. It has to be the current one, where the
     kernel is launched; ``_need`` holds the call's other tensors to it."""
+    if t is None:
+        raise ValueError(f"{name} is required")
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")

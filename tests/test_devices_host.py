@@ -103,6 +103,13 @@ def test_one_device_and_the_current_one(lib, name):
     assert len(lib.calls) == 1
 
 
+def test_missing_tensors_are_named(lib):
+    x = Tensor((4, 2, 64), BF16)
+    with pytest.raises(ValueError, match="positions"):
+        ds4idx.rotary([x], None, _freqs(), outs=[x])
+    assert not lib.calls
+
+
 def test_row_start_of_another_device(lib):
     t = [Tensor((4, 16, 576), BF16), Tensor((9, 416), U8), Tensor((4, 70), I32)]
     outs = dict(out=Tensor((4, 16, 512), BF16), lse=Tensor((4, 16), F32))
