@@ -396,6 +396,72 @@ int ds4idx_sparse_attention_q4(const void* q, const uint8_t* cache, int64_t kv_r
                                float sm_scale, void* out, float* lse, float* weights,
                                void* stream);
 
+/* ---- The 8-bit latent cache: a latent row in 640 bytes and an fp32 scale (kept apart, as the index
+ * cache's scales are), between the 1152 of bf16 and the 416 of 4 bits. One row: bytes 0..511 the E4M3
+ * (OCP E4M3FN) codes of the first 512 dims in order, bytes 512..639 the 64 rotary dims as bf16. The
+ * scale is the least power of two 2^e, e in -24..7, with absmax <= 448 * 2^e (2^7 where none is: larger
+ * values saturate); a code is the E4M3 number nearest to x / scale, ties to even. A dim is code * scale,
+ * exact in bf16. The bytes are a function of the inputs, which must be finite. The cache pointer is
+ * 32-byte aligned. */
+
+/* Writes n rows x [n, 576] (in_dtype DS4IDX_F32 or DS4IDX_BF16, 16-byte aligned) into cache rows
+ * slots[i] or dst_offset + i and their scales into scale [cache_rows]: as ds4idx_quantize_latents. */
+int ds4idx_quantize_latents_fp8(const void* x, int32_t in_dtype, int64_t n, const int64_t* slots,
+                                int64_t dst_offset, uint8_t* cache, float* scale, int64_t cache_rows,
+                                void* stream);
+
+/* Reads n rows back as values, as ds4idx_read_latents. */
+int ds4idx_read_latents_fp8(const uint8_t* cache, const float* scale, int64_t cache_rows,
+                            const int64_t* rows, int64_t start, int64_t n, void* out,
+                            int32_t out_dtype, void* stream);
+
+/* ---- A tree of drafted tokens: a decode step that verifies several drafted tokens at once. The latent
+ * rows of the N drafted tokens (nodes) of a sequence stand in the cache behind its kv_lens[b] rows, node
+ * j at position kv_lens[b] + j (whatever its depth; its rotary position is kv_lens[b] + depth). mask
+ * [B, N] says which nodes a node sees: bit j of mask[b, i] is set where node j is i itself or lies above
+ * it. A chain of tokens has the masks 1, 3, 7, ...; a mask of 0 is padding. */
+
+typedef enum {
+  DS4IDX_CACHE_BF16 = 0, /* rows of 576 bf16 */
+  DS4IDX_CACHE_FP8 = 1,  /* rows of 640 bytes and their scales, as ds4idx_quantize_latents_fp8 writes */
+  DS4IDX_CACHE_Q4 = 2    /* rows of 416 bytes, as ds4idx_quantize_latents writes */
+} ds4idx_cache_format;
+
+/* Attention of every node over all of its sequence's rows and the drafted rows that it sees:
+ *     s_j = sm_scale * q[b,i,h,:] . row_j,    out[b,i,h,:] = sum_j softmax(s)_j * row_j[0:512],
+ *     lse[b,i,h] = log sum_j exp(s_j) (natural),
+ * over positions j < kv_lens[b], and j = kv_lens[b] + k where bit k of mask[b,i] is set.
+ *  q        [B, n_nodes, n_heads, 576] bf16, 16-byte aligned; n_nodes 1..64, n_heads 1..128.
+ *  cache    [kv_rows, ...] in `format`, 32-byte aligned, 1 <= kv_rows < 2^31; scale [kv_rows] fp32 for
+ *           DS4IDX_CACHE_FP8 (powers of two, 2^-24 .. 2^7), else NULL.
+ *  kv_lens  DEVICE int32 [B] (>= 0; less counts as 0), mask DEVICE int64 [B, n_nodes].
+ *  where    HOST, may be NULL (row = position); its "tokens" are the B sequences. A position past a
+ *           sequence's table row or outside the pool is not there; a sequence whose kv_row0 is negative
+ *           has no rows.
+ *  max_kv_len  the largest of kv_lens, or a bound of it: the work is laid out for it. With a longer
+ *           sequence the results stay right and the call gets slower.
+ *  out      [B, n_nodes, n_heads, 512] bf16, 16-byte aligned; lse [B, n_nodes, n_heads] fp32 or NULL.
+ *           Of a node of mask 0, or that sees no row, out is 0 and lse -infinity.
+ *  workspace  DEVICE, 16-byte aligned, at least the bytes that ds4idx_tree_attention_workspace
+ *           gives for these sizes (may be 0, then NULL): partial sums of sequences
+ *           whose keys are split. Calls that can overlap need one each.
+ * Cache values are exact in bf16; products accumulate in fp32, softmax and sums are fp32, the
+ * probabilities are rounded to bf16 for the value product. What a row that is not seen holds (NaN
+ * included) does not reach the results. Scores that are not finite follow the formulas, as in
+ * ds4idx_sparse_attention_q4. Asynchronous on `stream`, allocates nothing. Bounded device waits that run
+ * out are recorded for ds4idx_sparse_attention_status.
+ * Errors: INVALID_ARG, UNSUPPORTED (d_qk != 576, d_v != 512), LAUNCH, CUDA. B = 0 is a no-op. */
+int ds4idx_tree_attention(const void* q, int32_t format, const void* cache, const float* scale,
+                          int64_t kv_rows, const int32_t* kv_lens, const int64_t* mask,
+                          const ds4idx_placement* where, int32_t B, int32_t n_nodes,
+                          int32_t n_heads, int32_t d_qk, int32_t d_v, int64_t max_kv_len,
+                          float sm_scale, void* out, float* lse, void* workspace,
+                          int64_t workspace_size, void* stream);
+
+/* *bytes: the workspace of a call of these sizes on the current device. Errors: INVALID_ARG. */
+int ds4idx_tree_attention_workspace(int32_t B, int32_t n_nodes, int32_t n_heads, int64_t max_kv_len,
+                                    int64_t* bytes);
+
 /* ---- Eviction by accumulated attention weight. Each pool row has a total, int64 in units of
  * 2^-32 (fixed point: integer adds commute, so the order of atomics does not change a result). */
 
@@ -436,6 +502,21 @@ typedef struct {
 int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t B, const int64_t* src_starts,
                          const int64_t* src_lens, const int64_t* dst_starts, const int64_t* counts,
                          int32_t n_arrays, const ds4idx_row_array* arrays, void* stream);
+
+/* Keeps the accepted path of each drafted tree: in every array, the row of position kv_lens[b] + j
+ * becomes the row of position kv_lens[b] + path[b][j], j < n_accepted[b], and new_lens[b] = kv_lens[b] +
+ * n_accepted[b] (counts outside 0..n_nodes are clamped). In place: all rows of a path are read before one
+ * is written, so that a path may name any nodes. An entry of path outside 0..n_nodes-1, or a position
+ * that is not there, leaves its row as it is.
+ *  kv_lens, n_accepted DEVICE int32 [B]; path DEVICE int32 [B, n_nodes], n_nodes 1..64; new_lens DEVICE
+ *  int32 [B]; where as in ds4idx_tree_attention; rows: the pool's, of every array (1 <= rows < 2^31).
+ *  arrays HOST, 0 <= n_arrays <= 8, src = dst and src_rows = dst_rows = rows in each.
+ * No written array may overlap another or anything that the call reads: refused. The rows of two
+ * sequences must differ. Asynchronous, allocates nothing. Errors: INVALID_ARG, LAUNCH. B = 0 is a
+ * no-op. */
+int ds4idx_tree_commit(const int32_t* kv_lens, const int32_t* path, const int32_t* n_accepted,
+                       int32_t* new_lens, const ds4idx_placement* where, int32_t B, int32_t n_nodes,
+                       int64_t rows, int32_t n_arrays, const ds4idx_row_array* arrays, void* stream);
 
 /* Test support for the bounded device waits (the pages have no counterpart). Every mbarrier
  * wait in the kernels gives up after a limit (2 s by default), records DS4IDX_ERR_DEVICE_TIMEOUT

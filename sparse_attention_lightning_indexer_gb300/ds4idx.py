@@ -42,7 +42,9 @@ EXPORTS = ("ds4idx_create", "ds4idx_score_topk", "ds4idx_score_topk_batched",
            "ds4idx_merge_topk", "ds4idx_sparse_attention", "ds4idx_sparse_attention_status",
            "ds4idx_rotary_freqs", "ds4idx_rotary", "ds4idx_quantize_latents",
            "ds4idx_read_latents", "ds4idx_sparse_attention_q4", "ds4idx_evict_accumulate",
-           "ds4idx_evict_select", "ds4idx_evict_compact")
+           "ds4idx_evict_select", "ds4idx_evict_compact", "ds4idx_quantize_latents_fp8",
+           "ds4idx_read_latents_fp8", "ds4idx_tree_attention", "ds4idx_tree_attention_workspace",
+           "ds4idx_tree_commit")
 
 _lock = threading.Lock()
 _lib = None
@@ -148,7 +150,14 @@ def load(path: str | None = None):
         lib.ds4idx_evict_accumulate.argtypes = [vp, i64, vp, vp, vp, i64, i32, vp]
         lib.ds4idx_evict_select.argtypes = [vp, i64, i32, vp, vp, vp, i64, i64, vp, i64, vp]
         lib.ds4idx_evict_compact.argtypes = [vp, i64, i32, vp, vp, vp, vp, i32, vp, vp]
-        for name in ("rotary_freqs", "rotary", "quantize_latents", "read_latents",
+        lib.ds4idx_quantize_latents_fp8.argtypes = [vp, i32, i64, vp, i64, vp, vp, i64, vp]
+        lib.ds4idx_read_latents_fp8.argtypes = [vp, vp, i64, vp, i64, i64, vp, i32, vp]
+        lib.ds4idx_tree_attention.argtypes = [vp, i32, vp, vp, i64, vp, vp, vp, i32, i32, i32, i32,
+                                              i32, i64, f32, vp, vp, vp, i64, vp]
+        lib.ds4idx_tree_attention_workspace.argtypes = [i32, i32, i32, i64, vp]
+        lib.ds4idx_tree_commit.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i32, vp, vp]
+        for name in ("quantize_latents_fp8", "read_latents_fp8", "tree_attention",
+                     "tree_attention_workspace", "tree_commit", "rotary_freqs", "rotary", "quantize_latents", "read_latents",
                      "sparse_attention_q4", "evict_accumulate", "evict_select", "evict_compact"):
             getattr(lib, "ds4idx_" + name).restype = ctypes.c_int
         if path is None:
@@ -511,6 +520,158 @@ def sparse_attention_q4(q, cache, idx, sm_scale: float, kv_row0=None, page_table
                                              _ptr(lse), _ptr(weights), _stream_ptr(stream, dev)),
            "ds4idx_sparse_attention_q4")
     return out, lse, weights
+
+
+# ---- the 8-bit latent cache
+
+F8_ROW_BYTES = 640
+
+
+def _cache_f8_rows(cache, scale, dev) -> int:
+    rows = cache.shape[0]
+    _need(cache, (rows, F8_ROW_BYTES), "cache", torch.uint8, dev)
+    _need(scale, (rows,), "scale", torch.float32, dev)
+    return rows
+
+
+def quantize_latents_fp8(x, cache, scale, dst_offset: int = 0, slots=None, stream=None):
+    """Writes latent rows x [n, 576] (fp32/bf16) as E4M3 codes and bf16 rotary dims into cache [R, 640]
+    uint8 and their scales, powers of two, into scale [R] fp32, at rows dst_offset.. or at slots [n]
+    (int64, -1 skips a row)."""
+    n = x.shape[0]
+    dev = _device(cache, "cache")
+    _need(x, (n, SA_DQK), "x", None, dev)
+    R = _cache_f8_rows(cache, scale, dev)
+    if slots is not None:
+        _need(slots, (n,), "slots", torch.int64, dev)
+    _check(load().ds4idx_quantize_latents_fp8(_ptr(x), _in_dtype(x, "x"), n, _ptr(slots),
+                                              int(dst_offset), _ptr(cache), _ptr(scale), R,
+                                              _stream_ptr(stream, dev)),
+           "ds4idx_quantize_latents_fp8")
+    return cache, scale
+
+
+def read_latents_fp8(cache, scale, rows=None, start: int = 0, n: int | None = None, out=None,
+                     dtype=torch.bfloat16, stream=None):
+    """The values of 8-bit cache rows ``rows`` [n] (int64; rows outside the cache give zeros) or of rows
+    start .. start + n - 1 (n None: to the end), as [n, 576] bf16 or fp32."""
+    dev = _device(cache, "cache")
+    R = _cache_f8_rows(cache, scale, dev)
+    if rows is not None:
+        n = rows.shape[0]
+        _need(rows, (n,), "rows", torch.int64, dev)
+    elif n is None:
+        n = R - int(start)
+    if out is None:
+        out = _new((n, SA_DQK), dtype, cache.device, stream)
+    _need(out, (n, SA_DQK), "out", None, dev)
+    _check(load().ds4idx_read_latents_fp8(_ptr(cache), _ptr(scale), R, _ptr(rows), int(start), n,
+                                          _ptr(out), _in_dtype(out, "out"), _stream_ptr(stream, dev)),
+           "ds4idx_read_latents_fp8")
+    return out
+
+
+# ---- trees of drafted tokens
+
+CACHE_BF16, CACHE_FP8, CACHE_Q4 = 0, 1, 2
+TREE_NODES = 64
+
+
+def _cache_format(cache, scale, dev):
+    """(ds4idx_cache_format, rows) of a latent cache."""
+    rows = cache.shape[0]
+    if cache.dtype == torch.bfloat16:
+        _need(cache, (rows, SA_DQK), "cache", torch.bfloat16, dev)
+        fmt = CACHE_BF16
+    elif cache.shape[-1] == F8_ROW_BYTES:
+        return CACHE_FP8, _cache_f8_rows(cache, scale, dev)
+    else:
+        fmt = CACHE_Q4
+        _cache_rows(cache, dev)
+    if scale is not None:
+        raise ValueError("scale belongs to an 8-bit cache")
+    return fmt, rows
+
+
+def tree_attention(q, cache, kv_lens, mask, sm_scale: float, scale=None, kv_row0=None,
+                   page_table=None, page_size: int = 0, token_seq=None,
+                   max_kv_len: int | None = None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of the nodes of B drafted trees, q [B, N, H, 576] (bf16, N <= 64, H <= 128), over all
+    rows of their sequences and the drafted rows that each node sees (see include/ds4idx.h).
+
+    cache: bf16 [R, 576], or uint8 [R, 640] with its ``scale`` [R], or the 4-bit uint8 [R, 416]. The
+    drafted rows stand behind the kv_lens [B] (int32) rows of their sequence; bit j of mask [B, N]
+    (int64) says that a node sees drafted row j (itself among them; 0: padding). Position s of sequence
+    b is row kv_row0[b] + s, or is found through page_table as in ``sparse_attention_q4`` (token_seq:
+    the table row of each sequence). max_kv_len: a bound of kv_lens that the work is laid out for (None:
+    what the pool or a table row holds). Returns (out [B, N, H, 512] bf16, lse [B, N, H] fp32)."""
+    B, N, H = q.shape[0], q.shape[1], q.shape[2]
+    dev = _device(q, "q")
+    _need(q, (B, N, H, SA_DQK), "q", torch.bfloat16, dev)
+    fmt, R = _cache_format(cache, scale, dev)
+    _need(kv_lens, (B,), "kv_lens", torch.int32, dev)
+    _need(mask, (B, N), "mask", torch.int64, dev)
+    where = _placement(B, kv_row0, page_table, page_size, token_seq, dev)
+    if max_kv_len is None:
+        max_kv_len = R if page_table is None else min(R, page_table.shape[1] * int(page_size))
+    need = tree_attention_workspace(B, N, H, max_kv_len)
+    if out is None:
+        out = _new((B, N, H, SA_DV), torch.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _new((B, N, H), torch.float32, q.device, stream)
+    if workspace is None and need:
+        workspace = _new((need,), torch.uint8, q.device, stream)
+    _need(out, (B, N, H, SA_DV), "out", torch.bfloat16, dev)
+    _need(lse, (B, N, H), "lse", torch.float32, dev)
+    have = 0
+    if workspace is not None:
+        have = workspace.shape[0]
+        _need(workspace, (have,), "workspace", torch.uint8, dev)
+    _check(load().ds4idx_tree_attention(_ptr(q), fmt, _ptr(cache), _ptr(scale), R, _ptr(kv_lens),
+                                        _ptr(mask), _ref(where), B, N, H, SA_DQK, SA_DV,
+                                        int(max_kv_len), float(sm_scale), _ptr(out), _ptr(lse),
+                                        _ptr(workspace), have, _stream_ptr(stream, dev)),
+           "ds4idx_tree_attention")
+    return out, lse
+
+
+def tree_attention_workspace(B: int, N: int, H: int, max_kv_len: int) -> int:
+    """Bytes of a ``workspace`` that tree_attention calls of these sizes may share (on one stream)."""
+    n = ctypes.c_int64()
+    _check(load().ds4idx_tree_attention_workspace(B, N, H, int(max_kv_len), ctypes.addressof(n)),
+           "ds4idx_tree_attention_workspace")
+    return n.value
+
+
+def tree_commit(arrays, kv_lens, path, n_accepted, kv_row0=None, page_table=None, page_size: int = 0,
+                token_seq=None, new_lens=None, stream=None):
+    """Keeps the accepted path of each drafted tree, in place in up to 8 per-row arrays of one pool: the
+    row of position kv_lens[b] + j becomes that of kv_lens[b] + path[b, j], j < n_accepted[b]. kv_lens,
+    n_accepted [B] and path [B, N] int32 on the device; the placement as in ``tree_attention``. Returns
+    the new lengths, kv_lens + n_accepted."""
+    B, N = path.shape[0], path.shape[1]
+    arrays = list(arrays)
+    dev = _device(path, "path")
+    _need(path, (B, N), "path", torch.int32, dev)
+    _need(kv_lens, (B,), "kv_lens", torch.int32, dev)
+    _need(n_accepted, (B,), "n_accepted", torch.int32, dev)
+    where = _placement(B, kv_row0, page_table, page_size, token_seq, dev)
+    n = len(arrays)
+    if n > 8:
+        raise ValueError("at most 8 arrays")
+    rows = arrays[0].shape[0] if n else 1
+    d = ctypes.create_string_buffer(max(1, n) * _ROW_ARRAY.size)
+    for k, a in enumerate(arrays):
+        _need(a, (rows, *a.shape[1:]), f"arrays[{k}]", None, dev)
+        row = a.element_size() * math.prod(a.shape[1:])
+        _ROW_ARRAY.pack_into(d, k * _ROW_ARRAY.size, a.data_ptr(), a.data_ptr(), rows, rows, row, 0)
+    if new_lens is None:
+        new_lens = _new((B,), torch.int32, path.device, stream)
+    _need(new_lens, (B,), "new_lens", torch.int32, dev)
+    _check(load().ds4idx_tree_commit(_ptr(kv_lens), _ptr(path), _ptr(n_accepted), _ptr(new_lens),
+                                     _ref(where), B, N, rows, n, ctypes.addressof(d),
+                                     _stream_ptr(stream, dev)), "ds4idx_tree_commit")
+    return new_lens
 
 
 # ---- eviction by accumulated attention weight
