@@ -34,6 +34,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "attn_ptx.cuh"
 #include "launch.cuh"
 #include "placement.cuh"
 #include "ptx.cuh"
@@ -123,14 +124,6 @@ struct Params {
   float scale_log2;
 };
 
-// One 32-byte sector. Without allocation in L1: every row is another line, and the few lines that
-// the shared memory leaves to L1 would bound the loads in flight (chunk of 4096: 988 -> 838 us).
-__device__ __forceinline__ void ld32(const void* p, uint32_t (&r)[8]) {
-  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                 "=r"(r[7])
-               : "l"(p));
-}
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar,
                                             int32_t x, int32_t y) {
   asm volatile(
@@ -162,48 +155,9 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout: blocks of 64 N
-// `stride` bytes apart, atoms of 8 keys (1 KB) along K.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t stride) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(stride >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// One lane of a converged warp, the same at every call.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
-
 // ---- other CTAs of the cluster
-__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
 __device__ __forceinline__ void st_peer(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void arrive_peer(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_t bytes,
                                              uint32_t bar) {
@@ -212,41 +166,6 @@ __device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_
           dst),
       "r"(src), "r"(bytes), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// mbar_wait with acquire at cluster scope, for data other CTAs stored here.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity,
-                                             volatile uint32_t* abort_flag, uint32_t* err) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63u) == 0u) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *abort_flag = 1u;
-        atomicOr(err, 1u);
-        return false;
-      }
-    }
-  }
-}
-
-// 16 bytes to a shared-memory address.
-__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
 }
 // One 64-dim chunk of a latent row to the 128 swizzled bytes of row `r` at `base`. Where several
 // lanes share a row (each its own chunk, chunks a multiple of 1 KB apart), lane x of them writes
