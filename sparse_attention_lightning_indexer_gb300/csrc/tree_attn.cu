@@ -2,23 +2,23 @@
 // attends over all of the sequence's rows and over the drafted rows on its own path. One latent row per
 // position, shared by all heads; 576-wide keys, the first 512 dims are values.
 //
-// The (node, head) rows of a sequence are taken 128 at a time (the lanes of TMEM). A pair of CTAs owns
-// such a tile and a range of keys, and each CTA half of the dims: O of 128 rows x 512 dims would fill an
-// SM's whole TMEM and leave no place for S. With rank r holding latent dims 256 r .. and rotary dims
-// 32 r .. of every key:
-//   S  each CTA forms S_r[128 x 64 keys] over its 288 dims, sends it to the other and adds what comes:
-//      S = S_0 + S_1 is the same number in both, so both hold the same softmax, and nothing else is
-//      exchanged. A row of a key is read, unpacked and kept once in the pair, as key and as value.
-//   P  p = exp2(s - m) in bf16, m a maximum that is left alone until a score passes it by 2^8;
-//   O  O[128 x 256 own dims] += P V, in TMEM over the whole range. A raised m rescales O first.
+// The (node, head) rows of a sequence are taken 128 at a time (the lanes of TMEM). O of 128 rows x 512
+// dims fills an SM's TMEM, so a pair of CTAs owns such a tile and a range of keys: one (rank 0) the
+// keys' products and the softmax, the other the values' products:
+//   S[128 x 64 keys] = Q K^T        rank 0; Q stays in TMEM as the A operand, three tiles of S beside it
+//   p = exp2(s - m) in bf16         rank 0; m is left alone until a score passes it by 2^8
+//   O[128 x 512] += P V             rank 1; O fills its TMEM over the whole range
+// P, and the factors of O where m was raised, are all that goes from one CTA to the other (16 KB a tile;
+// shared memory of the pair moves 18.7 bytes a clock in each direction when all SMs do it). A tile
+// takes both CTAs about as long: 36 x 32 and 8 x 128 clocks of products. Splitting the dims instead
+// reads and unpacks a row once in the pair, but exchanges S, 32 KB a tile both ways: slower.
 // Ranges of a split sequence leave (O, m, l) in fp32, and a second kernel joins them.
 //
-// TMEM: O 256 columns, Q (latent dims, the A operand) 128, S 2 x 64. Shared memory: three stages of 64
-// keys in bf16 (36 KB), P and the other CTA's S twice each.
+// Both CTAs read the rows themselves and turn them into bf16 (exact) in a ring of parts, 64 keys x 256
+// dims in the 128-byte-swizzled layout that serves as K-major and as MN-major operand.
 //
-// Warps 0..7: softmax, warps 0..3 on even tiles and 4..7 on odd ones, so that the exchange of one tile
-// runs behind the arithmetic of another; m is handed from tile to tile. Warps 8..15: read rows, turn
-// them into bf16 (exact) and write the 128-byte-swizzled operand. Warp 16 issues tcgen05.mma.
+// Warps 0..7: softmax, warps 0..3 on even tiles and 4..7 on odd ones, m handed from tile to tile (rank
+// 1: the rescaling of O and the output). Warps 8..15: rows to bf16. Warp 16 issues tcgen05.mma.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -43,25 +43,28 @@ using namespace ds4;
 constexpr int kDims = 576, kLatent = 512, kNodes = 64, kMaxHeads = 128;
 constexpr int kRows = 128;             // (node, head) rows of a tile = TMEM lanes
 constexpr int kKeys = 64;              // keys of a step
-constexpr int kHalf = 256;             // latent dims of a CTA
+constexpr int kHalf = 256;             // latent dims of a part
 constexpr int kLoad0 = 8, kMmaWarp = 16;
-constexpr int kThreads = 17 * 32;
-constexpr int kChunk = kKeys * 128;    // 64 dims of a step's keys
-constexpr int kOffRope = 4 * kChunk;   // in a stage: the 32 rotary dims, 64-byte swizzle
-constexpr int kStage = kOffRope + kKeys * 64, kStages = 3;
-constexpr int kOffQRope = kStages * kStage;
-constexpr int kOffP = kOffQRope + kRows * 64, kP = kRows * kKeys * 2;
-constexpr int kOffX = kOffP + 2 * kP, kX = kRows * kKeys * 4;
-constexpr int kOffM = kOffX + 2 * kX;              // float [2][128]: m after an even, an odd tile
+constexpr int kThreads = 20 * 32;
+// Registers a thread: at launch, and as the warpgroups then share them (two of softmax, two of loading,
+// the MMA warp's): 256 * 136 + 256 * 80 + 128 * 40 of 640 * 96.
+constexpr int kRegLaunch = 96, kRegSoftmax = 136, kRegLoad = 80, kRegMma = 40;
+static_assert(256 * (kRegSoftmax + kRegLoad) + 128 * kRegMma <= kThreads * kRegLaunch, "registers");
+constexpr int kChunk = kKeys * 128;    // 64 dims of a tile's keys
+constexpr int kPart = 4 * kChunk, kParts = 5;
+constexpr int kOffRope = kParts * kPart;           // the rotary dims of three tiles' keys (rank 0)
+constexpr int kOffP = kOffRope + 3 * kChunk, kP = kRows * kKeys * 2;  // P of two tiles
+constexpr int kOffF = kOffP + 2 * kP;              // float [2][128]: factors of O before P V
+constexpr int kOffM = kOffF + 2 * kRows * 4;       // float [2][128]: m after an even, an odd tile
 constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l and its m of both groups
-constexpr int kOffKeyBits = kOffL + 4 * kRows * 4; // uint32 [kStages][2] keys that are there
-constexpr int kOffOddBits = kOffKeyBits + kStages * 8;  // [kStages][4][2] keys not finite, by chunk
-constexpr int kOffBars = kOffOddBits + kStages * 32;
-constexpr int kNumBars = 2 * kStages + 1 + 4 * 2 + 1 + 2 * 8 + 8;
+constexpr int kOffThere = kOffL + 4 * kRows * 4;   // uint32 [8 tiles][2]: keys that are there
+constexpr int kOffOdd = kOffThere + 8 * 8;         // uint32 [8 tiles][8 chunks][2]: keys not finite
+constexpr int kOffBars = kOffOdd + 8 * 64;
+constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 8 + 2;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
-constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
+constexpr uint32_t kColRope = 256, kColS = 320;    // rank 0: Q from column 0, S; rank 1: O from 0
 constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
 constexpr float kSlack = 8.f;          // log2 of what a probability may exceed 1 by
 
@@ -73,7 +76,7 @@ struct Params {
   const int64_t* mask;
   uint16_t* out;
   float* lse;
-  float* part_o;   // [item][2 ranks][64 column quads][128 rows][4]
+  float* part_o;   // [item][128 column quads][128 rows][4]
   float* part_ml;  // [item][2][128]
   uint32_t* err;
   Placement place;
@@ -83,9 +86,8 @@ struct Params {
 
 // The range of keys of a work item: steps lo .. lo + n - 1 of 64 positions.
 struct Range {
-  int64_t len, end;  // rows of the sequence; positions from `end` on are not there
-  int64_t lo;
-  int32_t n;
+  int32_t len, end;  // rows of the sequence; positions from `end` on are not there
+  int32_t lo, n;
   uint64_t seen;     // drafted rows that some node of the tile sees
 };
 
@@ -107,48 +109,38 @@ __device__ __forceinline__ Range make_range(const Params& p, int b, int tile, in
   const TokenPlace tp = place_token(p.place, b);
   int64_t room = static_cast<int64_t>(p.place.pages) * p.place.page;
   if (!tp.table) room = tp.row0 < 0 ? 0 : p.place.rows - tp.row0;
-  g.end = any ? max(min(g.len + (64 - __clzll(static_cast<long long>(g.seen))), room),
-                    static_cast<int64_t>(0))
+  const int32_t end = g.len + (64 - __clzll(static_cast<long long>(g.seen)));
+  g.end = any ? static_cast<int32_t>(max(min(static_cast<int64_t>(end), room), static_cast<int64_t>(0)))
               : 0;
-  const int64_t total = (g.end + kKeys - 1) / kKeys;
-  const int64_t per = max(static_cast<int64_t>(p.steps), (total + p.splits - 1) / p.splits);
-  g.lo = min(total, split * per);
-  g.n = static_cast<int32_t>(min(total, g.lo + per) - g.lo);
+  const int32_t total = g.end / kKeys + (g.end % kKeys ? 1 : 0);
+  const int32_t per = max(p.steps, (total - 1) / p.splits + 1);
+  g.lo = static_cast<int32_t>(min(static_cast<int64_t>(total), static_cast<int64_t>(split) * per));
+  g.n = min(total - g.lo, per);
   return g;
 }
 
-// 16 bytes to another CTA's shared memory.
-__device__ __forceinline__ void st_peer16(uint32_t at, const uint32_t* v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3])
-               : "memory");
+__device__ __forceinline__ void st_peer(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-__device__ __forceinline__ float4 ld_shared16(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
+__device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_t bytes,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void st_global32(void* at, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-// Descriptor of a K-major operand of 64-byte rows in the 64-byte swizzle layout: atoms of 8 rows.
-__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(1u) << 16;
-  d |= static_cast<uint64_t>(512u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(4u) << 61;
-  return d;
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
 }
 
-// ---- reading rows: what one thread takes of a key, 64 dims (chunk c of this CTA's half) and 8 rotary
-// ones, raw; unpacked as 8 x 16 bytes of bf16.
+// ---- reading rows: what one thread takes of a key, chunk c of 64 dims and, in rank 0, 8 rotary ones,
+// raw; unpacked as 8 x 16 bytes of bf16.
 template <int kFormat>
 struct RowPart {
   static constexpr int kWords = kFormat == DS4IDX_CACHE_BF16 ? 32 : kFormat == DS4IDX_CACHE_FP8 ? 16 : 8;
@@ -156,7 +148,7 @@ struct RowPart {
   uint32_t scale;
   uint4 rope;
 
-  __device__ __forceinline__ void load(const Params& p, int64_t r, int rank, int c) {
+  __device__ __forceinline__ void load(const Params& p, int64_t r, int c, bool rotary) {
 #pragma unroll
     for (int j = 0; j < kWords; ++j) w[j] = kFormat == DS4IDX_CACHE_Q4 ? ds4q::kEmptyWord : 0u;
     scale = 0u;
@@ -166,22 +158,22 @@ struct RowPart {
     int at, rot;
     if constexpr (kFormat == DS4IDX_CACHE_BF16) {
       row = p.cache + r * (2 * kDims);
-      at = rank * 2 * kHalf + c * 128;
+      at = c * 128;
       rot = 2 * kLatent;
     } else if constexpr (kFormat == DS4IDX_CACHE_FP8) {
       row = p.cache + r * ds4f8::kRowBytes;
-      at = rank * kHalf + c * 64;
+      at = c * 64;
       rot = ds4f8::kOffRope;
       scale = __float_as_uint(p.scale[r]);
     } else {
       row = p.cache + r * ds4q::kRowBytes;
-      at = rank * (kHalf / 2) + c * 32;
+      at = c * 32;
       rot = ds4q::kOffRope;
-      scale = *reinterpret_cast<const uint32_t*>(row + ds4q::kOffScale + 4 * (4 * rank + c));
+      scale = *reinterpret_cast<const uint32_t*>(row + ds4q::kOffScale + 4 * c);
     }
 #pragma unroll
     for (int j = 0; j < kWords; j += 8) ld32(row + at + 4 * j, reinterpret_cast<uint32_t(&)[8]>(w[j]));
-    rope = *reinterpret_cast<const uint4*>(row + rot + rank * 64 + c * 16);
+    if (rotary) rope = *reinterpret_cast<const uint4*>(row + rot + c * 16);
   }
   // Whether a value is not finite (the 4-bit format has none).
   __device__ __forceinline__ bool odd() const {
@@ -210,9 +202,9 @@ struct RowPart {
     lo = ds4q::mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), s2);
     hi = ds4q::mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), s2);
   }
-  // To row `key` of a stage.
-  __device__ __forceinline__ void store(uint32_t stage, int key, int c) const {
-    const uint32_t at = stage + c * kChunk + key * 128 + (key & 7) * 16;
+  // To row `key` of a chunk in shared memory.
+  __device__ __forceinline__ void store(uint32_t chunk, int key) const {
+    const uint32_t at = chunk + key * 128 + (key & 7) * 16;
     uint32_t s2 = 0;
     if constexpr (kFormat == DS4IDX_CACHE_FP8) s2 = ((scale >> 23) + 120u) * 0x00800080u;
 #pragma unroll
@@ -230,7 +222,6 @@ struct RowPart {
       }
       st_shared16(at ^ (16 * u), v);
     }
-    st_shared16(stage + kOffRope + key * 64 + ((c ^ (key >> 1)) & 3) * 16, rope);
   }
 };
 
@@ -241,46 +232,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t smem0 = smem_u32(smem);
+  float* s_f = reinterpret_cast<float*>(smem + kOffF);
   float* s_m = reinterpret_cast<float*>(smem + kOffM);
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
-  volatile uint32_t* s_there = reinterpret_cast<uint32_t*>(smem + kOffKeyBits);
-  volatile uint32_t* s_odd = reinterpret_cast<uint32_t*>(smem + kOffOddBits);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kOffBars);
-  uint64_t* k_empty = k_full + kStages;
-  uint64_t* q_full = k_empty + kStages;
-  uint64_t* s_ready = q_full + 1;   // [2] S_r of a tile is formed
-  uint64_t* s_free = s_ready + 2;   // [2] and read
-  uint64_t* p_full = s_free + 2;    // [2]
-  uint64_t* pv_done = p_full + 2;   // [2] P V of a tile is done
-  uint64_t* done = pv_done + 2;     // every MMA has completed
-  uint64_t* x_full = done + 1;      // [8] by softmax warp: the other CTA's S of its rows has come
-  uint64_t* x_empty = x_full + 8;   // [8] the other CTA has read what was sent
-  uint64_t* m_full = x_empty + 8;   // [8] the warp's m is in s_m
+  volatile uint32_t* s_there = reinterpret_cast<uint32_t*>(smem + kOffThere);
+  volatile uint32_t* s_odd = reinterpret_cast<uint32_t*>(smem + kOffOdd);
+  uint64_t* part_full = reinterpret_cast<uint64_t*>(smem + kOffBars);
+  uint64_t* part_empty = part_full + kParts;
+  uint64_t* q_full = part_empty + kParts;
+  uint64_t* s_ready = q_full + 1;   // [3] S of a tile is formed
+  uint64_t* s_free = s_ready + 3;   // [3] and read
+  uint64_t* p_free = s_free + 3;    // [2] rank 1 is done with P (in rank 0)
+  uint64_t* p_full = p_free + 2;    // [2] P has come (in rank 1)
+  uint64_t* scaled = p_full + 2;    // [2] O is ready for P V
+  uint64_t* pv_done = scaled + 2;   // [2] P V of a tile is done
+  uint64_t* m_full = pv_done + 2;   // [8] a softmax warp's m is in s_m
+  uint64_t* l_full = m_full + 8;    // the rows' sums have come (in rank 1)
+  uint64_t* done = l_full + 1;      // every MMA has completed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x & 1, item = blockIdx.x >> 1;
   const int split = item % p.splits, tile = item / p.splits % p.tiles, b = item / (p.splits * p.tiles);
   uint32_t* err = p.err;
+  constexpr uint32_t kPBytes = kP + kRows * 4;  // what comes with a tile: P and the factors
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&k_full[i], 8);
-      mbar_init(&k_empty[i], 1);
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&part_full[i], 8);
+      mbar_init(&part_empty[i], 1);
     }
     mbar_init(q_full, 8);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&s_ready[i], 1);
       mbar_init(&s_free[i], 4);
-      mbar_init(&p_full[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&p_free[i], 8);
+      mbar_init(&p_full[i], 1);
+      mbar_init(&scaled[i], 8);
       mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&m_full[i], 1);
+    mbar_init(l_full, 4);
     mbar_init(done, 1);
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&x_full[i], 1);
-      mbar_init(&x_empty[i], 1);
-      mbar_init(&m_full[i], 1);
-    }
     *s_abort = 0u;
     fence_mbar_init();
   }
@@ -296,244 +291,251 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   cluster_sync();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  // Between the softmax warps' giving their registers back and the others' taking them: a warp of the
+  // MMA warpgroup that has nothing to do would else take its back first, and the softmax warps wait for
+  // registers that come free only when they are done.
+  auto registers_back = [] { asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory"); };
 
   if (warp < kLoad0) {
-    // ---------------- softmax: this thread's row, the tiles of its group's parity
+    setmaxnreg_inc<kRegSoftmax>();
     const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int row = tile * kRows + r, node = row / p.H;
     const bool used = node < p.N;
     const int64_t out_row = static_cast<int64_t>(b) * p.N * p.H + row;
-    uint64_t mask = used ? static_cast<uint64_t>(p.mask[static_cast<int64_t>(b) * p.N + node]) : 0ull;
-    const bool padding = mask == 0ull;
-    mask &= ~0ull >> (64 - p.N);
     bool ok = true;
-    if (g.n > 0) {
-      // Q: latent dims to TMEM (64 columns by each group), rotary dims to shared memory
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * kDims + rank * kHalf + grp * 128);
+    if (rank == 0) {
+      // ---------------- softmax: this thread's row, the tiles of its group's parity
+      uint64_t mask = used ? static_cast<uint64_t>(p.mask[static_cast<int64_t>(b) * p.N + node]) : 0ull;
+      const bool padding = mask == 0ull;
+      mask &= ~0ull >> (64 - p.N);
+      if (g.n > 0) {
+        // Q to TMEM: a half of the latent dims and of the rotary ones by each group
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * kDims);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t v[32];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 x = used ? src[8 * h + j] : make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < 8; ++j) {
+            const uint4 x = used ? src[grp * 32 + 8 * h + j] : zero;
+            v[4 * j] = x.x;
+            v[4 * j + 1] = x.y;
+            v[4 * j + 2] = x.z;
+            v[4 * j + 3] = x.w;
+          }
+          tmem_st32(lanes + grp * 128 + h * 32, v);
+        }
+        uint32_t v[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = used ? src[64 + grp * 4 + j] : zero;
           v[4 * j] = x.x;
           v[4 * j + 1] = x.y;
           v[4 * j + 2] = x.z;
           v[4 * j + 3] = x.w;
         }
-        tmem_st32(tmem + lanes + kColQ + grp * 64 + h * 32, v);
+        tmem_st16(lanes + kColRope + grp * 16, v);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
       }
-      const uint4* rot = reinterpret_cast<const uint4*>(p.q + out_row * kDims + kLatent + rank * 32);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int u = grp * 2 + j;
-        st_shared16(smem0 + kOffQRope + r * 64 + ((u ^ (r >> 1)) & 3) * 16,
-                    used ? rot[u] : make_uint4(0, 0, 0, 0));
-      }
-      tmem_wait_st();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    }
-    float m = kNegInf, l = 0.f;
-    const uint32_t x_own = smem0 + kOffX + grp * kX + r * 16;
-    const uint32_t x_peer = peer(x_own, rank ^ 1);
-    const uint32_t s_col = tmem + lanes + kColS + grp * kKeys;
+      float m = kNegInf, l = 0.f;
+      const uint32_t rows_at = quad * 32 * 128;  // this warp's rows of P
 #pragma unroll 1
-    for (int i = grp; i < g.n; i += 2) {
-      const uint32_t use = i >> 1;
-      const int st = i % kStages;
-      // this CTA's part of S to the other one
-      ok = ok && mbar_wait_warp(&s_ready[grp], use & 1, s_abort, err) &&
-           mbar_wait_warp(&k_full[st], (i / kStages) & 1, s_abort, err) &&
-           __all_sync(0xffffffffu, wait_cluster(&x_empty[warp], (use & 1) ^ 1u, s_abort, err));
-      if (!ok) break;
-      tc_fence_after();
-      const int64_t pos = (g.lo + i) * kKeys;
-      uint64_t there = static_cast<uint64_t>(s_there[2 * st + 1]) << 32 | s_there[2 * st];
-      uint64_t bad = 0ull;  // keys whose score is NaN because of values here
-      if (pos + kKeys > g.len) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          bad |= static_cast<uint64_t>(s_odd[8 * st + 2 * c + 1]) << 32 | s_odd[8 * st + 2 * c];
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        tmem_ld32(s_col + 32 * h, v);
-        tmem_wait_ld();
-        if (bad) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (bad >> (32 * h + j) & 1) v[j] = 0x7FC00000u;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) st_peer16(x_peer + (8 * h + j) * (kRows * 16), &v[4 * j]);
-      }
-      __syncwarp();
-      if (lane == 0) arrive_peer(peer(smem_u32(&x_full[warp]), rank ^ 1));
-      // the sum of both
-      ok = __all_sync(0xffffffffu, wait_cluster(&x_full[warp], use & 1, s_abort, err));
-      if (!ok) break;
-      float s[kKeys];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        tmem_ld32(s_col + 32 * h, v);
-        float4 x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = ld_shared16(x_own + (8 * h + j) * (kRows * 16));
-        tmem_wait_ld();
-        // (the smaller rank's part first: the same sum, bit for bit, in both CTAs; a sum of two does
-        // not depend on the order)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[32 * h + j] = __uint_as_float(v[j]) + (&x[j >> 2].x)[j & 3];
-      }
-      if (bad) {
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j)
-          if (bad >> j & 1) s[j] = __uint_as_float(0x7FC00000u);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s_free[grp]);
-        arrive_peer(peer(smem_u32(&x_empty[warp]), rank ^ 1));
-      }
-      // which keys this row sees
-      uint64_t see = padding ? 0ull : ~0ull;
-      if (pos + kKeys > g.len && !padding) {
-        const int64_t d = g.len - pos;  // < 64
-        see = d >= 0 ? (1ull << d) - 1ull | mask << d : d > -64 ? mask >> -d : 0ull;
-      }
-      see &= there;
-      const bool all = __all_sync(0xffffffffu, see == ~0ull);
-      float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-      if (all) {
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-          if (see >> j & 1) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
-        }
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-      // m of the tile before; raised where a score passes it by more than the slack. Finite once a key
-      // was seen: a score of +-infinity keeps its meaning in s - m.
-      float before = kNegInf;
-      if (i > 0) {
-        ok = mbar_wait_warp(&m_full[warp ^ 4], ((i - 1) >> 1) & 1, s_abort, err);
-        if (!ok) break;
-        before = s_m[(grp ^ 1) * kRows + r];
-      }
-      float now = before;
-      if (see != 0ull && (before == kNegInf || top > before + kSlack))
-        now = fminf(fmaxf(top, -kMax), kMax);
-      s_m[grp * kRows + r] = now;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&m_full[warp]);
-      const bool raise = now != before && before != kNegInf;
-      if (__any_sync(0xffffffffu, raise)) {
-        // O of the tiles before, all columns of these rows
-        ok = mbar_wait_warp(&pv_done[grp ^ 1], ((i - 1) >> 1) & 1, s_abort, err);
+      for (int i = grp; i < g.n; i += 2) {
+        const uint32_t use = i >> 1;
+        const int slot = i % 3;
+        ok = mbar_wait_warp(&s_ready[slot], (i / 3) & 1, s_abort, err);
         if (!ok) break;
         tc_fence_after();
-        const float f = raise ? exp2_approx(before - now) : 1.f;
-#pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(tmem + lanes + kColO + c, v);
-          tmem_wait_ld();
+        float s[kKeys];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-          tmem_st32(tmem + lanes + kColO + c, v);
-        }
-        tmem_wait_st();
-      }
-      if (now != m) {
-        l *= exp2_approx(m - now);
-        m = now;
-      }
-      // P, in the layout of an MMA A operand
-      ok = mbar_wait_warp(&pv_done[grp], (use & 1) ^ 1u, s_abort, err);
-      if (!ok) break;
-      const uint32_t p_at = smem0 + kOffP + grp * kP + r * 128 + (r & 7) * 16;
-      float sum[2] = {0.f, 0.f};
+        for (int h = 0; h < 2; ++h)
+          tmem_ld32(lanes + kColS + slot * kKeys + 32 * h, reinterpret_cast<uint32_t(&)[32]>(s[32 * h]));
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[slot]);
+        // which keys this row sees
+        const int32_t left = g.len - (g.lo + i) * kKeys;  // rows of the sequence from this tile on
+        const int at = i & 7;
+        uint64_t see = padding ? 0ull : ~0ull;
+        if (left < kKeys && !padding) {
+          see = left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
+          uint64_t bad = 0ull;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        uint32_t pk[4];
+          for (int c = 0; c < 8; ++c)
+            bad |= static_cast<uint64_t>(s_odd[16 * at + 2 * c + 1]) << 32 | s_odd[16 * at + 2 * c];
+          if (bad) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = 8 * u + 2 * j;
-          float p0 = exp2_approx(fmaf(s[k], p.scale_log2, -m));
-          float p1 = exp2_approx(fmaf(s[k + 1], p.scale_log2, -m));
-          if (!all) {
-            p0 = see >> k & 1 ? p0 : 0.f;
-            p1 = see >> (k + 1) & 1 ? p1 : 0.f;
+            for (int j = 0; j < kKeys; ++j)
+              if (bad >> j & 1) s[j] = __uint_as_float(0x7FC00000u);
           }
-          sum[0] += p0;
-          sum[1] += p1;
-          pk[j] = pack_bf16x2(p0, p1);
         }
-        st_shared16(p_at ^ (16 * u), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+        see &= static_cast<uint64_t>(s_there[2 * at + 1]) << 32 | s_there[2 * at];
+        const bool all = __all_sync(0xffffffffu, see == ~0ull);
+        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        if (all) {
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) {
+            if (see >> j & 1) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+          }
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        // m of the tile before; raised where a score passes it by more than the slack. Finite once a
+        // key was seen: a score of +-infinity keeps its meaning in s - m.
+        float before = kNegInf;
+        if (i > 0) {
+          ok = mbar_wait_warp(&m_full[warp ^ 4], ((i - 1) >> 1) & 1, s_abort, err);
+          if (!ok) break;
+          before = s_m[(grp ^ 1) * kRows + r];
+        }
+        float now = before;
+        if (see != 0ull && (before == kNegInf || top > before + kSlack))
+          now = fminf(fmaxf(top, -kMax), kMax);
+        s_m[grp * kRows + r] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m_full[warp]);
+        if (now != m) {
+          l *= exp2_approx(m - now);
+          m = now;
+        }
+        // P, in the layout of an MMA A operand, and the factor of the O before it
+        ok = __all_sync(0xffffffffu, wait_cluster(&p_free[grp], (use & 1) ^ 1u, s_abort, err));
+        if (!ok) break;
+        s_f[grp * kRows + r] = now != before && before != kNegInf ? exp2_approx(before - now) : 1.f;
+        const uint32_t p_at = smem0 + kOffP + grp * kP + r * 128 + (r & 7) * 16;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = 8 * u + 2 * j;
+            float p0 = exp2_approx(fmaf(s[k], p.scale_log2, -m));
+            float p1 = exp2_approx(fmaf(s[k + 1], p.scale_log2, -m));
+            if (!all) {
+              p0 = see >> k & 1 ? p0 : 0.f;
+              p1 = see >> (k + 1) & 1 ? p1 : 0.f;
+            }
+            sum[0] += p0;
+            sum[1] += p1;
+            pk[j] = pack_bf16x2(p0, p1);
+          }
+          st_shared16(p_at ^ (16 * u), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+        }
+        l += sum[0] + sum[1];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = peer(smem_u32(&p_full[grp]), 1);
+          const uint32_t from = smem0 + kOffP + grp * kP + rows_at;
+          copy_to_peer(peer(from, 1), from, 32 * 128, bar);
+          const uint32_t f_at = smem_u32(s_f + grp * kRows + quad * 32);
+          copy_to_peer(peer(f_at, 1), f_at, 128, bar);
+        }
       }
-      l += sum[0] + sum[1];
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[grp]);
-    }
-    // ---------------- both groups' sums, and this group's 128 columns of the output
-    s_l[grp * kRows + r] = l;
-    s_l[(2 + grp) * kRows + r] = m;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float last = g.n > 0 ? s_m[((g.n - 1) & 1) * kRows + r] : kNegInf;
-    l = 0.f;
+      // ---------------- both groups' sums, to rank 1
+      s_l[grp * kRows + r] = l;
+      s_l[(2 + grp) * kRows + r] = m;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (grp == 0) {
+        const float last = g.n > 0 ? s_m[((g.n - 1) & 1) * kRows + r] : kNegInf;
+        l = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float mk = s_l[(2 + k) * kRows + r];
-      if (mk != kNegInf) l += s_l[k * kRows + r] * (mk == last ? 1.f : exp2_approx(mk - last));
-    }
-    if (ok && g.n > 0) ok = mbar_wait_warp(&pv_done[(g.n - 1) & 1], ((g.n - 1) >> 1) & 1, s_abort, err);
-    tc_fence_after();
-    const bool none = last == kNegInf;
-    if (p.splits == 1) {
-      if (used && rank == 0 && grp == 0 && p.lse)
-        p.lse[out_row] = none ? kNegInf : (last + __log2f(l)) * 0.69314718055994531f;
-      const float inv = none ? 0.f : 1.f / l;
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t v[32], pk[16];
-        if (g.n > 0) {
-          tmem_ld32(tmem + lanes + kColO + grp * 128 + c, v);
-          tmem_wait_ld();
+        for (int k = 0; k < 2; ++k) {
+          const float mk = s_l[(2 + k) * kRows + r];
+          if (mk != kNegInf) l += s_l[k * kRows + r] * (mk == last ? 1.f : exp2_approx(mk - last));
         }
-#pragma unroll
-        for (int j = 0; j < 32; j += 2)
-          pk[j / 2] = none ? 0u : pack_bf16x2(__uint_as_float(v[j]) * inv, __uint_as_float(v[j + 1]) * inv);
-        if (used && ok) {
-          uint16_t* dst = p.out + out_row * kLatent + rank * kHalf + grp * 128 + c;
-          reinterpret_cast<uint4*>(dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          reinterpret_cast<uint4*>(dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          reinterpret_cast<uint4*>(dst)[2] = make_uint4(pk[8], pk[9], pk[10], pk[11]);
-          reinterpret_cast<uint4*>(dst)[3] = make_uint4(pk[12], pk[13], pk[14], pk[15]);
+        st_peer(peer(smem_u32(s_l + r), 1), l);
+        st_peer(peer(smem_u32(s_l + kRows + r), 1), last);
+        __syncwarp();
+        if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
+        if (p.splits > 1) {
+          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = last;
+          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l;
+        } else if (used && p.lse) {
+          p.lse[out_row] = last == kNegInf ? kNegInf : (last + __log2f(l)) * 0.69314718055994531f;
         }
       }
     } else {
-      if (rank == 0 && grp == 0) {
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = last;
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l;
-      }
-      if (g.n > 0 && ok) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o) +
-                      ((static_cast<int64_t>(item) * 2 + rank) * 64 + grp * 32) * kRows + r;
+      // ---------------- O: rescaled where m was raised, at the end written; 256 columns a group
+      uint32_t seen = 0;  // P tiles that have come
+      if (tid == 0)
+        for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
+      const uint32_t o = lanes + grp * kHalf;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+      for (int i = 0; i < g.n; ++i) {
+        const int slot = i & 1;
+        const uint32_t parity = (i >> 1) & 1;
+        ok = mbar_wait_warp(&p_full[slot], parity, s_abort, err);
+        if (!ok) break;
+        ++seen;
+        const float f = s_f[slot * kRows + r];
+        if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kHalf; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(o + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            tmem_st32(o + c, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scaled[slot]);
+        ok = mbar_wait_warp(&pv_done[slot], parity, s_abort, err);
+        if (!ok) break;
+        if (tid == 0 && i + 2 < g.n) mbar_arrive_expect_tx(&p_full[slot], kPBytes);
+        __syncwarp();
+        if (lane == 0) arrive_peer(peer(smem_u32(&p_free[slot]), 0));
+      }
+      // never leave with copies in flight to here (after an abort: bounded)
+      if (!ok && tid == 0)
+        for (uint32_t i = seen; i < min(seen + 2, static_cast<uint32_t>(g.n)); ++i)
+          mbar_drain(&p_full[i & 1], (i >> 1) & 1);
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, wait_cluster(l_full, 0u, s_abort, err)) && ok;
+      tc_fence_after();
+      const float l = s_l[r];
+      const bool none = s_l[kRows + r] == kNegInf;
+      if (p.splits == 1) {
+        const float inv = none ? 0.f : 1.f / l;
+        uint16_t* dst = p.out + out_row * kLatent + grp * kHalf;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+          uint32_t v[32], pk[16];
+          if (g.n > 0) {
+            tmem_ld32(o + c, v);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            pk[j / 2] =
+                none ? 0u : pack_bf16x2(__uint_as_float(v[j]) * inv, __uint_as_float(v[j + 1]) * inv);
+          if (used && ok) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              reinterpret_cast<uint4*>(dst + c)[j] =
+                  make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          }
+        }
+      } else if (g.n > 0 && ok) {
+        float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                      (static_cast<int64_t>(item) * 128 + grp * 64) * kRows + r;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
           uint32_t v[32];
-          tmem_ld32(tmem + lanes + kColO + grp * 128 + c, v);
+          tmem_ld32(o + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -543,107 +545,153 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
       }
     }
+    setmaxnreg_dec<kRegLaunch>();
+    registers_back();
   } else if (warp < kMmaWarp) {
-    // ---------------- rows to bf16: one (key, chunk of 64 dims) a thread, two steps in flight
+    setmaxnreg_dec<kRegLoad>();
+    // ---------------- rows to bf16: one (key, chunk of 64 dims) a thread in each half of the dims
     const int w = warp - kLoad0, key = (w & 1) * 32 + lane, c = w >> 1;
     const TokenPlace tp = place_token(p.place, b);
-    auto row_of = [&](int i) -> int64_t {
-      const int64_t s = (g.lo + i) * kKeys + key;
+    auto row_of = [&](int i) -> int32_t {
+      const int32_t s = (g.lo + i) * kKeys + key;
       if (i >= g.n || s >= g.end || (s >= g.len && !(g.seen >> (s - g.len) & 1))) return -1;
-      return place_row(p.place, tp, static_cast<int32_t>(s));
+      return static_cast<int32_t>(place_row(p.place, tp, s));
     };
-    RowPart<kFormat> part[2];
-    bool there[2];
-    int64_t next = row_of(0);
-    auto fetch = [&](int i, RowPart<kFormat>& x, bool& t) {
-      t = next >= 0;
-      x.load(p, next, rank, c);
-      next = row_of(i + 1);
-    };
+    // Reads in flight: the next two parts, of 128-byte pieces the next one.
+    constexpr int kFlight = kFormat == DS4IDX_CACHE_BF16 ? 1 : 2;
+    RowPart<kFormat> part[kFlight];
+    int32_t row = row_of(0), next = row_of(1);  // of the tile that is read, and of the one after it
     bool ok = true;
-    auto put = [&](int i, RowPart<kFormat>& x, bool t) {
-      if (!ok || i >= g.n) return;
-      const int st = i % kStages;
-      ok = mbar_wait_warp(&k_empty[st], ((i / kStages) & 1) ^ 1u, s_abort, err);
+    int st = 0;           // place in the ring
+    uint32_t parity = 1;  // of its part_empty
+    auto put = [&](int i, int h, const int32_t here, RowPart<kFormat>& x) {
+      ok = mbar_wait_warp(&part_empty[st], parity, s_abort, err);
       if (!ok) return;
       // A drafted row that some rows of the tile see and others do not may hold values that are not
       // finite: cleared, since 0 * NaN would reach all of O, and its scores become NaN instead.
-      const bool drafts = (g.lo + i) * kKeys + kKeys > g.len;
-      if (drafts) {
-        const bool odd = (g.lo + i) * kKeys + key >= g.len && x.odd();
+      const int32_t left = g.len - (g.lo + i) * kKeys;
+      if (left < kKeys) {
+        const bool odd = key >= left && x.odd();
         const uint32_t bits = __ballot_sync(0xffffffffu, odd);
         if (odd) x.clear();
-        if (lane == 0) s_odd[8 * st + 2 * c + (w & 1)] = bits;
+        if (lane == 0) s_odd[16 * (i & 7) + 2 * (4 * h + c) + (w & 1)] = bits;
       }
-      if (c == 0) {
-        const uint32_t bits = __ballot_sync(0xffffffffu, t);
-        if (lane == 0) s_there[2 * st + (w & 1)] = bits;
+      if (c == 0 && h == 0) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, here >= 0);
+        if (lane == 0) s_there[2 * (i & 7) + (w & 1)] = bits;
       }
-      x.store(smem0 + st * kStage, key, c);
+      x.store(smem0 + st * kPart + c * kChunk, key);
+      if (rank == 0)
+        st_shared16(smem0 + kOffRope + (i % 3) * kChunk + key * 128 + (((4 * h + c) ^ key) & 7) * 16, x.rope);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[st]);
+      if (lane == 0) mbar_arrive(&part_full[st]);
+      if (++st == kParts) st = 0, parity ^= 1u;
     };
-    fetch(0, part[0], there[0]);
-    fetch(1, part[1], there[1]);
+    part[0].load(p, row, c, rank == 0);
+    if (kFlight == 2) part[kFlight - 1].load(p, row, 4 + c, rank == 0);
 #pragma unroll 1
-    for (int i = 0; i < g.n && ok; i += 2) {
-      put(i, part[0], there[0]);
-      fetch(i + 2, part[0], there[0]);
-      put(i + 1, part[1], there[1]);
-      fetch(i + 3, part[1], there[1]);
-    }
-  } else {
-    // ---------------- MMA issue: the warp waits together, one elected lane issues
-    const bool lead = elect_one();
-    bool ok = true;
-    const uint64_t k0 = smem_desc_sw128(smem0), v0 = smem_desc_mn_sw128(smem0, kChunk);
-    const uint64_t kr0 = smem_desc_sw64(smem0 + kOffRope), qr = smem_desc_sw64(smem0 + kOffQRope);
-    const uint64_t p0 = smem_desc_sw128(smem0 + kOffP);
-    constexpr uint32_t s_idesc = instr_desc(1u, 1u, kRows, kKeys);
-    constexpr uint32_t o_idesc = instr_desc(1u, 1u, kRows, kHalf) | (1u << 16);  // B MN-major
-    auto commit = [&](uint64_t* bar) {
-      if (lead) mma_commit(bar);
-    };
-    auto value_product = [&](int i) {
-      const int st = i % kStages, slot = i & 1;
-      ok = mbar_wait_warp(&p_full[slot], (i >> 1) & 1, s_abort, err);
-      if (!ok) return;
-      tc_fence_after();
-      const uint64_t pd = p0 + slot * (kP >> 4), vd = v0 + st * (kStage >> 4);
-      if (lead) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16(tmem + kColO, pd + 2 * k, vd + k * (16 * 128 >> 4), o_idesc, (i | k) ? 1u : 0u);
-      }
-      commit(&k_empty[st]);
-      commit(&pv_done[slot]);
-    };
-    if (g.n > 0) ok = mbar_wait_warp(q_full, 0u, s_abort, err);
-#pragma unroll 1
-    for (int i = 0; ok && i < g.n; ++i) {
-      const int st = i % kStages, slot = i & 1;
-      ok = mbar_wait_warp(&k_full[st], (i / kStages) & 1, s_abort, err) &&
-           mbar_wait_warp(&s_free[slot], ((i >> 1) & 1) ^ 1u, s_abort, err);
+    for (int i = 0; i < g.n; ++i) {
+      const int32_t here = row;
+      put(i, 0, here, part[0]);
       if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + kColS + slot * kKeys;
-      const uint64_t kd = k0 + st * (kStage >> 4), kr = kr0 + st * (kStage >> 4);
-      if (lead) {
-        mma_bf16(d, qr, kr, s_idesc, 0u);
-        mma_bf16(d, qr + 2, kr + 2, s_idesc, 1u);
-#pragma unroll
-        for (int k = 0; k < kHalf / 16; ++k)
-          mma_bf16_ts(d, tmem + kColQ + k * 8, kd + (k >> 2) * (kChunk >> 4) + (k & 3) * 2, s_idesc, 1u);
-      }
-      commit(&s_ready[slot]);
-      if (i > 0) value_product(i - 1);
+      row = next;
+      next = row_of(i + 2);
+      if (kFlight == 2) part[0].load(p, row, c, rank == 0);
+      else part[0].load(p, here, 4 + c, rank == 0);
+      put(i, 1, here, part[kFlight - 1]);
+      if (!ok) break;
+      if (kFlight == 2) part[kFlight - 1].load(p, row, 4 + c, rank == 0);
+      else part[0].load(p, row, c, rank == 0);
     }
-    if (ok && g.n > 0) value_product(g.n - 1);
-    // every MMA has completed before TMEM is released (bounded, also after an abort)
-    commit(done);
-    if (lead) mbar_drain(done, 0u);
-    __syncwarp();
+    registers_back();
+    setmaxnreg_inc<kRegLaunch>();
+  } else {
+    setmaxnreg_dec<kRegMma>();
+    if (warp == kMmaWarp) {
+      // ---------------- MMA issue: the warp waits together, one elected lane issues
+      const bool lead = elect_one();
+      bool ok = true;
+      int st = 0;
+      uint32_t parity = 0;  // of part_full
+      auto commit = [&](uint64_t* bar) {
+        if (lead) mma_commit(bar);
+      };
+      auto part_ready = [&] {
+        ok = ok && mbar_wait_warp(&part_full[st], parity, s_abort, err);
+        tc_fence_after();
+      };
+      auto part_taken = [&] {
+        commit(&part_empty[st]);
+        if (++st == kParts) st = 0, parity ^= 1u;
+      };
+      if (rank == 0) {
+        const uint64_t k0 = smem_desc_sw128(smem0), r0 = smem_desc_sw128(smem0 + kOffRope);
+        constexpr uint32_t idesc = instr_desc(1u, 1u, kRows, kKeys);
+        if (g.n > 0) ok = mbar_wait_warp(q_full, 0u, s_abort, err);
+        int slot = 0;
+        uint32_t s_parity = 1;
+#pragma unroll 1
+        for (int i = 0; ok && i < g.n; ++i) {
+          ok = mbar_wait_warp(&s_free[slot], s_parity, s_abort, err);
+          const uint32_t d = tmem + kColS + slot * kKeys;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            part_ready();
+            if (!ok) break;
+            const uint64_t kd = k0 + st * (kPart >> 4);
+            if (lead) {
+#pragma unroll
+              for (int k = 0; k < kHalf / 16; ++k)
+                mma_bf16_ts(d, tmem + h * 128 + k * 8, kd + (k >> 2) * (kChunk >> 4) + (k & 3) * 2, idesc,
+                            (h | k) ? 1u : 0u);
+            }
+            if (h == 1 && lead) {
+              const uint64_t rd = r0 + slot * (kChunk >> 4);  // (i % 3 = slot)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ts(d, tmem + kColRope + k * 8, rd + 2 * k, idesc, 1u);
+            }
+            part_taken();
+          }
+          if (!ok) break;
+          commit(&s_ready[slot]);
+          if (++slot == 3) slot = 0, s_parity ^= 1u;
+        }
+      } else {
+        const uint64_t p0 = smem_desc_sw128(smem0 + kOffP), v0 = smem_desc_mn_sw128(smem0, kChunk);
+        constexpr uint32_t idesc = instr_desc(1u, 1u, kRows, kHalf) | (1u << 16);  // B MN-major
+#pragma unroll 1
+        for (int i = 0; ok && i < g.n; ++i) {
+          const int slot = i & 1;
+          ok = mbar_wait_warp(&p_full[slot], (i >> 1) & 1, s_abort, err);
+          if (!ok) break;
+          const float4 f = reinterpret_cast<const float4*>(s_f + slot * kRows)[lane];
+          if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f))
+            ok = mbar_wait_warp(&scaled[slot], (i >> 1) & 1, s_abort, err);
+          const uint64_t pd = p0 + slot * (kP >> 4);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            part_ready();
+            if (!ok) break;
+            const uint64_t vd = v0 + st * (kPart >> 4);
+            if (lead) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16(tmem + h * kHalf, pd + 2 * k, vd + k * (16 * 128 >> 4), idesc, (i | k) ? 1u : 0u);
+            }
+            part_taken();
+          }
+          commit(&pv_done[slot]);
+        }
+      }
+      // every MMA has completed before TMEM is released (bounded, also after an abort)
+      commit(done);
+      if (lead) mbar_drain(done, 0u);
+      __syncwarp();
+    }
+    registers_back();
+    setmaxnreg_inc<kRegLaunch>();
   }
   __syncwarp();
   tc_fence_before();
@@ -652,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  cluster_sync();  // no CTA leaves while the other may still write or arrive here
+  cluster_sync();  // no CTA leaves while the other may still write, read or arrive here
 }
 
 // Joins the ranges of a row tile: a thread four columns of one row. Ranges without a seen key carry
@@ -673,7 +721,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* src = reinterpret_cast<const float4*>(p.part_o) +
-                      ((group * p.splits * 2 + quad / 64) * 64 + quad % 64) * kRows + r;
+                      (group * p.splits * 128 + quad) * kRows + r;
   if (m != kNegInf) {
 #pragma unroll 4
     for (int i = 0; i < p.splits; ++i) {
@@ -730,8 +778,22 @@ bool sizes_ok(int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
 
 template <int kFormat>
 int launch(const Params& p, int64_t items, void* stream) {
-  static std::atomic<uint64_t> done{0};
+  static std::atomic<uint64_t> done{0}, regs_ok{0};
   if (!allow_shared(tree_attn_kernel<kFormat>, kSmem, done)) return DS4IDX_ERR_CUDA;
+  // The warpgroups' exchange of registers ends only at exactly kRegLaunch a thread: a build of another
+  // number is refused.
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DS4IDX_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(regs_ok.load(std::memory_order_relaxed) & bit)) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, tree_attn_kernel<kFormat>) != cudaSuccess ||
+        fa.numRegs != kRegLaunch) {
+      cudaGetLastError();
+      return DS4IDX_ERR_CUDA;
+    }
+    regs_ok.fetch_or(bit, std::memory_order_relaxed);
+  }
   return launch_dependent(tree_attn_kernel<kFormat>, static_cast<unsigned>(2 * items), kThreads, kSmem,
                           2, stream, p);
 }
