@@ -17,8 +17,13 @@
 // Both CTAs read the rows themselves and turn them into bf16 (exact) in a ring of parts, 64 keys x 256
 // dims in the 128-byte-swizzled layout that serves as K-major and as MN-major operand.
 //
-// Warps 0..7: softmax, warps 0..3 on even tiles and 4..7 on odd ones, m handed from tile to tile (rank
-// 1: the rescaling of O and the output). Warps 8..15: rows to bf16. Warp 16 issues tcgen05.mma.
+// Warps 0..3: softmax, a row a thread (rank 1: the rescaling of O and the output). Warps 4..11: rows to
+// operands. Warp 12 issues tcgen05.mma.
+//
+// 8-bit rows are f16 in the key product: E4M3 to f16 is one conversion for two values, to bf16 five
+// instructions. The row's scale is applied to S, the rotary dims (bf16) are divided by it before, and Q is
+// scaled by a power of two to f16's range: all exact, but for what of a row of Q lies 2^38 below its largest
+// value. As values they are bf16 (P times the scales would leave f16's range).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -44,23 +49,19 @@ constexpr int kDims = 576, kLatent = 512, kNodes = 64, kMaxHeads = 128;
 constexpr int kRows = 128;             // (node, head) rows of a tile = TMEM lanes
 constexpr int kKeys = 64;              // keys of a step
 constexpr int kHalf = 256;             // latent dims of a part
-constexpr int kLoad0 = 8, kMmaWarp = 16;
-constexpr int kThreads = 20 * 32;
-// Registers a thread: at launch, and as the warpgroups then share them (two of softmax, two of loading,
-// the MMA warp's): 256 * 136 + 256 * 80 + 128 * 40 of 640 * 96.
-constexpr int kRegLaunch = 96, kRegSoftmax = 136, kRegLoad = 80, kRegMma = 40;
-static_assert(256 * (kRegSoftmax + kRegLoad) + 128 * kRegMma <= kThreads * kRegLaunch, "registers");
+constexpr int kLoad0 = 4, kLoaders = 8, kMmaWarp = 12;
+constexpr int kThreads = 13 * 32;
 constexpr int kChunk = kKeys * 128;    // 64 dims of a tile's keys
 constexpr int kPart = 4 * kChunk, kParts = 5;
 constexpr int kOffRope = kParts * kPart;           // the rotary dims of three tiles' keys (rank 0)
 constexpr int kOffP = kOffRope + 3 * kChunk, kP = kRows * kKeys * 2;  // P of two tiles
 constexpr int kOffF = kOffP + 2 * kP;              // float [2][128]: factors of O before P V
-constexpr int kOffM = kOffF + 2 * kRows * 4;       // float [2][128]: m after an even, an odd tile
-constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l and its m of both groups
-constexpr int kOffThere = kOffL + 4 * kRows * 4;   // uint32 [8 tiles][2]: keys that are there
+constexpr int kOffL = kOffF + 2 * kRows * 4;       // float [2][128]: l, m (rank 1)
+constexpr int kOffScale = kOffL + 2 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit rows)
+constexpr int kOffThere = kOffScale + 8 * kKeys * 4;  // uint32 [8 tiles][2]: keys that are there
 constexpr int kOffOdd = kOffThere + 8 * 8;         // uint32 [8 tiles][8 chunks][2]: keys not finite
 constexpr int kOffBars = kOffOdd + 8 * 64;
-constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 8 + 2;
+constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 2;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
@@ -202,8 +203,8 @@ struct RowPart {
     lo = ds4q::mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), s2);
     hi = ds4q::mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), s2);
   }
-  // To row `key` of a chunk in shared memory.
-  __device__ __forceinline__ void store(uint32_t chunk, int key) const {
+  // To row `key` of a chunk in shared memory; 8-bit rows in f16 without their scale, or in bf16.
+  __device__ __forceinline__ void store(uint32_t chunk, int key, bool f16) const {
     const uint32_t at = chunk + key * 128 + (key & 7) * 16;
     uint32_t s2 = 0;
     if constexpr (kFormat == DS4IDX_CACHE_FP8) s2 = ((scale >> 23) + 120u) * 0x00800080u;
@@ -213,8 +214,13 @@ struct RowPart {
       if constexpr (kFormat == DS4IDX_CACHE_BF16) {
         v = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
       } else if constexpr (kFormat == DS4IDX_CACHE_FP8) {
-        unpack(w[2 * u], s2, v.x, v.y);
-        unpack(w[2 * u + 1], s2, v.z, v.w);
+        if (f16) {
+          ds4f8::codes_to_f16(w[2 * u], v.x, v.y);
+          ds4f8::codes_to_f16(w[2 * u + 1], v.z, v.w);
+        } else {
+          unpack(w[2 * u], s2, v.x, v.y);
+          unpack(w[2 * u + 1], s2, v.z, v.w);
+        }
       } else {
         const int g = u >> 1;
         const uint32_t q2 = __byte_perm(scale, 0, 0x4040u | (g << 8) | g) * 16u + 0x35803580u;
@@ -225,6 +231,15 @@ struct RowPart {
   }
 };
 
+// Two bf16 to two f16, times a power of two.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float f) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+      : "=r"(d)
+      : "f"(__uint_as_float(v & 0xFFFF0000u) * f), "f"(__uint_as_float(v << 16) * f));
+  return d;
+}
+
 template <int kFormat>
 __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -233,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t smem0 = smem_u32(smem);
   float* s_f = reinterpret_cast<float*>(smem + kOffF);
-  float* s_m = reinterpret_cast<float*>(smem + kOffM);
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
+  float* s_scale = reinterpret_cast<float*>(smem + kOffScale);
   volatile uint32_t* s_there = reinterpret_cast<uint32_t*>(smem + kOffThere);
   volatile uint32_t* s_odd = reinterpret_cast<uint32_t*>(smem + kOffOdd);
   uint64_t* part_full = reinterpret_cast<uint64_t*>(smem + kOffBars);
@@ -246,8 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint64_t* p_full = p_free + 2;    // [2] P has come (in rank 1)
   uint64_t* scaled = p_full + 2;    // [2] O is ready for P V
   uint64_t* pv_done = scaled + 2;   // [2] P V of a tile is done
-  uint64_t* m_full = pv_done + 2;   // [8] a softmax warp's m is in s_m
-  uint64_t* l_full = m_full + 8;    // the rows' sums have come (in rank 1)
+  uint64_t* l_full = pv_done + 2;   // the rows' sums have come (in rank 1)
   uint64_t* done = l_full + 1;      // every MMA has completed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
@@ -259,21 +273,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 
   if (tid == 0) {
     for (int i = 0; i < kParts; ++i) {
-      mbar_init(&part_full[i], 8);
+      mbar_init(&part_full[i], kLoaders);
       mbar_init(&part_empty[i], 1);
     }
-    mbar_init(q_full, 8);
+    mbar_init(q_full, 4);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&s_ready[i], 1);
       mbar_init(&s_free[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_free[i], 8);
+      mbar_init(&p_free[i], 4);
       mbar_init(&p_full[i], 1);
-      mbar_init(&scaled[i], 8);
+      mbar_init(&scaled[i], 4);
       mbar_init(&pv_done[i], 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&m_full[i], 1);
     mbar_init(l_full, 4);
     mbar_init(done, 1);
     *s_abort = 0u;
@@ -291,63 +304,85 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   cluster_sync();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  // Between the softmax warps' giving their registers back and the others' taking them: a warp of the
-  // MMA warpgroup that has nothing to do would else take its back first, and the softmax warps wait for
-  // registers that come free only when they are done.
-  auto registers_back = [] { asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory"); };
+  constexpr bool kF16 = kFormat == DS4IDX_CACHE_FP8;  // the key product's type
 
   if (warp < kLoad0) {
-    setmaxnreg_inc<kRegSoftmax>();
-    const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int r = tid;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int row = tile * kRows + r, node = row / p.H;
     const bool used = node < p.N;
     const int64_t out_row = static_cast<int64_t>(b) * p.N * p.H + row;
     bool ok = true;
     if (rank == 0) {
-      // ---------------- softmax: this thread's row, the tiles of its group's parity
+      // ---------------- softmax: this thread's row
       uint64_t mask = used ? static_cast<uint64_t>(p.mask[static_cast<int64_t>(b) * p.N + node]) : 0ull;
       const bool padding = mask == 0ull;
       mask &= ~0ull >> (64 - p.N);
+      float to_log2 = p.scale_log2;  // of a score, from S
       if (g.n > 0) {
-        // Q to TMEM: a half of the latent dims and of the rotary ones by each group
+        // Q to TMEM
         const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * kDims);
         const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        float f = 1.f;
+        uint32_t f2 = 0;
+        if constexpr (kF16) {
+          // the power of two that takes the row's largest value to 2^13 .. 2^14
+          uint32_t top = 0;
+#pragma unroll 8
+          for (int j = 0; j < kDims / 8; ++j) {
+            const uint4 x = used ? src[j] : zero;
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                         __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+          }
+          const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);   // biased by 127
+          const int a = max(-110, min(110, e == 0 ? 0 : 127 + 13 - e));         // (zero: any)
+          f = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
+          f2 = static_cast<uint32_t>(127 + a) * 0x00800080u;
+          to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+        }
+#pragma unroll 1
+        for (int h = 0; h < 8; ++h) {
           uint32_t v[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint4 x = used ? src[grp * 32 + 8 * h + j] : zero;
+            const uint4 x = used ? src[8 * h + j] : zero;
             v[4 * j] = x.x;
             v[4 * j + 1] = x.y;
             v[4 * j + 2] = x.z;
             v[4 * j + 3] = x.w;
           }
-          tmem_st32(lanes + grp * 128 + h * 32, v);
-        }
-        uint32_t v[16];
+          if constexpr (kF16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 x = used ? src[64 + grp * 4 + j] : zero;
+            for (int j = 0; j < 32; ++j) v[j] = bf16x2_to_f16x2(v[j], f);
+          }
+          tmem_st32(lanes + h * 32, v);
+        }
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 x = used ? src[64 + j] : zero;
           v[4 * j] = x.x;
           v[4 * j + 1] = x.y;
           v[4 * j + 2] = x.z;
           v[4 * j + 3] = x.w;
         }
-        tmem_st16(lanes + kColRope + grp * 16, v);
+        if constexpr (kF16) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
+        }
+        tmem_st32(lanes + kColRope, v);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
       float m = kNegInf, l = 0.f;
-      const uint32_t rows_at = quad * 32 * 128;  // this warp's rows of P
+      const uint32_t rows_at = warp * 32 * 128;  // this warp's rows of P
+      int slot = 0;                              // i % 3
+      uint32_t s_parity = 0;
 #pragma unroll 1
-      for (int i = grp; i < g.n; i += 2) {
-        const uint32_t use = i >> 1;
-        const int slot = i % 3;
-        ok = mbar_wait_warp(&s_ready[slot], (i / 3) & 1, s_abort, err);
+      for (int i = 0; i < g.n; ++i) {
+        ok = mbar_wait_warp(&s_ready[slot], s_parity, s_abort, err);
         if (!ok) break;
         tc_fence_after();
         float s[kKeys];
@@ -358,12 +393,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[slot]);
+        if (++slot == 3) slot = 0, s_parity ^= 1u;
+        const int at = i & 7;
+        if constexpr (kF16) {
+          const float4* sc = reinterpret_cast<const float4*>(s_scale + at * kKeys);
+#pragma unroll
+          for (int j = 0; j < kKeys / 4; ++j) {
+            const float4 x = sc[j];
+            s[4 * j] *= x.x;
+            s[4 * j + 1] *= x.y;
+            s[4 * j + 2] *= x.z;
+            s[4 * j + 3] *= x.w;
+          }
+        }
         // which keys this row sees
         const int32_t left = g.len - (g.lo + i) * kKeys;  // rows of the sequence from this tile on
-        const int at = i & 7;
         uint64_t see = padding ? 0ull : ~0ull;
-        if (left < kKeys && !padding) {
-          see = left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
+        if (left < kKeys) {
+          if (!padding)
+            see = left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
           uint64_t bad = 0ull;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
@@ -379,37 +427,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
         if (all) {
 #pragma unroll
-          for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+          for (int j = 0; j < kKeys; j += 2) mx[j / 2 & 3] = fmaxf(fmaxf(mx[j / 2 & 3], s[j]), s[j + 1]);
         } else {
 #pragma unroll
           for (int j = 0; j < kKeys; ++j) {
             if (see >> j & 1) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
           }
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        // m of the tile before; raised where a score passes it by more than the slack. Finite once a
-        // key was seen: a score of +-infinity keeps its meaning in s - m.
-        float before = kNegInf;
-        if (i > 0) {
-          ok = mbar_wait_warp(&m_full[warp ^ 4], ((i - 1) >> 1) & 1, s_abort, err);
-          if (!ok) break;
-          before = s_m[(grp ^ 1) * kRows + r];
-        }
-        float now = before;
-        if (see != 0ull && (before == kNegInf || top > before + kSlack))
-          now = fminf(fmaxf(top, -kMax), kMax);
-        s_m[grp * kRows + r] = now;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m_full[warp]);
-        if (now != m) {
-          l *= exp2_approx(m - now);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * to_log2;
+        // m is raised where a score passes it by more than the slack. Finite once a key was seen: a
+        // score of +-infinity keeps its meaning in s - m.
+        float f = 1.f;
+        if (see != 0ull && (m == kNegInf || top > m + kSlack)) {
+          const float now = fminf(fmaxf(top, -kMax), kMax);
+          if (m != kNegInf) {
+            f = exp2_approx(m - now);
+            l *= f;
+          }
           m = now;
         }
         // P, in the layout of an MMA A operand, and the factor of the O before it
-        ok = __all_sync(0xffffffffu, wait_cluster(&p_free[grp], (use & 1) ^ 1u, s_abort, err));
+        const int ps = i & 1;
+        ok = __all_sync(0xffffffffu, wait_cluster(&p_free[ps], (i >> 1 & 1) ^ 1u, s_abort, err));
         if (!ok) break;
-        s_f[grp * kRows + r] = now != before && before != kNegInf ? exp2_approx(before - now) : 1.f;
-        const uint32_t p_at = smem0 + kOffP + grp * kP + r * 128 + (r & 7) * 16;
+        s_f[ps * kRows + r] = f;
+        const uint32_t p_at = smem0 + kOffP + ps * kP + r * 128 + (r & 7) * 16;
+        const float off = m == kNegInf ? 0.f : m;  // (a row that has seen nothing: p = 0 below)
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -417,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int k = 8 * u + 2 * j;
-            float p0 = exp2_approx(fmaf(s[k], p.scale_log2, -m));
-            float p1 = exp2_approx(fmaf(s[k + 1], p.scale_log2, -m));
+            float p0 = exp2_approx(fmaf(s[k], to_log2, -off));
+            float p1 = exp2_approx(fmaf(s[k + 1], to_log2, -off));
             if (!all) {
               p0 = see >> k & 1 ? p0 : 0.f;
               p1 = see >> (k + 1) & 1 ? p1 : 0.f;
@@ -433,42 +476,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          const uint32_t bar = peer(smem_u32(&p_full[grp]), 1);
-          const uint32_t from = smem0 + kOffP + grp * kP + rows_at;
+          const uint32_t bar = peer(smem_u32(&p_full[ps]), 1);
+          const uint32_t from = smem0 + kOffP + ps * kP + rows_at;
           copy_to_peer(peer(from, 1), from, 32 * 128, bar);
-          const uint32_t f_at = smem_u32(s_f + grp * kRows + quad * 32);
+          const uint32_t f_at = smem_u32(s_f + ps * kRows + warp * 32);
           copy_to_peer(peer(f_at, 1), f_at, 128, bar);
         }
-      }
-      // ---------------- both groups' sums, to rank 1
-      s_l[grp * kRows + r] = l;
-      s_l[(2 + grp) * kRows + r] = m;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (grp == 0) {
-        const float last = g.n > 0 ? s_m[((g.n - 1) & 1) * kRows + r] : kNegInf;
-        l = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float mk = s_l[(2 + k) * kRows + r];
-          if (mk != kNegInf) l += s_l[k * kRows + r] * (mk == last ? 1.f : exp2_approx(mk - last));
-        }
-        st_peer(peer(smem_u32(s_l + r), 1), l);
-        st_peer(peer(smem_u32(s_l + kRows + r), 1), last);
         __syncwarp();
-        if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
-        if (p.splits > 1) {
-          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = last;
-          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l;
-        } else if (used && p.lse) {
-          p.lse[out_row] = last == kNegInf ? kNegInf : (last + __log2f(l)) * 0.69314718055994531f;
-        }
+      }
+      // ---------------- the rows' sums, to rank 1
+      st_peer(peer(smem_u32(s_l + r), 1), l);
+      st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
+      __syncwarp();
+      if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
+      if (p.splits > 1) {
+        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m;
+        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l;
+      } else if (used && p.lse) {
+        p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
       }
     } else {
-      // ---------------- O: rescaled where m was raised, at the end written; 256 columns a group
+      // ---------------- O: rescaled where m was raised, at the end written
       uint32_t seen = 0;  // P tiles that have come
       if (tid == 0)
         for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
-      const uint32_t o = lanes + grp * kHalf;
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i) {
         const int slot = i & 1;
@@ -480,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < kHalf; c += 32) {
+          for (int c = 0; c < kLatent; c += 32) {
             uint32_t v[32];
-            tmem_ld32(o + c, v);
+            tmem_ld32(lanes + c, v);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-            tmem_st32(o + c, v);
+            tmem_st32(lanes + c, v);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -510,12 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const bool none = s_l[kRows + r] == kNegInf;
       if (p.splits == 1) {
         const float inv = none ? 0.f : 1.f / l;
-        uint16_t* dst = p.out + out_row * kLatent + grp * kHalf;
+        uint16_t* dst = p.out + out_row * kLatent;
 #pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
+        for (int c = 0; c < kLatent; c += 32) {
           uint32_t v[32], pk[16];
           if (g.n > 0) {
-            tmem_ld32(o + c, v);
+            tmem_ld32(lanes + c, v);
             tmem_wait_ld();
           }
 #pragma unroll
@@ -530,12 +561,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
         }
       } else if (g.n > 0 && ok) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o) +
-                      (static_cast<int64_t>(item) * 128 + grp * 64) * kRows + r;
+        float4* dst =
+            reinterpret_cast<float4*>(p.part_o) + static_cast<int64_t>(item) * 128 * kRows + r;
 #pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
+        for (int c = 0; c < kLatent; c += 32) {
           uint32_t v[32];
-          tmem_ld32(o + c, v);
+          tmem_ld32(lanes + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -545,10 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
       }
     }
-    setmaxnreg_dec<kRegLaunch>();
-    registers_back();
   } else if (warp < kMmaWarp) {
-    setmaxnreg_dec<kRegLoad>();
     // ---------------- rows to bf16: one (key, chunk of 64 dims) a thread in each half of the dims
     const int w = warp - kLoad0, key = (w & 1) * 32 + lane, c = w >> 1;
     const TokenPlace tp = place_token(p.place, b);
@@ -557,13 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (i >= g.n || s >= g.end || (s >= g.len && !(g.seen >> (s - g.len) & 1))) return -1;
       return static_cast<int32_t>(place_row(p.place, tp, s));
     };
-    // Reads in flight: the next two parts, of 128-byte pieces the next one.
-    constexpr int kFlight = kFormat == DS4IDX_CACHE_BF16 ? 1 : 2;
-    RowPart<kFormat> part[kFlight];
+    RowPart<kFormat> part[2];                  // reads in flight, of each half the next
     int32_t row = row_of(0), next = row_of(1);  // of the tile that is read, and of the one after it
     bool ok = true;
     int st = 0;           // place in the ring
     uint32_t parity = 1;  // of its part_empty
+    int rope = 0;         // i % 3
     auto put = [&](int i, int h, const int32_t here, RowPart<kFormat>& x) {
       ok = mbar_wait_warp(&part_empty[st], parity, s_abort, err);
       if (!ok) return;
@@ -579,36 +606,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (c == 0 && h == 0) {
         const uint32_t bits = __ballot_sync(0xffffffffu, here >= 0);
         if (lane == 0) s_there[2 * (i & 7) + (w & 1)] = bits;
+        if (kF16) s_scale[(i & 7) * kKeys + key] = __uint_as_float(x.scale);
       }
-      x.store(smem0 + st * kPart + c * kChunk, key);
-      if (rank == 0)
-        st_shared16(smem0 + kOffRope + (i % 3) * kChunk + key * 128 + (((4 * h + c) ^ key) & 7) * 16, x.rope);
+      if (rank == 0) {
+        x.store(smem0 + st * kPart + c * kChunk, key, kF16);
+        uint4 v = x.rope;
+        if constexpr (kF16) {  // divided by the scale
+          const uint32_t s2 = (254u - (x.scale >> 23)) * 0x00800080u;
+          v = make_uint4(ds4q::mul_bf16x2(v.x, s2), ds4q::mul_bf16x2(v.y, s2), ds4q::mul_bf16x2(v.z, s2),
+                         ds4q::mul_bf16x2(v.w, s2));
+        }
+        st_shared16(smem0 + kOffRope + rope * kChunk + key * 128 + (((4 * h + c) ^ key) & 7) * 16, v);
+      } else {
+        x.store(smem0 + st * kPart + c * kChunk, key, false);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&part_full[st]);
       if (++st == kParts) st = 0, parity ^= 1u;
     };
     part[0].load(p, row, c, rank == 0);
-    if (kFlight == 2) part[kFlight - 1].load(p, row, 4 + c, rank == 0);
+    part[1].load(p, row, 4 + c, rank == 0);
 #pragma unroll 1
     for (int i = 0; i < g.n; ++i) {
       const int32_t here = row;
-      put(i, 0, here, part[0]);
-      if (!ok) break;
       row = next;
       next = row_of(i + 2);
-      if (kFlight == 2) part[0].load(p, row, c, rank == 0);
-      else part[0].load(p, here, 4 + c, rank == 0);
-      put(i, 1, here, part[kFlight - 1]);
+      put(i, 0, here, part[0]);
       if (!ok) break;
-      if (kFlight == 2) part[kFlight - 1].load(p, row, 4 + c, rank == 0);
-      else part[0].load(p, row, c, rank == 0);
+      part[0].load(p, row, c, rank == 0);
+      put(i, 1, here, part[1]);
+      if (!ok) break;
+      part[1].load(p, row, 4 + c, rank == 0);
+      if (++rope == 3) rope = 0;
     }
-    registers_back();
-    setmaxnreg_inc<kRegLaunch>();
   } else {
-    setmaxnreg_dec<kRegMma>();
-    if (warp == kMmaWarp) {
       // ---------------- MMA issue: the warp waits together, one elected lane issues
       const bool lead = elect_one();
       bool ok = true;
@@ -627,7 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       };
       if (rank == 0) {
         const uint64_t k0 = smem_desc_sw128(smem0), r0 = smem_desc_sw128(smem0 + kOffRope);
-        constexpr uint32_t idesc = instr_desc(1u, 1u, kRows, kKeys);
+        constexpr uint32_t rope_idesc = instr_desc(1u, 1u, kRows, kKeys);
+        constexpr uint32_t idesc = kF16 ? instr_desc(0u, 0u, kRows, kKeys) : rope_idesc;
         if (g.n > 0) ok = mbar_wait_warp(q_full, 0u, s_abort, err);
         int slot = 0;
         uint32_t s_parity = 1;
@@ -650,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
               const uint64_t rd = r0 + slot * (kChunk >> 4);  // (i % 3 = slot)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_bf16_ts(d, tmem + kColRope + k * 8, rd + 2 * k, idesc, 1u);
+                mma_bf16_ts(d, tmem + kColRope + k * 8, rd + 2 * k, rope_idesc, 1u);
             }
             part_taken();
           }
@@ -689,9 +722,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       commit(done);
       if (lead) mbar_drain(done, 0u);
       __syncwarp();
-    }
-    registers_back();
-    setmaxnreg_inc<kRegLaunch>();
   }
   __syncwarp();
   tc_fence_before();
@@ -778,22 +808,8 @@ bool sizes_ok(int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
 
 template <int kFormat>
 int launch(const Params& p, int64_t items, void* stream) {
-  static std::atomic<uint64_t> done{0}, regs_ok{0};
+  static std::atomic<uint64_t> done{0};
   if (!allow_shared(tree_attn_kernel<kFormat>, kSmem, done)) return DS4IDX_ERR_CUDA;
-  // The warpgroups' exchange of registers ends only at exactly kRegLaunch a thread: a build of another
-  // number is refused.
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DS4IDX_ERR_CUDA;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(regs_ok.load(std::memory_order_relaxed) & bit)) {
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, tree_attn_kernel<kFormat>) != cudaSuccess ||
-        fa.numRegs != kRegLaunch) {
-      cudaGetLastError();
-      return DS4IDX_ERR_CUDA;
-    }
-    regs_ok.fetch_or(bit, std::memory_order_relaxed);
-  }
   return launch_dependent(tree_attn_kernel<kFormat>, static_cast<unsigned>(2 * items), kThreads, kSmem,
                           2, stream, p);
 }
