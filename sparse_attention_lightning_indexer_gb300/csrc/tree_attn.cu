@@ -6,7 +6,7 @@
 // dims fills an SM's TMEM, so a pair of CTAs owns such a tile and a range of keys: one (rank 0) the
 // keys' products and the softmax, the other the values' products:
 //   S[128 x 64 keys] = Q K^T        rank 0; Q stays in TMEM as the A operand, three tiles of S beside it
-//   p = exp2(s - m) in bf16         rank 0; m is left alone until a score passes it by 2^8
+//   p = exp2(s - m) in bf16         rank 0; m is left alone until a score passes it by 64
 //   O[128 x 512] += P V             rank 1; O fills its TMEM over the whole range
 // P, and the factors of O where m was raised, are all that goes from one CTA to the other (16 KB a tile;
 // shared memory of the pair moves 18.7 bytes a clock in each direction when all SMs do it). A tile
@@ -67,7 +67,11 @@ constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
 constexpr uint32_t kColRope = 256, kColS = 320;    // rank 0: Q from column 0, S; rank 1: O from 0
 constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
-constexpr float kSlack = 8.f;          // log2 of what a probability may exceed 1 by
+// log2 of what exp2(s - m) may be before m is raised. P and the sums are floating point with 2^127 of
+// range, so a stale m costs no precision: 2^64 leaves 2^63 for the count and size of the values. (With 2^8
+// some row of 128 raised m in most of the first hundred tiles; a rescaling holds P V up for 4000 clocks,
+// and 4 sequences of 64 nodes over 16384 rows took 2.05 ms.)
+constexpr float kSlack = 64.f;
 
 struct Params {
   const uint16_t* q;
@@ -230,6 +234,16 @@ struct RowPart {
     }
   }
 };
+
+// A range's sum may be far above 1, as its m is stale: its power of two goes into the m that the ranges
+// are joined by (0 for a sum of nothing, infinite or NaN).
+__device__ __forceinline__ int excess(float l) {
+  const int e = static_cast<int>(__float_as_uint(l) >> 23);
+  return e == 0 || e >= 255 ? 0 : e - 127;
+}
+__device__ __forceinline__ float power(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
 
 // Two bf16 to two f16, times a power of two.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float f) {
@@ -441,12 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (see != 0ull && (m == kNegInf || top > m + kSlack)) {
           const float now = fminf(fmaxf(top, -kMax), kMax);
           if (m != kNegInf) {
-            f = exp2_approx(m - now);
-            l *= f;
+            f = exp2_approx(0.5f * (m - now));  // its square: what is 2^64 above m may matter 2^-126
+            l = l * f * f;                      // above the new one, where 2^(m - now) is long zero
           }
           m = now;
         }
-        // P, in the layout of an MMA A operand, and the factor of the O before it
+        // P, in the layout of an MMA A operand, and the root of the factor of the O before it
         const int ps = i & 1;
         ok = __all_sync(0xffffffffu, wait_cluster(&p_free[ps], (i >> 1 & 1) ^ 1u, s_abort, err));
         if (!ok) break;
@@ -490,8 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
       if (p.splits > 1) {
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m;
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l;
+        const int k = excess(l);
+        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
+        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
       } else if (used && p.lse) {
         p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
       }
@@ -516,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             tmem_ld32(lanes + c, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f * f);
             tmem_st32(lanes + c, v);
           }
           tmem_wait_st();
@@ -561,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
         }
       } else if (g.n > 0 && ok) {
+        const float f = power(-excess(l));
         float4* dst =
             reinterpret_cast<float4*>(p.part_o) + static_cast<int64_t>(item) * 128 * kRows + r;
 #pragma unroll 1
@@ -571,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             dst[(c / 4 + j) * kRows] =
-                make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                            __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                make_float4(__uint_as_float(v[4 * j]) * f, __uint_as_float(v[4 * j + 1]) * f,
+                            __uint_as_float(v[4 * j + 2]) * f, __uint_as_float(v[4 * j + 3]) * f);
         }
       }
     }
