@@ -17,8 +17,9 @@
 // Both CTAs read the rows themselves and turn them into bf16 (exact) in a ring of parts, 64 keys x 256
 // dims in the 128-byte-swizzled layout that serves as K-major and as MN-major operand.
 //
-// Warps 0..3: softmax, a row a thread (rank 1: the rescaling of O and the output). Warps 4..11: rows to
-// operands. Warp 12 issues tcgen05.mma.
+// Warps 0..7: softmax, a row a thread, warps 0..3 on even tiles and 4..7 on odd ones, m handed from tile
+// to tile (rank 1: the rescaling of O and the output). Warps 8..15: rows to operands. Warp 16 issues
+// tcgen05.mma.
 //
 // 8-bit rows are f16 in the key product: E4M3 to f16 is one conversion for two values, to bf16 five
 // instructions. The row's scale is applied to S, the rotary dims (bf16) are divided by it before, and Q is
@@ -49,19 +50,26 @@ constexpr int kDims = 576, kLatent = 512, kNodes = 64, kMaxHeads = 128;
 constexpr int kRows = 128;             // (node, head) rows of a tile = TMEM lanes
 constexpr int kKeys = 64;              // keys of a step
 constexpr int kHalf = 256;             // latent dims of a part
-constexpr int kLoad0 = 4, kLoaders = 8, kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kLoad0 = 8, kLoaders = 8, kMmaWarp = 16;
+constexpr int kThreads = 20 * 32;
+// Registers a thread: at launch, and as the warpgroups then share them (two of softmax, two of loading,
+// the MMA warp's).
+constexpr int kRegLaunch = 96, kRegSoftmax = 136, kRegLoad = 80, kRegMma = 40;
+static_assert(256 * (kRegSoftmax + kRegLoad) + 128 * kRegMma <= kThreads * kRegLaunch, "registers");
 constexpr int kChunk = kKeys * 128;    // 64 dims of a tile's keys
-constexpr int kPart = 4 * kChunk, kParts = 5;
-constexpr int kOffRope = kParts * kPart;           // the rotary dims of three tiles' keys (rank 0)
+constexpr int kPart = 4 * kChunk, kParts = 3;
+constexpr int kRaw = kKeys * 256, kRaws = 4;       // codes of a part as they are read
+constexpr int kOffRaw = kParts * kPart;
+constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of three tiles' keys (rank 0)
 constexpr int kOffP = kOffRope + 3 * kChunk, kP = kRows * kKeys * 2;  // P of two tiles
 constexpr int kOffF = kOffP + 2 * kP;              // float [2][128]: factors of O before P V
-constexpr int kOffL = kOffF + 2 * kRows * 4;       // float [2][128]: l, m (rank 1)
-constexpr int kOffScale = kOffL + 2 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit rows)
-constexpr int kOffThere = kOffScale + 8 * kKeys * 4;  // uint32 [8 tiles][2]: keys that are there
-constexpr int kOffOdd = kOffThere + 8 * 8;         // uint32 [8 tiles][8 chunks][2]: keys not finite
-constexpr int kOffBars = kOffOdd + 8 * 64;
-constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 2;
+constexpr int kOffM = kOffF + 2 * kRows * 4;       // float [2][128]: m after an even, an odd tile
+constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
+constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit rows)
+constexpr int kOffThere = kOffScale + 8 * kKeys * 4;  // uint64 [8 tiles]: keys that are there
+constexpr int kOffOdd = kOffThere + 8 * 8;         // uint64 [8 tiles][2 halves]: keys not finite
+constexpr int kOffBars = kOffOdd + 8 * 16;
+constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 8 + 2;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
@@ -93,7 +101,15 @@ struct Params {
 struct Range {
   int32_t len, end;  // rows of the sequence; positions from `end` on are not there
   int32_t lo, n;
+  int32_t turn;
   uint64_t seen;     // drafted rows that some node of the tile sees
+
+  // First position of the i-th step. The tiles of a sequence start at different places of the range and
+  // go around: all pairs reading the same rows at the same time would crowd a few slices of L2.
+  __device__ __forceinline__ int32_t position(int i) const {
+    const int32_t t = i + turn;
+    return (lo + (t < n ? t : t - n)) * kKeys;
+  }
 };
 
 // What every warp works out for itself (warp-uniform): one pass over the tile's masks.
@@ -121,9 +137,49 @@ __device__ __forceinline__ Range make_range(const Params& p, int b, int tile, in
   const int32_t per = max(p.steps, (total - 1) / p.splits + 1);
   g.lo = static_cast<int32_t>(min(static_cast<int64_t>(total), static_cast<int64_t>(split) * per));
   g.n = min(total - g.lo, per);
+  g.turn = static_cast<int32_t>(static_cast<int64_t>(tile) * g.n / p.tiles);
   return g;
 }
 
+// Waits of a whole warp for a phase of a barrier, bounded like every wait of the library: after 2^32 clocks
+// (2 s) or when the CTA has given up it returns false. The clock is first read after some hundred tries; a
+// read of the global timer for each wait that does not succeed at once took a third of the kernel's time.
+template <bool kCluster>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                           uint32_t* err) {
+  auto ready = [&] {
+    uint32_t ok;
+    if constexpr (kCluster)  // acquires what another CTA released
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    return ok != 0;
+  };
+  bool ok = ready();
+  if (!__all_sync(0xffffffffu, ok)) {
+    long long since = 0;
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, ok = ok || ready()); ++i) {
+      if (i & 255u) continue;
+      const long long now = clock64();
+      if (since == 0) since = now;
+      const bool late = now - since > (1ll << 32);
+      if (__any_sync(0xffffffffu, late || *abort_flag)) {
+        if (late) {
+          *abort_flag = 1u;
+          atomicOr(err, 1u);
+        }
+        return false;
+      }
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ void st_peer(uint32_t at, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
@@ -144,96 +200,382 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-// ---- reading rows: what one thread takes of a key, chunk c of 64 dims and, in rank 0, 8 rotary ones,
-// raw; unpacked as 8 x 16 bytes of bf16.
-template <int kFormat>
-struct RowPart {
-  static constexpr int kWords = kFormat == DS4IDX_CACHE_BF16 ? 32 : kFormat == DS4IDX_CACHE_FP8 ? 16 : 8;
-  uint32_t w[kWords];
-  uint32_t scale;
-  uint4 rope;
+// ---- reading rows: eight warps, each eight keys of a tile. Eight lanes read 128 adjacent bytes of a row
+// (a lane for each key instead, 32 bytes at 32 different lines an access, bound the L1's look-ups: 2.0 ms
+// where the listed order now takes TIME).
 
-  __device__ __forceinline__ void load(const Params& p, int64_t r, int c, bool rotary) {
+// 16 bytes of row r at p, zeros where there is no row. One predicated load into registers that hold them:
+// with a branch around it the value is moved where the paths meet, and the move waits for it.
+__device__ __forceinline__ uint4 ld_row16(const uint8_t* p, int32_t r) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  asm volatile(
+      "{\n\t.reg .pred there;\n\tsetp.ge.s32 there, %5, 0;\n\t"
+      "@there ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"(r));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_row2(const void* p, int32_t r) {
+  uint16_t v = 0;
+  asm volatile(
+      "{\n\t.reg .pred there;\n\tsetp.ge.s32 there, %2, 0;\n\t@there ld.global.b16 %0, [%1];\n\t}"
+      : "+h"(v)
+      : "l"(p), "r"(r));
+  return v;
+}
+// 16 (4) bytes of row r at src to shared memory, zeros where there is no row.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src, int32_t r) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r >= 0 ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int32_t r) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(r >= 0 ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Four E4M3 codes times their scale to bf16 (exact), by way of f16 and fp32: the conversions and products
+// run on other pipes than shifting the bits into place would (32768 codes in 850 clocks, 1110 that way).
+__device__ __forceinline__ void codes_to_bf16(uint32_t c, float scale, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  ds4f8::codes_to_f16(c, a, b);
+  const float2 u = ds4f8::f16x2_to_f32(a), v = ds4f8::f16x2_to_f32(b);
+  lo = pack_bf16x2(u.x * scale, u.y * scale);
+  hi = pack_bf16x2(v.x * scale, v.y * scale);
+}
+__device__ __forceinline__ bool odd_f8(const uint4& v) {
+  return (__vcmpeq4(v.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(v.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+          __vcmpeq4(v.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(v.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0u;
+}
+__device__ __forceinline__ bool odd_bf16(const uint4& v) {
+  auto odd = [](uint32_t u) { return (u & 0x7F80u) == 0x7F80u || (u & 0x7F800000u) == 0x7F800000u; };
+  return odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w);
+}
+template <typename T>
+__device__ __forceinline__ void swap_if(bool c, T& a, T& b) {
+  const T x = c ? b : a;
+  b = c ? a : b;
+  a = x;
+}
+
+// One loader warp's work. kKey: this CTA forms the key products (and takes the rotary dims), or the
+// values'. Codes go to shared memory as they are, by asynchronous copies two tiles ahead, and are turned
+// into the operand by the thread that copied them. (Held in registers they were waited for as soon as the
+// next ones were on their way, 1600 clocks a tile: the scoreboards are too few to tell them apart.)
+template <int kFormat, bool kKey>
+__device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b, int w, int lane,
+                                          uint8_t* smem, uint64_t* part_full, uint64_t* part_empty,
+                                          volatile uint32_t* abort_flag) {
+  constexpr bool kF16 = kKey && kFormat == DS4IDX_CACHE_FP8;
+  constexpr int kStride = kFormat == DS4IDX_CACHE_FP8    ? ds4f8::kRowBytes
+                          : kFormat == DS4IDX_CACHE_BF16 ? 2 * kDims
+                                                         : ds4q::kRowBytes;
+  const uint32_t smem0 = smem_u32(smem);
+  const int l8 = lane & 7, sub = lane >> 3;
+  const TokenPlace tp = place_token(p.place, b);
+  // The row of key 8 w + key of tile i.
+  auto row_of = [&](int i, int key) -> int32_t {
+    const int32_t s = g.position(i) + 8 * w + key;
+    if (i >= g.n || s >= g.end || (s >= g.len && !(g.seen >> (s - g.len) & 1))) return -1;
+    return static_cast<int32_t>(place_row(p.place, tp, s));
+  };
+  auto row_at = [&](int32_t r) { return p.cache + static_cast<int64_t>(r) * kStride; };
+  bool ok = true;
+  int st = 0, rope_slot = 0;  // places in the rings
+  uint32_t parity = 1;        // of part_empty
+  auto claim = [&] { ok = ok && wait_phase<false>(&part_empty[st], parity, abort_flag, p.err); };
+  auto step = [&] {
+    if (++st == kParts) st = 0, parity ^= 1u;
+  };
+  auto publish = [&](int at) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&part_full[at]);
+  };
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // Keys 8 w + first .. + 3, one for each eight lanes.
+  auto quad_bits = [&](bool c) -> uint32_t {
+    const uint32_t bits = __ballot_sync(0xffffffffu, c);
+    uint32_t keys = 0;
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = kFormat == DS4IDX_CACHE_Q4 ? ds4q::kEmptyWord : 0u;
-    scale = 0u;
-    rope = make_uint4(0, 0, 0, 0);
-    if (r < 0) return;
-    const uint8_t* row;
-    int at, rot;
-    if constexpr (kFormat == DS4IDX_CACHE_BF16) {
-      row = p.cache + r * (2 * kDims);
-      at = c * 128;
-      rot = 2 * kLatent;
-    } else if constexpr (kFormat == DS4IDX_CACHE_FP8) {
-      row = p.cache + r * ds4f8::kRowBytes;
-      at = c * 64;
-      rot = ds4f8::kOffRope;
-      scale = __float_as_uint(p.scale[r]);
-    } else {
-      row = p.cache + r * ds4q::kRowBytes;
-      at = c * 32;
-      rot = ds4q::kOffRope;
-      scale = *reinterpret_cast<const uint32_t*>(row + ds4q::kOffScale + 4 * c);
-    }
+    for (int j = 0; j < 4; ++j) keys |= bits >> (8 * j) & 0xFFu ? 1u << j : 0u;
+    return keys;
+  };
+  auto note_there = [&](int i, uint32_t bits) {
+    if (lane == 0) smem[kOffThere + 8 * (i & 7) + w] = static_cast<uint8_t>(bits);
+  };
+  auto note_odd = [&](int i, int h, uint32_t bits) {
+    if (lane == 0) smem[kOffOdd + 16 * (i & 7) + 8 * h + w] = static_cast<uint8_t>(bits);
+  };
+  // A drafted row that some rows of the tile see and others do not may hold values that are not finite:
+  // what is not is cleared, since 0 * NaN would reach all of O, and the key's scores become NaN instead.
+  auto drafts = [&](int i) { return g.len - g.position(i) < kKeys; };
+  auto drafted = [&](int i, int key) { return g.position(i) + 8 * w + key >= g.len; };
+  auto rope_address = [&](int key) {
+    return smem0 + kOffRope + rope_slot * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
+  };
+  // This thread's rows (keys sub and 4 + sub) of the tile that is read, and of the one after it.
+  int32_t row[2], next[2];
 #pragma unroll
-    for (int j = 0; j < kWords; j += 8) ld32(row + at + 4 * j, reinterpret_cast<uint32_t(&)[8]>(w[j]));
-    if (rotary) rope = *reinterpret_cast<const uint4*>(row + rot + c * 16);
-  }
-  // Whether a value is not finite (the 4-bit format has none).
-  __device__ __forceinline__ bool odd() const {
-    bool bad = false;
-    if constexpr (kFormat == DS4IDX_CACHE_BF16) {
+  for (int k = 0; k < 2; ++k) row[k] = row_of(0, 4 * k + sub), next[k] = row_of(1, 4 * k + sub);
+  uint32_t there = 0;  // bytes: the keys that are there, of the tiles that are read and not yet written
+  int read = 0;        // tiles whose reads are on their way
+  auto advance_rows = [&] {
+    ++read;
 #pragma unroll
-      for (int j = 0; j < kWords; ++j)
-        bad |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
-    } else if constexpr (kFormat == DS4IDX_CACHE_FP8) {
-      bad = (scale & 0x7F800000u) == 0x7F800000u;
+    for (int k = 0; k < 2; ++k) row[k] = next[k], next[k] = row_of(read + 1, 4 * k + sub);
+  };
+  auto there_bits = [&] { return quad_bits(row[0] >= 0) | quad_bits(row[1] >= 0) << 4; };
+
+  if constexpr (kFormat == DS4IDX_CACHE_FP8) {
+    // access k of a half: rows sub and 4 + sub (k & 1), 128 codes (k >> 1), 16 codes a lane
+    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw part, + 512 k
+    const uint32_t scales = smem0 + kOffScale;
+    auto copy = [&](int h) {
 #pragma unroll
-      for (int j = 0; j < kWords; ++j)
-        bad |= __vcmpeq4(w[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
-    }
-    return bad;
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = kFormat == DS4IDX_CACHE_Q4 ? ds4q::kEmptyWord : 0u;
-    scale = 0u;
-  }
-  // Four E4M3 codes to bf16: sign and magnitude bits to a bf16's places give value * 2^-120 (bf16's
-  // exponent bias is 120 larger), one packed product with scale * 2^120 the value, exactly.
-  __device__ __forceinline__ static void unpack(uint32_t c, uint32_t s2, uint32_t& lo, uint32_t& hi) {
-    const uint32_t a = __byte_perm(c, 0, 0x1404), b = __byte_perm(c, 0, 0x3424);
-    lo = ds4q::mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), s2);
-    hi = ds4q::mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), s2);
-  }
-  // To row `key` of a chunk in shared memory; 8-bit rows in f16 without their scale, or in bf16.
-  __device__ __forceinline__ void store(uint32_t chunk, int key, bool f16) const {
-    const uint32_t at = chunk + key * 128 + (key & 7) * 16;
-    uint32_t s2 = 0;
-    if constexpr (kFormat == DS4IDX_CACHE_FP8) s2 = ((scale >> 23) + 120u) * 0x00800080u;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      uint4 v;
-      if constexpr (kFormat == DS4IDX_CACHE_BF16) {
-        v = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-      } else if constexpr (kFormat == DS4IDX_CACHE_FP8) {
-        if (f16) {
-          ds4f8::codes_to_f16(w[2 * u], v.x, v.y);
-          ds4f8::codes_to_f16(w[2 * u + 1], v.z, v.w);
-        } else {
-          unpack(w[2 * u], s2, v.x, v.y);
-          unpack(w[2 * u + 1], s2, v.z, v.w);
-        }
-      } else {
-        const int g = u >> 1;
-        const uint32_t q2 = __byte_perm(scale, 0, 0x4040u | (g << 8) | g) * 16u + 0x35803580u;
-        v = ds4q::word_to_bf16(w[u], q2, ds4q::offset_bf16x2(q2));
+      for (int k = 0; k < 4; ++k) {
+        const int32_t r = row[k & 1];
+        cp_async16(raw0 + (2 * (read & 1) + h) * kRaw + 512 * k,
+                   row_at(max(r, 0)) + (2 * h + (k >> 1)) * 128 + l8 * 16, r);
       }
-      st_shared16(at ^ (16 * u), v);
+      if (h == 0) {
+        if (l8 < 2) {
+          const int32_t r = l8 ? row[1] : row[0];
+          cp_async4(scales + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4, p.scale + max(r, 0), r);
+        }
+        there |= there_bits() << (8 * (read & 1));
+      }
+      cp_async_commit();
+    };
+    uint4 rope[2];
+    int32_t late[2] = {row[0], row[1]};  // rows of the tile before the one that is copied
+    auto load_rope = [&] {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        rope[k] = ld_row16(row_at(late[k]) + ds4f8::kOffRope + l8 * 16, late[k]);
+    };
+    copy(0);
+    copy(1);
+    if (kKey) load_rope();
+    advance_rows();
+    late[0] = row[0];
+    late[1] = row[1];
+    copy(0);
+    copy(1);
+    advance_rows();
+#pragma unroll 1
+    for (int i = 0; i < g.n; ++i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        cp_async_wait<3>();
+        __syncwarp();
+        claim();
+        if (!ok) break;
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = ld_shared16(raw0 + (2 * (i & 1) + h) * kRaw + 512 * k);
+        const float* sc_at = reinterpret_cast<const float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
+        float sc[2] = {sc_at[sub], sc_at[4 + sub]};
+        if (drafts(i)) {
+          uint32_t odd_keys = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = (k & 1) * 4 + sub;
+            const bool bad = (__float_as_uint(sc[k & 1]) & 0x7F800000u) == 0x7F800000u;
+            const bool odd = drafted(i, key) && (bad || odd_f8(x[k]));
+            if (odd) x[k] = zero;
+            odd_keys |= quad_bits(odd) << (4 * (k & 1));
+            if (k >= 2 && bad && drafted(i, key)) sc[k & 1] = 0.f;
+          }
+          note_odd(i, h, odd_keys);
+        }
+        if (h == 0) note_there(i, there >> (8 * (i & 1)) & 0xFFu);
+        const bool swap = l8 >= 4;  // the lanes of the second chunk write their two pieces in turn
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = (k & 1) * 4 + sub;
+          uint4 c = x[k];
+          swap_if(swap, c.x, c.z);
+          swap_if(swap, c.y, c.w);
+          const uint32_t at = smem0 + st * kPart + ((k >> 1) * 2 + (l8 >> 2)) * kChunk +
+                              (8 * w + key) * 128 + ((((l8 & 3) * 2 + (l8 >> 2)) ^ key) * 16);
+          uint4 v, u;
+          if constexpr (kF16) {
+            ds4f8::codes_to_f16(c.x, v.x, v.y);
+            ds4f8::codes_to_f16(c.y, v.z, v.w);
+            ds4f8::codes_to_f16(c.z, u.x, u.y);
+            ds4f8::codes_to_f16(c.w, u.z, u.w);
+          } else {
+            codes_to_bf16(c.x, sc[k & 1], v.x, v.y);
+            codes_to_bf16(c.y, sc[k & 1], v.z, v.w);
+            codes_to_bf16(c.z, sc[k & 1], u.x, u.y);
+            codes_to_bf16(c.w, sc[k & 1], u.z, u.w);
+          }
+          st_shared16(at, v);
+          st_shared16(at ^ 16, u);
+        }
+        if (kKey && h == 1) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {  // divided by the scale
+            const uint32_t s2 = (254u - (__float_as_uint(sc[k]) >> 23)) * 0x00800080u;
+            st_shared16(rope_address(4 * k + sub),
+                        make_uint4(ds4q::mul_bf16x2(rope[k].x, s2), ds4q::mul_bf16x2(rope[k].y, s2),
+                                   ds4q::mul_bf16x2(rope[k].z, s2), ds4q::mul_bf16x2(rope[k].w, s2)));
+          }
+          load_rope();
+          late[0] = row[0];
+          late[1] = row[1];
+        }
+        publish(st);
+        step();
+        if (h == 0) there &= ~(0xFFu << (8 * (i & 1)));
+        copy(h);
+        if (h == 1) advance_rows();
+      }
+      if (!ok) break;
+      if (++rope_slot == 3) rope_slot = 0;
     }
+    cp_async_wait<0>();
+  } else if constexpr (kFormat == DS4IDX_CACHE_BF16) {
+    // straight to the operand; a part is published when the next one's copies are on their way
+    int last = -1;
+#pragma unroll 1
+    for (int i = 0; i < g.n; ++i) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        claim();
+        if (!ok) break;
+        const bool check = drafts(i);
+        uint32_t odd_keys = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {  // rows sub and 4 + sub, a chunk of 64 dims (k >> 1)
+          const int key = (k & 1) * 4 + sub;
+          const int32_t r = row[k & 1];
+          const uint32_t at =
+              smem0 + st * kPart + (k >> 1) * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
+          const uint8_t* src = row_at(max(r, 0)) + h * 2 * kHalf + (k >> 1) * 128 + l8 * 16;
+          if (check) {
+            const uint4 v = ld_row16(src, r);
+            const bool odd = drafted(i, key) && odd_bf16(v);
+            st_shared16(at, odd ? zero : v);
+            odd_keys |= quad_bits(odd) << (4 * (k & 1));
+          } else {
+            cp_async16(at, src, r);
+          }
+          if (kKey && h == 0 && k < 2)
+            cp_async16(rope_address(key), row_at(max(r, 0)) + 2 * kLatent + l8 * 16, r);
+        }
+        cp_async_commit();
+        if (check) note_odd(i, h, odd_keys);
+        if (h == 0) note_there(i, there_bits());
+        if (last >= 0) {
+          cp_async_wait<1>();
+          publish(last);
+        }
+        last = st;
+        step();
+      }
+      if (!ok) break;
+      advance_rows();
+      if (++rope_slot == 3) rope_slot = 0;
+    }
+    cp_async_wait<0>();
+    if (ok && last >= 0) publish(last);
+  } else {
+    // access k: rows 2 k and 2 k + 1, 32 codes a lane: two of the four scales of a chunk
+    const int l16 = lane & 15, hi = lane >> 4, x = l16 >> 1 & 3;
+    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw tile, + 512 k
+    uint4 rope[2];
+    uint32_t sc[2][4];
+    int32_t late[2] = {row[0], row[1]};
+    auto copy = [&](uint32_t(&scale)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int32_t r = __shfl_sync(0xffffffffu, row[k >> 1], 8 * (2 * (k & 1) + hi));
+        cp_async16(raw0 + (read % 3) * kRaw + 512 * k, row_at(max(r, 0)) + l16 * 16, r);
+        scale[k] = ld_row2(row_at(r) + ds4q::kOffScale + 2 * l16, r);
+      }
+      there |= there_bits() << (8 * (read & 1));
+      cp_async_commit();
+    };
+    auto load_rope = [&] {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        rope[k] = ld_row16(row_at(late[k]) + ds4q::kOffRope + l8 * 16, late[k]);
+    };
+    auto tile = [&](int i, uint32_t(&scale)[4]) {
+      cp_async_wait<1>();
+      const int first = st;
+      claim();
+      step();
+      const int second = st;
+      claim();
+      step();
+      if (!ok) return;
+      note_there(i, there >> (8 * (i & 1)) & 0xFFu);
+      there &= ~(0xFFu << (8 * (i & 1)));
+      if (drafts(i)) note_odd(i, 0, 0), note_odd(i, 1, 0);  // (the format has only finite values)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = 2 * k + hi;
+        uint4 c = ld_shared16(raw0 + (i % 3) * kRaw + 512 * k);
+        // piece j ^ x at step j: the lanes of the other chunks write other banks
+        swap_if(x & 1, c.x, c.y);
+        swap_if(x & 1, c.z, c.w);
+        swap_if(x & 2, c.x, c.z);
+        swap_if(x & 2, c.y, c.w);
+        const uint32_t s = x & 2 ? __byte_perm(scale[k], 0, 0x4401) : scale[k];
+        const uint32_t at = smem0 + (l16 < 8 ? first : second) * kPart + x * kChunk + (8 * w + key) * 128 +
+                            ((((l16 & 1) * 4 + x) ^ key) * 16);
+        const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t s2 = __byte_perm(s, 0, j < 2 ? 0x4040u : 0x4141u) * 16u + 0x35803580u;
+          uint4 v = ds4q::word_to_bf16(words[j], s2, ds4q::offset_bf16x2(s2));
+          // (the zeros of a row that is not there are -8 times the least scale, and are not seen; as a
+          // value they must be finite, which they are)
+          st_shared16(at ^ (16 * j), v);
+        }
+      }
+      if (kKey) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) st_shared16(rope_address(k * 4 + sub), rope[k]);
+        load_rope();
+        late[0] = row[0];
+        late[1] = row[1];
+      }
+      publish(first);
+      publish(second);
+      copy(scale);
+      advance_rows();
+      if (++rope_slot == 3) rope_slot = 0;
+    };
+    copy(sc[0]);
+    if (kKey) load_rope();
+    advance_rows();
+    late[0] = row[0];
+    late[1] = row[1];
+    copy(sc[1]);
+    advance_rows();
+#pragma unroll 1
+    for (int i = 0; i < g.n && ok; i += 2) {
+      tile(i, sc[0]);
+      if (ok && i + 1 < g.n) tile(i + 1, sc[1]);
+    }
+    cp_async_wait<0>();
   }
-};
+}
 
 // A range's sum may be far above 1, as its m is stale: its power of two goes into the m that the ranges
 // are joined by (0 for a sum of nothing, infinite or NaN).
@@ -243,6 +585,19 @@ __device__ __forceinline__ int excess(float l) {
 }
 __device__ __forceinline__ float power(int e) {
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// Two fp32 numbers, as bits, times two others.
+__device__ __forceinline__ void mul_pair(uint32_t& a, uint32_t& b, uint32_t x, uint32_t y) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t"
+      "mul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+r"(a), "+r"(b)
+      : "r"(x), "r"(y));
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // Two bf16 to two f16, times a power of two.
@@ -262,10 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t smem0 = smem_u32(smem);
   float* s_f = reinterpret_cast<float*>(smem + kOffF);
+  float* s_m = reinterpret_cast<float*>(smem + kOffM);
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
-  float* s_scale = reinterpret_cast<float*>(smem + kOffScale);
-  volatile uint32_t* s_there = reinterpret_cast<uint32_t*>(smem + kOffThere);
-  volatile uint32_t* s_odd = reinterpret_cast<uint32_t*>(smem + kOffOdd);
+  volatile uint64_t* s_there = reinterpret_cast<uint64_t*>(smem + kOffThere);
+  volatile uint64_t* s_odd = reinterpret_cast<uint64_t*>(smem + kOffOdd);
   uint64_t* part_full = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint64_t* part_empty = part_full + kParts;
   uint64_t* q_full = part_empty + kParts;
@@ -275,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint64_t* p_full = p_free + 2;    // [2] P has come (in rank 1)
   uint64_t* scaled = p_full + 2;    // [2] O is ready for P V
   uint64_t* pv_done = scaled + 2;   // [2] P V of a tile is done
-  uint64_t* l_full = pv_done + 2;   // the rows' sums have come (in rank 1)
+  uint64_t* m_full = pv_done + 2;   // [8] a softmax warp's m is in s_m
+  uint64_t* l_full = m_full + 8;    // the rows' sums have come (in rank 1)
   uint64_t* done = l_full + 1;      // every MMA has completed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
@@ -290,17 +646,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mbar_init(&part_full[i], kLoaders);
       mbar_init(&part_empty[i], 1);
     }
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 8);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&s_ready[i], 1);
       mbar_init(&s_free[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_free[i], 4);
+      mbar_init(&p_free[i], 8);
       mbar_init(&p_full[i], 1);
-      mbar_init(&scaled[i], 4);
+      mbar_init(&scaled[i], 8);
       mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&m_full[i], 1);
     mbar_init(l_full, 4);
     mbar_init(done, 1);
     *s_abort = 0u;
@@ -320,21 +677,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const uint32_t tmem = *s_tmem;
   constexpr bool kF16 = kFormat == DS4IDX_CACHE_FP8;  // the key product's type
 
+  // Between the softmax warps' giving their registers back and the others' taking them: a warp of the
+  // MMA warpgroup that has nothing to do would else take its back first, and the softmax warps wait for
+  // registers that come free only when they are done.
+  auto registers_back = [] { asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory"); };
+
   if (warp < kLoad0) {
-    const int r = tid;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    setmaxnreg_inc<kRegSoftmax>();
+    const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int row = tile * kRows + r, node = row / p.H;
     const bool used = node < p.N;
     const int64_t out_row = static_cast<int64_t>(b) * p.N * p.H + row;
     bool ok = true;
     if (rank == 0) {
-      // ---------------- softmax: this thread's row
+      // ---------------- softmax: this thread's row, the tiles of its group's parity
       uint64_t mask = used ? static_cast<uint64_t>(p.mask[static_cast<int64_t>(b) * p.N + node]) : 0ull;
       const bool padding = mask == 0ull;
       mask &= ~0ull >> (64 - p.N);
       float to_log2 = p.scale_log2;  // of a score, from S
       if (g.n > 0) {
-        // Q to TMEM
+        // Q to TMEM, a half of the latent dims and of the rotary ones by each group
         const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * kDims);
         const uint4 zero = make_uint4(0, 0, 0, 0);
         float f = 1.f;
@@ -355,11 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
         }
 #pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
+        for (int h = 0; h < 4; ++h) {
           uint32_t v[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint4 x = used ? src[8 * h + j] : zero;
+            const uint4 x = used ? src[grp * 32 + 8 * h + j] : zero;
             v[4 * j] = x.x;
             v[4 * j + 1] = x.y;
             v[4 * j + 2] = x.z;
@@ -369,12 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = bf16x2_to_f16x2(v[j], f);
           }
-          tmem_st32(lanes + h * 32, v);
+          tmem_st32(lanes + grp * 128 + h * 32, v);
         }
-        uint32_t v[32];
+        uint32_t v[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 x = used ? src[64 + j] : zero;
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = used ? src[64 + grp * 4 + j] : zero;
           v[4 * j] = x.x;
           v[4 * j + 1] = x.y;
           v[4 * j + 2] = x.z;
@@ -382,136 +745,156 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         if constexpr (kF16) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
+          for (int j = 0; j < 16; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
         }
-        tmem_st32(lanes + kColRope, v);
+        tmem_st16(lanes + kColRope + grp * 16, v);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
       float m = kNegInf, l = 0.f;
-      const uint32_t rows_at = warp * 32 * 128;  // this warp's rows of P
-      int slot = 0;                              // i % 3
-      uint32_t s_parity = 0;
+      const uint32_t rows_at = quad * 32 * 128;  // this warp's rows of P
+      const uint32_t p_at = smem0 + kOffP + grp * kP + r * 128 + (r & 7) * 16;
 #pragma unroll 1
-      for (int i = 0; i < g.n; ++i) {
-        ok = mbar_wait_warp(&s_ready[slot], s_parity, s_abort, err);
+      for (int i = grp; i < g.n; i += 2) {
+        const uint32_t use = i >> 1;
+        const int slot = i % 3, at = i & 7;
+        ok = wait_phase<false>(&s_ready[slot], (i / 3) & 1, s_abort, err);
         if (!ok) break;
         tc_fence_after();
-        float s[kKeys];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          tmem_ld32(lanes + kColS + slot * kKeys + 32 * h, reinterpret_cast<uint32_t(&)[32]>(s[32 * h]));
+        uint32_t s[kKeys];  // fp32 bits
+        tmem_ld32(lanes + kColS + slot * kKeys, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+        tmem_ld32(lanes + kColS + slot * kKeys + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+        uint64_t see = s_there[at];
         tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[slot]);
-        if (++slot == 3) slot = 0, s_parity ^= 1u;
-        const int at = i & 7;
         if constexpr (kF16) {
-          const float4* sc = reinterpret_cast<const float4*>(s_scale + at * kKeys);
+          const uint32_t sc = smem0 + kOffScale + at * kKeys * 4;
 #pragma unroll
-          for (int j = 0; j < kKeys / 4; ++j) {
-            const float4 x = sc[j];
-            s[4 * j] *= x.x;
-            s[4 * j + 1] *= x.y;
-            s[4 * j + 2] *= x.z;
-            s[4 * j + 3] *= x.w;
+          for (int j = 0; j < kKeys; j += 4) {
+            const uint4 x = ld_shared16(sc + 4 * j);
+            mul_pair(s[j], s[j + 1], x.x, x.y);
+            mul_pair(s[j + 2], s[j + 3], x.z, x.w);
           }
         }
         // which keys this row sees
-        const int32_t left = g.len - (g.lo + i) * kKeys;  // rows of the sequence from this tile on
-        uint64_t see = padding ? 0ull : ~0ull;
+        const int32_t left = g.len - g.position(i);  // rows of the sequence from this tile on
+        if (padding) see = 0ull;
         if (left < kKeys) {
           if (!padding)
-            see = left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
-          uint64_t bad = 0ull;
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            bad |= static_cast<uint64_t>(s_odd[16 * at + 2 * c + 1]) << 32 | s_odd[16 * at + 2 * c];
+            see &= left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
+          const uint64_t bad = s_odd[2 * at] | s_odd[2 * at + 1];
           if (bad) {
 #pragma unroll
             for (int j = 0; j < kKeys; ++j)
-              if (bad >> j & 1) s[j] = __uint_as_float(0x7FC00000u);
+              if (bad >> j & 1) s[j] = 0x7FC00000u;
           }
         }
-        see &= static_cast<uint64_t>(s_there[2 * at + 1]) << 32 | s_there[2 * at];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[slot]);
         const bool all = __all_sync(0xffffffffu, see == ~0ull);
-        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-        if (all) {
+        if (!all) {  // a masked score is -infinity: p = 0 whatever m, and no maximum
+          const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-          for (int j = 0; j < kKeys; j += 2) mx[j / 2 & 3] = fmaxf(fmaxf(mx[j / 2 & 3], s[j]), s[j + 1]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kKeys; ++j) {
-            if (see >> j & 1) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+          for (int j = 0; j < 32; ++j) {
+            s[j] = lo >> j & 1 ? s[j] : 0xFF800000u;
+            s[32 + j] = hi >> j & 1 ? s[32 + j] : 0xFF800000u;
           }
         }
+        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int j = 0; j < kKeys; j += 2)
+          mx[j / 2 & 3] = fmaxf(fmaxf(mx[j / 2 & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * to_log2;
-        // m is raised where a score passes it by more than the slack. Finite once a key was seen: a
-        // score of +-infinity keeps its meaning in s - m.
-        float f = 1.f;
-        if (see != 0ull && (m == kNegInf || top > m + kSlack)) {
-          const float now = fminf(fmaxf(top, -kMax), kMax);
-          if (m != kNegInf) {
-            f = exp2_approx(0.5f * (m - now));  // its square: what is 2^64 above m may matter 2^-126
-            l = l * f * f;                      // above the new one, where 2^(m - now) is long zero
-          }
+        // m of the tile before; raised where a score passes it by more than the slack. Finite once a key
+        // was seen: a score of +-infinity keeps its meaning in s - m.
+        float before = kNegInf;
+        if (i > 0) {
+          ok = wait_phase<false>(&m_full[warp ^ 4], ((i - 1) >> 1) & 1, s_abort, err);
+          if (!ok) break;
+          before = s_m[(grp ^ 1) * kRows + r];
+        }
+        float now = before;
+        if (see != 0ull && (before == kNegInf || top > before + kSlack))
+          now = fminf(fmaxf(top, -kMax), kMax);
+        s_m[grp * kRows + r] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m_full[warp]);
+        if (now != m) {
+          const float f = exp2_approx(0.5f * (m - now));
+          l = l * f * f;
           m = now;
         }
-        // P, in the layout of an MMA A operand, and the root of the factor of the O before it
-        const int ps = i & 1;
-        ok = __all_sync(0xffffffffu, wait_cluster(&p_free[ps], (i >> 1 & 1) ^ 1u, s_abort, err));
+        ok = wait_phase<true>(&p_free[grp], (use & 1) ^ 1u, s_abort, err);
         if (!ok) break;
-        s_f[ps * kRows + r] = f;
-        const uint32_t p_at = smem0 + kOffP + ps * kP + r * 128 + (r & 7) * 16;
-        const float off = m == kNegInf ? 0.f : m;  // (a row that has seen nothing: p = 0 below)
-        float sum[2] = {0.f, 0.f};
+        // The root of the factor of the O before: what is 2^64 above the old m may matter 2^-126 above the
+        // new one, where 2^(before - now) is long zero.
+        s_f[grp * kRows + r] =
+            now != before && before != kNegInf ? exp2_approx(0.5f * (before - now)) : 1.f;
+        // P, in the layout of an MMA A operand
+        const float off = m == kNegInf ? 0.f : -m;  // (a row that has seen nothing: p = 0)
+        const uint64_t off2 = pack_f32x2(off, off), scale2 = pack_f32x2(to_log2, to_log2);
+        uint64_t sum = 0ull;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           uint32_t pk[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int k = 8 * u + 2 * j;
-            float p0 = exp2_approx(fmaf(s[k], to_log2, -off));
-            float p1 = exp2_approx(fmaf(s[k + 1], to_log2, -off));
-            if (!all) {
-              p0 = see >> k & 1 ? p0 : 0.f;
-              p1 = see >> (k + 1) & 1 ? p1 : 0.f;
-            }
-            sum[0] += p0;
-            sum[1] += p1;
-            pk[j] = pack_bf16x2(p0, p1);
+            float x0, x1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2,
+                                   off2),
+                         x0, x1);
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+            sum = add_f32x2(sum, pack_f32x2(x0, x1));
+            pk[j] = pack_bf16x2(x0, x1);
           }
           st_shared16(p_at ^ (16 * u), make_uint4(pk[0], pk[1], pk[2], pk[3]));
         }
-        l += sum[0] + sum[1];
+        float l0, l1;
+        unpack_f32x2(sum, l0, l1);
+        l += l0 + l1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          const uint32_t bar = peer(smem_u32(&p_full[ps]), 1);
-          const uint32_t from = smem0 + kOffP + ps * kP + rows_at;
+          const uint32_t bar = peer(smem_u32(&p_full[grp]), 1);
+          const uint32_t from = smem0 + kOffP + grp * kP + rows_at;
           copy_to_peer(peer(from, 1), from, 32 * 128, bar);
-          const uint32_t f_at = smem_u32(s_f + ps * kRows + warp * 32);
+          const uint32_t f_at = smem_u32(s_f + grp * kRows + quad * 32);
           copy_to_peer(peer(f_at, 1), f_at, 128, bar);
         }
         __syncwarp();
       }
-      // ---------------- the rows' sums, to rank 1
-      st_peer(peer(smem_u32(s_l + r), 1), l);
-      st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
-      __syncwarp();
-      if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
-      if (p.splits > 1) {
-        const int k = excess(l);
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
-      } else if (used && p.lse) {
-        p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
+      // ---------------- both groups' sums, to rank 1
+      s_l[grp * kRows + r] = l;
+      s_l[(2 + grp) * kRows + r] = m;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (grp == 0) {
+        m = g.n > 0 ? s_m[((g.n - 1) & 1) * kRows + r] : kNegInf;
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float mk = s_l[(2 + k) * kRows + r];
+          const float f = mk == m ? 1.f : exp2_approx(0.5f * (mk - m));
+          if (mk != kNegInf) l += s_l[k * kRows + r] * f * f;
+        }
+        st_peer(peer(smem_u32(s_l + r), 1), l);
+        st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
+        __syncwarp();
+        if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
+        if (p.splits > 1) {
+          const int k = excess(l);
+          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
+          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
+        } else if (used && p.lse) {
+          p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
+        }
       }
     } else {
-      // ---------------- O: rescaled where m was raised, at the end written
+      // ---------------- O: rescaled where m was raised, at the end written; 256 columns a group
+      const uint32_t o = lanes + grp * kHalf;
       uint32_t seen = 0;  // P tiles that have come
       if (tid == 0)
         for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
@@ -519,27 +902,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       for (int i = 0; i < g.n; ++i) {
         const int slot = i & 1;
         const uint32_t parity = (i >> 1) & 1;
-        ok = mbar_wait_warp(&p_full[slot], parity, s_abort, err);
+        ok = wait_phase<false>(&p_full[slot], parity, s_abort, err);
         if (!ok) break;
         ++seen;
         const float f = s_f[slot * kRows + r];
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < kLatent; c += 32) {
+          for (int c = 0; c < kHalf; c += 32) {
             uint32_t v[32];
-            tmem_ld32(lanes + c, v);
+            tmem_ld32(o + c, v);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f * f);
-            tmem_st32(lanes + c, v);
+            tmem_st32(o + c, v);
           }
           tmem_wait_st();
           tc_fence_before();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&scaled[slot]);
-        ok = mbar_wait_warp(&pv_done[slot], parity, s_abort, err);
+        ok = wait_phase<false>(&pv_done[slot], parity, s_abort, err);
         if (!ok) break;
         if (tid == 0 && i + 2 < g.n) mbar_arrive_expect_tx(&p_full[slot], kPBytes);
         __syncwarp();
@@ -550,18 +933,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         for (uint32_t i = seen; i < min(seen + 2, static_cast<uint32_t>(g.n)); ++i)
           mbar_drain(&p_full[i & 1], (i >> 1) & 1);
       __syncwarp();
-      ok = __all_sync(0xffffffffu, wait_cluster(l_full, 0u, s_abort, err)) && ok;
+      ok = wait_phase<true>(l_full, 0u, s_abort, err) && ok;
       tc_fence_after();
       const float l = s_l[r];
       const bool none = s_l[kRows + r] == kNegInf;
       if (p.splits == 1) {
         const float inv = none ? 0.f : 1.f / l;
-        uint16_t* dst = p.out + out_row * kLatent;
+        uint16_t* dst = p.out + out_row * kLatent + grp * kHalf;
 #pragma unroll 1
-        for (int c = 0; c < kLatent; c += 32) {
+        for (int c = 0; c < kHalf; c += 32) {
           uint32_t v[32], pk[16];
           if (g.n > 0) {
-            tmem_ld32(lanes + c, v);
+            tmem_ld32(o + c, v);
             tmem_wait_ld();
           }
 #pragma unroll
@@ -578,11 +961,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       } else if (g.n > 0 && ok) {
         const float f = power(-excess(l));
         float4* dst =
-            reinterpret_cast<float4*>(p.part_o) + static_cast<int64_t>(item) * 128 * kRows + r;
+            reinterpret_cast<float4*>(p.part_o) + (static_cast<int64_t>(item) * 128 + grp * 64) * kRows + r;
 #pragma unroll 1
-        for (int c = 0; c < kLatent; c += 32) {
+        for (int c = 0; c < kHalf; c += 32) {
           uint32_t v[32];
-          tmem_ld32(lanes + c, v);
+          tmem_ld32(o + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -592,71 +975,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
       }
     }
+    setmaxnreg_dec<kRegLaunch>();
+    registers_back();
   } else if (warp < kMmaWarp) {
-    // ---------------- rows to bf16: one (key, chunk of 64 dims) a thread in each half of the dims
-    const int w = warp - kLoad0, key = (w & 1) * 32 + lane, c = w >> 1;
-    const TokenPlace tp = place_token(p.place, b);
-    auto row_of = [&](int i) -> int32_t {
-      const int32_t s = (g.lo + i) * kKeys + key;
-      if (i >= g.n || s >= g.end || (s >= g.len && !(g.seen >> (s - g.len) & 1))) return -1;
-      return static_cast<int32_t>(place_row(p.place, tp, s));
-    };
-    RowPart<kFormat> part[2];                  // reads in flight, of each half the next
-    int32_t row = row_of(0), next = row_of(1);  // of the tile that is read, and of the one after it
-    bool ok = true;
-    int st = 0;           // place in the ring
-    uint32_t parity = 1;  // of its part_empty
-    int rope = 0;         // i % 3
-    auto put = [&](int i, int h, const int32_t here, RowPart<kFormat>& x) {
-      ok = mbar_wait_warp(&part_empty[st], parity, s_abort, err);
-      if (!ok) return;
-      // A drafted row that some rows of the tile see and others do not may hold values that are not
-      // finite: cleared, since 0 * NaN would reach all of O, and its scores become NaN instead.
-      const int32_t left = g.len - (g.lo + i) * kKeys;
-      if (left < kKeys) {
-        const bool odd = key >= left && x.odd();
-        const uint32_t bits = __ballot_sync(0xffffffffu, odd);
-        if (odd) x.clear();
-        if (lane == 0) s_odd[16 * (i & 7) + 2 * (4 * h + c) + (w & 1)] = bits;
-      }
-      if (c == 0 && h == 0) {
-        const uint32_t bits = __ballot_sync(0xffffffffu, here >= 0);
-        if (lane == 0) s_there[2 * (i & 7) + (w & 1)] = bits;
-        if (kF16) s_scale[(i & 7) * kKeys + key] = __uint_as_float(x.scale);
-      }
-      if (rank == 0) {
-        x.store(smem0 + st * kPart + c * kChunk, key, kF16);
-        uint4 v = x.rope;
-        if constexpr (kF16) {  // divided by the scale
-          const uint32_t s2 = (254u - (x.scale >> 23)) * 0x00800080u;
-          v = make_uint4(ds4q::mul_bf16x2(v.x, s2), ds4q::mul_bf16x2(v.y, s2), ds4q::mul_bf16x2(v.z, s2),
-                         ds4q::mul_bf16x2(v.w, s2));
-        }
-        st_shared16(smem0 + kOffRope + rope * kChunk + key * 128 + (((4 * h + c) ^ key) & 7) * 16, v);
-      } else {
-        x.store(smem0 + st * kPart + c * kChunk, key, false);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&part_full[st]);
-      if (++st == kParts) st = 0, parity ^= 1u;
-    };
-    part[0].load(p, row, c, rank == 0);
-    part[1].load(p, row, 4 + c, rank == 0);
-#pragma unroll 1
-    for (int i = 0; i < g.n; ++i) {
-      const int32_t here = row;
-      row = next;
-      next = row_of(i + 2);
-      put(i, 0, here, part[0]);
-      if (!ok) break;
-      part[0].load(p, row, c, rank == 0);
-      put(i, 1, here, part[1]);
-      if (!ok) break;
-      part[1].load(p, row, 4 + c, rank == 0);
-      if (++rope == 3) rope = 0;
-    }
+    setmaxnreg_dec<kRegLoad>();
+    // ---------------- rows to operands
+    if (rank == 0)
+      load_rows<kFormat, true>(p, g, b, warp - kLoad0, lane, smem, part_full, part_empty, s_abort);
+    else
+      load_rows<kFormat, false>(p, g, b, warp - kLoad0, lane, smem, part_full, part_empty, s_abort);
+    registers_back();
+    setmaxnreg_inc<kRegLaunch>();
   } else {
+    setmaxnreg_dec<kRegMma>();
+    if (warp == kMmaWarp) {
       // ---------------- MMA issue: the warp waits together, one elected lane issues
       const bool lead = elect_one();
       bool ok = true;
@@ -666,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (lead) mma_commit(bar);
       };
       auto part_ready = [&] {
-        ok = ok && mbar_wait_warp(&part_full[st], parity, s_abort, err);
+        ok = ok && wait_phase<false>(&part_full[st], parity, s_abort, err);
         tc_fence_after();
       };
       auto part_taken = [&] {
@@ -677,12 +1009,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         const uint64_t k0 = smem_desc_sw128(smem0), r0 = smem_desc_sw128(smem0 + kOffRope);
         constexpr uint32_t rope_idesc = instr_desc(1u, 1u, kRows, kKeys);
         constexpr uint32_t idesc = kF16 ? instr_desc(0u, 0u, kRows, kKeys) : rope_idesc;
-        if (g.n > 0) ok = mbar_wait_warp(q_full, 0u, s_abort, err);
+        if (g.n > 0) ok = wait_phase<false>(q_full, 0u, s_abort, err);
         int slot = 0;
         uint32_t s_parity = 1;
 #pragma unroll 1
         for (int i = 0; ok && i < g.n; ++i) {
-          ok = mbar_wait_warp(&s_free[slot], s_parity, s_abort, err);
+          ok = wait_phase<false>(&s_free[slot], s_parity, s_abort, err);
           const uint32_t d = tmem + kColS + slot * kKeys;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -713,11 +1045,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll 1
         for (int i = 0; ok && i < g.n; ++i) {
           const int slot = i & 1;
-          ok = mbar_wait_warp(&p_full[slot], (i >> 1) & 1, s_abort, err);
+          ok = wait_phase<false>(&p_full[slot], (i >> 1) & 1, s_abort, err);
           if (!ok) break;
           const float4 f = reinterpret_cast<const float4*>(s_f + slot * kRows)[lane];
           if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f))
-            ok = mbar_wait_warp(&scaled[slot], (i >> 1) & 1, s_abort, err);
+            ok = wait_phase<false>(&scaled[slot], (i >> 1) & 1, s_abort, err);
           const uint64_t pd = p0 + slot * (kP >> 4);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -738,6 +1070,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       commit(done);
       if (lead) mbar_drain(done, 0u);
       __syncwarp();
+    }
+    registers_back();
+    setmaxnreg_inc<kRegLaunch>();
   }
   __syncwarp();
   tc_fence_before();
@@ -824,8 +1159,22 @@ bool sizes_ok(int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
 
 template <int kFormat>
 int launch(const Params& p, int64_t items, void* stream) {
-  static std::atomic<uint64_t> done{0};
+  static std::atomic<uint64_t> done{0}, regs_ok{0};
   if (!allow_shared(tree_attn_kernel<kFormat>, kSmem, done)) return DS4IDX_ERR_CUDA;
+  // The warpgroups' exchange of registers ends only at exactly kRegLaunch a thread: a build of another
+  // number is refused.
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DS4IDX_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(regs_ok.load(std::memory_order_relaxed) & bit)) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, tree_attn_kernel<kFormat>) != cudaSuccess ||
+        fa.numRegs != kRegLaunch) {
+      cudaGetLastError();
+      return DS4IDX_ERR_CUDA;
+    }
+    regs_ok.fetch_or(bit, std::memory_order_relaxed);
+  }
   return launch_dependent(tree_attn_kernel<kFormat>, static_cast<unsigned>(2 * items), kThreads, kSmem,
                           2, stream, p);
 }
