@@ -17,9 +17,10 @@
 // Both CTAs read the rows themselves and turn them into bf16 (exact) in a ring of parts, 64 keys x 256
 // dims in the 128-byte-swizzled layout that serves as K-major and as MN-major operand.
 //
-// Warps 0..7: softmax, a row a thread, warps 0..3 on even tiles and 4..7 on odd ones, m handed from tile
-// to tile (rank 1: the rescaling of O and the output). Warps 8..15: rows to operands. Warp 16 issues
-// tcgen05.mma.
+// Warps 0..3: softmax, a row a thread (rank 1: the rescaling of O and the output). Warps 4..11: rows to
+// operands. Warp 12 issues tcgen05.mma. The roles' loops are kept rolled: they run side by side out of one
+// instruction cache, and with everything unrolled (126 KB of code) more than half of its look-ups missed
+// and a tile took 7000 clocks.
 //
 // 8-bit rows are f16 in the key product: E4M3 to f16 is one conversion for two values, to bf16 five
 // instructions. The row's scale is applied to S, the rotary dims (bf16) are divided by it before, and Q is
@@ -50,12 +51,8 @@ constexpr int kDims = 576, kLatent = 512, kNodes = 64, kMaxHeads = 128;
 constexpr int kRows = 128;             // (node, head) rows of a tile = TMEM lanes
 constexpr int kKeys = 64;              // keys of a step
 constexpr int kHalf = 256;             // latent dims of a part
-constexpr int kLoad0 = 8, kLoaders = 8, kMmaWarp = 16;
-constexpr int kThreads = 20 * 32;
-// Registers a thread: at launch, and as the warpgroups then share them (two of softmax, two of loading,
-// the MMA warp's).
-constexpr int kRegLaunch = 96, kRegSoftmax = 136, kRegLoad = 80, kRegMma = 40;
-static_assert(256 * (kRegSoftmax + kRegLoad) + 128 * kRegMma <= kThreads * kRegLaunch, "registers");
+constexpr int kLoad0 = 4, kLoaders = 8, kMmaWarp = 12;
+constexpr int kThreads = 13 * 32;
 constexpr int kChunk = kKeys * 128;    // 64 dims of a tile's keys
 constexpr int kPart = 4 * kChunk, kParts = 3;
 constexpr int kRaw = kKeys * 256, kRaws = 4;       // codes of a part as they are read
@@ -63,13 +60,12 @@ constexpr int kOffRaw = kParts * kPart;
 constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of three tiles' keys (rank 0)
 constexpr int kOffP = kOffRope + 3 * kChunk, kP = kRows * kKeys * 2;  // P of two tiles
 constexpr int kOffF = kOffP + 2 * kP;              // float [2][128]: factors of O before P V
-constexpr int kOffM = kOffF + 2 * kRows * 4;       // float [2][128]: m after an even, an odd tile
-constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
-constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit rows)
+constexpr int kOffL = kOffF + 2 * kRows * 4;       // float [2][128]: l, m (rank 1)
+constexpr int kOffScale = kOffL + 2 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit rows)
 constexpr int kOffThere = kOffScale + 8 * kKeys * 4;  // uint64 [8 tiles]: keys that are there
 constexpr int kOffOdd = kOffThere + 8 * 8;         // uint64 [8 tiles][2 halves]: keys not finite
 constexpr int kOffBars = kOffOdd + 8 * 16;
-constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 8 + 2;
+constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 2;
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
@@ -215,14 +211,6 @@ __device__ __forceinline__ uint4 ld_row16(const uint8_t* p, int32_t r) {
       : "l"(p), "r"(r));
   return v;
 }
-__device__ __forceinline__ uint32_t ld_row2(const void* p, int32_t r) {
-  uint16_t v = 0;
-  asm volatile(
-      "{\n\t.reg .pred there;\n\tsetp.ge.s32 there, %2, 0;\n\t@there ld.global.b16 %0, [%1];\n\t}"
-      : "+h"(v)
-      : "l"(p), "r"(r));
-  return v;
-}
 // 16 (4) bytes of row r at src to shared memory, zeros where there is no row.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src, int32_t r) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r >= 0 ? 16 : 0)
@@ -339,24 +327,21 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   auto there_bits = [&] { return quad_bits(row[0] >= 0) | quad_bits(row[1] >= 0) << 4; };
 
   if constexpr (kFormat == DS4IDX_CACHE_FP8) {
-    // access k of a half: rows sub and 4 + sub (k & 1), 128 codes (k >> 1), 16 codes a lane
-    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw part, + 512 k
-    const uint32_t scales = smem0 + kOffScale;
-    auto copy = [&](int h) {
+    // a part: two lines of 128 codes (c) of rows sub and 4 + sub (k), 16 codes a lane
+    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw part, + 1024 c + 512 k
+    const uint8_t* from[2];
+    auto start = [&] {  // the rows' addresses and scales, for the tile that is read next
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int32_t r = row[k & 1];
-        cp_async16(raw0 + (2 * (read & 1) + h) * kRaw + 512 * k,
-                   row_at(max(r, 0)) + (2 * h + (k >> 1)) * 128 + l8 * 16, r);
+      for (int k = 0; k < 2; ++k) from[k] = row_at(max(row[k], 0)) + l8 * 16;
+      if (l8 < 2) {
+        const int32_t r = l8 ? row[1] : row[0];
+        cp_async4(smem0 + kOffScale + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4, p.scale + max(r, 0),
+                  r);
       }
-      if (h == 0) {
-        if (l8 < 2) {
-          const int32_t r = l8 ? row[1] : row[0];
-          cp_async4(scales + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4, p.scale + max(r, 0), r);
-        }
-        there |= there_bits() << (8 * (read & 1));
-      }
-      cp_async_commit();
+      there |= there_bits() << (8 * (read & 1));
+    };
+    auto copy = [&](int h, int c, int k) {
+      cp_async16(raw0 + (2 * (read & 1) + h) * kRaw + 1024 * c + 512 * k, from[k] + (2 * h + c) * 128, row[k]);
     };
     uint4 rope[2];
     int32_t late[2] = {row[0], row[1]};  // rows of the tile before the one that is copied
@@ -365,66 +350,75 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       for (int k = 0; k < 2; ++k)
         rope[k] = ld_row16(row_at(late[k]) + ds4f8::kOffRope + l8 * 16, late[k]);
     };
-    copy(0);
-    copy(1);
     if (kKey) load_rope();
-    advance_rows();
-    late[0] = row[0];
-    late[1] = row[1];
-    copy(0);
-    copy(1);
-    advance_rows();
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j) {
+      late[0] = row[0];
+      late[1] = row[1];
+      start();
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) copy(h, c, 0), copy(h, c, 1);
+        cp_async_commit();
+      }
+      advance_rows();
+    }
 #pragma unroll 1
     for (int i = 0; i < g.n; ++i) {
-#pragma unroll
+      const float* sc_at = reinterpret_cast<const float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
+      const uint32_t here = there >> (8 * (i & 1)) & 0xFFu;
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         cp_async_wait<3>();
         __syncwarp();
         claim();
         if (!ok) break;
-        uint4 x[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = ld_shared16(raw0 + (2 * (i & 1) + h) * kRaw + 512 * k);
-        const float* sc_at = reinterpret_cast<const float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
         float sc[2] = {sc_at[sub], sc_at[4 + sub]};
-        if (drafts(i)) {
-          uint32_t odd_keys = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int key = (k & 1) * 4 + sub;
-            const bool bad = (__float_as_uint(sc[k & 1]) & 0x7F800000u) == 0x7F800000u;
-            const bool odd = drafted(i, key) && (bad || odd_f8(x[k]));
-            if (odd) x[k] = zero;
-            odd_keys |= quad_bits(odd) << (4 * (k & 1));
-            if (k >= 2 && bad && drafted(i, key)) sc[k & 1] = 0.f;
-          }
-          note_odd(i, h, odd_keys);
+        if (h == 0) {
+          note_there(i, here);
+          there &= ~(0xFFu << (8 * (i & 1)));
+          start();
         }
-        if (h == 0) note_there(i, there >> (8 * (i & 1)) & 0xFFu);
-        const bool swap = l8 >= 4;  // the lanes of the second chunk write their two pieces in turn
+        const bool check = drafts(i);
+        uint32_t odd_keys = 0;
+        const uint32_t raw = raw0 + (2 * (i & 1) + h) * kRaw;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t chunk = smem0 + st * kPart + (2 * c + (l8 >> 2)) * kChunk + 8 * w * 128;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = (k & 1) * 4 + sub;
-          uint4 c = x[k];
-          swap_if(swap, c.x, c.z);
-          swap_if(swap, c.y, c.w);
-          const uint32_t at = smem0 + st * kPart + ((k >> 1) * 2 + (l8 >> 2)) * kChunk +
-                              (8 * w + key) * 128 + ((((l8 & 3) * 2 + (l8 >> 2)) ^ key) * 16);
-          uint4 v, u;
-          if constexpr (kF16) {
-            ds4f8::codes_to_f16(c.x, v.x, v.y);
-            ds4f8::codes_to_f16(c.y, v.z, v.w);
-            ds4f8::codes_to_f16(c.z, u.x, u.y);
-            ds4f8::codes_to_f16(c.w, u.z, u.w);
-          } else {
-            codes_to_bf16(c.x, sc[k & 1], v.x, v.y);
-            codes_to_bf16(c.y, sc[k & 1], v.z, v.w);
-            codes_to_bf16(c.z, sc[k & 1], u.x, u.y);
-            codes_to_bf16(c.w, sc[k & 1], u.z, u.w);
+          for (int k = 0; k < 2; ++k) {
+            const int key = 4 * k + sub;
+            uint4 x = ld_shared16(raw + 1024 * c + 512 * k);
+            float scale = sc[k];
+            if (check) {
+              const bool bad = (__float_as_uint(scale) & 0x7F800000u) == 0x7F800000u;
+              const bool odd = drafted(i, key) && (bad || odd_f8(x));
+              if (odd) x = zero, scale = 0.f;
+              odd_keys |= quad_bits(odd) << (4 * k);
+            }
+            swap_if(l8 >= 4, x.x, x.z);  // the lanes of the second chunk write their two pieces in turn
+            swap_if(l8 >= 4, x.y, x.w);
+            const uint32_t at = chunk + key * 128 + ((((l8 & 3) * 2 + (l8 >> 2)) ^ key) * 16);
+            uint4 v, u;
+            if constexpr (kF16) {
+              ds4f8::codes_to_f16(x.x, v.x, v.y);
+              ds4f8::codes_to_f16(x.y, v.z, v.w);
+              ds4f8::codes_to_f16(x.z, u.x, u.y);
+              ds4f8::codes_to_f16(x.w, u.z, u.w);
+            } else {
+              codes_to_bf16(x.x, scale, v.x, v.y);
+              codes_to_bf16(x.y, scale, v.z, v.w);
+              codes_to_bf16(x.z, scale, u.x, u.y);
+              codes_to_bf16(x.w, scale, u.z, u.w);
+            }
+            st_shared16(at, v);
+            st_shared16(at ^ 16, u);
+            copy(h, c, k);
           }
-          st_shared16(at, v);
-          st_shared16(at ^ 16, u);
         }
+        cp_async_commit();
+        if (check) note_odd(i, h, odd_keys);
         if (kKey && h == 1) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {  // divided by the scale
@@ -439,11 +433,9 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         }
         publish(st);
         step();
-        if (h == 0) there &= ~(0xFFu << (8 * (i & 1)));
-        copy(h);
-        if (h == 1) advance_rows();
       }
       if (!ok) break;
+      advance_rows();
       if (++rope_slot == 3) rope_slot = 0;
     }
     cp_async_wait<0>();
@@ -458,10 +450,10 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         if (!ok) break;
         const bool check = drafts(i);
         uint32_t odd_keys = 0;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k) {  // rows sub and 4 + sub, a chunk of 64 dims (k >> 1)
           const int key = (k & 1) * 4 + sub;
-          const int32_t r = row[k & 1];
+          const int32_t r = k & 1 ? row[1] : row[0];
           const uint32_t at =
               smem0 + st * kPart + (k >> 1) * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
           const uint8_t* src = row_at(max(r, 0)) + h * 2 * kHalf + (k >> 1) * 128 + l8 * 16;
@@ -495,17 +487,25 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   } else {
     // access k: rows 2 k and 2 k + 1, 32 codes a lane: two of the four scales of a chunk
     const int l16 = lane & 15, hi = lane >> 4, x = l16 >> 1 & 3;
-    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw tile, + 512 k
+    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;            // + raw tile, + 512 k
+    const uint32_t raw_scale = smem0 + kOffRaw + 3 * kRaw + w * 256;         // + 2048 raw tile
     uint4 rope[2];
-    uint32_t sc[2][4];
-    int32_t late[2] = {row[0], row[1]};
-    auto copy = [&](uint32_t(&scale)[4]) {
-#pragma unroll
+    int32_t late[2] = {row[0], row[1]};  // rows of the tile before the one that is copied
+    // Row of key j (the same in all lanes of a group of eight that holds it).
+    auto row_of_key = [&](int j) {
+      const int32_t a = __shfl_sync(0xffffffffu, row[0], 8 * (j & 3)), c = __shfl_sync(0xffffffffu, row[1], 8 * (j & 3));
+      return j < 4 ? a : c;
+    };
+    auto copy = [&] {
+      const int slot = read % 3;
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        const int32_t r = __shfl_sync(0xffffffffu, row[k >> 1], 8 * (2 * (k & 1) + hi));
-        cp_async16(raw0 + (read % 3) * kRaw + 512 * k, row_at(max(r, 0)) + l16 * 16, r);
-        scale[k] = ld_row2(row_at(r) + ds4q::kOffScale + 2 * l16, r);
+        const int32_t r = row_of_key(2 * k + hi);
+        cp_async16(raw0 + slot * kRaw + 512 * k, row_at(max(r, 0)) + l16 * 16, r);
       }
+      const int32_t r = row_of_key(l16 >> 1);
+      if (lane < 16)
+        cp_async16(raw_scale + slot * 2048 + lane * 16, row_at(max(r, 0)) + ds4q::kOffScale + (lane & 1) * 16, r);
       there |= there_bits() << (8 * (read & 1));
       cp_async_commit();
     };
@@ -514,38 +514,49 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       for (int k = 0; k < 2; ++k)
         rope[k] = ld_row16(row_at(late[k]) + ds4q::kOffRope + l8 * 16, late[k]);
     };
-    auto tile = [&](int i, uint32_t(&scale)[4]) {
+    if (kKey) load_rope();
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j) {
+      late[0] = row[0];
+      late[1] = row[1];
+      copy();
+      advance_rows();
+    }
+#pragma unroll 1
+    for (int i = 0; i < g.n; ++i) {
       cp_async_wait<1>();
+      __syncwarp();
       const int first = st;
       claim();
       step();
       const int second = st;
       claim();
       step();
-      if (!ok) return;
+      if (!ok) break;
       note_there(i, there >> (8 * (i & 1)) & 0xFFu);
       there &= ~(0xFFu << (8 * (i & 1)));
       if (drafts(i)) note_odd(i, 0, 0), note_odd(i, 1, 0);  // (the format has only finite values)
-#pragma unroll
+      const uint32_t raw = raw0 + i % 3 * kRaw;
+      const uint8_t* scales = smem + kOffRaw + 3 * kRaw + w * 256 + i % 3 * 2048;
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const int key = 2 * k + hi;
-        uint4 c = ld_shared16(raw0 + (i % 3) * kRaw + 512 * k);
+        uint4 c = ld_shared16(raw + 512 * k);
+        uint32_t s = *reinterpret_cast<const uint16_t*>(scales + key * 32 + l16 * 2);
         // piece j ^ x at step j: the lanes of the other chunks write other banks
         swap_if(x & 1, c.x, c.y);
         swap_if(x & 1, c.z, c.w);
         swap_if(x & 2, c.x, c.z);
         swap_if(x & 2, c.y, c.w);
-        const uint32_t s = x & 2 ? __byte_perm(scale[k], 0, 0x4401) : scale[k];
+        s = x & 2 ? __byte_perm(s, 0, 0x4401) : s;
         const uint32_t at = smem0 + (l16 < 8 ? first : second) * kPart + x * kChunk + (8 * w + key) * 128 +
                             ((((l16 & 1) * 4 + x) ^ key) * 16);
         const uint32_t words[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          // (a row that is not there: codes and scales of zeros, -8 * 2^-20, finite and not seen)
           const uint32_t s2 = __byte_perm(s, 0, j < 2 ? 0x4040u : 0x4141u) * 16u + 0x35803580u;
-          uint4 v = ds4q::word_to_bf16(words[j], s2, ds4q::offset_bf16x2(s2));
-          // (the zeros of a row that is not there are -8 times the least scale, and are not seen; as a
-          // value they must be finite, which they are)
-          st_shared16(at ^ (16 * j), v);
+          st_shared16(at ^ (16 * j), ds4q::word_to_bf16(words[j], s2, ds4q::offset_bf16x2(s2)));
         }
       }
       if (kKey) {
@@ -557,21 +568,9 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       }
       publish(first);
       publish(second);
-      copy(scale);
+      copy();
       advance_rows();
       if (++rope_slot == 3) rope_slot = 0;
-    };
-    copy(sc[0]);
-    if (kKey) load_rope();
-    advance_rows();
-    late[0] = row[0];
-    late[1] = row[1];
-    copy(sc[1]);
-    advance_rows();
-#pragma unroll 1
-    for (int i = 0; i < g.n && ok; i += 2) {
-      tile(i, sc[0]);
-      if (ok && i + 1 < g.n) tile(i + 1, sc[1]);
     }
     cp_async_wait<0>();
   }
@@ -617,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t smem0 = smem_u32(smem);
   float* s_f = reinterpret_cast<float*>(smem + kOffF);
-  float* s_m = reinterpret_cast<float*>(smem + kOffM);
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
   volatile uint64_t* s_there = reinterpret_cast<uint64_t*>(smem + kOffThere);
   volatile uint64_t* s_odd = reinterpret_cast<uint64_t*>(smem + kOffOdd);
@@ -630,8 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint64_t* p_full = p_free + 2;    // [2] P has come (in rank 1)
   uint64_t* scaled = p_full + 2;    // [2] O is ready for P V
   uint64_t* pv_done = scaled + 2;   // [2] P V of a tile is done
-  uint64_t* m_full = pv_done + 2;   // [8] a softmax warp's m is in s_m
-  uint64_t* l_full = m_full + 8;    // the rows' sums have come (in rank 1)
+  uint64_t* l_full = pv_done + 2;   // the rows' sums have come (in rank 1)
   uint64_t* done = l_full + 1;      // every MMA has completed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
@@ -646,18 +643,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mbar_init(&part_full[i], kLoaders);
       mbar_init(&part_empty[i], 1);
     }
-    mbar_init(q_full, 8);
+    mbar_init(q_full, 4);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&s_ready[i], 1);
       mbar_init(&s_free[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_free[i], 8);
+      mbar_init(&p_free[i], 4);
       mbar_init(&p_full[i], 1);
-      mbar_init(&scaled[i], 8);
+      mbar_init(&scaled[i], 4);
       mbar_init(&pv_done[i], 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&m_full[i], 1);
     mbar_init(l_full, 4);
     mbar_init(done, 1);
     *s_abort = 0u;
@@ -677,27 +673,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const uint32_t tmem = *s_tmem;
   constexpr bool kF16 = kFormat == DS4IDX_CACHE_FP8;  // the key product's type
 
-  // Between the softmax warps' giving their registers back and the others' taking them: a warp of the
-  // MMA warpgroup that has nothing to do would else take its back first, and the softmax warps wait for
-  // registers that come free only when they are done.
-  auto registers_back = [] { asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory"); };
-
   if (warp < kLoad0) {
-    setmaxnreg_inc<kRegSoftmax>();
-    const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int r = tid;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int row = tile * kRows + r, node = row / p.H;
     const bool used = node < p.N;
     const int64_t out_row = static_cast<int64_t>(b) * p.N * p.H + row;
     bool ok = true;
     if (rank == 0) {
-      // ---------------- softmax: this thread's row, the tiles of its group's parity
+      // ---------------- softmax: this thread's row
       uint64_t mask = used ? static_cast<uint64_t>(p.mask[static_cast<int64_t>(b) * p.N + node]) : 0ull;
       const bool padding = mask == 0ull;
       mask &= ~0ull >> (64 - p.N);
       float to_log2 = p.scale_log2;  // of a score, from S
       if (g.n > 0) {
-        // Q to TMEM, a half of the latent dims and of the rotary ones by each group
+        // Q to TMEM
         const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * kDims);
         const uint4 zero = make_uint4(0, 0, 0, 0);
         float f = 1.f;
@@ -718,11 +708,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
         }
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < 9; ++h) {  // the rotary dims last
           uint32_t v[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint4 x = used ? src[grp * 32 + 8 * h + j] : zero;
+            const uint4 x = used ? src[8 * h + j] : zero;
             v[4 * j] = x.x;
             v[4 * j + 1] = x.y;
             v[4 * j + 2] = x.z;
@@ -730,171 +720,134 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
           if constexpr (kF16) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = bf16x2_to_f16x2(v[j], f);
+            for (int j = 0; j < 32; ++j)
+              v[j] = h < 8 ? bf16x2_to_f16x2(v[j], f) : ds4q::mul_bf16x2(v[j], f2);
           }
-          tmem_st32(lanes + grp * 128 + h * 32, v);
+          tmem_st32(lanes + h * 32, v);
         }
-        uint32_t v[16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 x = used ? src[64 + grp * 4 + j] : zero;
-          v[4 * j] = x.x;
-          v[4 * j + 1] = x.y;
-          v[4 * j + 2] = x.z;
-          v[4 * j + 3] = x.w;
-        }
-        if constexpr (kF16) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
-        }
-        tmem_st16(lanes + kColRope + grp * 16, v);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
       float m = kNegInf, l = 0.f;
-      const uint32_t rows_at = quad * 32 * 128;  // this warp's rows of P
-      const uint32_t p_at = smem0 + kOffP + grp * kP + r * 128 + (r & 7) * 16;
+      const uint32_t rows_at = warp * 32 * 128;  // this warp's rows of P
+      int slot = 0;                              // i % 3
+      uint32_t s_parity = 0;
 #pragma unroll 1
-      for (int i = grp; i < g.n; i += 2) {
-        const uint32_t use = i >> 1;
-        const int slot = i % 3, at = i & 7;
-        ok = wait_phase<false>(&s_ready[slot], (i / 3) & 1, s_abort, err);
+      for (int i = 0; i < g.n; ++i) {
+        const int ps = i & 1, at = i & 7;
+        ok = wait_phase<false>(&s_ready[slot], s_parity, s_abort, err) &&
+             wait_phase<true>(&p_free[ps], (i >> 1 & 1) ^ 1u, s_abort, err);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[kKeys];  // fp32 bits
-        tmem_ld32(lanes + kColS + slot * kKeys, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-        tmem_ld32(lanes + kColS + slot * kKeys + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-        uint64_t see = s_there[at];
-        tmem_wait_ld();
-        if constexpr (kF16) {
-          const uint32_t sc = smem0 + kOffScale + at * kKeys * 4;
-#pragma unroll
-          for (int j = 0; j < kKeys; j += 4) {
-            const uint4 x = ld_shared16(sc + 4 * j);
-            mul_pair(s[j], s[j + 1], x.x, x.y);
-            mul_pair(s[j + 2], s[j + 3], x.z, x.w);
-          }
-        }
         // which keys this row sees
         const int32_t left = g.len - g.position(i);  // rows of the sequence from this tile on
-        if (padding) see = 0ull;
+        uint64_t see = padding ? 0ull : s_there[at], bad = 0ull;
         if (left < kKeys) {
-          if (!padding)
-            see &= left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
-          const uint64_t bad = s_odd[2 * at] | s_odd[2 * at + 1];
-          if (bad) {
+          see &= left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
+          bad = s_odd[2 * at] | s_odd[2 * at + 1];
+        }
+        const bool plain = __all_sync(0xffffffffu, see == ~0ull && bad == 0ull);
+        // P with the m so far, in the layout of an MMA A operand; once more where that has to be raised
+        const uint32_t p_at = smem0 + kOffP + ps * kP + r * 128 + (r & 7) * 16;
+        float f = 1.f, sum;
+        for (int pass = 0;; ++pass) {  // (at most twice: then m holds the tile's largest score)
+          const float off = m == kNegInf ? 0.f : -m;
+          const uint64_t off2 = pack_f32x2(off, off), scale2 = pack_f32x2(to_log2, to_log2);
+          uint64_t sum2 = 0ull;
+          float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[32];  // fp32 bits
+            tmem_ld32(lanes + kColS + slot * kKeys + 32 * h, s);
+            tmem_wait_ld();
+            if constexpr (kF16) {
+              const uint32_t sc = smem0 + kOffScale + (at * kKeys + 32 * h) * 4;
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j)
-              if (bad >> j & 1) s[j] = 0x7FC00000u;
+              for (int j = 0; j < 32; j += 4) {
+                const uint4 x = ld_shared16(sc + 4 * j);
+                mul_pair(s[j], s[j + 1], x.x, x.y);
+                mul_pair(s[j + 2], s[j + 3], x.z, x.w);
+              }
+            }
+            if (!plain) {  // a masked score is -infinity: p = 0 whatever m, and no maximum
+              const uint32_t on = static_cast<uint32_t>(see >> (32 * h));
+              const uint32_t nan = static_cast<uint32_t>(bad >> (32 * h));
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                s[j] = on >> j & 1 ? (nan >> j & 1 ? 0x7FC00000u : s[j]) : 0xFF800000u;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mx[j / 2 & 3] = fmaxf(fmaxf(mx[j / 2 & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int k = 8 * u + 2 * j;
+                float x0, x1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                       scale2, off2),
+                             x0, x1);
+                x0 = exp2_approx(x0);
+                x1 = exp2_approx(x1);
+                sum2 = add_f32x2(sum2, pack_f32x2(x0, x1));
+                pk[j] = pack_bf16x2(x0, x1);
+              }
+              st_shared16(p_at ^ (16 * (4 * h + u)), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+            }
+          }
+          float l0, l1;
+          unpack_f32x2(sum2, l0, l1);
+          sum = l0 + l1;
+          // m is raised where a score passes it by more than the slack. Finite once a key was seen: a score
+          // of +-infinity keeps its meaning in s - m.
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * to_log2;
+          const float now = fminf(fmaxf(top, -kMax), kMax);
+          const bool raise = see != 0ull && (m == kNegInf || now > m + kSlack);
+          if (pass == 1 || !__any_sync(0xffffffffu, raise)) break;
+          if (raise) {
+            if (m != kNegInf) {
+              // the root of the factor: what is 2^64 above the old m may matter 2^-126 above the new one,
+              // where 2^(m - now) is long zero
+              f = exp2_approx(0.5f * (m - now));
+              l = l * f * f;
+            }
+            m = now;
           }
         }
+        l += sum;
+        s_f[ps * kRows + r] = f;
+        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[slot]);
-        const bool all = __all_sync(0xffffffffu, see == ~0ull);
-        if (!all) {  // a masked score is -infinity: p = 0 whatever m, and no maximum
-          const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            s[j] = lo >> j & 1 ? s[j] : 0xFF800000u;
-            s[32 + j] = hi >> j & 1 ? s[32 + j] : 0xFF800000u;
-          }
-        }
-        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-        for (int j = 0; j < kKeys; j += 2)
-          mx[j / 2 & 3] = fmaxf(fmaxf(mx[j / 2 & 3], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * to_log2;
-        // m of the tile before; raised where a score passes it by more than the slack. Finite once a key
-        // was seen: a score of +-infinity keeps its meaning in s - m.
-        float before = kNegInf;
-        if (i > 0) {
-          ok = wait_phase<false>(&m_full[warp ^ 4], ((i - 1) >> 1) & 1, s_abort, err);
-          if (!ok) break;
-          before = s_m[(grp ^ 1) * kRows + r];
-        }
-        float now = before;
-        if (see != 0ull && (before == kNegInf || top > before + kSlack))
-          now = fminf(fmaxf(top, -kMax), kMax);
-        s_m[grp * kRows + r] = now;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m_full[warp]);
-        if (now != m) {
-          const float f = exp2_approx(0.5f * (m - now));
-          l = l * f * f;
-          m = now;
-        }
-        ok = wait_phase<true>(&p_free[grp], (use & 1) ^ 1u, s_abort, err);
-        if (!ok) break;
-        // The root of the factor of the O before: what is 2^64 above the old m may matter 2^-126 above the
-        // new one, where 2^(before - now) is long zero.
-        s_f[grp * kRows + r] =
-            now != before && before != kNegInf ? exp2_approx(0.5f * (before - now)) : 1.f;
-        // P, in the layout of an MMA A operand
-        const float off = m == kNegInf ? 0.f : -m;  // (a row that has seen nothing: p = 0)
-        const uint64_t off2 = pack_f32x2(off, off), scale2 = pack_f32x2(to_log2, to_log2);
-        uint64_t sum = 0ull;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = 8 * u + 2 * j;
-            float x0, x1;
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2,
-                                   off2),
-                         x0, x1);
-            x0 = exp2_approx(x0);
-            x1 = exp2_approx(x1);
-            sum = add_f32x2(sum, pack_f32x2(x0, x1));
-            pk[j] = pack_bf16x2(x0, x1);
-          }
-          st_shared16(p_at ^ (16 * u), make_uint4(pk[0], pk[1], pk[2], pk[3]));
-        }
-        float l0, l1;
-        unpack_f32x2(sum, l0, l1);
-        l += l0 + l1;
-        fence_proxy_async_smem();
-        __syncwarp();
         if (lane == 0) {
-          const uint32_t bar = peer(smem_u32(&p_full[grp]), 1);
-          const uint32_t from = smem0 + kOffP + grp * kP + rows_at;
+          mbar_arrive(&s_free[slot]);
+          const uint32_t bar = peer(smem_u32(&p_full[ps]), 1);
+          const uint32_t from = smem0 + kOffP + ps * kP + rows_at;
           copy_to_peer(peer(from, 1), from, 32 * 128, bar);
-          const uint32_t f_at = smem_u32(s_f + grp * kRows + quad * 32);
+          const uint32_t f_at = smem_u32(s_f + ps * kRows + warp * 32);
           copy_to_peer(peer(f_at, 1), f_at, 128, bar);
         }
         __syncwarp();
+        if (++slot == 3) slot = 0, s_parity ^= 1u;
       }
-      // ---------------- both groups' sums, to rank 1
-      s_l[grp * kRows + r] = l;
-      s_l[(2 + grp) * kRows + r] = m;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (grp == 0) {
-        m = g.n > 0 ? s_m[((g.n - 1) & 1) * kRows + r] : kNegInf;
-        l = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float mk = s_l[(2 + k) * kRows + r];
-          const float f = mk == m ? 1.f : exp2_approx(0.5f * (mk - m));
-          if (mk != kNegInf) l += s_l[k * kRows + r] * f * f;
-        }
-        st_peer(peer(smem_u32(s_l + r), 1), l);
-        st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
-        __syncwarp();
-        if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
-        if (p.splits > 1) {
-          const int k = excess(l);
-          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
-          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
-        } else if (used && p.lse) {
-          p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
-        }
+      // ---------------- the rows' sums, to rank 1
+      st_peer(peer(smem_u32(s_l + r), 1), l);
+      st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
+      __syncwarp();
+      if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
+      if (p.splits > 1) {
+        const int k = excess(l);
+        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
+        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
+      } else if (used && p.lse) {
+        p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
       }
     } else {
-      // ---------------- O: rescaled where m was raised, at the end written; 256 columns a group
-      const uint32_t o = lanes + grp * kHalf;
+      // ---------------- O: rescaled where m was raised, at the end written
       uint32_t seen = 0;  // P tiles that have come
       if (tid == 0)
         for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
@@ -909,13 +862,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < kHalf; c += 32) {
+          for (int c = 0; c < kLatent; c += 32) {
             uint32_t v[32];
-            tmem_ld32(o + c, v);
+            tmem_ld32(lanes + c, v);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f * f);
-            tmem_st32(o + c, v);
+            tmem_st32(lanes + c, v);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -939,12 +892,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const bool none = s_l[kRows + r] == kNegInf;
       if (p.splits == 1) {
         const float inv = none ? 0.f : 1.f / l;
-        uint16_t* dst = p.out + out_row * kLatent + grp * kHalf;
+        uint16_t* dst = p.out + out_row * kLatent;
 #pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
+        for (int c = 0; c < kLatent; c += 32) {
           uint32_t v[32], pk[16];
           if (g.n > 0) {
-            tmem_ld32(o + c, v);
+            tmem_ld32(lanes + c, v);
             tmem_wait_ld();
           }
 #pragma unroll
@@ -961,11 +914,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       } else if (g.n > 0 && ok) {
         const float f = power(-excess(l));
         float4* dst =
-            reinterpret_cast<float4*>(p.part_o) + (static_cast<int64_t>(item) * 128 + grp * 64) * kRows + r;
+            reinterpret_cast<float4*>(p.part_o) + static_cast<int64_t>(item) * 128 * kRows + r;
 #pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
+        for (int c = 0; c < kLatent; c += 32) {
           uint32_t v[32];
-          tmem_ld32(o + c, v);
+          tmem_ld32(lanes + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -975,20 +928,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
       }
     }
-    setmaxnreg_dec<kRegLaunch>();
-    registers_back();
   } else if (warp < kMmaWarp) {
-    setmaxnreg_dec<kRegLoad>();
     // ---------------- rows to operands
     if (rank == 0)
       load_rows<kFormat, true>(p, g, b, warp - kLoad0, lane, smem, part_full, part_empty, s_abort);
     else
       load_rows<kFormat, false>(p, g, b, warp - kLoad0, lane, smem, part_full, part_empty, s_abort);
-    registers_back();
-    setmaxnreg_inc<kRegLaunch>();
   } else {
-    setmaxnreg_dec<kRegMma>();
-    if (warp == kMmaWarp) {
       // ---------------- MMA issue: the warp waits together, one elected lane issues
       const bool lead = elect_one();
       bool ok = true;
@@ -1022,10 +968,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             if (!ok) break;
             const uint64_t kd = k0 + st * (kPart >> 4);
             if (lead) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
 #pragma unroll
-              for (int k = 0; k < kHalf / 16; ++k)
-                mma_bf16_ts(d, tmem + h * 128 + k * 8, kd + (k >> 2) * (kChunk >> 4) + (k & 3) * 2, idesc,
-                            (h | k) ? 1u : 0u);
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16_ts(d, tmem + h * 128 + c * 32 + k * 8, kd + c * (kChunk >> 4) + k * 2, idesc,
+                              (h | c | k) ? 1u : 0u);
+              }
             }
             if (h == 1 && lead) {
               const uint64_t rd = r0 + slot * (kChunk >> 4);  // (i % 3 = slot)
@@ -1070,9 +1019,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       commit(done);
       if (lead) mbar_drain(done, 0u);
       __syncwarp();
-    }
-    registers_back();
-    setmaxnreg_inc<kRegLaunch>();
   }
   __syncwarp();
   tc_fence_before();
@@ -1159,22 +1105,8 @@ bool sizes_ok(int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
 
 template <int kFormat>
 int launch(const Params& p, int64_t items, void* stream) {
-  static std::atomic<uint64_t> done{0}, regs_ok{0};
+  static std::atomic<uint64_t> done{0};
   if (!allow_shared(tree_attn_kernel<kFormat>, kSmem, done)) return DS4IDX_ERR_CUDA;
-  // The warpgroups' exchange of registers ends only at exactly kRegLaunch a thread: a build of another
-  // number is refused.
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DS4IDX_ERR_CUDA;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(regs_ok.load(std::memory_order_relaxed) & bit)) {
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, tree_attn_kernel<kFormat>) != cudaSuccess ||
-        fa.numRegs != kRegLaunch) {
-      cudaGetLastError();
-      return DS4IDX_ERR_CUDA;
-    }
-    regs_ok.fetch_or(bit, std::memory_order_relaxed);
-  }
   return launch_dependent(tree_attn_kernel<kFormat>, static_cast<unsigned>(2 * items), kThreads, kSmem,
                           2, stream, p);
 }
