@@ -22,10 +22,10 @@
 // instruction cache, and with everything unrolled (126 KB of code) more than half of its look-ups missed
 // and a tile took 7000 clocks.
 //
-// 8-bit rows are f16 in the key product: E4M3 to f16 is one conversion for two values, to bf16 five
-// instructions. The row's scale is applied to S, the rotary dims (bf16) are divided by it before, and Q is
-// scaled by a power of two to f16's range: all exact, but for what of a row of Q lies 2^38 below its largest
-// value. As values they are bf16 (P times the scales would leave f16's range).
+// 8-bit rows are operands without their scales, which are powers of two: S is multiplied by them, and so is
+// P, exactly. As keys the codes are f16, one conversion for two of them; the rotary dims (bf16) are divided
+// by the scale before, and Q is scaled by a power of two to f16's range: exact too, but for what of a row of
+// Q lies 2^38 below its largest value. As values the codes are bf16 (P needs bf16's range).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -233,14 +233,14 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Four E4M3 codes times their scale to bf16 (exact), by way of f16 and fp32: the conversions and products
-// run on other pipes than shifting the bits into place would (32768 codes in 850 clocks, 1110 that way).
-__device__ __forceinline__ void codes_to_bf16(uint32_t c, float scale, uint32_t& lo, uint32_t& hi) {
+// Four E4M3 codes to bf16 (exact), by way of f16 and fp32: the conversions run on more pipes than
+// shifting the bits into place would.
+__device__ __forceinline__ void codes_to_bf16(uint32_t c, uint32_t& lo, uint32_t& hi) {
   uint32_t a, b;
   ds4f8::codes_to_f16(c, a, b);
   const float2 u = ds4f8::f16x2_to_f32(a), v = ds4f8::f16x2_to_f32(b);
-  lo = pack_bf16x2(u.x * scale, u.y * scale);
-  hi = pack_bf16x2(v.x * scale, v.y * scale);
+  lo = pack_bf16x2(u.x, u.y);
+  hi = pack_bf16x2(v.x, v.y);
 }
 __device__ __forceinline__ bool odd_f8(const uint4& v) {
   return (__vcmpeq4(v.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(v.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
@@ -333,7 +333,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     auto start = [&] {  // the rows' addresses and scales, for the tile that is read next
 #pragma unroll
       for (int k = 0; k < 2; ++k) from[k] = row_at(max(row[k], 0)) + l8 * 16;
-      if (l8 < 2) {
+      if (kKey && l8 < 2) {
         const int32_t r = l8 ? row[1] : row[0];
         cp_async4(smem0 + kOffScale + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4, p.scale + max(r, 0),
                   r);
@@ -366,7 +366,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     }
 #pragma unroll 1
     for (int i = 0; i < g.n; ++i) {
-      const float* sc_at = reinterpret_cast<const float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
+      float* scales = reinterpret_cast<float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
       const uint32_t here = there >> (8 * (i & 1)) & 0xFFu;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -374,7 +374,6 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         __syncwarp();
         claim();
         if (!ok) break;
-        float sc[2] = {sc_at[sub], sc_at[4 + sub]};
         if (h == 0) {
           note_there(i, here);
           there &= ~(0xFFu << (8 * (i & 1)));
@@ -383,18 +382,17 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         const bool check = drafts(i);
         uint32_t odd_keys = 0;
         const uint32_t raw = raw0 + (2 * (i & 1) + h) * kRaw;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t chunk = smem0 + st * kPart + (2 * c + (l8 >> 2)) * kChunk + 8 * w * 128;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int key = 4 * k + sub;
             uint4 x = ld_shared16(raw + 1024 * c + 512 * k);
-            float scale = sc[k];
             if (check) {
-              const bool bad = (__float_as_uint(scale) & 0x7F800000u) == 0x7F800000u;
+              const bool bad = kKey && (__float_as_uint(scales[key]) & 0x7F800000u) == 0x7F800000u;
               const bool odd = drafted(i, key) && (bad || odd_f8(x));
-              if (odd) x = zero, scale = 0.f;
+              if (odd) x = zero;
               odd_keys |= quad_bits(odd) << (4 * k);
             }
             swap_if(l8 >= 4, x.x, x.z);  // the lanes of the second chunk write their two pieces in turn
@@ -407,10 +405,10 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
               ds4f8::codes_to_f16(x.z, u.x, u.y);
               ds4f8::codes_to_f16(x.w, u.z, u.w);
             } else {
-              codes_to_bf16(x.x, scale, v.x, v.y);
-              codes_to_bf16(x.y, scale, v.z, v.w);
-              codes_to_bf16(x.z, scale, u.x, u.y);
-              codes_to_bf16(x.w, scale, u.z, u.w);
+              codes_to_bf16(x.x, v.x, v.y);
+              codes_to_bf16(x.y, v.z, v.w);
+              codes_to_bf16(x.z, u.x, u.y);
+              codes_to_bf16(x.w, u.z, u.w);
             }
             st_shared16(at, v);
             st_shared16(at ^ 16, u);
@@ -422,7 +420,10 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         if (kKey && h == 1) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {  // divided by the scale
-            const uint32_t s2 = (254u - (__float_as_uint(sc[k]) >> 23)) * 0x00800080u;
+            const uint32_t bits = __float_as_uint(scales[4 * k + sub]);
+            if (check && (bits & 0x7F800000u) == 0x7F800000u && drafted(i, 4 * k + sub))
+              scales[4 * k + sub] = 0.f;  // (all eight lanes; its scores are NaN already)
+            const uint32_t s2 = (254u - (bits >> 23)) * 0x00800080u;
             st_shared16(rope_address(4 * k + sub),
                         make_uint4(ds4q::mul_bf16x2(rope[k].x, s2), ds4q::mul_bf16x2(rope[k].y, s2),
                                    ds4q::mul_bf16x2(rope[k].z, s2), ds4q::mul_bf16x2(rope[k].w, s2)));
@@ -617,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const uint32_t smem0 = smem_u32(smem);
   float* s_f = reinterpret_cast<float*>(smem + kOffF);
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
+  const float* s_scale = reinterpret_cast<const float*>(smem + kOffScale);
   volatile uint64_t* s_there = reinterpret_cast<uint64_t*>(smem + kOffThere);
   volatile uint64_t* s_odd = reinterpret_cast<uint64_t*>(smem + kOffOdd);
   uint64_t* part_full = reinterpret_cast<uint64_t*>(smem + kOffBars);
@@ -784,6 +786,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t pk[4];
+              float4 sa, sb;
+              if constexpr (kF16) {
+                const float4* x = reinterpret_cast<const float4*>(s_scale + at * kKeys + 32 * h + 8 * u);
+                sa = x[0];
+                sb = x[1];
+              }
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int k = 8 * u + 2 * j;
@@ -794,6 +802,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                 x0 = exp2_approx(x0);
                 x1 = exp2_approx(x1);
                 sum2 = add_f32x2(sum2, pack_f32x2(x0, x1));
+                if constexpr (kF16) {  // the values are codes as well
+                  x0 *= j < 2 ? (j ? sa.z : sa.x) : (j == 3 ? sb.z : sb.x);
+                  x1 *= j < 2 ? (j ? sa.w : sa.y) : (j == 3 ? sb.w : sb.y);
+                }
                 pk[j] = pack_bf16x2(x0, x1);
               }
               st_shared16(p_at ^ (16 * (4 * h + u)), make_uint4(pk[0], pk[1], pk[2], pk[3]));
