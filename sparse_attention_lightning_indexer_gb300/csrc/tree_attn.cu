@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_ptx.cuh"
 #include "f8_format.cuh"
@@ -97,15 +98,10 @@ struct Params {
 struct Range {
   int32_t len, end;  // rows of the sequence; positions from `end` on are not there
   int32_t lo, n;
-  int32_t turn;
+  int32_t plain;     // the first steps, whose keys are all rows of the sequence
   uint64_t seen;     // drafted rows that some node of the tile sees
 
-  // First position of the i-th step. The tiles of a sequence start at different places of the range and
-  // go around: all pairs reading the same rows at the same time would crowd a few slices of L2.
-  __device__ __forceinline__ int32_t position(int i) const {
-    const int32_t t = i + turn;
-    return (lo + (t < n ? t : t - n)) * kKeys;
-  }
+  __device__ __forceinline__ int32_t position(int i) const { return (lo + i) * kKeys; }
 };
 
 // What every warp works out for itself (warp-uniform): one pass over the tile's masks.
@@ -133,48 +129,59 @@ __device__ __forceinline__ Range make_range(const Params& p, int b, int tile, in
   const int32_t per = max(p.steps, (total - 1) / p.splits + 1);
   g.lo = static_cast<int32_t>(min(static_cast<int64_t>(total), static_cast<int64_t>(split) * per));
   g.n = min(total - g.lo, per);
-  g.turn = static_cast<int32_t>(static_cast<int64_t>(tile) * g.n / p.tiles);
+  g.plain = max(0, min(g.n, min(g.len, g.end) / kKeys - g.lo));
   return g;
 }
 
 // Waits of a whole warp for a phase of a barrier, bounded like every wait of the library: after 2^32 clocks
-// (2 s) or when the CTA has given up it returns false. The clock is first read after some hundred tries; a
-// read of the global timer for each wait that does not succeed at once took a third of the kernel's time.
+// (2 s) or when the CTA has given up they return false. What follows a first try that fails is kept out of
+// the roles' loops.
 template <bool kCluster>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                           uint32_t* err) {
-  auto ready = [&] {
-    uint32_t ok;
-    if constexpr (kCluster)  // acquires what another CTA released
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity)
-          : "memory");
-    else
-      ok = mbar_try_wait(bar, parity);
-    return ok != 0;
-  };
-  bool ok = ready();
-  if (!__all_sync(0xffffffffu, ok)) {
-    long long since = 0;
-    for (uint32_t i = 1; !__all_sync(0xffffffffu, ok = ok || ready()); ++i) {
-      if (i & 255u) continue;
-      const long long now = clock64();
-      if (since == 0) since = now;
-      const bool late = now - since > (1ll << 32);
-      if (__any_sync(0xffffffffu, late || *abort_flag)) {
-        if (late) {
-          *abort_flag = 1u;
-          atomicOr(err, 1u);
-        }
-        return false;
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (kCluster)  // acquires what another CTA released
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return ok != 0;
+}
+template <bool kCluster>
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                         uint32_t* err) {
+  bool ok = false;
+  long long since = 0;
+  for (uint32_t i = 1; !__all_sync(0xffffffffu, ok = ok || phase_done<kCluster>(bar, parity)); ++i) {
+    if (i & 255u) continue;
+    const long long now = clock64();
+    if (since == 0) since = now;
+    const bool late = now - since > (1ll << 32);
+    if (__any_sync(0xffffffffu, late || *abort_flag)) {
+      if (late) {
+        *abort_flag = 1u;
+        atomicOr(err, 1u);
       }
+      return false;
     }
   }
   return true;
+}
+template <bool kCluster>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                           uint32_t* err) {
+  if (__all_sync(0xffffffffu, phase_done<kCluster>(smem_u32(bar), parity))) return true;
+  return wait_longer<kCluster>(smem_u32(bar), parity, abort_flag, err);
 }
 __device__ __forceinline__ void st_peer(uint32_t at, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
@@ -257,6 +264,10 @@ __device__ __forceinline__ void swap_if(bool c, T& a, T& b) {
   a = x;
 }
 
+__device__ __noinline__ int32_t paged_row(const Placement& p, const int32_t* table, int32_t s) {
+  return static_cast<int32_t>(place_row(p, TokenPlace{0, table, true}, s));
+}
+
 // One loader warp's work. kKey: this CTA forms the key products (and takes the rotary dims), or the
 // values'. Codes go to shared memory as they are, by asynchronous copies two tiles ahead, and are turned
 // into the operand by the thread that copied them. (Held in registers they were waited for as soon as the
@@ -275,8 +286,11 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   // The row of key 8 w + key of tile i.
   auto row_of = [&](int i, int key) -> int32_t {
     const int32_t s = g.position(i) + 8 * w + key;
-    if (i >= g.n || s >= g.end || (s >= g.len && !(g.seen >> (s - g.len) & 1))) return -1;
-    return static_cast<int32_t>(place_row(p.place, tp, s));
+    if (i >= g.n || s >= g.end) return -1;
+    if (i >= g.plain && s >= g.len && !(g.seen >> (s - g.len) & 1)) return -1;
+    // (contiguous: `end` ends at the pool's last row)
+    if (!tp.table) return static_cast<int32_t>(tp.row0 + s);
+    return tp.ok ? paged_row(p.place, tp.table, s) : -1;
   };
   auto row_at = [&](int32_t r) { return p.cache + static_cast<int64_t>(r) * kStride; };
   bool ok = true;
@@ -308,7 +322,6 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   };
   // A drafted row that some rows of the tile see and others do not may hold values that are not finite:
   // what is not is cleared, since 0 * NaN would reach all of O, and the key's scores become NaN instead.
-  auto drafts = [&](int i) { return g.len - g.position(i) < kKeys; };
   auto drafted = [&](int i, int key) { return g.position(i) + 8 * w + key >= g.len; };
   auto rope_address = [&](int key) {
     return smem0 + kOffRope + rope_slot * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
@@ -364,8 +377,8 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       }
       advance_rows();
     }
-#pragma unroll 1
-    for (int i = 0; i < g.n; ++i) {
+    auto tile = [&](int i, auto checked) {
+      constexpr bool check = decltype(checked)::value;
       float* scales = reinterpret_cast<float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
       const uint32_t here = there >> (8 * (i & 1)) & 0xFFu;
 #pragma unroll 1
@@ -379,17 +392,16 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           there &= ~(0xFFu << (8 * (i & 1)));
           start();
         }
-        const bool check = drafts(i);
         uint32_t odd_keys = 0;
         const uint32_t raw = raw0 + (2 * (i & 1) + h) * kRaw;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           const uint32_t chunk = smem0 + st * kPart + (2 * c + (l8 >> 2)) * kChunk + 8 * w * 128;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int key = 4 * k + sub;
             uint4 x = ld_shared16(raw + 1024 * c + 512 * k);
-            if (check) {
+            if constexpr (check) {
               const bool bad = kKey && (__float_as_uint(scales[key]) & 0x7F800000u) == 0x7F800000u;
               const bool odd = drafted(i, key) && (bad || odd_f8(x));
               if (odd) x = zero;
@@ -416,7 +428,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           }
         }
         cp_async_commit();
-        if (check) note_odd(i, h, odd_keys);
+        if constexpr (check) note_odd(i, h, odd_keys);
         if (kKey && h == 1) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {  // divided by the scale
@@ -435,10 +447,13 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         publish(st);
         step();
       }
-      if (!ok) break;
       advance_rows();
       if (++rope_slot == 3) rope_slot = 0;
-    }
+    };
+#pragma unroll 1
+    for (int i = 0; i < g.plain && ok; ++i) tile(i, std::false_type{});
+#pragma unroll 1
+    for (int i = g.plain; i < g.n && ok; ++i) tile(i, std::true_type{});
     cp_async_wait<0>();
   } else if constexpr (kFormat == DS4IDX_CACHE_BF16) {
     // straight to the operand; a part is published when the next one's copies are on their way
@@ -449,7 +464,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       for (int h = 0; h < 2; ++h) {
         claim();
         if (!ok) break;
-        const bool check = drafts(i);
+        const bool check = i >= g.plain;
         uint32_t odd_keys = 0;
 #pragma unroll 2
         for (int k = 0; k < 8; ++k) {  // rows sub and 4 + sub, a chunk of 64 dims (k >> 1)
@@ -536,7 +551,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       if (!ok) break;
       note_there(i, there >> (8 * (i & 1)) & 0xFFu);
       there &= ~(0xFFu << (8 * (i & 1)));
-      if (drafts(i)) note_odd(i, 0, 0), note_odd(i, 1, 0);  // (the format has only finite values)
+      if (i >= g.plain) note_odd(i, 0, 0), note_odd(i, 1, 0);  // (the format has only finite values)
       const uint32_t raw = raw0 + i % 3 * kRaw;
       const uint8_t* scales = smem + kOffRaw + 3 * kRaw + w * 256 + i % 3 * 2048;
 #pragma unroll 1
@@ -736,21 +751,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const uint32_t rows_at = warp * 32 * 128;  // this warp's rows of P
       int slot = 0;                              // i % 3
       uint32_t s_parity = 0;
-#pragma unroll 1
-      for (int i = 0; i < g.n; ++i) {
+      auto tile_step = [&](int i, auto masked) {
+        constexpr bool kMasked = decltype(masked)::value;
         const int ps = i & 1, at = i & 7;
         ok = wait_phase<false>(&s_ready[slot], s_parity, s_abort, err) &&
              wait_phase<true>(&p_free[ps], (i >> 1 & 1) ^ 1u, s_abort, err);
-        if (!ok) break;
+        if (!ok) return;
         tc_fence_after();
-        // which keys this row sees
-        const int32_t left = g.len - g.position(i);  // rows of the sequence from this tile on
-        uint64_t see = padding ? 0ull : s_there[at], bad = 0ull;
-        if (left < kKeys) {
-          see &= left >= 0 ? ((1ull << left) - 1ull) | mask << left : left > -64 ? mask >> -left : 0ull;
-          bad = s_odd[2 * at] | s_odd[2 * at + 1];
+        // which keys this row sees (all, of padding: what its row becomes is not used)
+        uint64_t see = ~0ull, bad = 0ull;
+        if constexpr (kMasked) {
+          see = s_there[at];
+          if (i >= g.plain) {
+            const int32_t left = g.len - g.position(i);  // rows of the sequence from this tile on
+            see &= left >= kKeys ? ~0ull
+                   : left >= 0   ? ((1ull << left) - 1ull) | mask << left
+                   : left > -64  ? mask >> -left
+                                 : 0ull;
+            bad = s_odd[2 * at] | s_odd[2 * at + 1];
+          }
         }
-        const bool plain = __all_sync(0xffffffffu, see == ~0ull && bad == 0ull);
         // P with the m so far, in the layout of an MMA A operand; once more where that has to be raised
         const uint32_t p_at = smem0 + kOffP + ps * kP + r * 128 + (r & 7) * 16;
         float f = 1.f, sum;
@@ -773,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                 mul_pair(s[j + 2], s[j + 3], x.z, x.w);
               }
             }
-            if (!plain) {  // a masked score is -infinity: p = 0 whatever m, and no maximum
+            if constexpr (kMasked) {  // a masked score is -infinity: p = 0 whatever m, and no maximum
               const uint32_t on = static_cast<uint32_t>(see >> (32 * h));
               const uint32_t nan = static_cast<uint32_t>(bad >> (32 * h));
 #pragma unroll
@@ -845,7 +865,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         __syncwarp();
         if (++slot == 3) slot = 0, s_parity ^= 1u;
+      };
+#pragma unroll 1
+      for (int i = 0; i < g.n && ok; ++i) {
+        // (a page that is missing leaves holes among the sequence's rows as well)
+        if (i < g.plain) {
+          ok = wait_phase<false>(&s_ready[slot], s_parity, s_abort, err);
+          if (!ok) break;
+          if (s_there[i & 7] == ~0ull) {
+            tile_step(i, std::false_type{});
+            continue;
+          }
+        }
+        tile_step(i, std::true_type{});
       }
+      if (padding) m = kNegInf, l = 0.f;
       // ---------------- the rows' sums, to rank 1
       st_peer(peer(smem_u32(s_l + r), 1), l);
       st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
