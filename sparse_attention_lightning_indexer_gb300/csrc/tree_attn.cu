@@ -56,14 +56,15 @@ constexpr int kLoad0 = 4, kLoaders = 8, kMmaWarp = 12;
 constexpr int kThreads = 13 * 32;
 constexpr int kChunk = kKeys * 128;    // 64 dims of a tile's keys
 constexpr int kPart = 4 * kChunk, kParts = 3;
-constexpr int kRaw = kKeys * 256, kRaws = 4;       // codes of a part as they are read
+constexpr int kRaw = kKeys * 256, kRaws = 3;       // codes of a part as they are read
 constexpr int kOffRaw = kParts * kPart;
-constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of three tiles' keys (rank 0)
-constexpr int kOffP = kOffRope + 3 * kChunk, kP = kRows * kKeys * 2;  // P of two tiles
+constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of four tiles' keys (rank 0)
+constexpr int kOffP = kOffRope + 4 * kChunk, kP = kRows * kKeys * 2;  // P of two tiles
 constexpr int kOffF = kOffP + 2 * kP;              // float [2][128]: factors of O before P V
 constexpr int kOffL = kOffF + 2 * kRows * 4;       // float [2][128]: l, m (rank 1)
-constexpr int kOffScale = kOffL + 2 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit rows)
-constexpr int kOffThere = kOffScale + 8 * kKeys * 4;  // uint64 [8 tiles]: keys that are there
+constexpr int kOffScale = kOffL + 2 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
+                                                   // rows), or two tiles' codes of scales (4-bit rows)
+constexpr int kOffThere = kOffScale + 4096;  // uint64 [8 tiles]: keys that are there
 constexpr int kOffOdd = kOffThere + 8 * 8;         // uint64 [8 tiles][2 halves]: keys not finite
 constexpr int kOffBars = kOffOdd + 8 * 16;
 constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 2;
@@ -294,7 +295,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   };
   auto row_at = [&](int32_t r) { return p.cache + static_cast<int64_t>(r) * kStride; };
   bool ok = true;
-  int st = 0, rope_slot = 0;  // places in the rings
+  int st = 0;                 // place in the ring
   uint32_t parity = 1;        // of part_empty
   auto claim = [&] { ok = ok && wait_phase<false>(&part_empty[st], parity, abort_flag, p.err); };
   auto step = [&] {
@@ -323,8 +324,8 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   // A drafted row that some rows of the tile see and others do not may hold values that are not finite:
   // what is not is cleared, since 0 * NaN would reach all of O, and the key's scores become NaN instead.
   auto drafted = [&](int i, int key) { return g.position(i) + 8 * w + key >= g.len; };
-  auto rope_address = [&](int key) {
-    return smem0 + kOffRope + rope_slot * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
+  auto rope_address = [&](int i, int key) {
+    return smem0 + kOffRope + (i & 3) * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
   };
   // This thread's rows (keys sub and 4 + sub) of the tile that is read, and of the one after it.
   int32_t row[2], next[2];
@@ -340,120 +341,109 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   auto there_bits = [&] { return quad_bits(row[0] >= 0) | quad_bits(row[1] >= 0) << 4; };
 
   if constexpr (kFormat == DS4IDX_CACHE_FP8) {
-    // a part: two lines of 128 codes (c) of rows sub and 4 + sub (k), 16 codes a lane
+    // a part: two lines of 128 codes (c) of rows sub and 4 + sub (k), 16 codes a lane. Three parts are on
+    // their way, each with a group of copies; a tile's scales and rotary dims come with its first half.
     const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw part, + 1024 c + 512 k
-    const uint8_t* from[2];
-    auto start = [&] {  // the rows' addresses and scales, for the tile that is read next
-#pragma unroll
-      for (int k = 0; k < 2; ++k) from[k] = row_at(max(row[k], 0)) + l8 * 16;
-      if (kKey && l8 < 2) {
-        const int32_t r = l8 ? row[1] : row[0];
-        cp_async4(smem0 + kOffScale + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4, p.scale + max(r, 0),
-                  r);
-      }
-      there |= there_bits() << (8 * (read & 1));
-    };
+    int raw_in = 0, raw_out = 0;  // places of the part to be read next, and of the one to be turned next
     auto copy = [&](int h, int c, int k) {
-      cp_async16(raw0 + (2 * (read & 1) + h) * kRaw + 1024 * c + 512 * k, from[k] + (2 * h + c) * 128, row[k]);
+      cp_async16(raw0 + raw_in * kRaw + 1024 * c + 512 * k,
+                 row_at(max(row[k], 0)) + (2 * h + c) * 128 + l8 * 16, row[k]);
     };
-    uint4 rope[2];
-    int32_t late[2] = {row[0], row[1]};  // rows of the tile before the one that is copied
-    auto load_rope = [&] {
+    auto copied = [&](int h) {
+      if (h == 0) {
+        if constexpr (kKey) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        rope[k] = ld_row16(row_at(late[k]) + ds4f8::kOffRope + l8 * 16, late[k]);
-    };
-    if (kKey) load_rope();
-#pragma unroll 1
-    for (int j = 0; j < 2; ++j) {
-      late[0] = row[0];
-      late[1] = row[1];
-      start();
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) copy(h, c, 0), copy(h, c, 1);
-        cp_async_commit();
+          for (int k = 0; k < 2; ++k)
+            cp_async16(rope_address(read, 4 * k + sub), row_at(max(row[k], 0)) + ds4f8::kOffRope + l8 * 16,
+                       row[k]);
+          if (l8 < 2) {
+            const int32_t r = l8 ? row[1] : row[0];
+            cp_async4(smem0 + kOffScale + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4,
+                      p.scale + max(r, 0), r);
+          }
+        }
+        there |= there_bits() << (8 * (read & 1));
+      } else {
+        advance_rows();
       }
-      advance_rows();
+      cp_async_commit();
+      if (++raw_in == kRaws) raw_in = 0;
+    };
+#pragma unroll 1
+    for (int n = 0; n < kRaws; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) copy(n & 1, c, 0), copy(n & 1, c, 1);
+      copied(n & 1);
     }
-    auto tile = [&](int i, auto checked) {
+    // The half h of tile i; the reads of the part three later go to where its codes were.
+    auto part = [&](int i, int h, auto checked) {
       constexpr bool check = decltype(checked)::value;
+      cp_async_wait<kRaws - 1>();
+      __syncwarp();
+      claim();
+      if (!ok) return;
       float* scales = reinterpret_cast<float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
-      const uint32_t here = there >> (8 * (i & 1)) & 0xFFu;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        cp_async_wait<3>();
-        __syncwarp();
-        claim();
-        if (!ok) break;
-        if (h == 0) {
-          note_there(i, here);
-          there &= ~(0xFFu << (8 * (i & 1)));
-          start();
-        }
-        uint32_t odd_keys = 0;
-        const uint32_t raw = raw0 + (2 * (i & 1) + h) * kRaw;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t chunk = smem0 + st * kPart + (2 * c + (l8 >> 2)) * kChunk + 8 * w * 128;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int key = 4 * k + sub;
-            uint4 x = ld_shared16(raw + 1024 * c + 512 * k);
-            if constexpr (check) {
-              const bool bad = kKey && (__float_as_uint(scales[key]) & 0x7F800000u) == 0x7F800000u;
-              const bool odd = drafted(i, key) && (bad || odd_f8(x));
-              if (odd) x = zero;
-              odd_keys |= quad_bits(odd) << (4 * k);
-            }
-            swap_if(l8 >= 4, x.x, x.z);  // the lanes of the second chunk write their two pieces in turn
-            swap_if(l8 >= 4, x.y, x.w);
-            const uint32_t at = chunk + key * 128 + ((((l8 & 3) * 2 + (l8 >> 2)) ^ key) * 16);
-            uint4 v, u;
-            if constexpr (kF16) {
-              ds4f8::codes_to_f16(x.x, v.x, v.y);
-              ds4f8::codes_to_f16(x.y, v.z, v.w);
-              ds4f8::codes_to_f16(x.z, u.x, u.y);
-              ds4f8::codes_to_f16(x.w, u.z, u.w);
-            } else {
-              codes_to_bf16(x.x, v.x, v.y);
-              codes_to_bf16(x.y, v.z, v.w);
-              codes_to_bf16(x.z, u.x, u.y);
-              codes_to_bf16(x.w, u.z, u.w);
-            }
-            st_shared16(at, v);
-            st_shared16(at ^ 16, u);
-            copy(h, c, k);
-          }
-        }
-        cp_async_commit();
-        if constexpr (check) note_odd(i, h, odd_keys);
-        if (kKey && h == 1) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {  // divided by the scale
-            const uint32_t bits = __float_as_uint(scales[4 * k + sub]);
-            if (check && (bits & 0x7F800000u) == 0x7F800000u && drafted(i, 4 * k + sub))
-              scales[4 * k + sub] = 0.f;  // (all eight lanes; its scores are NaN already)
-            const uint32_t s2 = (254u - (bits >> 23)) * 0x00800080u;
-            st_shared16(rope_address(4 * k + sub),
-                        make_uint4(ds4q::mul_bf16x2(rope[k].x, s2), ds4q::mul_bf16x2(rope[k].y, s2),
-                                   ds4q::mul_bf16x2(rope[k].z, s2), ds4q::mul_bf16x2(rope[k].w, s2)));
-          }
-          load_rope();
-          late[0] = row[0];
-          late[1] = row[1];
-        }
-        publish(st);
-        step();
+      if (h == 0) {
+        note_there(i, there >> (8 * (i & 1)) & 0xFFu);
+        there &= ~(0xFFu << (8 * (i & 1)));
       }
-      advance_rows();
-      if (++rope_slot == 3) rope_slot = 0;
+      uint32_t odd_keys = 0;
+      const uint32_t raw = raw0 + raw_out * kRaw;
+      if (++raw_out == kRaws) raw_out = 0;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t chunk = smem0 + st * kPart + (2 * c + (l8 >> 2)) * kChunk + 8 * w * 128;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int key = 4 * k + sub;
+          uint4 x = ld_shared16(raw + 1024 * c + 512 * k);
+          if constexpr (check) {
+            const bool bad = kKey && (__float_as_uint(scales[key]) & 0x7F800000u) == 0x7F800000u;
+            const bool odd = drafted(i, key) && (bad || odd_f8(x));
+            if (odd) x = zero;
+            odd_keys |= quad_bits(odd) << (4 * k);
+          }
+          swap_if(l8 >= 4, x.x, x.z);  // the lanes of the second chunk write their two pieces in turn
+          swap_if(l8 >= 4, x.y, x.w);
+          const uint32_t at = chunk + key * 128 + ((((l8 & 3) * 2 + (l8 >> 2)) ^ key) * 16);
+          uint4 v, u;
+          if constexpr (kF16) {
+            ds4f8::codes_to_f16(x.x, v.x, v.y);
+            ds4f8::codes_to_f16(x.y, v.z, v.w);
+            ds4f8::codes_to_f16(x.z, u.x, u.y);
+            ds4f8::codes_to_f16(x.w, u.z, u.w);
+          } else {
+            codes_to_bf16(x.x, v.x, v.y);
+            codes_to_bf16(x.y, v.z, v.w);
+            codes_to_bf16(x.z, u.x, u.y);
+            codes_to_bf16(x.w, u.z, u.w);
+          }
+          st_shared16(at, v);
+          st_shared16(at ^ 16, u);
+          copy(h ^ 1, c, k);
+        }
+      }
+      copied(h ^ 1);
+      if constexpr (check) note_odd(i, h, odd_keys);
+      if (kKey && h == 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // the rotary dims divided by the scale, in place
+          const uint32_t at = rope_address(i, 4 * k + sub), bits = __float_as_uint(scales[4 * k + sub]);
+          if (check && (bits & 0x7F800000u) == 0x7F800000u && drafted(i, 4 * k + sub))
+            scales[4 * k + sub] = 0.f;  // (all eight lanes; its scores are NaN already)
+          const uint32_t s2 = (254u - (bits >> 23)) * 0x00800080u;
+          const uint4 x = ld_shared16(at);
+          st_shared16(at, make_uint4(ds4q::mul_bf16x2(x.x, s2), ds4q::mul_bf16x2(x.y, s2),
+                                     ds4q::mul_bf16x2(x.z, s2), ds4q::mul_bf16x2(x.w, s2)));
+        }
+      }
+      publish(st);
+      step();
     };
 #pragma unroll 1
-    for (int i = 0; i < g.plain && ok; ++i) tile(i, std::false_type{});
+    for (int n = 0; n < 2 * g.plain && ok; ++n) part(n >> 1, n & 1, std::false_type{});
 #pragma unroll 1
-    for (int i = g.plain; i < g.n && ok; ++i) tile(i, std::true_type{});
+    for (int n = 2 * g.plain; n < 2 * g.n && ok; ++n) part(n >> 1, n & 1, std::true_type{});
     cp_async_wait<0>();
   } else if constexpr (kFormat == DS4IDX_CACHE_BF16) {
     // straight to the operand; a part is published when the next one's copies are on their way
@@ -482,7 +472,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
             cp_async16(at, src, r);
           }
           if (kKey && h == 0 && k < 2)
-            cp_async16(rope_address(key), row_at(max(r, 0)) + 2 * kLatent + l8 * 16, r);
+            cp_async16(rope_address(i, key), row_at(max(r, 0)) + 2 * kLatent + l8 * 16, r);
         }
         cp_async_commit();
         if (check) note_odd(i, h, odd_keys);
@@ -496,7 +486,6 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       }
       if (!ok) break;
       advance_rows();
-      if (++rope_slot == 3) rope_slot = 0;
     }
     cp_async_wait<0>();
     if (ok && last >= 0) publish(last);
@@ -504,16 +493,14 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     // access k: rows 2 k and 2 k + 1, 32 codes a lane: two of the four scales of a chunk
     const int l16 = lane & 15, hi = lane >> 4, x = l16 >> 1 & 3;
     const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;            // + raw tile, + 512 k
-    const uint32_t raw_scale = smem0 + kOffRaw + 3 * kRaw + w * 256;         // + 2048 raw tile
-    uint4 rope[2];
-    int32_t late[2] = {row[0], row[1]};  // rows of the tile before the one that is copied
+    const uint32_t raw_scale = smem0 + kOffScale + w * 256;                  // + 2048 raw tile
     // Row of key j (the same in all lanes of a group of eight that holds it).
     auto row_of_key = [&](int j) {
       const int32_t a = __shfl_sync(0xffffffffu, row[0], 8 * (j & 3)), c = __shfl_sync(0xffffffffu, row[1], 8 * (j & 3));
       return j < 4 ? a : c;
     };
     auto copy = [&] {
-      const int slot = read % 3;
+      const int slot = read & 1;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const int32_t r = row_of_key(2 * k + hi);
@@ -522,19 +509,16 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       const int32_t r = row_of_key(l16 >> 1);
       if (lane < 16)
         cp_async16(raw_scale + slot * 2048 + lane * 16, row_at(max(r, 0)) + ds4q::kOffScale + (lane & 1) * 16, r);
+      if (kKey) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          cp_async16(rope_address(read, 4 * k + sub), row_at(max(row[k], 0)) + ds4q::kOffRope + l8 * 16, row[k]);
+      }
       there |= there_bits() << (8 * (read & 1));
       cp_async_commit();
     };
-    auto load_rope = [&] {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        rope[k] = ld_row16(row_at(late[k]) + ds4q::kOffRope + l8 * 16, late[k]);
-    };
-    if (kKey) load_rope();
 #pragma unroll 1
     for (int j = 0; j < 2; ++j) {
-      late[0] = row[0];
-      late[1] = row[1];
       copy();
       advance_rows();
     }
@@ -552,8 +536,8 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       note_there(i, there >> (8 * (i & 1)) & 0xFFu);
       there &= ~(0xFFu << (8 * (i & 1)));
       if (i >= g.plain) note_odd(i, 0, 0), note_odd(i, 1, 0);  // (the format has only finite values)
-      const uint32_t raw = raw0 + i % 3 * kRaw;
-      const uint8_t* scales = smem + kOffRaw + 3 * kRaw + w * 256 + i % 3 * 2048;
+      const uint32_t raw = raw0 + (i & 1) * kRaw;
+      const uint8_t* scales = smem + kOffScale + w * 256 + (i & 1) * 2048;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const int key = 2 * k + hi;
@@ -575,18 +559,10 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           st_shared16(at ^ (16 * j), ds4q::word_to_bf16(words[j], s2, ds4q::offset_bf16x2(s2)));
         }
       }
-      if (kKey) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) st_shared16(rope_address(k * 4 + sub), rope[k]);
-        load_rope();
-        late[0] = row[0];
-        late[1] = row[1];
-      }
       publish(first);
       publish(second);
       copy();
       advance_rows();
-      if (++rope_slot == 3) rope_slot = 0;
     }
     cp_async_wait<0>();
   }
@@ -806,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t pk[4];
-              float4 sa, sb;
+              [[maybe_unused]] float4 sa, sb;
               if constexpr (kF16) {
                 const float4* x = reinterpret_cast<const float4*>(s_scale + at * kKeys + 32 * h + 8 * u);
                 sa = x[0];
@@ -1023,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
               }
             }
             if (h == 1 && lead) {
-              const uint64_t rd = r0 + slot * (kChunk >> 4);  // (i % 3 = slot)
+              const uint64_t rd = r0 + (i & 3) * (kChunk >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_bf16_ts(d, tmem + kColRope + k * 8, rd + 2 * k, rope_idesc, 1u);
