@@ -17,8 +17,8 @@
 // Both CTAs read the rows themselves and turn them into bf16 (exact) in a ring of parts, 64 keys x 256
 // dims in the 128-byte-swizzled layout that serves as K-major and as MN-major operand.
 //
-// Warps 0..3: softmax, a row a thread (rank 1: the rescaling of O and the output). Warps 4..11: rows to
-// operands. Warp 12 issues tcgen05.mma. The roles' loops are kept rolled: they run side by side out of one
+// Warps 0..7: softmax, a row a thread, warps 0..3 on even tiles and 4..7 on odd ones (rank 1: the
+// rescaling of O and the output). Warps 8..15: rows to operands. Warp 16 issues tcgen05.mma. The roles' loops are kept rolled: they run side by side out of one
 // instruction cache, and with everything unrolled (126 KB of code) more than half of its look-ups missed
 // and a tile took 7000 clocks.
 //
@@ -52,22 +52,26 @@ constexpr int kDims = 576, kLatent = 512, kNodes = 64, kMaxHeads = 128;
 constexpr int kRows = 128;             // (node, head) rows of a tile = TMEM lanes
 constexpr int kKeys = 64;              // keys of a step
 constexpr int kHalf = 256;             // latent dims of a part
-constexpr int kLoad0 = 4, kLoaders = 8, kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kLoad0 = 8, kLoaders = 8, kMmaWarp = 16;
+constexpr int kThreads = 17 * 32;
 constexpr int kChunk = kKeys * 128;    // 64 dims of a tile's keys
 constexpr int kPart = 4 * kChunk, kParts = 3;
 constexpr int kRaw = kKeys * 256, kRaws = 3;       // codes of a part as they are read
 constexpr int kOffRaw = kParts * kPart;
 constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of four tiles' keys (rank 0)
-constexpr int kOffP = kOffRope + 4 * kChunk, kP = kRows * kKeys * 2;  // P of two tiles
-constexpr int kOffF = kOffP + 2 * kP;              // float [2][128]: factors of O before P V
-constexpr int kOffL = kOffF + 2 * kRows * 4;       // float [2][128]: l, m (rank 1)
-constexpr int kOffScale = kOffL + 2 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
+constexpr int kOffP = kOffRope + 4 * kChunk, kP = kRows * kKeys * 2;  // P as it is made (rank 0)
+constexpr int kIn = 4;                             // tiles of P on their way to rank 1 or in use there
+constexpr int kOffPIn = kOffRope;                  // (rank 1 has no rotary dims)
+constexpr int kOffF = kOffP + 2 * kP;              // float [4][128]: roots of factors of O before P V
+constexpr int kOffM = kOffF + kIn * kRows * 4;       // float [2][128]: m after an even, an odd tile
+constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
+constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
                                                    // rows), or two tiles' codes of scales (4-bit rows)
 constexpr int kOffThere = kOffScale + 4096;  // uint64 [8 tiles]: keys that are there
 constexpr int kOffOdd = kOffThere + 8 * 8;         // uint64 [8 tiles][2 halves]: keys not finite
 constexpr int kOffBars = kOffOdd + 8 * 16;
-constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 4 * 2 + 2;
+constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 2 + 4 * kIn + 8 + 2;
+static_assert(kOffPIn + kIn * kP <= kOffF, "P of rank 1");
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
@@ -327,18 +331,33 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   auto rope_address = [&](int i, int key) {
     return smem0 + kOffRope + (i & 3) * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
   };
-  // This thread's rows (keys sub and 4 + sub) of the tile that is read, and of the one after it.
+  // This thread's rows (keys sub and 4 + sub) of the tile that is read; where they need a page table, those
+  // of the tile after it as well. Rows that follow one another are stepped through.
   int32_t row[2], next[2];
+  const bool steps = tp.table == nullptr;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) row[k] = row_of(0, 4 * k + sub), next[k] = row_of(1, 4 * k + sub);
+  for (int k = 0; k < 2; ++k) row[k] = row_of(0, 4 * k + sub), next[k] = steps ? 0 : row_of(1, 4 * k + sub);
+  const uint8_t* from[2] = {row_at(max(row[0], 0)) + l8 * 16, row_at(max(row[1], 0)) + l8 * 16};
   uint32_t there = 0;  // bytes: the keys that are there, of the tiles that are read and not yet written
   int read = 0;        // tiles whose reads are on their way
   auto advance_rows = [&] {
     ++read;
+    if (steps && read < g.plain) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) row[k] = next[k], next[k] = row_of(read + 1, 4 * k + sub);
+      for (int k = 0; k < 2; ++k) row[k] += kKeys, from[k] += kKeys * kStride;
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      row[k] = steps ? row_of(read, 4 * k + sub) : next[k];
+      if (!steps) next[k] = row_of(read + 1, 4 * k + sub);
+      from[k] = row_at(max(row[k], 0)) + l8 * 16;
+    }
   };
-  auto there_bits = [&] { return quad_bits(row[0] >= 0) | quad_bits(row[1] >= 0) << 4; };
+  auto there_bits = [&]() -> uint32_t {
+    if (steps && read < g.plain) return 0xFFu;
+    return quad_bits(row[0] >= 0) | quad_bits(row[1] >= 0) << 4;
+  };
 
   if constexpr (kFormat == DS4IDX_CACHE_FP8) {
     // a part: two lines of 128 codes (c) of rows sub and 4 + sub (k), 16 codes a lane. Three parts are on
@@ -347,15 +366,14 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     int raw_in = 0, raw_out = 0;  // places of the part to be read next, and of the one to be turned next
     auto copy = [&](int h, int c, int k) {
       cp_async16(raw0 + raw_in * kRaw + 1024 * c + 512 * k,
-                 row_at(max(row[k], 0)) + (2 * h + c) * 128 + l8 * 16, row[k]);
+                 from[k] + (2 * h + c) * 128, row[k]);
     };
     auto copied = [&](int h) {
       if (h == 0) {
         if constexpr (kKey) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            cp_async16(rope_address(read, 4 * k + sub), row_at(max(row[k], 0)) + ds4f8::kOffRope + l8 * 16,
-                       row[k]);
+            cp_async16(rope_address(read, 4 * k + sub), from[k] + ds4f8::kOffRope, row[k]);
           if (l8 < 2) {
             const int32_t r = l8 ? row[1] : row[0];
             cp_async4(smem0 + kOffScale + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4,
@@ -462,7 +480,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           const int32_t r = k & 1 ? row[1] : row[0];
           const uint32_t at =
               smem0 + st * kPart + (k >> 1) * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
-          const uint8_t* src = row_at(max(r, 0)) + h * 2 * kHalf + (k >> 1) * 128 + l8 * 16;
+          const uint8_t* src = (k & 1 ? from[1] : from[0]) + h * 2 * kHalf + (k >> 1) * 128;
           if (check) {
             const uint4 v = ld_row16(src, r);
             const bool odd = drafted(i, key) && odd_bf16(v);
@@ -472,7 +490,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
             cp_async16(at, src, r);
           }
           if (kKey && h == 0 && k < 2)
-            cp_async16(rope_address(i, key), row_at(max(r, 0)) + 2 * kLatent + l8 * 16, r);
+            cp_async16(rope_address(i, key), (k & 1 ? from[1] : from[0]) + 2 * kLatent, r);
         }
         cp_async_commit();
         if (check) note_odd(i, h, odd_keys);
@@ -512,7 +530,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       if (kKey) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          cp_async16(rope_address(read, 4 * k + sub), row_at(max(row[k], 0)) + ds4q::kOffRope + l8 * 16, row[k]);
+          cp_async16(rope_address(read, 4 * k + sub), from[k] + ds4q::kOffRope, row[k]);
       }
       there |= there_bits() << (8 * (read & 1));
       cp_async_commit();
@@ -608,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t smem0 = smem_u32(smem);
   float* s_f = reinterpret_cast<float*>(smem + kOffF);
+  float* s_m = reinterpret_cast<float*>(smem + kOffM);
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
   const float* s_scale = reinterpret_cast<const float*>(smem + kOffScale);
   volatile uint64_t* s_there = reinterpret_cast<uint64_t*>(smem + kOffThere);
@@ -617,11 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint64_t* q_full = part_empty + kParts;
   uint64_t* s_ready = q_full + 1;   // [3] S of a tile is formed
   uint64_t* s_free = s_ready + 3;   // [3] and read
-  uint64_t* p_free = s_free + 3;    // [2] rank 1 is done with P (in rank 0)
-  uint64_t* p_full = p_free + 2;    // [2] P has come (in rank 1)
-  uint64_t* scaled = p_full + 2;    // [2] O is ready for P V
-  uint64_t* pv_done = scaled + 2;   // [2] P V of a tile is done
-  uint64_t* l_full = pv_done + 2;   // the rows' sums have come (in rank 1)
+  uint64_t* p_sent = s_free + 3;    // [2] P has come to rank 1 (in rank 0)
+  uint64_t* p_free = p_sent + 2;    // [4] rank 1 is done with P (in rank 0)
+  uint64_t* p_full = p_free + kIn;  // [4] P has come (in rank 1)
+  uint64_t* scaled = p_full + kIn;  // [4] O is ready for P V
+  uint64_t* pv_done = scaled + kIn; // [4] P V of a tile is done
+  uint64_t* m_full = pv_done + kIn;  // [8] a softmax warp's m is in s_m
+  uint64_t* l_full = m_full + 8;    // the rows' sums have come (in rank 1)
   uint64_t* done = l_full + 1;      // every MMA has completed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
@@ -636,17 +657,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mbar_init(&part_full[i], kLoaders);
       mbar_init(&part_empty[i], 1);
     }
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 8);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&s_ready[i], 1);
       mbar_init(&s_free[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_free[i], 4);
+    mbar_init(&p_sent[0], 1);
+    mbar_init(&p_sent[1], 1);
+    for (int i = 0; i < kIn; ++i) {
+      mbar_init(&p_free[i], 8);
       mbar_init(&p_full[i], 1);
-      mbar_init(&scaled[i], 4);
+      mbar_init(&scaled[i], 8);
       mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&m_full[i], 1);
     mbar_init(l_full, 4);
     mbar_init(done, 1);
     *s_abort = 0u;
@@ -667,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   constexpr bool kF16 = kFormat == DS4IDX_CACHE_FP8;  // the key product's type
 
   if (warp < kLoad0) {
-    const int r = tid;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int row = tile * kRows + r, node = row / p.H;
     const bool used = node < p.N;
     const int64_t out_row = static_cast<int64_t>(b) * p.N * p.H + row;
@@ -701,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
         }
 #pragma unroll 1
-        for (int h = 0; h < 9; ++h) {  // the rotary dims last
+        for (int h = grp; h < 9; h += 2) {  // the rotary dims last
           uint32_t v[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -724,14 +748,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (lane == 0) mbar_arrive(q_full);
       }
       float m = kNegInf, l = 0.f;
-      const uint32_t rows_at = warp * 32 * 128;  // this warp's rows of P
-      int slot = 0;                              // i % 3
-      uint32_t s_parity = 0;
+      const uint32_t rows_at = quad * 32 * 128;  // this warp's rows of P
+      const uint32_t p_at = smem0 + kOffP + grp * kP + r * 128 + (r & 7) * 16;
       auto tile_step = [&](int i, auto masked) {
         constexpr bool kMasked = decltype(masked)::value;
-        const int ps = i & 1, at = i & 7;
-        ok = wait_phase<false>(&s_ready[slot], s_parity, s_abort, err) &&
-             wait_phase<true>(&p_free[ps], (i >> 1 & 1) ^ 1u, s_abort, err);
+        const uint32_t use = i >> 1;
+        const int slot = i % 3, at = i & 7, in = i & (kIn - 1);
+        ok = wait_phase<false>(&s_ready[slot], (i / 3) & 1, s_abort, err) &&
+             wait_phase<true>(&p_sent[grp], (use & 1) ^ 1u, s_abort, err);
         if (!ok) return;
         tc_fence_after();
         // which keys this row sees (all, of padding: what its row becomes is not used)
@@ -747,10 +771,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             bad = s_odd[2 * at] | s_odd[2 * at + 1];
           }
         }
-        // P with the m so far, in the layout of an MMA A operand; once more where that has to be raised
-        const uint32_t p_at = smem0 + kOffP + ps * kP + r * 128 + (r & 7) * 16;
+        // P with this group's m, in the layout of an MMA A operand; once more where m is another one now
         float f = 1.f, sum;
-        for (int pass = 0;; ++pass) {  // (at most twice: then m holds the tile's largest score)
+        for (int pass = 0;; ++pass) {  // (at most twice)
           const float off = m == kNegInf ? 0.f : -m;
           const uint64_t off2 = pack_f32x2(off, off), scale2 = pack_f32x2(to_log2, to_log2);
           uint64_t sum2 = 0ull;
@@ -810,87 +833,113 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           float l0, l1;
           unpack_f32x2(sum2, l0, l1);
           sum = l0 + l1;
-          // m is raised where a score passes it by more than the slack. Finite once a key was seen: a score
-          // of +-infinity keeps its meaning in s - m.
+          if (pass == 1) break;
+          // m after the tile before, which the other group took; raised where a score passes it by more
+          // than the slack. Finite once a key was seen: a score of +-infinity keeps its meaning in s - m.
+          float before = kNegInf;
+          if (i > 0) {
+            ok = wait_phase<false>(&m_full[warp ^ 4], ((i - 1) >> 1) & 1, s_abort, err);
+            if (!ok) return;
+            before = s_m[(grp ^ 1) * kRows + r];
+          }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * to_log2;
-          const float now = fminf(fmaxf(top, -kMax), kMax);
-          const bool raise = see != 0ull && (m == kNegInf || now > m + kSlack);
-          if (pass == 1 || !__any_sync(0xffffffffu, raise)) break;
-          if (raise) {
-            if (m != kNegInf) {
-              // the root of the factor: what is 2^64 above the old m may matter 2^-126 above the new one,
-              // where 2^(m - now) is long zero
-              f = exp2_approx(0.5f * (m - now));
-              l = l * f * f;
-            }
+          float now = fminf(fmaxf(top, -kMax), kMax);
+          if (see == 0ull || (before != kNegInf && now <= before + kSlack)) now = before;
+          s_m[grp * kRows + r] = now;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m_full[warp]);
+          // Roots of factors: what is 2^64 above an old m may matter 2^-126 above the new one, where
+          // 2^(old - new) is long zero.
+          if (now != before && before != kNegInf) f = exp2_approx(0.5f * (before - now));
+          const bool other = now != m;
+          if (other) {
+            const float fl = m == kNegInf ? 0.f : exp2_approx(0.5f * (m - now));
+            l = l * fl * fl;
             m = now;
           }
+          if (!__any_sync(0xffffffffu, other)) break;
         }
         l += sum;
-        s_f[ps * kRows + r] = f;
+        s_f[grp * kRows + r] = f;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[slot]);
+        ok = wait_phase<true>(&p_free[in], (i / kIn & 1) ^ 1u, s_abort, err);
+        if (!ok) return;
         if (lane == 0) {
-          mbar_arrive(&s_free[slot]);
-          const uint32_t bar = peer(smem_u32(&p_full[ps]), 1);
-          const uint32_t from = smem0 + kOffP + ps * kP + rows_at;
-          copy_to_peer(peer(from, 1), from, 32 * 128, bar);
-          const uint32_t f_at = smem_u32(s_f + ps * kRows + warp * 32);
-          copy_to_peer(peer(f_at, 1), f_at, 128, bar);
+          const uint32_t bar = peer(smem_u32(&p_full[in]), 1);
+          copy_to_peer(peer(smem0 + kOffPIn + in * kP + rows_at, 1), smem0 + kOffP + grp * kP + rows_at,
+                       32 * 128, bar);
+          copy_to_peer(peer(smem_u32(s_f + in * kRows + quad * 32), 1),
+                       smem_u32(s_f + grp * kRows + quad * 32), 128, bar);
         }
         __syncwarp();
-        if (++slot == 3) slot = 0, s_parity ^= 1u;
       };
+      const bool holes = p.place.table != nullptr;  // a page may be missing among the sequence's rows
 #pragma unroll 1
-      for (int i = 0; i < g.n && ok; ++i) {
-        // (a page that is missing leaves holes among the sequence's rows as well)
+      for (int i = grp; i < g.n && ok; i += 2) {
         if (i < g.plain) {
-          ok = wait_phase<false>(&s_ready[slot], s_parity, s_abort, err);
+          if (holes) ok = wait_phase<false>(&s_ready[i % 3], (i / 3) & 1, s_abort, err);
           if (!ok) break;
-          if (s_there[i & 7] == ~0ull) {
+          if (!holes || s_there[i & 7] == ~0ull) {
             tile_step(i, std::false_type{});
             continue;
           }
         }
         tile_step(i, std::true_type{});
       }
-      if (padding) m = kNegInf, l = 0.f;
-      // ---------------- the rows' sums, to rank 1
-      st_peer(peer(smem_u32(s_l + r), 1), l);
-      st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
-      __syncwarp();
-      if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
-      if (p.splits > 1) {
-        const int k = excess(l);
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
-        p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
-      } else if (used && p.lse) {
-        p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
+      // ---------------- both groups' sums, to rank 1
+      s_l[grp * kRows + r] = l;
+      s_l[(2 + grp) * kRows + r] = m;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (grp == 0) {
+        m = g.n > 0 ? s_m[((g.n - 1) & 1) * kRows + r] : kNegInf;
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float mk = s_l[(2 + k) * kRows + r];
+          const float fl = mk == m ? 1.f : exp2_approx(0.5f * (mk - m));
+          if (mk != kNegInf) l += s_l[k * kRows + r] * fl * fl;
+        }
+        if (padding) m = kNegInf, l = 0.f;
+        st_peer(peer(smem_u32(s_l + r), 1), l);
+        st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
+        __syncwarp();
+        if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
+        if (p.splits > 1) {
+          const int k = excess(l);
+          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
+          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
+        } else if (used && p.lse) {
+          p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
+        }
       }
     } else {
-      // ---------------- O: rescaled where m was raised, at the end written
+      // ---------------- O: rescaled where m was raised, at the end written; 256 columns a group
+      const uint32_t o = lanes + grp * kHalf;
       uint32_t seen = 0;  // P tiles that have come
       if (tid == 0)
-        for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
+        for (int i = 0; i < kIn; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i) {
-        const int slot = i & 1;
-        const uint32_t parity = (i >> 1) & 1;
+        const int slot = i & (kIn - 1);
+        const uint32_t parity = i / kIn & 1;
         ok = wait_phase<false>(&p_full[slot], parity, s_abort, err);
         if (!ok) break;
+        if (tid == 0) arrive_peer(peer(smem_u32(&p_sent[i & 1]), 0));
         ++seen;
         const float f = s_f[slot * kRows + r];
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < kLatent; c += 32) {
+          for (int c = 0; c < kHalf; c += 32) {
             uint32_t v[32];
-            tmem_ld32(lanes + c, v);
+            tmem_ld32(o + c, v);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f * f);
-            tmem_st32(lanes + c, v);
+            tmem_st32(o + c, v);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -899,14 +948,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&scaled[slot]);
         ok = wait_phase<false>(&pv_done[slot], parity, s_abort, err);
         if (!ok) break;
-        if (tid == 0 && i + 2 < g.n) mbar_arrive_expect_tx(&p_full[slot], kPBytes);
+        if (tid == 0 && i + kIn < g.n) mbar_arrive_expect_tx(&p_full[slot], kPBytes);
         __syncwarp();
         if (lane == 0) arrive_peer(peer(smem_u32(&p_free[slot]), 0));
       }
       // never leave with copies in flight to here (after an abort: bounded)
       if (!ok && tid == 0)
         for (uint32_t i = seen; i < min(seen + 2, static_cast<uint32_t>(g.n)); ++i)
-          mbar_drain(&p_full[i & 1], (i >> 1) & 1);
+          mbar_drain(&p_full[i & (kIn - 1)], i / kIn & 1);
       __syncwarp();
       ok = wait_phase<true>(l_full, 0u, s_abort, err) && ok;
       tc_fence_after();
@@ -914,12 +963,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const bool none = s_l[kRows + r] == kNegInf;
       if (p.splits == 1) {
         const float inv = none ? 0.f : 1.f / l;
-        uint16_t* dst = p.out + out_row * kLatent;
+        uint16_t* dst = p.out + out_row * kLatent + grp * kHalf;
 #pragma unroll 1
-        for (int c = 0; c < kLatent; c += 32) {
+        for (int c = 0; c < kHalf; c += 32) {
           uint32_t v[32], pk[16];
           if (g.n > 0) {
-            tmem_ld32(lanes + c, v);
+            tmem_ld32(o + c, v);
             tmem_wait_ld();
           }
 #pragma unroll
@@ -936,11 +985,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       } else if (g.n > 0 && ok) {
         const float f = power(-excess(l));
         float4* dst =
-            reinterpret_cast<float4*>(p.part_o) + static_cast<int64_t>(item) * 128 * kRows + r;
+            reinterpret_cast<float4*>(p.part_o) + (static_cast<int64_t>(item) * 128 + grp * 64) * kRows + r;
 #pragma unroll 1
-        for (int c = 0; c < kLatent; c += 32) {
+        for (int c = 0; c < kHalf; c += 32) {
           uint32_t v[32];
-          tmem_ld32(lanes + c, v);
+          tmem_ld32(o + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -1011,16 +1060,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           if (++slot == 3) slot = 0, s_parity ^= 1u;
         }
       } else {
-        const uint64_t p0 = smem_desc_sw128(smem0 + kOffP), v0 = smem_desc_mn_sw128(smem0, kChunk);
+        const uint64_t p0 = smem_desc_sw128(smem0 + kOffPIn), v0 = smem_desc_mn_sw128(smem0, kChunk);
         constexpr uint32_t idesc = instr_desc(1u, 1u, kRows, kHalf) | (1u << 16);  // B MN-major
 #pragma unroll 1
         for (int i = 0; ok && i < g.n; ++i) {
-          const int slot = i & 1;
-          ok = wait_phase<false>(&p_full[slot], (i >> 1) & 1, s_abort, err);
+          const int slot = i & (kIn - 1);
+          const uint32_t parity = i / kIn & 1;
+          ok = wait_phase<false>(&p_full[slot], parity, s_abort, err);
           if (!ok) break;
           const float4 f = reinterpret_cast<const float4*>(s_f + slot * kRows)[lane];
           if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f))
-            ok = wait_phase<false>(&scaled[slot], (i >> 1) & 1, s_abort, err);
+            ok = wait_phase<false>(&scaled[slot], parity, s_abort, err);
           const uint64_t pd = p0 + slot * (kP >> 4);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
