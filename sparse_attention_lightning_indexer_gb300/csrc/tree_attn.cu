@@ -23,9 +23,10 @@
 // and a tile took 7000 clocks.
 //
 // 8-bit rows are operands without their scales, which are powers of two: S is multiplied by them, and so is
-// P, exactly. As keys the codes are f16, one conversion for two of them; the rotary dims (bf16) are divided
-// by the scale before, and Q is scaled by a power of two to f16's range: exact too, but for what of a row of
-// Q lies 2^38 below its largest value. As values the codes are bf16 (P needs bf16's range).
+// P, exactly. As keys they are E4M3 operands as they stand, and Q, scaled by a power of two, is a sum of an
+// E4M3 and an E5M2 operand: two products at twice the rate, and nothing to unpack. That sum holds a bf16
+// exactly, but for what of a row of Q lies 2^13 and more below its largest value: that is off by at most
+// 2^-21 of the largest (bf16_to_f8_pair). As values the codes are bf16 (P needs its range and bits).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -55,7 +56,8 @@ constexpr int kHalf = 256;             // latent dims of a part
 constexpr int kLoad0 = 8, kLoaders = 8, kMmaWarp = 16;
 constexpr int kThreads = 17 * 32;
 constexpr int kChunk = kKeys * 128;    // 64 dims of a tile's keys
-constexpr int kPart = 4 * kChunk, kParts = 3;
+constexpr int kPart = 4 * kChunk, kParts = 3;      // the ring of operands
+constexpr int kPart8 = 2 * kChunk, kParts8 = 7;    // of 8-bit keys, 128 dims a chunk (in the same place)
 constexpr int kRaw = kKeys * 256, kRaws = 3;       // codes of a part as they are read
 constexpr int kOffRaw = kParts * kPart;
 constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of four tiles' keys (rank 0)
@@ -68,14 +70,15 @@ constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and 
 constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
                                                    // rows), or two tiles' codes of scales (4-bit rows)
 constexpr int kOffThere = kOffScale + 4096;  // uint64 [8 tiles]: keys that are there
-constexpr int kOffOdd = kOffThere + 8 * 8;         // uint64 [8 tiles][2 halves]: keys not finite
-constexpr int kOffBars = kOffOdd + 8 * 16;
-constexpr int kNumBars = 2 * kParts + 1 + 2 * 3 + 2 + 4 * kIn + 8 + 2;
+constexpr int kOffBars = kOffThere + 8 * 8;
+constexpr int kNumBars = 2 * kParts8 + 1 + 2 * 3 + 2 + 4 * kIn + 8 + 2;
+static_assert(kParts8 * kPart8 <= kOffRope && kParts8 >= kParts, "8-bit keys");
 static_assert(kOffPIn + kIn * kP <= kOffF, "P of rank 1");
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
 constexpr uint32_t kColRope = 256, kColS = 320;    // rank 0: Q from column 0, S; rank 1: O from 0
+constexpr uint32_t kColLow = 128;                  // the low parts of Q beside 8-bit keys
 constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
 // log2 of what exp2(s - m) may be before m is raised. P and the sums are floating point with 2^127 of
 // range, so a stale m costs no precision: 2^64 leaves 2^63 for the count and size of the values. (With 2^8
@@ -281,7 +284,7 @@ template <int kFormat, bool kKey>
 __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b, int w, int lane,
                                           uint8_t* smem, uint64_t* part_full, uint64_t* part_empty,
                                           volatile uint32_t* abort_flag) {
-  constexpr bool kF16 = kKey && kFormat == DS4IDX_CACHE_FP8;
+  constexpr bool k8 = kKey && kFormat == DS4IDX_CACHE_FP8;  // the operand is the codes
   constexpr int kStride = kFormat == DS4IDX_CACHE_FP8    ? ds4f8::kRowBytes
                           : kFormat == DS4IDX_CACHE_BF16 ? 2 * kDims
                                                          : ds4q::kRowBytes;
@@ -303,7 +306,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   uint32_t parity = 1;        // of part_empty
   auto claim = [&] { ok = ok && wait_phase<false>(&part_empty[st], parity, abort_flag, p.err); };
   auto step = [&] {
-    if (++st == kParts) st = 0, parity ^= 1u;
+    if (++st == (k8 ? kParts8 : kParts)) st = 0, parity ^= 1u;
   };
   auto publish = [&](int at) {
     fence_proxy_async_smem();
@@ -319,14 +322,9 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     for (int j = 0; j < 4; ++j) keys |= bits >> (8 * j) & 0xFFu ? 1u << j : 0u;
     return keys;
   };
-  auto note_there = [&](int i, uint32_t bits) {
-    if (lane == 0) smem[kOffThere + 8 * (i & 7) + w] = static_cast<uint8_t>(bits);
-  };
-  auto note_odd = [&](int i, int h, uint32_t bits) {
-    if (lane == 0) smem[kOffOdd + 16 * (i & 7) + 8 * h + w] = static_cast<uint8_t>(bits);
-  };
-  // A drafted row that some rows of the tile see and others do not may hold values that are not finite:
-  // what is not is cleared, since 0 * NaN would reach all of O, and the key's scores become NaN instead.
+  // A drafted row that some rows of the tile see and others do not may hold values that are not finite: as
+  // a value what is not is cleared, since 0 * NaN would reach all of O. (The nodes that see it have its
+  // scores, and from them NaN.)
   auto drafted = [&](int i, int key) { return g.position(i) + 8 * w + key >= g.len; };
   auto rope_address = [&](int i, int key) {
     return smem0 + kOffRope + (i & 3) * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
@@ -338,7 +336,6 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
 #pragma unroll
   for (int k = 0; k < 2; ++k) row[k] = row_of(0, 4 * k + sub), next[k] = steps ? 0 : row_of(1, 4 * k + sub);
   const uint8_t* from[2] = {row_at(max(row[0], 0)) + l8 * 16, row_at(max(row[1], 0)) + l8 * 16};
-  uint32_t there = 0;  // bytes: the keys that are there, of the tiles that are read and not yet written
   int read = 0;        // tiles whose reads are on their way
   auto advance_rows = [&] {
     ++read;
@@ -354,36 +351,82 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       from[k] = row_at(max(row[k], 0)) + l8 * 16;
     }
   };
-  auto there_bits = [&]() -> uint32_t {
-    if (steps && read < g.plain) return 0xFFu;
-    return quad_bits(row[0] >= 0) | quad_bits(row[1] >= 0) << 4;
+  auto note_there = [&] {  // of the tile that is read, for the softmax
+    if (!kKey || (steps && read < g.plain)) return;
+    const uint32_t bits = quad_bits(row[0] >= 0) | quad_bits(row[1] >= 0) << 4;
+    if (lane == 0) smem[kOffThere + 8 * (read & 7) + w] = static_cast<uint8_t>(bits);
   };
 
-  if constexpr (kFormat == DS4IDX_CACHE_FP8) {
-    // a part: two lines of 128 codes (c) of rows sub and 4 + sub (k), 16 codes a lane. Three parts are on
-    // their way, each with a group of copies; a tile's scales and rotary dims come with its first half.
-    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw part, + 1024 c + 512 k
-    int raw_in = 0, raw_out = 0;  // places of the part to be read next, and of the one to be turned next
-    auto copy = [&](int h, int c, int k) {
-      cp_async16(raw0 + raw_in * kRaw + 1024 * c + 512 * k,
-                 from[k] + (2 * h + c) * 128, row[k]);
-    };
-    auto copied = [&](int h) {
-      if (h == 0) {
-        if constexpr (kKey) {
+  if constexpr (k8) {
+    // Keys: the codes as they are. A part is two lines of 128 codes (c) of rows sub and 4 + sub (k); five
+    // parts are on their way. A tile's scales and rotary dims come with its first half; the rotary dims are
+    // divided by the scale in place, by the thread that copied them, with the second.
+    constexpr int kLag = 5;
+    auto finish = [&](int n, int at) {
+      if (n & 1) {
+        const float* scales = reinterpret_cast<const float*>(smem + kOffScale) + (n >> 1 & 7) * kKeys + 8 * w;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            cp_async16(rope_address(read, 4 * k + sub), from[k] + ds4f8::kOffRope, row[k]);
-          if (l8 < 2) {
-            const int32_t r = l8 ? row[1] : row[0];
-            cp_async4(smem0 + kOffScale + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4,
-                      p.scale + max(r, 0), r);
-          }
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t rope = rope_address(n >> 1, 4 * k + sub);
+          const uint32_t s2 = (254u - (__float_as_uint(scales[4 * k + sub]) >> 23 & 0xFFu)) * 0x00800080u;
+          const uint4 x = ld_shared16(rope);
+          st_shared16(rope, make_uint4(ds4q::mul_bf16x2(x.x, s2), ds4q::mul_bf16x2(x.y, s2),
+                                       ds4q::mul_bf16x2(x.z, s2), ds4q::mul_bf16x2(x.w, s2)));
         }
-        there |= there_bits() << (8 * (read & 1));
+      }
+      publish(at);
+    };
+    const uint32_t to = smem0 + (8 * w + sub) * 128 + ((l8 ^ sub) * 16);  // key sub; 4 + sub: ^ 64, + 512
+    int done = 0;  // place of the part to be published next
+#pragma unroll 1
+    for (int n = 0; n < 2 * g.n; ++n) {
+      claim();
+      if (!ok) break;
+      const int h = n & 1;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t at = to + st * kPart8 + c * kChunk;
+        cp_async16(at, from[0] + (2 * h + c) * 128, row[0]);
+        cp_async16((at ^ 64) + 512, from[1] + (2 * h + c) * 128, row[1]);
+      }
+      if (h == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          cp_async16(rope_address(read, 4 * k + sub), from[k] + ds4f8::kOffRope, row[k]);
+        if (l8 < 2) {
+          const int32_t r = l8 ? row[1] : row[0];
+          cp_async4(smem0 + kOffScale + ((read & 7) * kKeys + 8 * w + 4 * l8 + sub) * 4, p.scale + max(r, 0),
+                    r);
+        }
+        note_there();
       } else {
         advance_rows();
       }
+      cp_async_commit();
+      step();
+      if (n >= kLag) {
+        cp_async_wait<kLag>();
+        __syncwarp();
+        finish(n - kLag, done);
+        if (++done == kParts8) done = 0;
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    for (int n = max(0, 2 * g.n - kLag); ok && n < 2 * g.n; ++n) {
+      finish(n, done);
+      if (++done == kParts8) done = 0;
+    }
+  } else if constexpr (kFormat == DS4IDX_CACHE_FP8) {
+    // Values: a part is two lines of 128 codes (c) of rows sub and 4 + sub (k), 16 codes a lane. Three parts
+    // are on their way, each a group of copies.
+    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw part, + 1024 c + 512 k
+    int raw_in = 0, raw_out = 0;  // places of the part to be read next, and of the one to be turned next
+    auto copy = [&](int h, int c, int k) {
+      cp_async16(raw0 + raw_in * kRaw + 1024 * c + 512 * k, from[k] + (2 * h + c) * 128, row[k]);
+    };
+    auto copied = [&](int h) {
+      if (h == 1) advance_rows();
       cp_async_commit();
       if (++raw_in == kRaws) raw_in = 0;
     };
@@ -397,15 +440,8 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     auto part = [&](int i, int h, auto checked) {
       constexpr bool check = decltype(checked)::value;
       cp_async_wait<kRaws - 1>();
-      __syncwarp();
       claim();
       if (!ok) return;
-      float* scales = reinterpret_cast<float*>(smem + kOffScale) + (i & 7) * kKeys + 8 * w;
-      if (h == 0) {
-        note_there(i, there >> (8 * (i & 1)) & 0xFFu);
-        there &= ~(0xFFu << (8 * (i & 1)));
-      }
-      uint32_t odd_keys = 0;
       const uint32_t raw = raw0 + raw_out * kRaw;
       if (++raw_out == kRaws) raw_out = 0;
 #pragma unroll
@@ -416,45 +452,22 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           const int key = 4 * k + sub;
           uint4 x = ld_shared16(raw + 1024 * c + 512 * k);
           if constexpr (check) {
-            const bool bad = kKey && (__float_as_uint(scales[key]) & 0x7F800000u) == 0x7F800000u;
-            const bool odd = drafted(i, key) && (bad || odd_f8(x));
-            if (odd) x = zero;
-            odd_keys |= quad_bits(odd) << (4 * k);
+            if (drafted(i, key) && odd_f8(x)) x = zero;
           }
           swap_if(l8 >= 4, x.x, x.z);  // the lanes of the second chunk write their two pieces in turn
           swap_if(l8 >= 4, x.y, x.w);
           const uint32_t at = chunk + key * 128 + ((((l8 & 3) * 2 + (l8 >> 2)) ^ key) * 16);
           uint4 v, u;
-          if constexpr (kF16) {
-            ds4f8::codes_to_f16(x.x, v.x, v.y);
-            ds4f8::codes_to_f16(x.y, v.z, v.w);
-            ds4f8::codes_to_f16(x.z, u.x, u.y);
-            ds4f8::codes_to_f16(x.w, u.z, u.w);
-          } else {
-            codes_to_bf16(x.x, v.x, v.y);
-            codes_to_bf16(x.y, v.z, v.w);
-            codes_to_bf16(x.z, u.x, u.y);
-            codes_to_bf16(x.w, u.z, u.w);
-          }
+          codes_to_bf16(x.x, v.x, v.y);
+          codes_to_bf16(x.y, v.z, v.w);
+          codes_to_bf16(x.z, u.x, u.y);
+          codes_to_bf16(x.w, u.z, u.w);
           st_shared16(at, v);
           st_shared16(at ^ 16, u);
           copy(h ^ 1, c, k);
         }
       }
       copied(h ^ 1);
-      if constexpr (check) note_odd(i, h, odd_keys);
-      if (kKey && h == 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {  // the rotary dims divided by the scale, in place
-          const uint32_t at = rope_address(i, 4 * k + sub), bits = __float_as_uint(scales[4 * k + sub]);
-          if (check && (bits & 0x7F800000u) == 0x7F800000u && drafted(i, 4 * k + sub))
-            scales[4 * k + sub] = 0.f;  // (all eight lanes; its scores are NaN already)
-          const uint32_t s2 = (254u - (bits >> 23)) * 0x00800080u;
-          const uint4 x = ld_shared16(at);
-          st_shared16(at, make_uint4(ds4q::mul_bf16x2(x.x, s2), ds4q::mul_bf16x2(x.y, s2),
-                                     ds4q::mul_bf16x2(x.z, s2), ds4q::mul_bf16x2(x.w, s2)));
-        }
-      }
       publish(st);
       step();
     };
@@ -472,8 +485,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       for (int h = 0; h < 2; ++h) {
         claim();
         if (!ok) break;
-        const bool check = i >= g.plain;
-        uint32_t odd_keys = 0;
+        const bool check = !kKey && i >= g.plain;
 #pragma unroll 2
         for (int k = 0; k < 8; ++k) {  // rows sub and 4 + sub, a chunk of 64 dims (k >> 1)
           const int key = (k & 1) * 4 + sub;
@@ -483,9 +495,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           const uint8_t* src = (k & 1 ? from[1] : from[0]) + h * 2 * kHalf + (k >> 1) * 128;
           if (check) {
             const uint4 v = ld_row16(src, r);
-            const bool odd = drafted(i, key) && odd_bf16(v);
-            st_shared16(at, odd ? zero : v);
-            odd_keys |= quad_bits(odd) << (4 * (k & 1));
+            st_shared16(at, drafted(i, key) && odd_bf16(v) ? zero : v);
           } else {
             cp_async16(at, src, r);
           }
@@ -493,8 +503,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
             cp_async16(rope_address(i, key), (k & 1 ? from[1] : from[0]) + 2 * kLatent, r);
         }
         cp_async_commit();
-        if (check) note_odd(i, h, odd_keys);
-        if (h == 0) note_there(i, there_bits());
+        if (h == 0) note_there();
         if (last >= 0) {
           cp_async_wait<1>();
           publish(last);
@@ -532,7 +541,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         for (int k = 0; k < 2; ++k)
           cp_async16(rope_address(read, 4 * k + sub), from[k] + ds4q::kOffRope, row[k]);
       }
-      there |= there_bits() << (8 * (read & 1));
+      note_there();
       cp_async_commit();
     };
 #pragma unroll 1
@@ -551,9 +560,6 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       claim();
       step();
       if (!ok) break;
-      note_there(i, there >> (8 * (i & 1)) & 0xFFu);
-      there &= ~(0xFFu << (8 * (i & 1)));
-      if (i >= g.plain) note_odd(i, 0, 0), note_odd(i, 1, 0);  // (the format has only finite values)
       const uint32_t raw = raw0 + (i & 1) * kRaw;
       const uint8_t* scales = smem + kOffScale + w * 256 + (i & 1) * 2048;
 #pragma unroll 1
@@ -609,13 +615,23 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Two bf16 to two f16, times a power of two.
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float f) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-      : "=r"(d)
-      : "f"(__uint_as_float(v & 0xFFFF0000u) * f), "f"(__uint_as_float(v << 16) * f));
-  return d;
+// Four bf16 times a power of two as sums of an E4M3 and an E5M2 number: four significant bits, and three of
+// the rest, which hold a bf16's eight exactly where the first is normal, 2^-6 and above; below that the error
+// is at most 2^-14.
+__device__ __forceinline__ void bf16_to_f8_pair(uint32_t a, uint32_t b, float f, uint32_t& hi, uint32_t& lo) {
+  const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xFFFF0000u) * f,
+                      __uint_as_float(b << 16) * f, __uint_as_float(b & 0xFFFF0000u) * f};
+  asm("{\n\t.reg .b16 u, v;\n\tcvt.rn.satfinite.e4m3x2.f32 u, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 v, %4, %3;\n\tmov.b32 %0, {u, v};\n\t}"
+      : "=r"(hi)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  uint32_t h0, h1;
+  ds4f8::codes_to_f16(hi, h0, h1);
+  const float2 y0 = ds4f8::f16x2_to_f32(h0), y1 = ds4f8::f16x2_to_f32(h1);
+  asm("{\n\t.reg .b16 u, v;\n\tcvt.rn.satfinite.e5m2x2.f32 u, %2, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 v, %4, %3;\n\tmov.b32 %0, {u, v};\n\t}"
+      : "=r"(lo)
+      : "f"(x[0] - y0.x), "f"(x[1] - y0.y), "f"(x[2] - y1.x), "f"(x[3] - y1.y));
 }
 
 template <int kFormat>
@@ -630,10 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
   const float* s_scale = reinterpret_cast<const float*>(smem + kOffScale);
   volatile uint64_t* s_there = reinterpret_cast<uint64_t*>(smem + kOffThere);
-  volatile uint64_t* s_odd = reinterpret_cast<uint64_t*>(smem + kOffOdd);
   uint64_t* part_full = reinterpret_cast<uint64_t*>(smem + kOffBars);
-  uint64_t* part_empty = part_full + kParts;
-  uint64_t* q_full = part_empty + kParts;
+  uint64_t* part_empty = part_full + kParts8;
+  uint64_t* q_full = part_empty + kParts8;
   uint64_t* s_ready = q_full + 1;   // [3] S of a tile is formed
   uint64_t* s_free = s_ready + 3;   // [3] and read
   uint64_t* p_sent = s_free + 3;    // [2] P has come to rank 1 (in rank 0)
@@ -653,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   constexpr uint32_t kPBytes = kP + kRows * 4;  // what comes with a tile: P and the factors
 
   if (tid == 0) {
-    for (int i = 0; i < kParts; ++i) {
+    for (int i = 0; i < kParts8; ++i) {
       mbar_init(&part_full[i], kLoaders);
       mbar_init(&part_empty[i], 1);
     }
@@ -688,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   cluster_sync();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  constexpr bool kF16 = kFormat == DS4IDX_CACHE_FP8;  // the key product's type
+  constexpr bool k8 = kFormat == DS4IDX_CACHE_FP8;
 
   if (warp < kLoad0) {
     const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
@@ -709,8 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         const uint4 zero = make_uint4(0, 0, 0, 0);
         float f = 1.f;
         uint32_t f2 = 0;
-        if constexpr (kF16) {
-          // the power of two that takes the row's largest value to 2^13 .. 2^14
+        if constexpr (k8) {
+          // the power of two that takes the row's largest value to 2^7 .. 2^8
           uint32_t top = 0;
 #pragma unroll 8
           for (int j = 0; j < kDims / 8; ++j) {
@@ -719,10 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                                          __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
           }
           const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);   // biased by 127
-          const int a = max(-110, min(110, e == 0 ? 0 : 127 + 13 - e));         // (zero: any)
-          f = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
+          const int a = max(-110, min(110, e == 0 ? 0 : 127 + 7 - e));          // (zero: any)
+          f = power(a);
           f2 = static_cast<uint32_t>(127 + a) * 0x00800080u;
-          to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+          to_log2 *= power(-a);
         }
 #pragma unroll 1
         for (int h = grp; h < 9; h += 2) {  // the rotary dims last
@@ -735,12 +750,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             v[4 * j + 2] = x.z;
             v[4 * j + 3] = x.w;
           }
-          if constexpr (kF16) {
+          if (k8 && h < 8) {
+            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = h < 8 ? bf16x2_to_f16x2(v[j], f) : ds4q::mul_bf16x2(v[j], f2);
+            for (int j = 0; j < 16; ++j) bf16_to_f8_pair(v[2 * j], v[2 * j + 1], f, hi[j], lo[j]);
+            tmem_st16(lanes + h * 16, hi);
+            tmem_st16(lanes + kColLow + h * 16, lo);
+          } else {
+            if constexpr (k8) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
+            }
+            tmem_st32(lanes + h * 32, v);
           }
-          tmem_st32(lanes + h * 32, v);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -759,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (!ok) return;
         tc_fence_after();
         // which keys this row sees (all, of padding: what its row becomes is not used)
-        uint64_t see = ~0ull, bad = 0ull;
+        uint64_t see = ~0ull;
         if constexpr (kMasked) {
           see = s_there[at];
           if (i >= g.plain) {
@@ -768,7 +790,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                    : left >= 0   ? ((1ull << left) - 1ull) | mask << left
                    : left > -64  ? mask >> -left
                                  : 0ull;
-            bad = s_odd[2 * at] | s_odd[2 * at + 1];
           }
         }
         // P with this group's m, in the layout of an MMA A operand; once more where m is another one now
@@ -783,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             uint32_t s[32];  // fp32 bits
             tmem_ld32(lanes + kColS + slot * kKeys + 32 * h, s);
             tmem_wait_ld();
-            if constexpr (kF16) {
+            if constexpr (k8) {
               const uint32_t sc = smem0 + kOffScale + (at * kKeys + 32 * h) * 4;
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
@@ -794,10 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             }
             if constexpr (kMasked) {  // a masked score is -infinity: p = 0 whatever m, and no maximum
               const uint32_t on = static_cast<uint32_t>(see >> (32 * h));
-              const uint32_t nan = static_cast<uint32_t>(bad >> (32 * h));
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                s[j] = on >> j & 1 ? (nan >> j & 1 ? 0x7FC00000u : s[j]) : 0xFF800000u;
+              for (int j = 0; j < 32; ++j) s[j] = on >> j & 1 ? s[j] : 0xFF800000u;
             }
 #pragma unroll
             for (int j = 0; j < 32; j += 2)
@@ -806,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             for (int u = 0; u < 4; ++u) {
               uint32_t pk[4];
               [[maybe_unused]] float4 sa, sb;
-              if constexpr (kF16) {
+              if constexpr (k8) {
                 const float4* x = reinterpret_cast<const float4*>(s_scale + at * kKeys + 32 * h + 8 * u);
                 sa = x[0];
                 sb = x[1];
@@ -821,9 +840,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                 x0 = exp2_approx(x0);
                 x1 = exp2_approx(x1);
                 sum2 = add_f32x2(sum2, pack_f32x2(x0, x1));
-                if constexpr (kF16) {  // the values are codes as well
+                if constexpr (k8) {  // the values are codes as well
                   x0 *= j < 2 ? (j ? sa.z : sa.x) : (j == 3 ? sb.z : sb.x);
                   x1 *= j < 2 ? (j ? sa.w : sa.y) : (j == 3 ? sb.w : sb.y);
+                  if constexpr (kMasked) {  // (0 times a scale that is not finite)
+                    x0 = see >> (32 * h + k) & 1 ? x0 : 0.f;
+                    x1 = see >> (32 * h + k + 1) & 1 ? x1 : 0.f;
+                  }
                 }
                 pk[j] = pack_bf16x2(x0, x1);
               }
@@ -1020,12 +1043,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       };
       auto part_taken = [&] {
         commit(&part_empty[st]);
-        if (++st == kParts) st = 0, parity ^= 1u;
+        if (++st == (k8 && rank == 0 ? kParts8 : kParts)) st = 0, parity ^= 1u;
       };
       if (rank == 0) {
         const uint64_t k0 = smem_desc_sw128(smem0), r0 = smem_desc_sw128(smem0 + kOffRope);
-        constexpr uint32_t rope_idesc = instr_desc(1u, 1u, kRows, kKeys);
-        constexpr uint32_t idesc = kF16 ? instr_desc(0u, 0u, kRows, kKeys) : rope_idesc;
+        constexpr uint32_t idesc = instr_desc(1u, 1u, kRows, kKeys);
+        constexpr uint32_t hi_idesc = instr_desc(0u, 0u, kRows, kKeys);  // E4M3 x E4M3
+        constexpr uint32_t lo_idesc = instr_desc(1u, 0u, kRows, kKeys);  // E5M2 x E4M3
         if (g.n > 0) ok = wait_phase<false>(q_full, 0u, s_abort, err);
         int slot = 0;
         uint32_t s_parity = 1;
@@ -1037,21 +1061,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           for (int h = 0; h < 2; ++h) {
             part_ready();
             if (!ok) break;
-            const uint64_t kd = k0 + st * (kPart >> 4);
-            if (lead) {
+            if constexpr (k8) {
+              const uint64_t kd = k0 + st * (kPart8 >> 4);
+              if (lead) {
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_bf16_ts(d, tmem + h * 128 + c * 32 + k * 8, kd + c * (kChunk >> 4) + k * 2, idesc,
-                              (h | c | k) ? 1u : 0u);
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t col = tmem + h * 64 + c * 32 + k * 8;
+                    const uint64_t b_desc = kd + c * (kChunk >> 4) + k * 2;
+                    mma_fp8_ts(d, col, b_desc, hi_idesc, (h | c | k) ? 1u : 0u);
+                    mma_fp8_ts(d, col + kColLow, b_desc, lo_idesc, 1u);
+                  }
+                }
+              }
+            } else {
+              const uint64_t kd = k0 + st * (kPart >> 4);
+              if (lead) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    mma_bf16_ts(d, tmem + h * 128 + c * 32 + k * 8, kd + c * (kChunk >> 4) + k * 2, idesc,
+                                (h | c | k) ? 1u : 0u);
+                }
               }
             }
             if (h == 1 && lead) {
               const uint64_t rd = r0 + (i & 3) * (kChunk >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_bf16_ts(d, tmem + kColRope + k * 8, rd + 2 * k, rope_idesc, 1u);
+                mma_bf16_ts(d, tmem + kColRope + k * 8, rd + 2 * k, idesc, 1u);
             }
             part_taken();
           }
