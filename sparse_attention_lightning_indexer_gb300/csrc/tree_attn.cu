@@ -63,6 +63,12 @@ constexpr int kOffRaw = kParts * kPart;
 constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of four tiles' keys (rank 0)
 constexpr int kOffP = kOffRope + 4 * kChunk, kP = kRows * kKeys * 2;  // P as it is made (rank 0)
 constexpr int kIn = 4;                             // tiles of P on their way to rank 1 or in use there
+// Tiles of P in rank 0: it takes some 2500 clocks until rank 1 has said that a tile has come, so four, two of
+// them where 4-bit rows keep codes as they are read.
+__host__ __device__ constexpr int out_slots(int format) { return format == DS4IDX_CACHE_Q4 ? 2 : 4; }
+__host__ __device__ constexpr int out_offset(int slot) {
+  return slot < 2 ? kOffP + slot * kP : kOffRaw + kRaw + (slot - 2) * kP;
+}
 constexpr int kOffPIn = kOffRope;                  // (rank 1 has no rotary dims)
 constexpr int kOffF = kOffP + 2 * kP;              // float [4][128]: roots of factors of O before P V
 constexpr int kOffM = kOffF + kIn * kRows * 4;       // float [2][128]: m after an even, an odd tile
@@ -71,8 +77,8 @@ constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scale
                                                    // rows), or two tiles' codes of scales (4-bit rows)
 constexpr int kOffThere = kOffScale + 4096;  // uint64 [8 tiles]: keys that are there
 constexpr int kOffBars = kOffThere + 8 * 8;
-constexpr int kNumBars = 2 * kParts8 + 1 + 2 * 3 + 2 + 4 * kIn + 8 + 2;
-static_assert(kParts8 * kPart8 <= kOffRope && kParts8 >= kParts, "8-bit keys");
+constexpr int kNumBars = 2 * kParts8 + 1 + 2 * 3 + 5 * kIn + 8 + 2;
+static_assert(kParts8 * kPart8 <= out_offset(2) && out_offset(3) + kP <= kOffRope && kParts8 >= kParts, "8-bit keys");
 static_assert(kOffPIn + kIn * kP <= kOffF, "P of rank 1");
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
@@ -651,8 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint64_t* q_full = part_empty + kParts8;
   uint64_t* s_ready = q_full + 1;   // [3] S of a tile is formed
   uint64_t* s_free = s_ready + 3;   // [3] and read
-  uint64_t* p_sent = s_free + 3;    // [2] P has come to rank 1 (in rank 0)
-  uint64_t* p_free = p_sent + 2;    // [4] rank 1 is done with P (in rank 0)
+  uint64_t* p_sent = s_free + 3;    // [4] P has come to rank 1 (in rank 0)
+  uint64_t* p_free = p_sent + kIn;   // [4] rank 1 is done with P (in rank 0)
   uint64_t* p_full = p_free + kIn;  // [4] P has come (in rank 1)
   uint64_t* scaled = p_full + kIn;  // [4] O is ready for P V
   uint64_t* pv_done = scaled + kIn; // [4] P V of a tile is done
@@ -677,9 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mbar_init(&s_ready[i], 1);
       mbar_init(&s_free[i], 4);
     }
-    mbar_init(&p_sent[0], 1);
-    mbar_init(&p_sent[1], 1);
     for (int i = 0; i < kIn; ++i) {
+      mbar_init(&p_sent[i], 1);
       mbar_init(&p_free[i], 8);
       mbar_init(&p_full[i], 1);
       mbar_init(&scaled[i], 8);
@@ -771,13 +776,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
       float m = kNegInf, l = 0.f;
       const uint32_t rows_at = quad * 32 * 128;  // this warp's rows of P
-      const uint32_t p_at = smem0 + kOffP + grp * kP + r * 128 + (r & 7) * 16;
+      constexpr int kOut = out_slots(kFormat);
       auto tile_step = [&](int i, auto masked) {
         constexpr bool kMasked = decltype(masked)::value;
-        const uint32_t use = i >> 1;
-        const int slot = i % 3, at = i & 7, in = i & (kIn - 1);
+        const int slot = i % 3, at = i & 7, in = i & (kIn - 1), made = i & (kOut - 1);
+        const uint32_t tile_at = smem0 + out_offset(made), p_at = tile_at + r * 128 + (r & 7) * 16;
         ok = wait_phase<false>(&s_ready[slot], (i / 3) & 1, s_abort, err) &&
-             wait_phase<true>(&p_sent[grp], (use & 1) ^ 1u, s_abort, err);
+             wait_phase<true>(&p_sent[made], (i / kOut & 1) ^ 1u, s_abort, err);
         if (!ok) return;
         tc_fence_after();
         // which keys this row sees (all, of padding: what its row becomes is not used)
@@ -883,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           if (!__any_sync(0xffffffffu, other)) break;
         }
         l += sum;
-        s_f[grp * kRows + r] = f;
+        s_f[made * kRows + r] = f;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -892,10 +897,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (!ok) return;
         if (lane == 0) {
           const uint32_t bar = peer(smem_u32(&p_full[in]), 1);
-          copy_to_peer(peer(smem0 + kOffPIn + in * kP + rows_at, 1), smem0 + kOffP + grp * kP + rows_at,
+          copy_to_peer(peer(smem0 + kOffPIn + in * kP + rows_at, 1), tile_at + rows_at,
                        32 * 128, bar);
           copy_to_peer(peer(smem_u32(s_f + in * kRows + quad * 32), 1),
-                       smem_u32(s_f + grp * kRows + quad * 32), 128, bar);
+                       smem_u32(s_f + made * kRows + quad * 32), 128, bar);
         }
         __syncwarp();
       };
@@ -950,7 +955,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         const uint32_t parity = i / kIn & 1;
         ok = wait_phase<false>(&p_full[slot], parity, s_abort, err);
         if (!ok) break;
-        if (tid == 0) arrive_peer(peer(smem_u32(&p_sent[i & 1]), 0));
         ++seen;
         const float f = s_f[slot * kRows + r];
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
@@ -977,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
       // never leave with copies in flight to here (after an abort: bounded)
       if (!ok && tid == 0)
-        for (uint32_t i = seen; i < min(seen + 2, static_cast<uint32_t>(g.n)); ++i)
+        for (uint32_t i = seen; i < min(seen + kIn, static_cast<uint32_t>(g.n)); ++i)
           mbar_drain(&p_full[i & (kIn - 1)], i / kIn & 1);
       __syncwarp();
       ok = wait_phase<true>(l_full, 0u, s_abort, err) && ok;
@@ -1108,6 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           const uint32_t parity = i / kIn & 1;
           ok = wait_phase<false>(&p_full[slot], parity, s_abort, err);
           if (!ok) break;
+          if (lane == 0) arrive_peer(peer(smem_u32(&p_sent[i & (out_slots(kFormat) - 1)]), 0));
           const float4 f = reinterpret_cast<const float4*>(s_f + slot * kRows)[lane];
           if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f))
             ok = wait_phase<false>(&scaled[slot], parity, s_abort, err);
