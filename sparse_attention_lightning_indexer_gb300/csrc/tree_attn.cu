@@ -61,25 +61,18 @@ constexpr int kPart8 = 2 * kChunk, kParts8 = 7;    // of 8-bit keys, 128 dims a 
 constexpr int kRaw = kKeys * 256, kRaws = 3;       // codes of a part as they are read
 constexpr int kOffRaw = kParts * kPart;
 constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of four tiles' keys (rank 0)
-constexpr int kOffP = kOffRope + 4 * kChunk, kP = kRows * kKeys * 2;  // P as it is made (rank 0)
+constexpr int kP = kRows * kKeys * 2;              // P of a tile
 constexpr int kIn = 4;                             // tiles of P on their way to rank 1 or in use there
-// Tiles of P in rank 0: it takes some 2500 clocks until rank 1 has said that a tile has come, so four, two of
-// them where 4-bit rows keep codes as they are read.
-__host__ __device__ constexpr int out_slots(int format) { return format == DS4IDX_CACHE_Q4 ? 2 : 4; }
-__host__ __device__ constexpr int out_offset(int slot) {
-  return slot < 2 ? kOffP + slot * kP : kOffRaw + kRaw + (slot - 2) * kP;
-}
-constexpr int kOffPIn = kOffRope;                  // (rank 1 has no rotary dims)
-constexpr int kOffF = kOffP + 2 * kP;              // float [4][128]: roots of factors of O before P V
+constexpr int kOffP = kOffRope;                    // in rank 1, which has no rotary dims
+constexpr int kOffF = kOffP + kIn * kP;              // float [4][128]: roots of factors of O before P V
 constexpr int kOffM = kOffF + kIn * kRows * 4;       // float [2][128]: m after an even, an odd tile
 constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
 constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
                                                    // rows), or two tiles' codes of scales (4-bit rows)
 constexpr int kOffThere = kOffScale + 4096;  // uint64 [8 tiles]: keys that are there
 constexpr int kOffBars = kOffThere + 8 * 8;
-constexpr int kNumBars = 2 * kParts8 + 1 + 2 * 3 + 5 * kIn + 8 + 2;
-static_assert(kParts8 * kPart8 <= out_offset(2) && out_offset(3) + kP <= kOffRope && kParts8 >= kParts, "8-bit keys");
-static_assert(kOffPIn + kIn * kP <= kOffF, "P of rank 1");
+constexpr int kNumBars = 2 * kParts8 + 1 + 2 * 3 + 4 * kIn + 8 + 2;
+static_assert(kParts8 * kPart8 <= kOffRope && kParts8 >= kParts, "8-bit keys");
 constexpr int kOffMisc = kOffBars + kNumBars * 8;
 constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
@@ -200,14 +193,13 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 __device__ __forceinline__ void st_peer(uint32_t at, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-__device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_t bytes,
-                                             uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "r"(src), "r"(bytes), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void st_peer16(uint32_t at, const uint32_t (&v)[4]) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
 }
+// Orders generic accesses, those to another CTA's shared memory among them, before later ones of MMAs.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -657,8 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint64_t* q_full = part_empty + kParts8;
   uint64_t* s_ready = q_full + 1;   // [3] S of a tile is formed
   uint64_t* s_free = s_ready + 3;   // [3] and read
-  uint64_t* p_sent = s_free + 3;    // [4] P has come to rank 1 (in rank 0)
-  uint64_t* p_free = p_sent + kIn;   // [4] rank 1 is done with P (in rank 0)
+  uint64_t* p_free = s_free + 3;      // [4] rank 1 is done with P (in rank 0)
   uint64_t* p_full = p_free + kIn;  // [4] P has come (in rank 1)
   uint64_t* scaled = p_full + kIn;  // [4] O is ready for P V
   uint64_t* pv_done = scaled + kIn; // [4] P V of a tile is done
@@ -671,7 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const int rank = blockIdx.x & 1, item = blockIdx.x >> 1;
   const int split = item % p.splits, tile = item / p.splits % p.tiles, b = item / (p.splits * p.tiles);
   uint32_t* err = p.err;
-  constexpr uint32_t kPBytes = kP + kRows * 4;  // what comes with a tile: P and the factors
 
   if (tid == 0) {
     for (int i = 0; i < kParts8; ++i) {
@@ -684,9 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mbar_init(&s_free[i], 4);
     }
     for (int i = 0; i < kIn; ++i) {
-      mbar_init(&p_sent[i], 1);
       mbar_init(&p_free[i], 8);
-      mbar_init(&p_full[i], 1);
+      mbar_init(&p_full[i], 4);
       mbar_init(&scaled[i], 8);
       mbar_init(&pv_done[i], 1);
     }
@@ -775,14 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (lane == 0) mbar_arrive(q_full);
       }
       float m = kNegInf, l = 0.f;
-      const uint32_t rows_at = quad * 32 * 128;  // this warp's rows of P
-      constexpr int kOut = out_slots(kFormat);
+      const uint32_t p_row = peer(smem0 + kOffP + r * 128 + (r & 7) * 16, 1);  // + kP * place
+      const uint32_t f_row = peer(smem_u32(s_f + r), 1);
       auto tile_step = [&](int i, auto masked) {
         constexpr bool kMasked = decltype(masked)::value;
-        const int slot = i % 3, at = i & 7, in = i & (kIn - 1), made = i & (kOut - 1);
-        const uint32_t tile_at = smem0 + out_offset(made), p_at = tile_at + r * 128 + (r & 7) * 16;
+        const int slot = i % 3, at = i & 7, in = i & (kIn - 1);
+        const uint32_t p_at = p_row + in * kP;
         ok = wait_phase<false>(&s_ready[slot], (i / 3) & 1, s_abort, err) &&
-             wait_phase<true>(&p_sent[made], (i / kOut & 1) ^ 1u, s_abort, err);
+             wait_phase<true>(&p_free[in], (i / kIn & 1) ^ 1u, s_abort, err);
         if (!ok) return;
         tc_fence_after();
         // which keys this row sees (all, of padding: what its row becomes is not used)
@@ -797,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                                  : 0ull;
           }
         }
-        // P with this group's m, in the layout of an MMA A operand; once more where m is another one now
+        // P with this group's m, in the layout of an MMA A operand, to rank 1; once more where m is another now
         float f = 1.f, sum;
         for (int pass = 0;; ++pass) {  // (at most twice)
           const float off = m == kNegInf ? 0.f : -m;
@@ -855,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                 }
                 pk[j] = pack_bf16x2(x0, x1);
               }
-              st_shared16(p_at ^ (16 * (4 * h + u)), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+              st_peer16(p_at ^ (16 * (4 * h + u)), pk);
             }
           }
           float l0, l1;
@@ -888,19 +877,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           if (!__any_sync(0xffffffffu, other)) break;
         }
         l += sum;
-        s_f[made * kRows + r] = f;
-        fence_proxy_async_smem();
+        st_peer(f_row + in * kRows * 4, f);
+        fence_proxy_async();  // P before the products that read it
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[slot]);
-        ok = wait_phase<true>(&p_free[in], (i / kIn & 1) ^ 1u, s_abort, err);
-        if (!ok) return;
         if (lane == 0) {
-          const uint32_t bar = peer(smem_u32(&p_full[in]), 1);
-          copy_to_peer(peer(smem0 + kOffPIn + in * kP + rows_at, 1), tile_at + rows_at,
-                       32 * 128, bar);
-          copy_to_peer(peer(smem_u32(s_f + in * kRows + quad * 32), 1),
-                       smem_u32(s_f + made * kRows + quad * 32), 128, bar);
+          mbar_arrive(&s_free[slot]);
+          arrive_peer(peer(smem_u32(&p_full[in]), 1));
         }
         __syncwarp();
       };
@@ -946,16 +929,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     } else {
       // ---------------- O: rescaled where m was raised, at the end written; 256 columns a group
       const uint32_t o = lanes + grp * kHalf;
-      uint32_t seen = 0;  // P tiles that have come
-      if (tid == 0)
-        for (int i = 0; i < kIn; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i) {
         const int slot = i & (kIn - 1);
         const uint32_t parity = i / kIn & 1;
-        ok = wait_phase<false>(&p_full[slot], parity, s_abort, err);
+        ok = wait_phase<true>(&p_full[slot], parity, s_abort, err);
         if (!ok) break;
-        ++seen;
         const float f = s_f[slot * kRows + r];
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
           tc_fence_after();
@@ -975,15 +954,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&scaled[slot]);
         ok = wait_phase<false>(&pv_done[slot], parity, s_abort, err);
         if (!ok) break;
-        if (tid == 0 && i + kIn < g.n) mbar_arrive_expect_tx(&p_full[slot], kPBytes);
-        __syncwarp();
         if (lane == 0) arrive_peer(peer(smem_u32(&p_free[slot]), 0));
       }
-      // never leave with copies in flight to here (after an abort: bounded)
-      if (!ok && tid == 0)
-        for (uint32_t i = seen; i < min(seen + kIn, static_cast<uint32_t>(g.n)); ++i)
-          mbar_drain(&p_full[i & (kIn - 1)], i / kIn & 1);
-      __syncwarp();
       ok = wait_phase<true>(l_full, 0u, s_abort, err) && ok;
       tc_fence_after();
       const float l = s_l[r];
@@ -1104,15 +1076,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           if (++slot == 3) slot = 0, s_parity ^= 1u;
         }
       } else {
-        const uint64_t p0 = smem_desc_sw128(smem0 + kOffPIn), v0 = smem_desc_mn_sw128(smem0, kChunk);
+        const uint64_t p0 = smem_desc_sw128(smem0 + kOffP), v0 = smem_desc_mn_sw128(smem0, kChunk);
         constexpr uint32_t idesc = instr_desc(1u, 1u, kRows, kHalf) | (1u << 16);  // B MN-major
 #pragma unroll 1
         for (int i = 0; ok && i < g.n; ++i) {
           const int slot = i & (kIn - 1);
           const uint32_t parity = i / kIn & 1;
-          ok = wait_phase<false>(&p_full[slot], parity, s_abort, err);
+          ok = wait_phase<true>(&p_full[slot], parity, s_abort, err);
           if (!ok) break;
-          if (lane == 0) arrive_peer(peer(smem_u32(&p_sent[i & (out_slots(kFormat) - 1)]), 0));
+          fence_proxy_async();
           const float4 f = reinterpret_cast<const float4*>(s_f + slot * kRows)[lane];
           if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f))
             ok = wait_phase<false>(&scaled[slot], parity, s_abort, err);
