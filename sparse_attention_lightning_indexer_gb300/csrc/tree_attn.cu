@@ -198,8 +198,10 @@ __device__ __forceinline__ void st_peer16(uint32_t at, const uint32_t (&v)[4]) {
                "r"(v[2]), "r"(v[3])
                : "memory");
 }
-// Orders generic accesses, those to another CTA's shared memory among them, before later ones of MMAs.
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// Orders generic accesses to the cluster's shared memory before later ones of MMAs.
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -419,6 +421,11 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     // Values: a part is two lines of 128 codes (c) of rows sub and 4 + sub (k), 16 codes a lane. Three parts
     // are on their way, each a group of copies.
     const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;  // + raw part, + 1024 c + 512 k
+    // Turned are the line's first 64 codes of row `sub` by lanes 0..3 of eight, and the last 64 of the row
+    // beside it by lanes 4..7: their 16-byte pieces go to different banks.
+    const int turn = sub ^ (l8 >> 2);
+    const uint32_t raw1 = smem0 + kOffRaw + w * 2048 + turn * 128 + l8 * 16;
+    const uint32_t to = smem0 + (l8 >> 2) * kChunk + (8 * w + turn) * 128 + (((l8 & 3) * 2 ^ turn) * 16);
     int raw_in = 0, raw_out = 0;  // places of the part to be read next, and of the one to be turned next
     auto copy = [&](int h, int c, int k) {
       cp_async16(raw0 + raw_in * kRaw + 1024 * c + 512 * k, from[k] + (2 * h + c) * 128, row[k]);
@@ -438,23 +445,20 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     auto part = [&](int i, int h, auto checked) {
       constexpr bool check = decltype(checked)::value;
       cp_async_wait<kRaws - 1>();
+      __syncwarp();
       claim();
       if (!ok) return;
-      const uint32_t raw = raw0 + raw_out * kRaw;
+      const uint32_t raw = raw1 + raw_out * kRaw;
       if (++raw_out == kRaws) raw_out = 0;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const uint32_t chunk = smem0 + st * kPart + (2 * c + (l8 >> 2)) * kChunk + 8 * w * 128;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int key = 4 * k + sub;
           uint4 x = ld_shared16(raw + 1024 * c + 512 * k);
           if constexpr (check) {
-            if (drafted(i, key) && odd_f8(x)) x = zero;
+            if (drafted(i, 4 * k + turn) && odd_f8(x)) x = zero;
           }
-          swap_if(l8 >= 4, x.x, x.z);  // the lanes of the second chunk write their two pieces in turn
-          swap_if(l8 >= 4, x.y, x.w);
-          const uint32_t at = chunk + key * 128 + ((((l8 & 3) * 2 + (l8 >> 2)) ^ key) * 16);
+          const uint32_t at = (to ^ (k * 64)) + st * kPart + 2 * c * kChunk + k * 512;
           uint4 v, u;
           codes_to_bf16(x.x, v.x, v.y);
           codes_to_bf16(x.y, v.z, v.w);
@@ -462,9 +466,11 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           codes_to_bf16(x.w, u.z, u.w);
           st_shared16(at, v);
           st_shared16(at ^ 16, u);
-          copy(h ^ 1, c, k);
         }
       }
+      __syncwarp();  // (another lane's copies go where these codes were)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) copy(h ^ 1, c, 0), copy(h ^ 1, c, 1);
       copied(h ^ 1);
       publish(st);
       step();
@@ -878,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         l += sum;
         st_peer(f_row + in * kRows * 4, f);
-        fence_proxy_async();  // P before the products that read it
+        fence_proxy_async_cluster();  // P before the products that read it
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -1084,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           const uint32_t parity = i / kIn & 1;
           ok = wait_phase<true>(&p_full[slot], parity, s_abort, err);
           if (!ok) break;
-          fence_proxy_async();
+          fence_proxy_async_cluster();
           const float4 f = reinterpret_cast<const float4*>(s_f + slot * kRows)[lane];
           if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f))
             ok = wait_phase<false>(&scaled[slot], parity, s_abort, err);
