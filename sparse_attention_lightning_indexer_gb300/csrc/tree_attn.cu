@@ -64,7 +64,10 @@ constexpr int kOffRope = kOffRaw + kRaws * kRaw;   // the rotary dims of four ti
 constexpr int kP = kRows * kKeys * 2;              // P of a tile
 constexpr int kIn = 4;                             // tiles of P on their way to rank 1 or in use there
 constexpr int kOffP = kOffRope;                    // in rank 1, which has no rotary dims
-constexpr int kOffF = kOffP + kIn * kP;              // float [4][128]: roots of factors of O before P V
+constexpr int kOffMade = kOffRope + 4 * kChunk;    // P of an even and of an odd tile as it is made (rank 0)
+constexpr int kOffF = kOffP + kIn * kP;
+static_assert(kOffMade + 2 * kP <= kOffF, "P");
+              // float [4][128]: roots of factors of O before P V
 constexpr int kOffM = kOffF + kIn * kRows * 4;       // float [2][128]: m after an even, an odd tile
 constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
 constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
@@ -193,9 +196,17 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 __device__ __forceinline__ void st_peer(uint32_t at, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-__device__ __forceinline__ void st_peer16(uint32_t at, const uint32_t (&v)[4]) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3])
+// Stores to another CTA's shared memory that count as bytes at a barrier there: nothing here waits for them.
+__device__ __forceinline__ void st_async16(uint32_t at, uint4 v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          at),
+      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void st_async4(uint32_t at, float v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at),
+               "r"(__float_as_uint(v)), "r"(bar)
                : "memory");
 }
 // Orders generic accesses to the cluster's shared memory before later ones of MMAs.
@@ -648,7 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   float* s_f = reinterpret_cast<float*>(smem + kOffF);
   float* s_m = reinterpret_cast<float*>(smem + kOffM);
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
-  const float* s_scale = reinterpret_cast<const float*>(smem + kOffScale);
   volatile uint64_t* s_there = reinterpret_cast<uint64_t*>(smem + kOffThere);
   uint64_t* part_full = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint64_t* part_empty = part_full + kParts8;
@@ -668,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const int rank = blockIdx.x & 1, item = blockIdx.x >> 1;
   const int split = item % p.splits, tile = item / p.splits % p.tiles, b = item / (p.splits * p.tiles);
   uint32_t* err = p.err;
+  constexpr uint32_t kPBytes = kP + kRows * 4;  // what comes with a tile: P and the factors
 
   if (tid == 0) {
     for (int i = 0; i < kParts8; ++i) {
@@ -681,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     }
     for (int i = 0; i < kIn; ++i) {
       mbar_init(&p_free[i], 8);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 1);
       mbar_init(&scaled[i], 8);
       mbar_init(&pv_done[i], 1);
     }
@@ -771,13 +782,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
       float m = kNegInf, l = 0.f;
       const uint32_t p_row = peer(smem0 + kOffP + r * 128 + (r & 7) * 16, 1);  // + kP * place
-      const uint32_t f_row = peer(smem_u32(s_f + r), 1);
+      const uint32_t f_row = peer(smem_u32(s_f + r), 1), bar0 = peer(smem_u32(p_full), 1);
+      const uint32_t made = smem0 + kOffMade + grp * kP + r * 128 + (r & 7) * 16;
       auto tile_step = [&](int i, auto masked) {
         constexpr bool kMasked = decltype(masked)::value;
         const int slot = i % 3, at = i & 7, in = i & (kIn - 1);
-        const uint32_t p_at = p_row + in * kP;
-        ok = wait_phase<false>(&s_ready[slot], (i / 3) & 1, s_abort, err) &&
-             wait_phase<true>(&p_free[in], (i / kIn & 1) ^ 1u, s_abort, err);
+        ok = wait_phase<false>(&s_ready[slot], (i / 3) & 1, s_abort, err);
         if (!ok) return;
         tc_fence_after();
         // which keys this row sees (all, of padding: what its row becomes is not used)
@@ -792,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                                  : 0ull;
           }
         }
-        // P with this group's m, in the layout of an MMA A operand, to rank 1; once more where m is another now
+        // P with this group's m, in the layout of an MMA A operand; once more where m is another one now
         float f = 1.f, sum;
         for (int pass = 0;; ++pass) {  // (at most twice)
           const float off = m == kNegInf ? 0.f : -m;
@@ -824,11 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t pk[4];
-              [[maybe_unused]] float4 sa, sb;
+              [[maybe_unused]] uint4 sa, sb;
               if constexpr (k8) {
-                const float4* x = reinterpret_cast<const float4*>(s_scale + at * kKeys + 32 * h + 8 * u);
-                sa = x[0];
-                sb = x[1];
+                const uint32_t sc = smem0 + kOffScale + (at * kKeys + 32 * h + 8 * u) * 4;
+                sa = ld_shared16(sc);
+                sb = ld_shared16(sc + 16);
               }
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -837,20 +847,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                 unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
                                        scale2, off2),
                              x0, x1);
-                x0 = exp2_approx(x0);
-                x1 = exp2_approx(x1);
-                sum2 = add_f32x2(sum2, pack_f32x2(x0, x1));
+                uint32_t e0 = __float_as_uint(exp2_approx(x0)), e1 = __float_as_uint(exp2_approx(x1));
+                sum2 = add_f32x2(sum2, pack_f32x2(__uint_as_float(e0), __uint_as_float(e1)));
                 if constexpr (k8) {  // the values are codes as well
-                  x0 *= j < 2 ? (j ? sa.z : sa.x) : (j == 3 ? sb.z : sb.x);
-                  x1 *= j < 2 ? (j ? sa.w : sa.y) : (j == 3 ? sb.w : sb.y);
+                  mul_pair(e0, e1, j == 0 ? sa.x : j == 1 ? sa.z : j == 2 ? sb.x : sb.z,
+                           j == 0 ? sa.y : j == 1 ? sa.w : j == 2 ? sb.y : sb.w);
                   if constexpr (kMasked) {  // (0 times a scale that is not finite)
-                    x0 = see >> (32 * h + k) & 1 ? x0 : 0.f;
-                    x1 = see >> (32 * h + k + 1) & 1 ? x1 : 0.f;
+                    e0 = see >> (32 * h + k) & 1 ? e0 : 0u;
+                    e1 = see >> (32 * h + k + 1) & 1 ? e1 : 0u;
                   }
                 }
-                pk[j] = pack_bf16x2(x0, x1);
+                pk[j] = pack_bf16x2(__uint_as_float(e0), __uint_as_float(e1));
               }
-              st_peer16(p_at ^ (16 * (4 * h + u)), pk);
+              st_shared16(made ^ (16 * (4 * h + u)), make_uint4(pk[0], pk[1], pk[2], pk[3]));
             }
           }
           float l0, l1;
@@ -883,15 +892,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           if (!__any_sync(0xffffffffu, other)) break;
         }
         l += sum;
-        st_peer(f_row + in * kRows * 4, f);
-        fence_proxy_async_cluster();  // P before the products that read it
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s_free[slot]);
-          arrive_peer(peer(smem_u32(&p_full[in]), 1));
-        }
-        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[slot]);
+        // this row to rank 1
+        ok = wait_phase<true>(&p_free[in], (i / kIn & 1) ^ 1u, s_abort, err);
+        if (!ok) return;
+        const uint32_t bar = bar0 + in * 8, p_at = p_row + in * kP;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) st_async16(p_at ^ (16 * u), ld_shared16(made ^ (16 * u)), bar);
+        st_async4(f_row + in * kRows * 4, f, bar);
       };
       const bool holes = p.place.table != nullptr;  // a page may be missing among the sequence's rows
 #pragma unroll 1
@@ -935,12 +945,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     } else {
       // ---------------- O: rescaled where m was raised, at the end written; 256 columns a group
       const uint32_t o = lanes + grp * kHalf;
+      uint32_t seen = 0;  // tiles of P that have come
+      if (tid == 0)
+        for (int i = 0; i < kIn; ++i) mbar_arrive_expect_tx(&p_full[i], kPBytes);
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i) {
         const int slot = i & (kIn - 1);
         const uint32_t parity = i / kIn & 1;
         ok = wait_phase<true>(&p_full[slot], parity, s_abort, err);
         if (!ok) break;
+        ++seen;
         const float f = s_f[slot * kRows + r];
         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // (P V of the tile before was waited for)
           tc_fence_after();
@@ -960,8 +974,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&scaled[slot]);
         ok = wait_phase<false>(&pv_done[slot], parity, s_abort, err);
         if (!ok) break;
+        if (tid == 0 && i + kIn < g.n) mbar_arrive_expect_tx(&p_full[slot], kPBytes);
+        __syncwarp();
         if (lane == 0) arrive_peer(peer(smem_u32(&p_free[slot]), 0));
       }
+      // never leave with stores in flight to here (after an abort: bounded)
+      if (!ok && tid == 0)
+        for (uint32_t i = seen; i < min(seen + kIn, static_cast<uint32_t>(g.n)); ++i)
+          mbar_drain(&p_full[i & (kIn - 1)], i / kIn & 1);
+      __syncwarp();
       ok = wait_phase<true>(l_full, 0u, s_abort, err) && ok;
       tc_fence_after();
       const float l = s_l[r];
