@@ -440,7 +440,7 @@ typedef enum {
  *           has no rows.
  *  max_kv_len  the largest of kv_lens, or a bound of it: the work is laid out for it. With a longer
  *           sequence the results stay right and the call gets slower.
- *  out      [B, n_nodes, n_heads, 512] bf16, 16-byte aligned; lse [B, n_nodes, n_heads] fp32 or NULL.
+ *  out      [B, n_nodes, n_heads, 512] bf16, 32-byte aligned; lse [B, n_nodes, n_heads] fp32 or NULL.
  *           Of a node of mask 0, or that sees no row, out is 0 and lse -infinity.
  *  workspace  DEVICE, 16-byte aligned, at least the bytes that ds4idx_tree_attention_workspace
  *           gives for these sizes (may be 0, then NULL): partial sums of sequences

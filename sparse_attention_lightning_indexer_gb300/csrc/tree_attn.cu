@@ -196,6 +196,11 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 __device__ __forceinline__ void st_peer(uint32_t at, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
+__device__ __forceinline__ void st_global32(void* at, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // Stores to another CTA's shared memory that count as bytes at a barrier there: nothing here waits for them.
 __device__ __forceinline__ void st_async16(uint32_t at, uint4 v, uint32_t bar) {
   asm volatile(
@@ -212,6 +217,12 @@ __device__ __forceinline__ void st_async4(uint32_t at, float v, uint32_t bar) {
 // Orders generic accesses to the cluster's shared memory before later ones of MMAs.
 __device__ __forceinline__ void fence_proxy_async_cluster() {
   asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -730,51 +741,93 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mask &= ~0ull >> (64 - p.N);
       float to_log2 = p.scale_log2;  // of a score, from S
       if (g.n > 0) {
-        // Q to TMEM
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * kDims);
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+        // Q to TMEM by way of shared memory, so that it is read a line at a time: read by its rows' threads
+        // it took 6 us, twice that where the rows' maxima are needed first.
+        const int q_rows = min(kRows, p.N * p.H - tile * kRows);  // of the tile
+        const uint8_t* q0 = reinterpret_cast<const uint8_t*>(
+            p.q + (static_cast<int64_t>(b) * p.N * p.H + tile * kRows) * kDims);
         float f = 1.f;
         uint32_t f2 = 0;
         if constexpr (k8) {
-          // the power of two that takes the row's largest value to 2^7 .. 2^8
-          uint32_t top = 0;
-#pragma unroll 8
-          for (int j = 0; j < kDims / 8; ++j) {
-            const uint4 x = used ? src[j] : zero;
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                                         __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+          // The power of two that takes a row's largest value to 2^7 .. 2^8; a warp takes 16 rows, four at a
+          // time.
+#pragma unroll 1
+          for (int j = 0; j < 16; j += 4) {
+            uint4 v[4][3];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = warp * 16 + j + k;
+#pragma unroll
+              for (int c = 0; c < 3; ++c)
+                v[k][c] = ld_row16(q0 + at * (2 * kDims) + (lane + 32 * c) * 16,
+                                   at < q_rows && lane + 32 * c < kDims / 8 ? 0 : -1);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int c = 0; c < 3; ++c)
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k][c].x & 0x7FFF7FFFu, v[k][c].y & 0x7FFF7FFFu),
+                                             __vmaxu2(v[k][c].z & 0x7FFF7FFFu, v[k][c].w & 0x7FFF7FFFu)));
+              top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+              if (lane == 0) s_l[warp * 16 + j + k] = __uint_as_float(top);
+            }
           }
-          const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);   // biased by 127
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          const int e = static_cast<int>(__float_as_uint(s_l[r]) >> 7);         // biased by 127
           const int a = max(-110, min(110, e == 0 ? 0 : 127 + 7 - e));          // (zero: any)
           f = power(a);
           f2 = static_cast<uint32_t>(127 + a) * 0x00800080u;
           to_log2 *= power(-a);
         }
-#pragma unroll 1
-        for (int h = grp; h < 9; h += 2) {  // the rotary dims last
-          uint32_t v[32];
+        // Pieces of 32 dims, the groups in turn, two on their way: this warp's rows, 64 bytes each, in a
+        // swizzle that spreads a column over the banks. The rotary dims are the last two.
+        const uint32_t stage = smem0 + kOffMade + warp * 4096;
+        auto copy_q = [&](int h) {
+          if (h < 18) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 x = used ? src[8 * h + j] : zero;
-            v[4 * j] = x.x;
-            v[4 * j + 1] = x.y;
-            v[4 * j + 2] = x.z;
-            v[4 * j + 3] = x.w;
+            for (int k = 0; k < 4; ++k) {
+              const int at = 8 * k + (lane >> 2), u = lane & 3, from = quad * 32 + at;
+              const bool is = from < q_rows;
+              cp_async16(stage + (h >> 1 & 1) * 2048 + at * 64 + ((u ^ (at >> 1)) & 3) * 16,
+                         q0 + (is ? from : 0) * (2 * kDims) + h * 64 + u * 16, is ? 0 : -1);
+            }
           }
-          if (k8 && h < 8) {
-            uint32_t hi[16], lo[16];
+          cp_async_commit();
+        };
+        copy_q(grp);
+        copy_q(grp + 2);
+#pragma unroll 1
+        for (int h = grp; h < 18; h += 2) {
+          cp_async_wait<1>();
+          __syncwarp();
+          uint32_t v[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) bf16_to_f8_pair(v[2 * j], v[2 * j + 1], f, hi[j], lo[j]);
-            tmem_st16(lanes + h * 16, hi);
-            tmem_st16(lanes + kColLow + h * 16, lo);
+          for (int u = 0; u < 4; ++u) {
+            const uint4 x =
+                ld_shared16(stage + (h >> 1 & 1) * 2048 + lane * 64 + ((u ^ (lane >> 1)) & 3) * 16);
+            v[4 * u] = x.x;
+            v[4 * u + 1] = x.y;
+            v[4 * u + 2] = x.z;
+            v[4 * u + 3] = x.w;
+          }
+          __syncwarp();
+          copy_q(h + 4);
+          if (k8 && h < 16) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bf16_to_f8_pair(v[2 * j], v[2 * j + 1], f, hi[j], lo[j]);
+            tmem_st8(lanes + h * 8, hi);
+            tmem_st8(lanes + kColLow + h * 8, lo);
           } else {
             if constexpr (k8) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
+              for (int j = 0; j < 16; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
             }
-            tmem_st32(lanes + h * 32, v);
+            tmem_st16(lanes + h * 16, v);
           }
         }
+        cp_async_wait<0>();
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -1003,9 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                 none ? 0u : pack_bf16x2(__uint_as_float(v[j]) * inv, __uint_as_float(v[j + 1]) * inv);
           if (used && ok) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              reinterpret_cast<uint4*>(dst + c)[j] =
-                  make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+            for (int j = 0; j < 2; ++j) st_global32(dst + c + 16 * j, &pk[8 * j]);
           }
         }
       } else if (g.n > 0 && ok) {
@@ -1255,7 +1306,7 @@ extern "C" int ds4idx_tree_attention(const void* q, int32_t format, const void* 
   Params p{};
   if (!q || !cache || !kv_lens || !mask || !out || !aligned_to(q, 16) || !aligned_to(cache, 32) ||
       !aligned_to(scale, 4) || !aligned_to(kv_lens, 4) || !aligned_to(mask, 8) ||
-      !aligned_to(out, 16) || !aligned_to(lse, 4) || !aligned_to(workspace, 16) ||
+      !aligned_to(out, 32) || !aligned_to(lse, 4) || !aligned_to(workspace, 16) ||
       !make_placement(where, kv_rows, B, &p.place))
     return DS4IDX_ERR_INVALID_ARG;
   const int64_t pairs = pairs_at_once();
