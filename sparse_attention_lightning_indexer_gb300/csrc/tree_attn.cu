@@ -294,10 +294,6 @@ __device__ __forceinline__ void swap_if(bool c, T& a, T& b) {
   a = x;
 }
 
-__device__ __noinline__ int32_t paged_row(const Placement& p, const int32_t* table, int32_t s) {
-  return static_cast<int32_t>(place_row(p, TokenPlace{0, table, true}, s));
-}
-
 // One loader warp's work. kKey: this CTA forms the key products (and takes the rotary dims), or the
 // values'. Codes go to shared memory as they are, by asynchronous copies two tiles ahead, and are turned
 // into the operand by the thread that copied them. (Held in registers they were waited for as soon as the
@@ -313,15 +309,6 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   const uint32_t smem0 = smem_u32(smem);
   const int l8 = lane & 7, sub = lane >> 3;
   const TokenPlace tp = place_token(p.place, b);
-  // The row of key 8 w + key of tile i.
-  auto row_of = [&](int i, int key) -> int32_t {
-    const int32_t s = g.position(i) + 8 * w + key;
-    if (i >= g.n || s >= g.end) return -1;
-    if (i >= g.plain && s >= g.len && !(g.seen >> (s - g.len) & 1)) return -1;
-    // (contiguous: `end` ends at the pool's last row)
-    if (!tp.table) return static_cast<int32_t>(tp.row0 + s);
-    return tp.ok ? paged_row(p.place, tp.table, s) : -1;
-  };
   auto row_at = [&](int32_t r) { return p.cache + static_cast<int64_t>(r) * kStride; };
   bool ok = true;
   int st = 0;                 // place in the ring
@@ -351,12 +338,42 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   auto rope_address = [&](int i, int key) {
     return smem0 + kOffRope + (i & 3) * kChunk + (8 * w + key) * 128 + ((l8 ^ key) * 16);
   };
-  // This thread's rows (keys sub and 4 + sub) of the tile that is read; where they need a page table, those
-  // of the tile after it as well. Rows that follow one another are stepped through.
-  int32_t row[2], next[2];
+  // This thread's rows (keys sub and 4 + sub) of the tile that is read. Rows that follow one another are
+  // stepped through. Otherwise a key's page and its place there are stepped from tile to tile, and its entry
+  // of the page table is read a tile ahead.
   const bool steps = tp.table == nullptr;
+  const int32_t page = steps ? 1 : p.place.page, pages = tp.ok ? p.place.pages : 0;
+  const int32_t page_step = kKeys / page, place_step = kKeys % page;
+  int32_t row[2], page_no[2] = {}, place[2] = {}, id[2] = {};
+  auto look_up = [&](int k) { id[k] = page_no[k] < pages ? tp.table[page_no[k]] : -1; };
+  // Rows of tile i, whose entries are read, and the entries of the tile after it.
+  auto find_rows = [&](int i) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) row[k] = row_of(0, 4 * k + sub), next[k] = steps ? 0 : row_of(1, 4 * k + sub);
+    for (int k = 0; k < 2; ++k) {
+      const int32_t s = g.position(i) + 8 * w + 4 * k + sub;
+      bool is = i < g.plain || (i < g.n && s < g.end && (s < g.len || (g.seen >> (s - g.len) & 1)));
+      int64_t r = tp.row0 + s;  // (contiguous: `end` ends at the pool's last row)
+      if (!steps) {
+        r = static_cast<int64_t>(id[k]) * page + place[k];
+        is = is && id[k] >= 0 && r < p.place.rows;
+        page_no[k] += page_step;
+        place[k] += place_step;
+        if (place[k] >= page) place[k] -= page, ++page_no[k];
+        look_up(k);
+      }
+      row[k] = is ? static_cast<int32_t>(r) : -1;
+    }
+  };
+  if (!steps) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int32_t s = g.position(0) + 8 * w + 4 * k + sub;
+      page_no[k] = s / page;
+      place[k] = s % page;
+      look_up(k);
+    }
+  }
+  find_rows(0);
   const uint8_t* from[2] = {row_at(max(row[0], 0)) + l8 * 16, row_at(max(row[1], 0)) + l8 * 16};
   int read = 0;        // tiles whose reads are on their way
   auto advance_rows = [&] {
@@ -366,12 +383,9 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       for (int k = 0; k < 2; ++k) row[k] += kKeys, from[k] += kKeys * kStride;
       return;
     }
+    find_rows(read);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      row[k] = steps ? row_of(read, 4 * k + sub) : next[k];
-      if (!steps) next[k] = row_of(read + 1, 4 * k + sub);
-      from[k] = row_at(max(row[k], 0)) + l8 * 16;
-    }
+    for (int k = 0; k < 2; ++k) from[k] = row_at(max(row[k], 0)) + l8 * 16;
   };
   auto note_there = [&] {  // of the tile that is read, for the softmax
     if (!kKey || (steps && read < g.plain)) return;
@@ -543,23 +557,25 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     cp_async_wait<0>();
     if (ok && last >= 0) publish(last);
   } else {
-    // access k: rows 2 k and 2 k + 1, 32 codes a lane: two of the four scales of a chunk
-    const int l16 = lane & 15, hi = lane >> 4, x = l16 >> 1 & 3;
-    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + lane * 16;            // + raw tile, + 512 k
+    // Copied are 256 bytes of codes of two rows at a time; turned, in each half of the dims, 128 of four rows:
+    // 32 codes a lane, two of the four scales of a chunk.
+    const int x = l8 >> 1;
+    const uint32_t raw0 = smem0 + kOffRaw + w * 2048;                        // + raw tile
     const uint32_t raw_scale = smem0 + kOffScale + w * 256;                  // + 2048 raw tile
     // Row of key j (the same in all lanes of a group of eight that holds it).
     auto row_of_key = [&](int j) {
-      const int32_t a = __shfl_sync(0xffffffffu, row[0], 8 * (j & 3)), c = __shfl_sync(0xffffffffu, row[1], 8 * (j & 3));
+      const int32_t a = __shfl_sync(0xffffffffu, row[0], 8 * (j & 3)),
+                    c = __shfl_sync(0xffffffffu, row[1], 8 * (j & 3));
       return j < 4 ? a : c;
     };
     auto copy = [&] {
       const int slot = read & 1;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        const int32_t r = row_of_key(2 * k + hi);
-        cp_async16(raw0 + slot * kRaw + 512 * k, row_at(max(r, 0)) + l16 * 16, r);
+        const int32_t r = row_of_key(2 * k + (lane >> 4));
+        cp_async16(raw0 + slot * kRaw + lane * 16 + 512 * k, row_at(max(r, 0)) + (lane & 15) * 16, r);
       }
-      const int32_t r = row_of_key(l16 >> 1);
+      const int32_t r = row_of_key(lane >> 1 & 7);
       if (lane < 16)
         cp_async16(raw_scale + slot * 2048 + lane * 16, row_at(max(r, 0)) + ds4q::kOffScale + (lane & 1) * 16, r);
       if (kKey) {
@@ -576,31 +592,27 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       advance_rows();
     }
 #pragma unroll 1
-    for (int i = 0; i < g.n; ++i) {
-      cp_async_wait<1>();
+    for (int n = 0; n < 2 * g.n; ++n) {
+      const int i = n >> 1, h = n & 1;
+      if (h == 0) cp_async_wait<1>();
       __syncwarp();
-      const int first = st;
       claim();
-      step();
-      const int second = st;
-      claim();
-      step();
       if (!ok) break;
-      const uint32_t raw = raw0 + (i & 1) * kRaw;
-      const uint8_t* scales = smem + kOffScale + w * 256 + (i & 1) * 2048;
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        const int key = 2 * k + hi;
-        uint4 c = ld_shared16(raw + 512 * k);
-        uint32_t s = *reinterpret_cast<const uint16_t*>(scales + key * 32 + l16 * 2);
+      const uint8_t* scales = smem + kOffScale + w * 256 + (i & 1) * 2048 + (h * 8 + l8) * 2;
+      const uint32_t raw = raw0 + (i & 1) * kRaw + h * 128 + l8 * 16;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int key = 4 * k + sub;
+        uint4 c = ld_shared16(raw + key * 256);
+        uint32_t s = *reinterpret_cast<const uint16_t*>(scales + key * 32);
         // piece j ^ x at step j: the lanes of the other chunks write other banks
         swap_if(x & 1, c.x, c.y);
         swap_if(x & 1, c.z, c.w);
         swap_if(x & 2, c.x, c.z);
         swap_if(x & 2, c.y, c.w);
         s = x & 2 ? __byte_perm(s, 0, 0x4401) : s;
-        const uint32_t at = smem0 + (l16 < 8 ? first : second) * kPart + x * kChunk + (8 * w + key) * 128 +
-                            ((((l16 & 1) * 4 + x) ^ key) * 16);
+        const uint32_t at = smem0 + st * kPart + x * kChunk + (8 * w + key) * 128 +
+                            ((((l8 & 1) * 4 + x) ^ key) * 16);
         const uint32_t words[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -609,10 +621,12 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
           st_shared16(at ^ (16 * j), ds4q::word_to_bf16(words[j], s2, ds4q::offset_bf16x2(s2)));
         }
       }
-      publish(first);
-      publish(second);
-      copy();
-      advance_rows();
+      publish(st);
+      step();
+      if (h == 1) {
+        copy();
+        advance_rows();
+      }
     }
     cp_async_wait<0>();
   }
@@ -1245,8 +1259,11 @@ struct Plan {
   int32_t tiles, splits, steps;
   int64_t o_bytes, bytes;
 };
-// Key ranges: the number whose slowest pair takes the least, in steps of 64 keys (0.8 us); what a range
-// costs besides its steps, and what joining costs, as measured.
+// Key ranges: the number that takes the least time, in steps of 64 keys (1.25 us). A range costs some 14
+// steps besides its own (set-up, Q, its part of O), the join 4. Several sequences have lengths of their
+// own, so that not every pair of a last round has as much to do: half way between full rounds and ranges of
+// three quarters of the longest without a gap. (8 ragged sequences of 7 nodes and up to 5000 rows: 119 us as
+// one range each, 85 as two; 3 of 31 nodes, 16 heads, 12001 rows: 88 as six, 120 as nine.)
 Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
   Plan pl{};
   pl.tiles = (N * H + kRows - 1) / kRows;
@@ -1255,7 +1272,10 @@ Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_le
   int64_t best = 0, best_cost = 0;
   for (int64_t n = 1; n <= std::min<int64_t>(steps, 2 * pairs); ++n) {
     const int64_t per = (steps + n - 1) / n, waves = (items * n + pairs - 1) / pairs;
-    const int64_t cost = waves * (per + 5) + (n > 1 ? 5 : 0);
+    int64_t cost = waves * (per + 14);
+    if (B > 1 && waves > 1)
+      cost = (cost + std::max(per + 14, items * n * (3 * per / 4 + 14) / pairs)) / 2;
+    if (n > 1) cost += 4;
     if (best == 0 || cost < best_cost) best = n, best_cost = cost;
   }
   pl.splits = static_cast<int32_t>(best);
