@@ -760,6 +760,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         const int q_rows = min(kRows, p.N * p.H - tile * kRows);  // of the tile
         const uint8_t* q0 = reinterpret_cast<const uint8_t*>(
             p.q + (static_cast<int64_t>(b) * p.N * p.H + tile * kRows) * kDims);
+        // Pieces of 32 dims, the groups in turn, two on their way: this warp's rows, 64 bytes each, in a
+        // swizzle that spreads a column over the banks. The rotary dims are the last two.
+        const uint32_t stage = smem0 + kOffMade + warp * 4096;
+        auto copy_q = [&](int h) {
+          if (h < 18) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = 8 * k + (lane >> 2), u = lane & 3, from = quad * 32 + at;
+              const bool is = from < q_rows;
+              cp_async16(stage + (h >> 1 & 1) * 2048 + at * 64 + ((u ^ (at >> 1)) & 3) * 16,
+                         q0 + (is ? from : 0) * (2 * kDims) + h * 64 + u * 16, is ? 0 : -1);
+            }
+          }
+          cp_async_commit();
+        };
+        copy_q(grp);
+        copy_q(grp + 2);
         float f = 1.f;
         uint32_t f2 = 0;
         if constexpr (k8) {
@@ -794,23 +811,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           f2 = static_cast<uint32_t>(127 + a) * 0x00800080u;
           to_log2 *= power(-a);
         }
-        // Pieces of 32 dims, the groups in turn, two on their way: this warp's rows, 64 bytes each, in a
-        // swizzle that spreads a column over the banks. The rotary dims are the last two.
-        const uint32_t stage = smem0 + kOffMade + warp * 4096;
-        auto copy_q = [&](int h) {
-          if (h < 18) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int at = 8 * k + (lane >> 2), u = lane & 3, from = quad * 32 + at;
-              const bool is = from < q_rows;
-              cp_async16(stage + (h >> 1 & 1) * 2048 + at * 64 + ((u ^ (at >> 1)) & 3) * 16,
-                         q0 + (is ? from : 0) * (2 * kDims) + h * 64 + u * 16, is ? 0 : -1);
-            }
-          }
-          cp_async_commit();
-        };
-        copy_q(grp);
-        copy_q(grp + 2);
 #pragma unroll 1
         for (int h = grp; h < 18; h += 2) {
           cp_async_wait<1>();
@@ -1211,38 +1211,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   cluster_sync();  // no CTA leaves while the other may still write, read or arrive here
 }
 
-// Joins the ranges of a row tile: a thread four columns of one row. Ranges without a seen key carry
-// m = -infinity and no O.
-constexpr int kJoinThreads = 128;
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ Params p) {
+// Joins the ranges of a row tile: four columns of one row by one thread, or, from kJoinMany ranges on, by
+// four that take every fourth range each, since reading one range after the other is then what takes the
+// time. Measured, whole calls with 128 heads, one thread and four: one node over 64 ranges 39.9 and 28.6 us,
+// 5 nodes over 15 71.7 and 68.6, 7 over 10 103.3 and 102.8, 9 over 8 121.6 and 122.9, 13 over 5 177.4 and
+// 182.0. Ranges without a seen key carry m = -infinity and no O.
+constexpr int kJoinMany = 10;
+template <int kJoinParts>
+__global__ void __launch_bounds__(kRows * kJoinParts) tree_join_kernel(const __grid_constant__ Params p) {
+  __shared__ float s_m[kJoinParts][kRows], s_l[kJoinParts][kRows];
+  __shared__ float4 s_o[kJoinParts][kRows];
   griddep_wait();
   griddep_launch_dependents();
-  const int quad = blockIdx.x % 128, r = threadIdx.x;  // columns 4 quad ..
+  const int quad = blockIdx.x % 128, r = threadIdx.x % kRows, part = threadIdx.x / kRows;  // columns 4 quad ..
   const int64_t group = blockIdx.x / 128;              // (sequence, row tile)
   const int tile = static_cast<int>(group % p.tiles);
   const int64_t b = group / p.tiles;
   const int row = tile * kRows + r;
-  if (row >= p.N * p.H) return;
   const float* ml = p.part_ml + group * p.splits * 2 * kRows + r;
   float m = kNegInf;
-  for (int i = 0; i < p.splits; ++i) m = fmaxf(m, ml[i * 2 * kRows]);
+#pragma unroll 4
+  for (int i = part; i < p.splits; i += kJoinParts) m = fmaxf(m, ml[i * 2 * kRows]);
+  s_m[part][r] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kJoinParts; ++k) m = fmaxf(m, s_m[k][r]);
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* src = reinterpret_cast<const float4*>(p.part_o) +
                       (group * p.splits * 128 + quad) * kRows + r;
-  if (m != kNegInf) {
 #pragma unroll 4
-    for (int i = 0; i < p.splits; ++i) {
-      const float mi = ml[i * 2 * kRows];
-      if (mi == kNegInf) continue;
-      const float f = exp2_approx(mi - m);
-      const float4 v = src[static_cast<int64_t>(i) * 128 * kRows];
-      l = fmaf(ml[i * 2 * kRows + kRows], f, l);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
-    }
+  for (int i = part; i < p.splits; i += kJoinParts) {
+    const float mi = ml[i * 2 * kRows];
+    if (mi == kNegInf) continue;
+    const float f = exp2_approx(mi - m);
+    const float4 v = src[static_cast<int64_t>(i) * 128 * kRows];
+    l = fmaf(ml[i * 2 * kRows + kRows], f, l);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+  }
+  s_l[part][r] = l;
+  s_o[part][r] = o;
+  __syncthreads();
+  if (part > 0 || row >= p.N * p.H) return;
+#pragma unroll
+  for (int k = 1; k < kJoinParts; ++k) {
+    const float4 v = s_o[k][r];
+    l += s_l[k][r];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
   }
   const bool none = m == kNegInf;
   const float inv = none ? 0.f : 1.f / l;
@@ -1356,7 +1377,7 @@ extern "C" int ds4idx_tree_attention(const void* q, int32_t format, const void* 
                  : format == DS4IDX_CACHE_BF16 ? launch<DS4IDX_CACHE_BF16>(p, items, stream)
                                                : launch<DS4IDX_CACHE_Q4>(p, items, stream);
   if (st != DS4IDX_OK || pl.splits == 1) return st;
-  return launch_dependent(tree_join_kernel,
-                          static_cast<unsigned>(static_cast<int64_t>(B) * pl.tiles * 128), kJoinThreads,
-                          0, 1, stream, p);
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(B) * pl.tiles * 128);
+  return pl.splits < kJoinMany ? launch_dependent(tree_join_kernel<1>, blocks, kRows, 0, 1, stream, p)
+                               : launch_dependent(tree_join_kernel<4>, blocks, kRows * 4, 0, 1, stream, p);
 }
