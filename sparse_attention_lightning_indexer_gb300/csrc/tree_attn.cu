@@ -809,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           const int a = max(-110, min(110, e == 0 ? 0 : 127 + 7 - e));          // (zero: any)
           f = power(a);
           f2 = static_cast<uint32_t>(127 + a) * 0x00800080u;
-          to_log2 *= power(-a);
+          // (neither 0 nor infinite, which times a masked score's infinity or a score of 0 would be NaN)
+          to_log2 = fminf(fmaxf(to_log2 * power(-a), power(-126)), kMax);
         }
 #pragma unroll 1
         for (int h = grp; h < 18; h += 2) {
@@ -1370,7 +1371,7 @@ extern "C" int ds4idx_tree_attention(const void* q, int32_t format, const void* 
   p.tiles = pl.tiles;
   p.splits = pl.splits;
   p.steps = pl.steps;
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.scale_log2 = std::max(sm_scale * 1.4426950408889634f, 0x1p-126f);
   const int64_t items = static_cast<int64_t>(B) * pl.tiles * pl.splits;
   if (items * 2 > 0x7FFFFFFF) return DS4IDX_ERR_INVALID_ARG;
   const int st = format == DS4IDX_CACHE_FP8    ? launch<DS4IDX_CACHE_FP8>(p, items, stream)
