@@ -71,8 +71,8 @@ static_assert(kOffMade + 2 * kP <= kOffF, "P");
 constexpr int kOffM = kOffF + kIn * kRows * 4;       // float [2][128]: m after an even, an odd tile
 constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
 constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
-                                                   // rows), or two tiles' codes of scales (4-bit rows)
-constexpr int kOffThere = kOffScale + 4096;  // uint64 [8 tiles]: keys that are there
+                                                   // rows), or kRaws tiles' codes of scales (4-bit rows)
+constexpr int kOffThere = kOffScale + kRaws * 2048;  // uint64 [8 tiles]: keys that are there
 constexpr int kOffBars = kOffThere + 8 * 8;
 constexpr int kNumBars = 2 * kParts8 + 1 + 2 * 3 + 4 * kIn + 8 + 2;
 static_assert(kParts8 * kPart8 <= kOffRope && kParts8 >= kParts, "8-bit keys");
@@ -557,32 +557,26 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     cp_async_wait<0>();
     if (ok && last >= 0) publish(last);
   } else {
-    // Copied are 256 bytes of codes of two rows at a time; turned, in each half of the dims, 128 of four rows:
-    // 32 codes a lane, two of the four scales of a chunk.
+    // Eight lanes copy 128 bytes of codes (c) of rows sub and 4 + sub (k) at a time, four of them their scales.
+    // Turned are 32 codes a lane of each, in each half of the dims: those that it copied.
     const int x = l8 >> 1;
-    const uint32_t raw0 = smem0 + kOffRaw + w * 2048;                        // + raw tile
+    const uint32_t raw0 = smem0 + kOffRaw + w * 2048 + sub * 256 + l8 * 16;  // + raw tile, + 1024 k + 128 c
     const uint32_t raw_scale = smem0 + kOffScale + w * 256;                  // + 2048 raw tile
-    // Row of key j (the same in all lanes of a group of eight that holds it).
-    auto row_of_key = [&](int j) {
-      const int32_t a = __shfl_sync(0xffffffffu, row[0], 8 * (j & 3)),
-                    c = __shfl_sync(0xffffffffu, row[1], 8 * (j & 3));
-      return j < 4 ? a : c;
-    };
+    int raw_in = 0, raw_out = 0;  // places of the tile to be read next, and of the one to be turned
     auto copy = [&] {
-      const int slot = read & 1;
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        const int32_t r = row_of_key(2 * k + (lane >> 4));
-        cp_async16(raw0 + slot * kRaw + lane * 16 + 512 * k, row_at(max(r, 0)) + (lane & 15) * 16, r);
-      }
-      const int32_t r = row_of_key(lane >> 1 & 7);
-      if (lane < 16)
-        cp_async16(raw_scale + slot * 2048 + lane * 16, row_at(max(r, 0)) + ds4q::kOffScale + (lane & 1) * 16, r);
-      if (kKey) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          cp_async16(rope_address(read, 4 * k + sub), from[k] + ds4q::kOffRope, row[k]);
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          cp_async16(raw0 + raw_in * kRaw + 1024 * k + 128 * c, from[k] + 128 * c, row[k]);
+        if (kKey) cp_async16(rope_address(read, 4 * k + sub), from[k] + ds4q::kOffRope, row[k]);
       }
+      const bool upper = l8 & 2;  // of the two rows
+      if (l8 < 4)
+        cp_async16(raw_scale + raw_in * 2048 + (4 * upper + sub) * 32 + (l8 & 1) * 16,
+                   (upper ? from[1] : from[0]) + ds4q::kOffScale - l8 * 16 + (l8 & 1) * 16,
+                   upper ? row[1] : row[0]);
+      if (++raw_in == kRaws) raw_in = 0;
       note_there();
       cp_async_commit();
     };
@@ -593,18 +587,28 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     }
 #pragma unroll 1
     for (int n = 0; n < 2 * g.n; ++n) {
-      const int i = n >> 1, h = n & 1;
+      const int h = n & 1;
       if (h == 0) cp_async_wait<1>();
       __syncwarp();
       claim();
       if (!ok) break;
-      const uint8_t* scales = smem + kOffScale + w * 256 + (i & 1) * 2048 + (h * 8 + l8) * 2;
-      const uint32_t raw = raw0 + (i & 1) * kRaw + h * 128 + l8 * 16;
+      if (h == 0) {  // (a part of this tile has a place: tile i - 2 is done with, its rotary dims too)
+        copy();
+        advance_rows();
+      }
+      uint4 codes[2];
+      uint32_t scales[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        codes[k] = ld_shared16(raw0 + raw_out * kRaw + 1024 * k + 128 * h);
+        scales[k] = *reinterpret_cast<const uint16_t*>(smem + kOffScale + w * 256 + raw_out * 2048 +
+                                                       (4 * k + sub) * 32 + (h * 8 + l8) * 2);
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int key = 4 * k + sub;
-        uint4 c = ld_shared16(raw + key * 256);
-        uint32_t s = *reinterpret_cast<const uint16_t*>(scales + key * 32);
+        uint4 c = codes[k];
+        uint32_t s = scales[k];
         // piece j ^ x at step j: the lanes of the other chunks write other banks
         swap_if(x & 1, c.x, c.y);
         swap_if(x & 1, c.z, c.w);
@@ -623,10 +627,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
       }
       publish(st);
       step();
-      if (h == 1) {
-        copy();
-        advance_rows();
-      }
+      if (h == 1 && ++raw_out == kRaws) raw_out = 0;
     }
     cp_async_wait<0>();
   }
