@@ -318,7 +318,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     if (++st == (k8 ? kParts8 : kParts)) st = 0, parity ^= 1u;
   };
   auto publish = [&](int at) {
-    fence_proxy_async_smem();
+    if (!(kFormat == DS4IDX_CACHE_Q4)) fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&part_full[at]);
   };
@@ -1109,6 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       };
       auto part_ready = [&] {
         ok = ok && wait_phase<false>(&part_full[st], parity, s_abort, err);
+        if (kFormat == DS4IDX_CACHE_Q4) fence_proxy_async_smem();
         tc_fence_after();
       };
       auto part_taken = [&] {
