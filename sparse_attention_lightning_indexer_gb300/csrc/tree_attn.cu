@@ -8,19 +8,32 @@
 //   S[128 x 64 keys] = Q K^T        rank 0; Q stays in TMEM as the A operand, three tiles of S beside it
 //   p = exp2(s - m) in bf16         rank 0; m is left alone until a score passes it by 64
 //   O[128 x 512] += P V             rank 1; O fills its TMEM over the whole range
-// P, and the factors of O where m was raised, are all that goes from one CTA to the other (16 KB a tile;
-// shared memory of the pair moves 18.7 bytes a clock in each direction when all SMs do it). A tile
-// takes both CTAs about as long: 36 x 32 and 8 x 128 clocks of products. Splitting the dims instead
-// reads and unpacks a row once in the pair, but exchanges S, 32 KB a tile both ways: slower.
+// P, and the factors of O where m was raised, are all that goes from one CTA to the other: 16 KB a tile,
+// stored straight into rank 1's shared memory with the bytes counted at a barrier there (the shared memory of
+// a pair moves 18.7 bytes a clock in each direction when all SMs do it). Splitting the dims instead reads and
+// unpacks a row once in the pair, but exchanges S, 32 KB a tile both ways, before the softmax can go on: 3.27
+// against 2.78 ms when both were first built (4 sequences of 64 nodes over 16384 rows, 128 heads, 8 bits).
 // Ranges of a split sequence leave (O, m, l) in fp32, and a second kernel joins them.
 //
-// Both CTAs read the rows themselves and turn them into bf16 (exact) in a ring of parts, 64 keys x 256
-// dims in the 128-byte-swizzled layout that serves as K-major and as MN-major operand.
+// What bounds it: a tile of 64 keys takes a pair 2450 clocks, 1.29 us. Rank 0's products take 36 times 57 to
+// 64 clocks (32 is the tensor core's rate, which an A operand from TMEM reaches from 128 keys on). Rank 1's
+// shared memory moves 240 KB a tile, 1900 clocks at 128 bytes each: codes in and out, bf16 in, out for the
+// products, P. Timing-only copies in which one side is made light: the case below takes 1.28 ms, with half of
+// rank 0's products 1.27, with no value codes read 1.26, without either side's 0.94. A range costs 18 us
+// besides: set-up 2, Q 6, the end of the pipeline 2, O 4, the join 4.
+//
+// Measured on the device: 4 sequences of 64 nodes, 128 heads, 16384 8-bit rows 1.28 ms, 0.91 PFLOP/s; one
+// node over 262144 8-bit rows 98 us, 1.7 TB/s; 13 nodes over 32768 bf16 rows 152 us, 0.78 PFLOP/s; three sequences of 31 nodes
+// of 16 heads over 12001 4-bit rows in pages 80 us, where unpacking in both ranks is what bounds it (3500
+// clocks a tile).
+//
+// Both CTAs read the rows themselves and keep them in a ring of parts, 64 keys x 256 dims in the
+// 128-byte-swizzled layout that serves as K-major and as MN-major operand.
 //
 // Warps 0..7: softmax, a row a thread, warps 0..3 on even tiles and 4..7 on odd ones (rank 1: the
-// rescaling of O and the output). Warps 8..15: rows to operands. Warp 16 issues tcgen05.mma. The roles' loops are kept rolled: they run side by side out of one
-// instruction cache, and with everything unrolled (126 KB of code) more than half of its look-ups missed
-// and a tile took 7000 clocks.
+// rescaling of O and the output). Warps 8..15: rows to operands. Warp 16 issues tcgen05.mma. The roles' loops
+// are kept rolled: they run side by side out of one instruction cache, and with everything unrolled (126 KB of
+// code) more than half of its look-ups missed and a tile took 7000 clocks.
 //
 // 8-bit rows are operands without their scales, which are powers of two: S is multiplied by them, and so is
 // P, exactly. As keys they are E4M3 operands as they stand, and Q, scaled by a power of two, is a sum of an
@@ -66,8 +79,7 @@ constexpr int kIn = 4;                             // tiles of P on their way to
 constexpr int kOffP = kOffRope;                    // in rank 1, which has no rotary dims
 constexpr int kOffMade = kOffRope + 4 * kChunk;    // P of an even and of an odd tile as it is made (rank 0)
 constexpr int kOffF = kOffP + kIn * kP;
-static_assert(kOffMade + 2 * kP <= kOffF, "P");
-              // float [4][128]: roots of factors of O before P V
+static_assert(kOffMade + 2 * kP <= kOffF, "P");    // kOffF: float [4][128], roots of factors of O before P V
 constexpr int kOffM = kOffF + kIn * kRows * 4;       // float [2][128]: m after an even, an odd tile
 constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
 constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
@@ -84,8 +96,8 @@ constexpr uint32_t kColLow = 128;                  // the low parts of Q beside 
 constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
 // log2 of what exp2(s - m) may be before m is raised. P and the sums are floating point with 2^127 of
 // range, so a stale m costs no precision: 2^64 leaves 2^63 for the count and size of the values. (With 2^8
-// some row of 128 raised m in most of the first hundred tiles; a rescaling holds P V up for 4000 clocks,
-// and 4 sequences of 64 nodes over 16384 rows took 2.05 ms.)
+// some row of 128 raises m in most of the first hundred tiles, and a rescaling holds P V up for 4000 clocks:
+// one node over 262144 rows 150 us where it takes 98, 4 sequences of 64 nodes over 16384 1.78 and 1.28 ms.)
 constexpr float kSlack = 64.f;
 
 struct Params {
@@ -234,8 +246,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // ---- reading rows: eight warps, each eight keys of a tile. Eight lanes read 128 adjacent bytes of a row
-// (a lane for each key instead, 32 bytes at 32 different lines an access, bound the L1's look-ups: 2.0 ms
-// where the listed order now takes TIME).
+// (rows in L2, all SMs: 16.7 TB/s; a lane for each key instead, 32 bytes at 32 different lines an access,
+// 9.7 TB/s, bound by the L1's look-ups).
 
 // 16 bytes of row r at p, zeros where there is no row. One predicated load into registers that hold them:
 // with a branch around it the value is moved where the paths meet, and the move waits for it.
@@ -294,6 +306,13 @@ __device__ __forceinline__ void swap_if(bool c, T& a, T& b) {
   a = x;
 }
 
+// Who orders the writes of a part before the products that read it, by the proxy fence between them: its
+// writers, 300 clocks a part of each loader, or the one warp that issues the products. Beside 4-bit rows the
+// loaders are the slower (3 sequences of 31 nodes, 12001 rows: 84 us with their fence, 80 with the other's);
+// beside the others the products are (4 of 64 nodes over 16384 8-bit rows: 1.28 and 1.43 ms).
+template <int kFormat>
+constexpr bool kFenceByMma = kFormat == DS4IDX_CACHE_Q4;
+
 // One loader warp's work. kKey: this CTA forms the key products (and takes the rotary dims), or the
 // values'. Codes go to shared memory as they are, by asynchronous copies two tiles ahead, and are turned
 // into the operand by the thread that copied them. (Held in registers they were waited for as soon as the
@@ -318,7 +337,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
     if (++st == (k8 ? kParts8 : kParts)) st = 0, parity ^= 1u;
   };
   auto publish = [&](int at) {
-    if (!(kFormat == DS4IDX_CACHE_Q4)) fence_proxy_async_smem();
+    if constexpr (!kFenceByMma<kFormat>) fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&part_full[at]);
   };
@@ -756,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mask &= ~0ull >> (64 - p.N);
       float to_log2 = p.scale_log2;  // of a score, from S
       if (g.n > 0) {
-        // Q to TMEM by way of shared memory, so that it is read a line at a time: read by its rows' threads
-        // it took 6 us, twice that where the rows' maxima are needed first.
+        // Q to TMEM by way of shared memory, so that it is read a line at a time: 5.7 us beside 8-bit rows,
+        // whose queries' largest values are needed first, where reading by the rows' threads took 17.
         const int q_rows = min(kRows, p.N * p.H - tile * kRows);  // of the tile
         const uint8_t* q0 = reinterpret_cast<const uint8_t*>(
             p.q + (static_cast<int64_t>(b) * p.N * p.H + tile * kRows) * kDims);
@@ -1109,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       };
       auto part_ready = [&] {
         ok = ok && wait_phase<false>(&part_full[st], parity, s_abort, err);
-        if (kFormat == DS4IDX_CACHE_Q4) fence_proxy_async_smem();
+        if constexpr (kFenceByMma<kFormat>) fence_proxy_async_smem();
         tc_fence_after();
       };
       auto part_taken = [&] {
