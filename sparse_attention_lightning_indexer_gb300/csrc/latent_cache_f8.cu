@@ -1,9 +1,9 @@
 // The 8-bit latent cache's writer and reader (format: f8_format.cuh): a row is one warp, a lane 16
 // adjacent dims and two rotary ones. Both are streams of rows: bound by HBM. A warp has the loads of two rows
 // (the reader four) in flight before it uses the first. Measured on the device, partly out of L2: 262144 bf16
-// rows written in 66.6 us, 7.07 TB/s, and read in 69.9, 6.73; fp32 rows 106.4 us, 7.27 TB/s, and 157.0, 4.92
-// (a lane's 64 bytes of a row's output are four stores 64 bytes from its neighbours'); 65536 bf16 rows
-// both ways 37.1 us, 8 rows 3.0.
+// rows written in 66.3 us, 7.10 TB/s, and read in 69.4, 6.78; fp32 rows 106.8 us, 7.24 TB/s, and 113.3, 6.82
+// (157 with 16 adjacent dims a lane, whose stores leave gaps of 48 bytes); 65536 bf16 rows both ways
+// 37.0 us, 8 rows 3.0.
 #include <cuda_runtime.h>
 
 #include <algorithm>

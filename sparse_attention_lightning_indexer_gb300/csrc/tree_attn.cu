@@ -18,12 +18,13 @@
 // What bounds it: a tile of 64 keys takes a pair 2450 clocks, 1.29 us. Rank 0's products take 36 times 57 to
 // 64 clocks (32 is the tensor core's rate, which an A operand from TMEM reaches from 128 keys on). Rank 1's
 // shared memory moves 240 KB a tile, 1900 clocks at 128 bytes each: codes in and out, bf16 in, out for the
-// products, P. Timing-only copies in which one side is made light: the case below takes 1.28 ms, with half of
-// rank 0's products 1.27, with no value codes read 1.26, without either side's 0.94. A range costs 18 us
+// products, P. Timing-only copies in which one side is made light: the case below took 1.28 ms, with half of
+// rank 0's products 1.27, with no value codes read 1.26, with both sides light 0.94; the second sum of the
+// softmax came later. A range costs 18 us
 // besides: set-up 2, Q 6, the end of the pipeline 2, O 4, the join 4.
 //
-// Measured on the device: 4 sequences of 64 nodes, 128 heads, 16384 8-bit rows 1.28 ms, 0.91 PFLOP/s; one
-// node over 262144 8-bit rows 98 us, 1.7 TB/s; 13 nodes over 32768 bf16 rows 152 us, 0.78 PFLOP/s; three sequences of 31 nodes
+// Measured on the device: 4 sequences of 64 nodes, 128 heads, 16384 8-bit rows 1.34 ms, 0.87 PFLOP/s; one
+// node over 262144 8-bit rows 100 us, 1.7 TB/s; 13 nodes over 32768 bf16 rows 155 us, 0.77 PFLOP/s; three sequences of 31 nodes
 // of 16 heads over 12001 4-bit rows in pages 80 us, where unpacking in both ranks is what bounds it (3500
 // clocks a tile).
 //
@@ -81,8 +82,8 @@ constexpr int kOffMade = kOffRope + 4 * kChunk;    // P of an even and of an odd
 constexpr int kOffF = kOffP + kIn * kP;
 static_assert(kOffMade + 2 * kP <= kOffF, "P");    // kOffF: float [4][128], roots of factors of O before P V
 constexpr int kOffM = kOffF + kIn * kRows * 4;       // float [2][128]: m after an even, an odd tile
-constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [2][2][128]: l, and its m, of both groups
-constexpr int kOffScale = kOffL + 4 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
+constexpr int kOffL = kOffM + 2 * kRows * 4;       // float [3][2][128]: both sums, and their m, of both groups
+constexpr int kOffScale = kOffL + 6 * kRows * 4;   // float [8 tiles][64]: scales of the keys (8-bit
                                                    // rows), or kRaws tiles' codes of scales (4-bit rows)
 constexpr int kOffThere = kOffScale + kRaws * 2048;  // uint64 [8 tiles]: keys that are there
 constexpr int kOffBars = kOffThere + 8 * 8;
@@ -109,7 +110,7 @@ struct Params {
   uint16_t* out;
   float* lse;
   float* part_o;   // [item][128 column quads][128 rows][4]
-  float* part_ml;  // [item][2][128]
+  float* part_ml;  // [item][3][128]: m, l, and the sum of the rounded terms
   uint32_t* err;
   Placement place;
   int32_t N, H, tiles, splits, steps;  // row tiles a sequence, key ranges, least steps of a range
@@ -868,7 +869,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
-      float m = kNegInf, l = 0.f;
+      // Two sums: of the terms as they are, for lse, and of the bf16 terms that the values are multiplied by, for
+      // the output. Divided by the latter, a term that outweighs the others loses nothing by its rounding: of
+      // random rows with 13 keys that count the output is 1.1 times as far off as its own rounding leaves it,
+      // where it is 1.5 times with the former. (The second sum costs 4% where most is to do, 4 sequences of 64
+      // nodes over 16384 rows; terms cut to bf16 instead of rounded 3%, and further off where many keys count.)
+      float m = kNegInf, l = 0.f, lr = 0.f;
       const uint32_t p_row = peer(smem0 + kOffP + r * 128 + (r & 7) * 16, 1);  // + kP * place
       const uint32_t f_row = peer(smem_u32(s_f + r), 1), bar0 = peer(smem_u32(p_full), 1);
       const uint32_t made = smem0 + kOffMade + grp * kP + r * 128 + (r & 7) * 16;
@@ -891,11 +897,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
         }
         // P with this group's m, in the layout of an MMA A operand; once more where m is another one now
-        float f = 1.f, sum;
+        float f = 1.f, sum, sum_r;
         for (int pass = 0;; ++pass) {  // (at most twice)
           const float off = m == kNegInf ? 0.f : -m;
           const uint64_t off2 = pack_f32x2(off, off), scale2 = pack_f32x2(to_log2, to_log2);
-          uint64_t sum2 = 0ull;
+          uint64_t sum2 = 0ull, sum2_r = 0ull;
           float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -935,17 +941,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                 unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
                                        scale2, off2),
                              x0, x1);
-                uint32_t e0 = __float_as_uint(exp2_approx(x0)), e1 = __float_as_uint(exp2_approx(x1));
-                sum2 = add_f32x2(sum2, pack_f32x2(__uint_as_float(e0), __uint_as_float(e1)));
-                if constexpr (k8) {  // the values are codes as well
-                  mul_pair(e0, e1, j == 0 ? sa.x : j == 1 ? sa.z : j == 2 ? sb.x : sb.z,
-                           j == 0 ? sa.y : j == 1 ? sa.w : j == 2 ? sb.y : sb.w);
-                  if constexpr (kMasked) {  // (0 times a scale that is not finite)
-                    e0 = see >> (32 * h + k) & 1 ? e0 : 0u;
-                    e1 = see >> (32 * h + k + 1) & 1 ? e1 : 0u;
-                  }
+                const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
+                sum2 = add_f32x2(sum2, pack_f32x2(e0, e1));
+                uint32_t r2 = pack_bf16x2(e0, e1);
+                sum2_r = add_f32x2(sum2_r, pack_f32x2(__uint_as_float(r2 << 16),
+                                                      __uint_as_float(r2 & 0xFFFF0000u)));
+                if constexpr (k8) {  // the values are codes as well; a scale's upper half is all of it
+                  r2 = ds4q::mul_bf16x2(r2, j == 0   ? __byte_perm(sa.x, sa.y, 0x7632)
+                                            : j == 1 ? __byte_perm(sa.z, sa.w, 0x7632)
+                                            : j == 2 ? __byte_perm(sb.x, sb.y, 0x7632)
+                                                     : __byte_perm(sb.z, sb.w, 0x7632));
+                  if constexpr (kMasked)  // (0 times a scale that is not finite)
+                    r2 &= (see >> (32 * h + k) & 1 ? 0xFFFFu : 0u) |
+                          (see >> (32 * h + k + 1) & 1 ? 0xFFFF0000u : 0u);
                 }
-                pk[j] = pack_bf16x2(__uint_as_float(e0), __uint_as_float(e1));
+                pk[j] = r2;
               }
               st_shared16(made ^ (16 * (4 * h + u)), make_uint4(pk[0], pk[1], pk[2], pk[3]));
             }
@@ -953,6 +963,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           float l0, l1;
           unpack_f32x2(sum2, l0, l1);
           sum = l0 + l1;
+          unpack_f32x2(sum2_r, l0, l1);
+          sum_r = l0 + l1;
           if (pass == 1) break;
           // m after the tile before, which the other group took; raised where a score passes it by more
           // than the slack. Finite once a key was seen: a score of +-infinity keeps its meaning in s - m.
@@ -975,11 +987,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           if (other) {
             const float fl = m == kNegInf ? 0.f : exp2_approx(0.5f * (m - now));
             l = l * fl * fl;
+            lr = lr * fl * fl;
             m = now;
           }
           if (!__any_sync(0xffffffffu, other)) break;
         }
         l += sum;
+        lr += sum_r;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[slot]);
@@ -1007,25 +1021,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       // ---------------- both groups' sums, to rank 1
       s_l[grp * kRows + r] = l;
       s_l[(2 + grp) * kRows + r] = m;
+      s_l[(4 + grp) * kRows + r] = lr;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (grp == 0) {
         m = g.n > 0 ? s_m[((g.n - 1) & 1) * kRows + r] : kNegInf;
-        l = 0.f;
+        l = lr = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float mk = s_l[(2 + k) * kRows + r];
           const float fl = mk == m ? 1.f : exp2_approx(0.5f * (mk - m));
-          if (mk != kNegInf) l += s_l[k * kRows + r] * fl * fl;
+          if (mk != kNegInf) l += s_l[k * kRows + r] * fl * fl, lr += s_l[(4 + k) * kRows + r] * fl * fl;
         }
-        if (padding) m = kNegInf, l = 0.f;
-        st_peer(peer(smem_u32(s_l + r), 1), l);
+        if (padding) m = kNegInf, l = lr = 0.f;
+        st_peer(peer(smem_u32(s_l + r), 1), lr);
         st_peer(peer(smem_u32(s_l + kRows + r), 1), m);
         __syncwarp();
         if (lane == 0) arrive_peer(peer(smem_u32(l_full), 1));
         if (p.splits > 1) {
-          const int k = excess(l);
-          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + r] = m + static_cast<float>(k);
-          p.part_ml[static_cast<int64_t>(item) * 2 * kRows + kRows + r] = l * power(-k);
+          const int k = excess(lr);
+          float* ml = p.part_ml + static_cast<int64_t>(item) * 3 * kRows + r;
+          ml[0] = m + static_cast<float>(k);
+          ml[kRows] = l * power(-k);
+          ml[2 * kRows] = lr * power(-k);
         } else if (used && p.lse) {
           p.lse[out_row] = m == kNegInf ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
         }
@@ -1241,7 +1258,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 constexpr int kJoinMany = 10;
 template <int kJoinParts>
 __global__ void __launch_bounds__(kRows * kJoinParts) tree_join_kernel(const __grid_constant__ Params p) {
-  __shared__ float s_m[kJoinParts][kRows], s_l[kJoinParts][kRows];
+  __shared__ float s_m[kJoinParts][kRows], s_l[kJoinParts][kRows], s_r[kJoinParts][kRows];
   __shared__ float4 s_o[kJoinParts][kRows];
   griddep_wait();
   griddep_launch_dependents();
@@ -1250,31 +1267,33 @@ __global__ void __launch_bounds__(kRows * kJoinParts) tree_join_kernel(const __g
   const int tile = static_cast<int>(group % p.tiles);
   const int64_t b = group / p.tiles;
   const int row = tile * kRows + r;
-  const float* ml = p.part_ml + group * p.splits * 2 * kRows + r;
+  const float* ml = p.part_ml + group * p.splits * 3 * kRows + r;
   float m = kNegInf;
 #pragma unroll 4
-  for (int i = part; i < p.splits; i += kJoinParts) m = fmaxf(m, ml[i * 2 * kRows]);
+  for (int i = part; i < p.splits; i += kJoinParts) m = fmaxf(m, ml[i * 3 * kRows]);
   s_m[part][r] = m;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kJoinParts; ++k) m = fmaxf(m, s_m[k][r]);
-  float l = 0.f;
+  float l = 0.f, lr = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* src = reinterpret_cast<const float4*>(p.part_o) +
                       (group * p.splits * 128 + quad) * kRows + r;
 #pragma unroll 4
   for (int i = part; i < p.splits; i += kJoinParts) {
-    const float mi = ml[i * 2 * kRows];
+    const float mi = ml[i * 3 * kRows];
     if (mi == kNegInf) continue;
     const float f = exp2_approx(mi - m);
     const float4 v = src[static_cast<int64_t>(i) * 128 * kRows];
-    l = fmaf(ml[i * 2 * kRows + kRows], f, l);
+    l = fmaf(ml[i * 3 * kRows + kRows], f, l);
+    lr = fmaf(ml[i * 3 * kRows + 2 * kRows], f, lr);
     o.x = fmaf(v.x, f, o.x);
     o.y = fmaf(v.y, f, o.y);
     o.z = fmaf(v.z, f, o.z);
     o.w = fmaf(v.w, f, o.w);
   }
   s_l[part][r] = l;
+  s_r[part][r] = lr;
   s_o[part][r] = o;
   __syncthreads();
   if (part > 0 || row >= p.N * p.H) return;
@@ -1282,13 +1301,14 @@ __global__ void __launch_bounds__(kRows * kJoinParts) tree_join_kernel(const __g
   for (int k = 1; k < kJoinParts; ++k) {
     const float4 v = s_o[k][r];
     l += s_l[k][r];
+    lr += s_r[k][r];
     o.x += v.x;
     o.y += v.y;
     o.z += v.z;
     o.w += v.w;
   }
   const bool none = m == kNegInf;
-  const float inv = none ? 0.f : 1.f / l;
+  const float inv = none ? 0.f : 1.f / lr;
   const int64_t out_row = b * p.N * p.H + row;
   if (quad == 0 && p.lse) p.lse[out_row] = none ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
   *reinterpret_cast<uint2*>(p.out + out_row * kLatent + 4 * quad) =
@@ -1324,7 +1344,7 @@ Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_le
   pl.splits = static_cast<int32_t>(best);
   pl.steps = static_cast<int32_t>((steps + best - 1) / best);
   pl.o_bytes = items * best * 2 * 64 * kRows * 16;
-  if (best > 1) pl.bytes = pl.o_bytes + items * best * 2 * kRows * 4;
+  if (best > 1) pl.bytes = pl.o_bytes + items * best * 3 * kRows * 4;
   return pl;
 }
 
