@@ -6,7 +6,8 @@
 // dims fills an SM's TMEM, so a pair of CTAs owns such a tile and a range of keys: one (rank 0) the
 // keys' products and the softmax, the other the values' products:
 //   S[128 x 64 keys] = Q K^T        rank 0; Q stays in TMEM as the A operand, three tiles of S beside it
-//   p = exp2(s - m) in bf16         rank 0; m is left alone until a score passes it by 64
+//   p = exp2(s - m) in bf16         rank 0; m is left alone until a score passes it by 64. The sums of p
+//                                   are fp32, and so are m and O.
 //   O[128 x 512] += P V             rank 1; O fills its TMEM over the whole range
 // P, and the factors of O where m was raised, are all that goes from one CTA to the other: 16 KB a tile,
 // stored straight into rank 1's shared memory with the bytes counted at a barrier there (the shared memory of
@@ -15,18 +16,17 @@
 // against 2.78 ms when both were first built (4 sequences of 64 nodes over 16384 rows, 128 heads, 8 bits).
 // Ranges of a split sequence leave (O, m, l) in fp32, and a second kernel joins them.
 //
-// What bounds it: a tile of 64 keys takes a pair 2450 clocks, 1.29 us. Rank 0's products take 36 times 57 to
-// 64 clocks (32 is the tensor core's rate, which an A operand from TMEM reaches from 128 keys on). Rank 1's
-// shared memory moves 240 KB a tile, 1900 clocks at 128 bytes each: codes in and out, bf16 in, out for the
-// products, P. Timing-only copies in which one side is made light: the case below took 1.28 ms, with half of
-// rank 0's products 1.27, with no value codes read 1.26, with both sides light 0.94; the second sum of the
-// softmax came later. A range costs 18 us
-// besides: set-up 2, Q 6, the end of the pipeline 2, O 4, the join 4.
+// What bounds it: a tile of 64 keys takes a pair 2550 clocks, 1.35 us. Rank 0's products take 36 times 57 to
+// 64 clocks (32 is the tensor core's rate), its softmax groups 3000 and more each for every other tile. Rank
+// 1's shared memory moves 240 KB a tile, 1900 clocks at 128 bytes each: codes in and out, bf16 in, out for the
+// products, P. Timing-only copies with one side made light (the first case below, 1.28 ms at that time): half
+// of rank 0's products 1.27, no value codes read 1.26, both sides light 0.94. A range costs 18 us besides:
+// set-up 2, Q 6, the end of the pipeline 2, O 4, the join 4.
 //
 // Measured on the device: 4 sequences of 64 nodes, 128 heads, 16384 8-bit rows 1.34 ms, 0.87 PFLOP/s; one
-// node over 262144 8-bit rows 100 us, 1.7 TB/s; 13 nodes over 32768 bf16 rows 155 us, 0.77 PFLOP/s; three sequences of 31 nodes
-// of 16 heads over 12001 4-bit rows in pages 80 us, where unpacking in both ranks is what bounds it (3500
-// clocks a tile).
+// node over 262144 8-bit rows 100 us, 1.7 TB/s; 13 nodes over 32768 bf16 rows 155 us, 0.77 PFLOP/s; three
+// sequences of 31 nodes of 16 heads over 12001 4-bit rows in pages 79 us, where unpacking in both ranks is
+// what bounds it (3500 clocks a tile).
 //
 // Both CTAs read the rows themselves and keep them in a ring of parts, 64 keys x 256 dims in the
 // 128-byte-swizzled layout that serves as K-major and as MN-major operand.
