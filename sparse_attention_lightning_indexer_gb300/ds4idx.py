@@ -156,9 +156,10 @@ def load(path: str | None = None):
                                               i32, i64, f32, vp, vp, vp, i64, vp]
         lib.ds4idx_tree_attention_workspace.argtypes = [i32, i32, i32, i64, vp]
         lib.ds4idx_tree_commit.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i32, vp, vp]
-        for name in ("quantize_latents_fp8", "read_latents_fp8", "tree_attention",
-                     "tree_attention_workspace", "tree_commit", "rotary_freqs", "rotary", "quantize_latents", "read_latents",
-                     "sparse_attention_q4", "evict_accumulate", "evict_select", "evict_compact"):
+        for name in ("rotary_freqs", "rotary", "quantize_latents", "read_latents",
+                     "sparse_attention_q4", "quantize_latents_fp8", "read_latents_fp8",
+                     "tree_attention", "tree_attention_workspace", "tree_commit",
+                     "evict_accumulate", "evict_select", "evict_compact"):
             getattr(lib, "ds4idx_" + name).restype = ctypes.c_int
         if path is None:
             _lib = lib
@@ -564,7 +565,8 @@ def read_latents_fp8(cache, scale, rows=None, start: int = 0, n: int | None = No
         n = R - int(start)
     if out is None:
         out = _new((n, SA_DQK), dtype, cache.device, stream)
-    _need(out, (n, SA_DQK), "out", None, dev)
+    else:
+        _need(out, (n, SA_DQK), "out", None, dev)
     _check(load().ds4idx_read_latents_fp8(_ptr(cache), _ptr(scale), R, _ptr(rows), int(start), n,
                                           _ptr(out), _in_dtype(out, "out"), _stream_ptr(stream, dev)),
            "ds4idx_read_latents_fp8")
@@ -614,17 +616,19 @@ def tree_attention(q, cache, kv_lens, mask, sm_scale: float, scale=None, kv_row0
     where = _placement(B, kv_row0, page_table, page_size, token_seq, dev)
     if max_kv_len is None:
         max_kv_len = R if page_table is None else min(R, page_table.shape[1] * int(page_size))
-    need = tree_attention_workspace(B, N, H, max_kv_len)
     if out is None:
         out = _new((B, N, H, SA_DV), torch.bfloat16, q.device, stream)
+    else:
+        _need(out, (B, N, H, SA_DV), "out", torch.bfloat16, dev)
     if lse is None:
         lse = _new((B, N, H), torch.float32, q.device, stream)
-    if workspace is None and need:
-        workspace = _new((need,), torch.uint8, q.device, stream)
-    _need(out, (B, N, H, SA_DV), "out", torch.bfloat16, dev)
-    _need(lse, (B, N, H), "lse", torch.float32, dev)
-    have = 0
-    if workspace is not None:
+    else:
+        _need(lse, (B, N, H), "lse", torch.float32, dev)
+    if workspace is None:
+        have = tree_attention_workspace(B, N, H, max_kv_len)
+        if have:
+            workspace = _new((have,), torch.uint8, q.device, stream)
+    else:
         have = workspace.shape[0]
         _need(workspace, (have,), "workspace", torch.uint8, dev)
     _check(load().ds4idx_tree_attention(_ptr(q), fmt, _ptr(cache), _ptr(scale), R, _ptr(kv_lens),
@@ -662,12 +666,15 @@ def tree_commit(arrays, kv_lens, path, n_accepted, kv_row0=None, page_table=None
     rows = arrays[0].shape[0] if n else 1
     d = ctypes.create_string_buffer(max(1, n) * _ROW_ARRAY.size)
     for k, a in enumerate(arrays):
-        _need(a, (rows, *a.shape[1:]), f"arrays[{k}]", None, dev)
+        if a is None or a.get_device() != dev or a.shape[0] != rows or not a.is_contiguous():
+            _need(a, (rows,) if a is None else (rows, *a.shape[1:]), f"arrays[{k}]", None, dev)
+        at = a.data_ptr()
         row = a.element_size() * math.prod(a.shape[1:])
-        _ROW_ARRAY.pack_into(d, k * _ROW_ARRAY.size, a.data_ptr(), a.data_ptr(), rows, rows, row, 0)
+        _ROW_ARRAY.pack_into(d, k * _ROW_ARRAY.size, at, at, rows, rows, row, 0)
     if new_lens is None:
         new_lens = _new((B,), torch.int32, path.device, stream)
-    _need(new_lens, (B,), "new_lens", torch.int32, dev)
+    else:
+        _need(new_lens, (B,), "new_lens", torch.int32, dev)
     _check(load().ds4idx_tree_commit(_ptr(kv_lens), _ptr(path), _ptr(n_accepted), _ptr(new_lens),
                                      _ref(where), B, N, rows, n, ctypes.addressof(d),
                                      _stream_ptr(stream, dev)), "ds4idx_tree_commit")

@@ -155,3 +155,8 @@ def test_cache_formats(devices):  # noqa: F811
                  (Tensor((9, 512), U8), None), (Tensor((9, 640), BF16), None)):
         with pytest.raises(ValueError):
             fmt(c, s, 0)
+
+
+def test_tree_attention_output_is_32_byte_aligned(library):
+    assert library.ds4idx_tree_attention(P, 1, P, P, 100, P, P, None, 2, 4, 16, 576, 512, 64, 1.0,
+                                         P + 16, P, None, 0, None) == ds4idx.ERR_INVALID_ARG
