@@ -20,11 +20,11 @@
 // 64 clocks (32 is the tensor core's rate), its softmax groups 3000 and more each for every other tile. Rank
 // 1's shared memory moves 240 KB a tile, 1900 clocks at 128 bytes each: codes in and out, bf16 in, out for the
 // products, P. Timing-only copies with one side made light (the first case below, 1.28 ms at that time): half
-// of rank 0's products 1.27, no value codes read 1.26, both sides light 0.94. A range costs 18 us besides:
-// set-up 2, Q 6, the end of the pipeline 2, O 4, the join 4.
+// of rank 0's products 1.27, no value codes read 1.26, both sides light 0.94. A range costs 16 us besides:
+// set-up 2, Q 4, the end of the pipeline 2, O 4, the join 4.
 //
-// Measured on the device: 4 sequences of 64 nodes, 128 heads, 16384 8-bit rows 1.34 ms, 0.87 PFLOP/s; one
-// node over 262144 8-bit rows 100 us, 1.7 TB/s; 13 nodes over 32768 bf16 rows 155 us, 0.77 PFLOP/s; three
+// Measured on the device: 4 sequences of 64 nodes, 128 heads, 16384 8-bit rows 1.32 ms, 0.89 PFLOP/s; one
+// node over 262144 8-bit rows 99 us, 1.7 TB/s; 13 nodes over 32768 bf16 rows 155 us, 0.77 PFLOP/s; three
 // sequences of 31 nodes of 16 heads over 12001 4-bit rows in pages 79 us, where unpacking in both ranks is
 // what bounds it (3500 clocks a tile).
 //
@@ -94,6 +94,7 @@ constexpr int kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448 && kOffBars % 8 == 0, "shared memory");
 constexpr uint32_t kColRope = 256, kColS = 320;    // rank 0: Q from column 0, S; rank 1: O from 0
 constexpr uint32_t kColLow = 128;                  // the low parts of Q beside 8-bit keys
+constexpr uint32_t kColAside = 288;                // 224 columns that hold Q before it is turned
 constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
 // log2 of what exp2(s - m) may be before m is raised. P and the sums are floating point with 2^127 of
 // range, so a stale m costs no precision: 2^64 leaves 2^63 for the count and size of the values. (With 2^8
@@ -776,8 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       mask &= ~0ull >> (64 - p.N);
       float to_log2 = p.scale_log2;  // of a score, from S
       if (g.n > 0) {
-        // Q to TMEM by way of shared memory, so that it is read a line at a time: 5.7 us beside 8-bit rows,
-        // whose queries' largest values are needed first, where reading by the rows' threads took 17.
+        // Q to TMEM by way of shared memory, so that it is read a line at a time: 2.1 us, beside 8-bit rows 4.2.
+        // (There reading by the rows' threads took 17, and a pass of its own for the rows' largest values 5.7.)
         const int q_rows = min(kRows, p.N * p.H - tile * kRows);  // of the tile
         const uint8_t* q0 = reinterpret_cast<const uint8_t*>(
             p.q + (static_cast<int64_t>(b) * p.N * p.H + tile * kRows) * kDims);
@@ -798,50 +799,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         };
         copy_q(grp);
         copy_q(grp + 2);
-        float f = 1.f;
-        uint32_t f2 = 0;
-        if constexpr (k8) {
-          // The power of two that takes a row's largest value to 2^7 .. 2^8; a warp takes 16 rows, four at a
-          // time.
-#pragma unroll 1
-          for (int j = 0; j < 16; j += 4) {
-            uint4 v[4][3];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int at = warp * 16 + j + k;
-#pragma unroll
-              for (int c = 0; c < 3; ++c)
-                v[k][c] = ld_row16(q0 + at * (2 * kDims) + (lane + 32 * c) * 16,
-                                   at < q_rows && lane + 32 * c < kDims / 8 ? 0 : -1);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t top = 0;
-#pragma unroll
-              for (int c = 0; c < 3; ++c)
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k][c].x & 0x7FFF7FFFu, v[k][c].y & 0x7FFF7FFFu),
-                                             __vmaxu2(v[k][c].z & 0x7FFF7FFFu, v[k][c].w & 0x7FFF7FFFu)));
-              top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-              if (lane == 0) s_l[warp * 16 + j + k] = __uint_as_float(top);
-            }
-          }
-          asm volatile("bar.sync 1, 256;" ::: "memory");
-          const int e = static_cast<int>(__float_as_uint(s_l[r]) >> 7);         // biased by 127
-          const int a = max(-110, min(110, e == 0 ? 0 : 127 + 7 - e));          // (zero: any)
-          f = power(a);
-          f2 = static_cast<uint32_t>(127 + a) * 0x00800080u;
-          // (neither 0 nor infinite, which times a masked score's infinity or a score of 0 would be NaN)
-          to_log2 = fminf(fmaxf(to_log2 * power(-a), power(-126)), kMax);
-        }
-#pragma unroll 1
-        for (int h = grp; h < 18; h += 2) {
+        // The next of this group's pieces that are on their way.
+        auto take_q = [&](int h, uint32_t(&v)[16]) {
           cp_async_wait<1>();
           __syncwarp();
-          uint32_t v[16];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const uint4 x =
-                ld_shared16(stage + (h >> 1 & 1) * 2048 + lane * 64 + ((u ^ (lane >> 1)) & 3) * 16);
+            const uint4 x = ld_shared16(stage + (h >> 1 & 1) * 2048 + lane * 64 + ((u ^ (lane >> 1)) & 3) * 16);
             v[4 * u] = x.x;
             v[4 * u + 1] = x.y;
             v[4 * u + 2] = x.z;
@@ -849,17 +813,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
           __syncwarp();
           copy_q(h + 4);
-          if (k8 && h < 16) {
+        };
+        if constexpr (k8) {
+          // The pieces wait for the row's largest value, seven of a group's nine where S will be.
+          const uint32_t aside = lanes + kColAside + grp * 7 * 16;
+          uint32_t top = 0, v[16], latent[16], rope[16];
+          auto raise = [&](const uint32_t(&x)[16]) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) top = __vmaxu2(top, x[j] & 0x7FFF7FFFu);
+          };
+#pragma unroll 1
+          for (int j = 0; j < 7; ++j) {
+            take_q(grp + 2 * j, v);
+            raise(v);
+            tmem_st16(aside + j * 16, v);
+          }
+          take_q(grp + 14, latent);
+          raise(latent);
+          take_q(grp + 16, rope);
+          raise(rope);
+          top = max(top & 0xFFFFu, top >> 16);
+          s_l[grp * kRows + r] = __uint_as_float(top);
+          tmem_wait_st();
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          // the power of two that takes it to 2^7 .. 2^8
+          const int e =
+              static_cast<int>(max(top, __float_as_uint(s_l[(grp ^ 1) * kRows + r])) >> 7);  // biased by 127
+          const int a = max(-110, min(110, e == 0 ? 0 : 127 + 7 - e));                     // (zero: any)
+          const float f = power(a);
+          auto put = [&](int h, const uint32_t(&x)[16]) {
             uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) bf16_to_f8_pair(v[2 * j], v[2 * j + 1], f, hi[j], lo[j]);
+            for (int j = 0; j < 8; ++j) bf16_to_f8_pair(x[2 * j], x[2 * j + 1], f, hi[j], lo[j]);
             tmem_st8(lanes + h * 8, hi);
             tmem_st8(lanes + kColLow + h * 8, lo);
-          } else {
-            if constexpr (k8) {
+          };
+          put(grp + 14, latent);
+          const uint32_t f2 = static_cast<uint32_t>(127 + a) * 0x00800080u;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = ds4q::mul_bf16x2(v[j], f2);
-            }
+          for (int j = 0; j < 16; ++j) rope[j] = ds4q::mul_bf16x2(rope[j], f2);
+          tmem_st16(lanes + (grp + 16) * 16, rope);
+#pragma unroll 1
+          for (int j = 0; j < 7; ++j) {
+            tmem_ld16(aside + j * 16, v);
+            tmem_wait_ld();
+            put(grp + 2 * j, v);
+          }
+          // (neither 0 nor infinite, which times a masked score's infinity or a score of 0 would be NaN)
+          to_log2 = fminf(fmaxf(to_log2 * power(-a), power(-126)), kMax);
+        } else {
+#pragma unroll 1
+          for (int h = grp; h < 18; h += 2) {
+            uint32_t v[16];
+            take_q(h, v);
             tmem_st16(lanes + h * 16, v);
           }
         }
