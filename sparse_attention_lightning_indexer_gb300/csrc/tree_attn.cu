@@ -365,8 +365,10 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
   const bool steps = tp.table == nullptr;
   const int32_t page = steps ? 1 : p.place.page, pages = tp.ok ? p.place.pages : 0;
   const int32_t page_step = kKeys / page, place_step = kKeys % page;
-  int32_t row[2], page_no[2] = {}, place[2] = {}, id[2] = {};
-  auto look_up = [&](int k) { id[k] = page_no[k] < pages ? tp.table[page_no[k]] : -1; };
+  // (Unsigned: the tiles read ahead may lie past position 2^31, and there is no page.)
+  int32_t row[2], id[2] = {};
+  uint32_t page_no[2] = {}, place[2] = {};
+  auto look_up = [&](int k) { id[k] = page_no[k] < static_cast<uint32_t>(pages) ? tp.table[page_no[k]] : -1; };
   // Rows of tile i, whose entries are read, and the entries of the tile after it.
   auto find_rows = [&](int i) {
 #pragma unroll
@@ -379,7 +381,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
         is = is && id[k] >= 0 && r < p.place.rows;
         page_no[k] += page_step;
         place[k] += place_step;
-        if (place[k] >= page) place[k] -= page, ++page_no[k];
+        if (place[k] >= static_cast<uint32_t>(page)) place[k] -= page, ++page_no[k];
         look_up(k);
       }
       row[k] = is ? static_cast<int32_t>(r) : -1;

@@ -161,9 +161,10 @@ def test_a_page_of_half_the_positions_and_many_short_sequences():
     N, n = 2, 130
     cache, scale, kv = _cache("fp8", 200, 5)
     q, masks = _q(1, N, 128, 3), [[1, 3]]
-    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64(masks), 0.04, scale=scale,
-                                     page_table=_i32([[0, 7]]), page_size=1 << 30)
-    _check(q, kv, [list(range(n + N))], [n], masks, 0.04, out, lse)
+    for page in (1 << 30, 2 ** 31 - 1):
+        out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64(masks), 0.04, scale=scale,
+                                         page_table=_i32([[0, 7]]), page_size=page, max_kv_len=n)
+        _check(q, kv, [list(range(n + N))], [n], masks, 0.04, out, lse)
     B = 1500
     lens = [b % 5 for b in range(B)]
     starts, R, rows = _contiguous(lens, 1, gap=0)
