@@ -1330,11 +1330,12 @@ struct Plan {
   int32_t tiles, splits, steps;
   int64_t o_bytes, bytes;
 };
-// Key ranges: the number that takes the least time, in steps of 64 keys (1.25 us). A range costs some 14
-// steps besides its own (set-up, Q, its part of O), the join 4. Several sequences have lengths of their
-// own, so that not every pair of a last round has as much to do: half way between full rounds and ranges of
-// three quarters of the longest without a gap. (8 ragged sequences of 7 nodes and up to 5000 rows: 119 us as
-// one range each, 85 as two; 3 of 31 nodes, 16 heads, 12001 rows: 88 as six, 120 as nine.)
+// Key ranges: the number that takes the least time, in steps of 64 keys (1.35 us). A range costs some 14
+// steps besides its own (set-up, Q, its part of O, and what its last products wait for), the join 4. Several
+// sequences have lengths of their own, so that not every pair of a last round has as much to do: half way
+// between full rounds and ranges of three quarters of the longest without a gap. (8 ragged sequences of 7
+// nodes and up to 5000 rows: 127 us as one range each, 90 as two, 113 as three; 3 of 31 nodes, 16 heads, 12001
+// rows: 139 as three, 80 as six, 109 as nine; 13 nodes over 32768 rows: 247 as three, 156 as five, 179 as ten.)
 Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
   Plan pl{};
   pl.tiles = (N * H + kRows - 1) / kRows;
