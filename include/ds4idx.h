@@ -448,8 +448,8 @@ typedef enum {
  * Cache values are exact in bf16; products accumulate in fp32, softmax and sums are fp32, the
  * probabilities are rounded to bf16 for the value product and divided by the sum of the rounded ones.
  * Beside an 8-bit cache the first 512 dims of a query are the sum of two 8-bit numbers: exact, or off by
- * at most 2^-21 of the query's largest value; rotary dims are finite there and below 2^90, queries
- * finite. What a row that is not seen holds (NaN included) does not reach the results. Scores that are
+ * at most 2^-21 of the query's largest value or of 2^-119, whichever is larger; rotary dims are finite
+ * there and below 2^90, and a query that is not finite makes NaN of its output. What a row that is not seen holds (NaN included) does not reach the results. Scores that are
  * not finite follow the formulas, as in ds4idx_sparse_attention_q4; the values of a drafted row that
  * are not finite count as 0 (its scores still make NaN of the nodes that see it). Asynchronous on `stream`, allocates nothing. Bounded device waits that run
  * out are recorded for ds4idx_sparse_attention_status.

@@ -40,7 +40,7 @@
 // P, exactly. As keys they are E4M3 operands as they stand, and Q, scaled by a power of two, is a sum of an
 // E4M3 and an E5M2 operand: two products at twice the rate, and nothing to unpack. That sum holds a bf16
 // exactly, but for what of a row of Q lies 2^13 and more below its largest value: that is off by at most
-// 2^-21 of the largest (bf16_to_f8_pair). As values the codes are bf16 (P needs its range and bits).
+// 2^-21 of the largest, or of 2^-119 (bf16_to_f8_pair). As values the codes are bf16 (P needs its range and bits).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -838,10 +838,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           s_l[grp * kRows + r] = __uint_as_float(top);
           tmem_wait_st();
           asm volatile("bar.sync 1, 256;" ::: "memory");
-          // the power of two that takes it to 2^7 .. 2^8
+          // the power of two that takes it to 2^7 .. 2^8, or as near as a normal one whose inverse is normal
+          // too does: rows below 2^-119 stay below 2^7. (A row that is not finite is multiplied by 0: NaN, where
+          // the conversions would saturate.)
           const int e =
               static_cast<int>(max(top, __float_as_uint(s_l[(grp ^ 1) * kRows + r])) >> 7);  // biased by 127
-          const int a = max(-110, min(110, e == 0 ? 0 : 127 + 7 - e));                     // (zero: any)
+          const int a = e == 255 ? -127 : min(126, 127 + 7 - e);
           const float f = power(a);
           auto put = [&](int h, const uint32_t(&x)[16]) {
             uint32_t hi[8], lo[8];

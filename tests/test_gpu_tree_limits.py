@@ -1,0 +1,76 @@
+"""Tree attention and commit at the limits of their arguments.
+Tolerances: those of test_gpu_tree_attention and test_gpu_tree_edges where nothing else is said."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from sparse_attention_lightning_indexer_gb300 import ds4idx
+
+from . import tree_reference as ref
+from .test_gpu_tree_attention import _cache, _check, _contiguous, _i32, _i64, _masks, _q
+
+pytestmark = pytest.mark.gpu
+KINDS = ["fp8", "bf16", "q4"]
+
+
+def _fp8_rows(x):
+    """(cache, scale, values in 64 bits) of bf16 rows x."""
+    rope = x[:, 512:].contiguous().view(torch.int16).numpy().view(np.uint16)
+    rows, s = ref.quantize_f8(x.double().numpy(), rope)
+    return (torch.from_numpy(rows).cuda(), torch.from_numpy(s).float().cuda(),
+            torch.from_numpy(ref.dequantize_f8(rows, s)).cuda())
+
+
+# The query's error beside 8-bit rows, 2^-21 of the largest value of its row or of 2^-119, enters the scores'.
+def _check_ends(q, kv, rows, lens, masks, sm, out, lse, f8):
+    o_ref, l_ref, av, big, seen = ref.attention(q.double(), kv, rows, lens, masks, sm)
+    qe = torch.zeros_like(big)
+    if f8:
+        top = q.double().abs().amax(dim=-1).clamp_min(2.0 ** -119)
+        qe = 2.0 ** -21 * sm * top * kv[:, :512].abs().sum(dim=1).max()
+    d = 37 * 2.0 ** -22 * (big + qe) + 2.0 ** -20 * (1 + big + qe) + qe
+    t = seen * 2.0 ** -23 + 2.0 ** -20
+    bound = (2.0 ** -7 + 2.0 ** -15 + 2 * (d + t)[..., None]) * av
+    bound = bound + 2.0 ** -8 * (o_ref.abs() + bound) + seen[..., None] * 2.0 ** -126 * kv.abs().max()
+    assert bool(((out.double() - o_ref).abs() <= bound).all())
+    assert bool(((lse.double() - l_ref).abs() <= d + t).all())
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("size,sm,rows_up", [
+    (2.0 ** 110, 0.04 * 2.0 ** -110, 0), (2.0 ** 118, 0.04 * 2.0 ** -118, 0),
+    (2.0 ** 122, 0.04 * 2.0 ** -118, -4), (2.0 ** 125, 0.04 * 2.0 ** -118, -7), (2.0 ** -105, 2.0 ** 99, 2),
+    (2.0 ** -112, 2.0 ** 99, 9), (2.0 ** -118, 2.0 ** 99, 13), (2.0 ** -124, 2.0 ** 99, 13)])
+def test_queries_at_the_ends_of_their_range(kind, size, sm, rows_up):
+    n, N = 200, 2
+    g = torch.Generator().manual_seed(7)
+    x = (torch.randn(n + N, 576, generator=g) * 2.0 ** rows_up).to(torch.bfloat16)
+    cache, scale, kv = _fp8_rows(x) if kind == "fp8" else (x.cuda(), None, x.double().cuda())
+    q = (torch.randn(1, N, 128, 576, generator=g).clamp(-4, 4).double() * size).to(torch.bfloat16).cuda()
+    assert bool(q.isfinite().all())
+    sm = float(np.float32(sm))                    # (products stay below 2^128; more than 2^99 is refused)
+    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64([[1, 3]]), sm, scale=scale)
+    ds4idx.sparse_attention_status()
+    _check_ends(q, kv, [list(range(n + N))], [n], [[1, 3]], sm, out, lse, kind == "fp8")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("at", [5, 550])
+def test_queries_that_are_not_finite_make_nan_of_their_rows_alone(kind, at):
+    n, N, H = 130, 2, 16
+    cache, scale, kv = _cache(kind, n + N, 3)
+    q = _q(1, N, H, 3)
+    q[0, 0, 3, at] = float("inf")
+    q[0, 1, 0, at] = -float("inf")
+    q[0, 1, 7, at] = float("nan")
+    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64([[1, 3]]), 0.04, scale=scale)
+    ds4idx.sparse_attention_status()
+    bad = torch.zeros(N, H, dtype=torch.bool, device="cuda")
+    bad[0, 3] = bad[1, 0] = bad[1, 7] = True
+    assert bool(out[0][bad].isnan().all()) and not bool(lse[0][bad].isfinite().any())
+    clean = q.clone()
+    clean[0][bad] = 0
+    want, l_want = ds4idx.tree_attention(clean, cache, _i32([n]), _i64([[1, 3]]), 0.04, scale=scale)
+    assert torch.equal(out[0][~bad], want[0][~bad]) and torch.equal(lse[0][~bad], l_want[0][~bad])
