@@ -45,6 +45,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -115,7 +116,9 @@ struct Params {
   uint32_t* err;
   Placement place;
   int32_t N, H, tiles, splits, steps;  // row tiles a sequence, key ranges, least steps of a range
-  float scale_log2;
+  float scale_log2;      // of a score, from a product: may be subnormal
+  float scale_fraction;  // the same, of 0.5 .. 1, times 2^scale_exp
+  int32_t scale_exp;
 };
 
 // The range of keys of a work item: steps lo .. lo + n - 1 of 64 positions.
@@ -864,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             put(grp + 2 * j, v);
           }
           // (neither 0 nor infinite, which times a masked score's infinity or a score of 0 would be NaN)
-          to_log2 = fminf(fmaxf(to_log2 * power(-a), power(-126)), kMax);
+          to_log2 = p.scale_fraction * power(max(-125, min(127, p.scale_exp - a)));
         } else {
 #pragma unroll 1
           for (int h = grp; h < 18; h += 2) {
@@ -1423,7 +1426,11 @@ extern "C" int ds4idx_tree_attention(const void* q, int32_t format, const void* 
   p.tiles = pl.tiles;
   p.splits = pl.splits;
   p.steps = pl.steps;
-  p.scale_log2 = std::max(sm_scale * 1.4426950408889634f, 0x1p-126f);
+  // A subnormal scale of products below 2^128 leaves scores off by 2^-22 at most. Beside 8-bit rows, whose
+  // queries are scaled as well, it is held in full.
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.scale_fraction = static_cast<float>(std::frexp(
+      p.scale_log2 < 0x1p-126f ? sm_scale * 1.4426950408889634 : p.scale_log2, &p.scale_exp));
   const int64_t items = static_cast<int64_t>(B) * pl.tiles * pl.splits;
   if (items * 2 > 0x7FFFFFFF) return DS4IDX_ERR_INVALID_ARG;
   const int st = format == DS4IDX_CACHE_FP8    ? launch<DS4IDX_CACHE_FP8>(p, items, stream)

@@ -74,3 +74,34 @@ def test_queries_that_are_not_finite_make_nan_of_their_rows_alone(kind, at):
     clean[0][bad] = 0
     want, l_want = ds4idx.tree_attention(clean, cache, _i32([n]), _i64([[1, 3]]), 0.04, scale=scale)
     assert torch.equal(out[0][~bad], want[0][~bad]) and torch.equal(lse[0][~bad], l_want[0][~bad])
+
+
+# The least normal fp32 number is 2^-126.
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sm", [2.0 ** -125, 2.0 ** -126, 2.0 ** -127, 0.7 * 2.0 ** -129])
+def test_scales_of_scores_below_the_least_normal_number(kind, sm):
+    n, N = 200, 2
+    g = torch.Generator().manual_seed(5)
+    cache, scale, kv = _cache(kind, n + N, 5)
+    q = torch.randn(1, N, 128, 576, generator=g).clamp(-3, 3).double() * 2.0 ** 116
+    q = q.to(torch.bfloat16).cuda()
+    if kind != "fp8":                   # (products stay below 2^128)
+        assert float(q.double().norm(dim=-1).max() * kv.norm(dim=-1).max()) < 2.0 ** 128
+    sm = float(np.float32(sm))
+    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64([[1, 3]]), sm, scale=scale)
+    ds4idx.sparse_attention_status()
+    _check_ends(q, kv, [list(range(n + N))], [n], [[1, 3]], sm, out, lse, kind == "fp8")
+
+
+# Beside 8-bit rows the products may pass 2^128 before they are scaled.
+@pytest.mark.parametrize("sm", [0.04 * 2.0 ** -125, 2.0 ** -133, 3 * 2.0 ** -149])
+def test_subnormal_scales_beside_large_8_bit_rows(sm):
+    n, N = 200, 2
+    g = torch.Generator().manual_seed(6)
+    up = 1.0 if sm > 2.0 ** -131 else 2.0 ** 10
+    cache, scale, kv = _fp8_rows((torch.randn(n + N, 576, generator=g) * up).to(torch.bfloat16))
+    q = (torch.randn(1, N, 128, 576, generator=g).clamp(-3, 3).double() * 2.0 ** 125).to(torch.bfloat16).cuda()
+    sm = float(np.float32(sm))
+    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64([[1, 3]]), sm, scale=scale)
+    ds4idx.sparse_attention_status()
+    _check_ends(q, kv, [list(range(n + N))], [n], [[1, 3]], sm, out, lse, True)
