@@ -98,10 +98,14 @@ constexpr uint32_t kColLow = 128;                  // the low parts of Q beside 
 constexpr uint32_t kColAside = 288;                // 224 columns that hold Q before it is turned
 constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
 // log2 of what exp2(s - m) may be before m is raised. P and the sums are floating point with 2^127 of
-// range, so a stale m costs no precision: 2^64 leaves 2^63 for the count and size of the values. (With 2^8
+// range, so a stale m costs no precision, but it takes room from the values. Those of 8 and 4 bits are below 2^16,
+// which leaves 2^47 for their number. bf16 ones may be anything: 2^32 leaves room for values below 2^64 in
+// sequences of any length (2^31 of them), for 3% of the time of 13 nodes over 32768 rows (155 and 159 us). (With 2^8
 // some row of 128 raises m in most of the first hundred tiles, and a rescaling holds P V up for 4000 clocks:
-// one node over 262144 rows 150 us where it takes 98, 4 sequences of 64 nodes over 16384 1.78 and 1.28 ms.)
-constexpr float kSlack = 64.f;
+// one node over 262144 8-bit rows 150 us where it takes 98, 107 with 2^32; 4 sequences of 64 nodes over 16384
+// 1.78, 1.32 and 1.36 ms.)
+template <int kFormat>
+constexpr float kSlack = kFormat == DS4IDX_CACHE_BF16 ? 32.f : 64.f;
 
 struct Params {
   const uint16_t* q;
@@ -989,11 +993,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * to_log2;
           float now = fminf(fmaxf(top, -kMax), kMax);
-          if (see == 0ull || (before != kNegInf && now <= before + kSlack)) now = before;
+          if (see == 0ull || (before != kNegInf && now <= before + kSlack<kFormat>)) now = before;
           s_m[grp * kRows + r] = now;
           __syncwarp();
           if (lane == 0) mbar_arrive(&m_full[warp]);
-          // Roots of factors: what is 2^64 above an old m may matter 2^-126 above the new one, where
+          // Roots of factors: what is 2^kSlack above an old m may matter 2^-126 above the new one, where
           // 2^(old - new) is long zero.
           if (now != before && before != kNegInf) f = exp2_approx(0.5f * (before - now));
           const bool other = now != m;
