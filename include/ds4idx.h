@@ -433,7 +433,8 @@ typedef enum {
  * over positions j < kv_lens[b], and j = kv_lens[b] + k where bit k of mask[b,i] is set.
  *  q        [B, n_nodes, n_heads, 576] bf16, 16-byte aligned; n_nodes 1..64, n_heads 1..128.
  *  cache    [kv_rows, ...] in `format`, 32-byte aligned, 1 <= kv_rows < 2^31; scale [kv_rows] fp32 for
- *           DS4IDX_CACHE_FP8 (powers of two, 2^-24 .. 2^7), else NULL.
+ *           DS4IDX_CACHE_FP8 (powers of two, 2^-24 .. 2^7), else NULL. One that is negative or lies
+ *           between powers of two makes NaN of the nodes that see its row.
  *  kv_lens  DEVICE int32 [B] (>= 0; less counts as 0), mask DEVICE int64 [B, n_nodes].
  *  where    HOST, may be NULL (row = position); its "tokens" are the B sequences. A position past a
  *           sequence's table row or outside the pool is not there; a sequence whose kv_row0 is negative

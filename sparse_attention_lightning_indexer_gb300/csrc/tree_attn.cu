@@ -434,7 +434,9 @@ __device__ __forceinline__ void load_rows(const Params& p, const Range& g, int b
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t rope = rope_address(n >> 1, 4 * k + sub);
-          const uint32_t s2 = (254u - (__float_as_uint(scales[4 * k + sub]) >> 23 & 0xFFu)) * 0x00800080u;
+          // (a scale that is no power of two, which P and these dims cannot follow, makes NaN of the scores)
+          const uint32_t bits = __float_as_uint(scales[4 * k + sub]);
+          const uint32_t s2 = bits & 0x807FFFFFu ? 0x7FFF7FFFu : (254u - (bits >> 23)) * 0x00800080u;
           const uint4 x = ld_shared16(rope);
           st_shared16(rope, make_uint4(ds4q::mul_bf16x2(x.x, s2), ds4q::mul_bf16x2(x.y, s2),
                                        ds4q::mul_bf16x2(x.z, s2), ds4q::mul_bf16x2(x.w, s2)));

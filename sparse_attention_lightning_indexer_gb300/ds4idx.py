@@ -601,12 +601,13 @@ def tree_attention(q, cache, kv_lens, mask, sm_scale: float, scale=None, kv_row0
     """Attention of the nodes of B drafted trees, q [B, N, H, 576] (bf16, N <= 64, H <= 128), over all
     rows of their sequences and the drafted rows that each node sees (see include/ds4idx.h).
 
-    cache: bf16 [R, 576], or uint8 [R, 640] with its ``scale`` [R], or the 4-bit uint8 [R, 416]. The
-    drafted rows stand behind the kv_lens [B] (int32) rows of their sequence; bit j of mask [B, N]
-    (int64) says that a node sees drafted row j (itself among them; 0: padding). Position s of sequence
-    b is row kv_row0[b] + s, or is found through page_table as in ``sparse_attention_q4`` (token_seq:
-    the table row of each sequence). max_kv_len: a bound of kv_lens that the work is laid out for (None:
-    what the pool or a table row holds). Returns (out [B, N, H, 512] bf16, lse [B, N, H] fp32)."""
+    cache: bf16 [R, 576], or uint8 [R, 640] with its ``scale`` [R] (the powers of two that
+    ``quantize_latents_fp8`` writes; others make NaN), or the 4-bit uint8 [R, 416]. The drafted rows
+    stand behind the kv_lens [B] (int32) rows of their sequence; bit j of mask [B, N] (int64) says that
+    a node sees drafted row j (itself among them; 0: padding). Position s of sequence b is row
+    kv_row0[b] + s, or is found through page_table as in ``sparse_attention_q4`` (token_seq: the table
+    row of each sequence). max_kv_len: a bound of kv_lens that the work is laid out for (None: what the
+    pool or a table row holds). Returns (out [B, N, H, 512] bf16, lse [B, N, H] fp32)."""
     B, N, H = q.shape[0], q.shape[1], q.shape[2]
     dev = _device(q, "q")
     _need(q, (B, N, H, SA_DQK), "q", torch.bfloat16, dev)

@@ -125,3 +125,17 @@ def test_values_up_to_2_to_the_64(above):
     out, lse = ds4idx.tree_attention(q, x.cuda(), _i32([n]), _i64([[1]]), sm, max_kv_len=0)
     ds4idx.sparse_attention_status()
     _check(q, x.double().cuda(), [list(range(n + N))], [n], [[1]], sm, out, lse)
+
+
+@pytest.mark.parametrize("factor", [1.5, 1 + 2.0 ** -23, 1 - 2.0 ** -24, -1.0])
+def test_a_scale_that_is_no_power_of_two_makes_nan_of_the_nodes_that_see_its_row(factor):
+    n, N, H = 200, 3, 16
+    for row in (30, 150, n + 1):
+        cache, scale, kv = _cache("fp8", n + N, 5)
+        scale[row] *= factor
+        out, lse = ds4idx.tree_attention(_q(1, N, H, 1), cache, _i32([n]), _i64([[1, 3, 5]]), 0.04, scale=scale)
+        ds4idx.sparse_attention_status()
+        seen = [0, 1, 2] if row < n else [1]
+        rest = [i for i in range(N) if i not in seen]
+        assert bool(out[0, seen].isnan().all()) and bool(lse[0, seen].isnan().all())
+        assert bool(out[0, rest].isfinite().all()) and bool(lse[0, rest].isfinite().all())
