@@ -511,9 +511,10 @@ int ds4idx_evict_compact(const int32_t* kept, int64_t width, int32_t B, const in
 
 /* Keeps the accepted path of each drafted tree: in every array, the row of position kv_lens[b] + j
  * becomes the row of position kv_lens[b] + path[b][j], j < n_accepted[b], and new_lens[b] = kv_lens[b] +
- * n_accepted[b] (counts outside 0..n_nodes are clamped). In place: all rows of a path are read before one
- * is written, so that a path may name any nodes. An entry of path outside 0..n_nodes-1, or a position
- * that is not there, leaves its row as it is.
+ * n_accepted[b], at most 2^31 - 1 (counts outside 0..n_nodes are clamped). In place: all rows of a path are
+ * read before one is written, so that a path may name any nodes. An entry of path outside 0..n_nodes-1, or a
+ * position that is not there, leaves its row as it is; of a negative length no position is there, and its sum
+ * with n_accepted[b] is the new length all the same.
  *  kv_lens, n_accepted DEVICE int32 [B]; path DEVICE int32 [B, n_nodes], n_nodes 1..64; new_lens DEVICE
  *  int32 [B]; where as in ds4idx_tree_attention; rows: the pool's, of every array (1 <= rows < 2^31).
  *  arrays HOST, 0 <= n_arrays <= 8, src = dst and src_rows = dst_rows = rows in each.

@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
   const int b = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
   const int64_t len = p.lens[b];
   const int n = min(max(p.count[b], 0), p.n_nodes);
-  if (slice == 0 && threadIdx.x == 0) p.new_lens[b] = static_cast<int32_t>(len + n);
+  if (slice == 0 && threadIdx.x == 0)
+    p.new_lens[b] = static_cast<int32_t>(min(len + n, static_cast<int64_t>(0x7FFFFFFF)));
   if (p.n_arrays == 0) return;
   if (threadIdx.x < n) {
     const int j = threadIdx.x;

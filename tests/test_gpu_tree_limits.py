@@ -139,3 +139,9 @@ def test_a_scale_that_is_no_power_of_two_makes_nan_of_the_nodes_that_see_its_row
         rest = [i for i in range(N) if i not in seen]
         assert bool(out[0, seen].isnan().all()) and bool(lse[0, seen].isnan().all())
         assert bool(out[0, rest].isfinite().all()) and bool(lse[0, rest].isfinite().all())
+
+
+def test_new_lengths_end_at_the_largest_int32():
+    top = 2 ** 31 - 1
+    new = ds4idx.tree_commit([], _i32([top, top - 2, top - 3, 5, -1]), _i32([[0, 1, 2]] * 5), _i32([3] * 5))
+    assert new.tolist() == [top, top, top, 8, 2]
