@@ -119,7 +119,9 @@ struct Params {
   float* part_ml;  // [item][3][128]: m, l, and the sum of the rounded terms
   uint32_t* err;
   Placement place;
-  int32_t N, H, tiles, splits, steps;  // row tiles a sequence, key ranges, least steps of a range
+  int32_t N, H, tiles, splits;  // row tiles a sequence, key ranges at most
+  int32_t items;                // row tiles of all sequences
+  int32_t fill, steps;          // ranges that fill the device once, and the steps from which more may be made
   float scale_log2;      // of a score, from a product: may be subnormal
   float scale_fraction;  // the same, of 0.5 .. 1, times 2^scale_exp
   int32_t scale_exp;
@@ -157,7 +159,8 @@ __device__ __forceinline__ Range make_range(const Params& p, int b, int tile, in
   g.end = any ? static_cast<int32_t>(max(min(static_cast<int64_t>(end), room), static_cast<int64_t>(0)))
               : 0;
   const int32_t total = g.end / kKeys + (g.end % kKeys ? 1 : 0);
-  const int32_t per = max(p.steps, (total - 1) / p.splits + 1);
+  // By the sequence's own length: the grid is laid out for a bound, which may be far above it.
+  const int32_t per = max((total - 1) / p.splits + 1, min((total - 1) / p.fill + 1, p.steps));
   g.lo = static_cast<int32_t>(min(static_cast<int64_t>(total), static_cast<int64_t>(split) * per));
   g.n = min(total - g.lo, per);
   g.plain = max(0, min(g.n, min(g.len, g.end) / kKeys - g.lo));
@@ -733,8 +736,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile uint32_t* s_abort = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x & 1, item = blockIdx.x >> 1;
-  const int split = item % p.splits, tile = item / p.splits % p.tiles, b = item / (p.splits * p.tiles);
+  // The first ranges of all row tiles come first, so that those without keys are the last.
+  const int rank = blockIdx.x & 1, nth = blockIdx.x >> 1, split = nth / p.items, group = nth % p.items;
+  const int tile = group % p.tiles, b = group / p.tiles, item = group * p.splits + split;
   uint32_t* err = p.err;
   constexpr uint32_t kPBytes = kP + kRows * 4;  // what comes with a tile: P and the factors
 
@@ -760,13 +764,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     *s_abort = 0u;
     fence_mbar_init();
   }
+  griddep_wait();
+  griddep_launch_dependents();
+  const Range g = make_range(p, b, tile, split, lane);
+  if (g.n == 0 && p.splits > 1) {  // nothing to do (with both barriers, whatever the other CTA finds)
+    if (rank == 0 && tid < kRows) p.part_ml[static_cast<int64_t>(item) * 3 * kRows + tid] = kNegInf;
+    cluster_sync();
+    cluster_sync();
+    return;
+  }
   if (warp == kMmaWarp) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
-  griddep_wait();
-  griddep_launch_dependents();
-  const Range g = make_range(p, b, tile, split, lane);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are set up
@@ -1338,7 +1348,7 @@ __global__ void __launch_bounds__(kRows * kJoinParts) tree_join_kernel(const __g
 int64_t pairs_at_once() { return sm_count() / 2; }
 
 struct Plan {
-  int32_t tiles, splits, steps;
+  int32_t tiles, items, splits, fill, steps;
   int64_t o_bytes, bytes;
 };
 // Key ranges: the number that takes the least time, in steps of 64 keys (1.35 us). A range costs some 14
@@ -1347,6 +1357,13 @@ struct Plan {
 // between full rounds and ranges of three quarters of the longest without a gap. (8 ragged sequences of 7
 // nodes and up to 5000 rows: 127 us as one range each, 90 as two, 113 as three; 3 of 31 nodes, 16 heads, 12001
 // rows: 139 as three, 80 as six, 109 as nine; 13 nodes over 32768 rows: 247 as three, 156 as five, 179 as ten.)
+// The kernel divides each sequence by its own length, the bound may be far above it: into the ranges of the grid, but
+// not more than fill the device once while those are shorter than three times what a range costs besides, or six
+// times where there are row tiles for all pairs anyway. (Whole calls, bound as long as the longest sequence and far
+// above: one node over 8192 rows 28.4 and 29.3 us, 89 to 181 where a range was as long as the bound's; 8 ragged
+// sequences of 7 nodes, 800 to 5000 rows, 87 and 84, 128; 32 of 4 nodes over 4096 rows 198 and 225, 254; 64 of one
+// node over 1000 rows 37 and 65, 98: seven ranges a sequence, six of them without keys.)
+constexpr int64_t kRangeCost = 14, kJoinCost = 4;
 Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
   Plan pl{};
   pl.tiles = (N * H + kRows - 1) / kRows;
@@ -1355,14 +1372,17 @@ Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_le
   int64_t best = 0, best_cost = 0;
   for (int64_t n = 1; n <= std::min<int64_t>(steps, 2 * pairs); ++n) {
     const int64_t per = (steps + n - 1) / n, waves = (items * n + pairs - 1) / pairs;
-    int64_t cost = waves * (per + 14);
+    int64_t cost = waves * (per + kRangeCost);
     if (B > 1 && waves > 1)
-      cost = (cost + std::max(per + 14, items * n * (3 * per / 4 + 14) / pairs)) / 2;
-    if (n > 1) cost += 4;
+      cost = (cost + std::max(per + kRangeCost, items * n * (3 * per / 4 + kRangeCost) / pairs)) / 2;
+    if (n > 1) cost += kJoinCost;
     if (best == 0 || cost < best_cost) best = n, best_cost = cost;
   }
   pl.splits = static_cast<int32_t>(best);
-  pl.steps = static_cast<int32_t>((steps + best - 1) / best);
+  pl.items = static_cast<int32_t>(items);
+  pl.fill = static_cast<int32_t>(std::max<int64_t>(1, pairs / items));
+  pl.steps = static_cast<int32_t>(
+      std::min((steps + best - 1) / best, (items <= pairs ? 3 : 6) * kRangeCost));
   pl.o_bytes = items * best * 2 * 64 * kRows * 16;
   if (best > 1) pl.bytes = pl.o_bytes + items * best * 3 * kRows * 4;
   return pl;
@@ -1431,6 +1451,8 @@ extern "C" int ds4idx_tree_attention(const void* q, int32_t format, const void* 
   p.H = n_heads;
   p.tiles = pl.tiles;
   p.splits = pl.splits;
+  p.items = pl.items;
+  p.fill = pl.fill;
   p.steps = pl.steps;
   // A subnormal scale of products below 2^128 leaves scores off by 2^-22 at most. Beside 8-bit rows, whose
   // queries are scaled as well, it is held in full.

@@ -145,3 +145,25 @@ def test_new_lengths_end_at_the_largest_int32():
     top = 2 ** 31 - 1
     new = ds4idx.tree_commit([], _i32([top, top - 2, top - 3, 5, -1]), _i32([[0, 1, 2]] * 5), _i32([3] * 5))
     assert new.tolist() == [top, top, top, 8, 2]
+
+
+def _parts_written(N, H, n, bound):
+    """How many ranges of a sequence of n rows leave a partial output when the work is laid out for `bound`."""
+    R = n + N
+    cache = torch.randn(R, 576, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    q = _q(1, N, H, 2)
+    masks = [[1 << i for i in range(N)]]
+    ws = torch.zeros(ds4idx.tree_attention_workspace(1, N, H, bound), dtype=torch.uint8, device="cuda")
+    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64(masks), 0.04, max_kv_len=bound, workspace=ws)
+    ds4idx.sparse_attention_status()
+    _check(q, cache.double(), [list(range(R))], [n], masks, 0.04, out, lse)
+    part = 128 * 512 * 4
+    return int((ws[:ws.numel() // part * part].view(-1, part).view(torch.int64) != 0).any(dim=1).sum())
+
+
+@pytest.mark.parametrize("N,H,n", [(1, 128, 8192), (1, 128, 1500), (7, 16, 8192), (3, 128, 6000)])
+def test_a_loose_bound_leaves_the_work_spread(N, H, n):
+    exact = _parts_written(N, H, n, n)
+    assert exact > 8
+    for bound in (2 * n, 262144, 1 << 20):
+        assert _parts_written(N, H, n, bound) >= 0.8 * exact, bound
