@@ -465,7 +465,9 @@ int ds4idx_tree_attention(const void* q, int32_t format, const void* cache, cons
                           float sm_scale, void* out, float* lse, void* workspace,
                           int64_t workspace_size, void* stream);
 
-/* *bytes: the workspace of a call of these sizes on the current device. Errors: INVALID_ARG. */
+/* *bytes: a workspace for calls of these sizes and every max_kv_len up to this one, on the current device
+ * (with 152 SMs never more than 161 MB). Other batches, nodes or heads may need more, fewer of them too.
+ * Errors: INVALID_ARG. */
 int ds4idx_tree_attention_workspace(int32_t B, int32_t n_nodes, int32_t n_heads, int64_t max_kv_len,
                                     int64_t* bytes);
 

@@ -1363,7 +1363,9 @@ struct Plan {
 // above: one node over 8192 rows 28.4 and 29.3 us, 89 to 181 where a range was as long as the bound's; 8 ragged
 // sequences of 7 nodes, 800 to 5000 rows, 87 and 84, 128; 32 of 4 nodes over 4096 rows 198 and 225, 254; 64 of one
 // node over 1000 rows 37 and 65, 98: seven ranges a sequence, six of them without keys.)
-constexpr int64_t kRangeCost = 14, kJoinCost = 4;
+// At most eight rounds of pairs: more would save 0.6% at the most, and eight hold the workspace under 160 MB.
+constexpr int64_t kRangeCost = 14, kJoinCost = 4, kRounds = 8;
+constexpr int64_t kPartBytes = 2 * 64 * kRows * 16, kPartSums = 3 * kRows * 4;  // of a range
 Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
   Plan pl{};
   pl.tiles = (N * H + kRows - 1) / kRows;
@@ -1372,6 +1374,7 @@ Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_le
   int64_t best = 0, best_cost = 0;
   for (int64_t n = 1; n <= std::min<int64_t>(steps, 2 * pairs); ++n) {
     const int64_t per = (steps + n - 1) / n, waves = (items * n + pairs - 1) / pairs;
+    if (n > 1 && waves > kRounds) break;
     int64_t cost = waves * (per + kRangeCost);
     if (B > 1 && waves > 1)
       cost = (cost + std::max(per + kRangeCost, items * n * (3 * per / 4 + kRangeCost) / pairs)) / 2;
@@ -1383,9 +1386,28 @@ Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_le
   pl.fill = static_cast<int32_t>(std::max<int64_t>(1, pairs / items));
   pl.steps = static_cast<int32_t>(
       std::min((steps + best - 1) / best, (items <= pairs ? 3 : 6) * kRangeCost));
-  pl.o_bytes = items * best * 2 * 64 * kRows * 16;
-  if (best > 1) pl.bytes = pl.o_bytes + items * best * 3 * kRows * 4;
+  pl.o_bytes = items * best * kPartBytes;
+  if (best > 1) pl.bytes = pl.o_bytes + items * best * kPartSums;
   return pl;
+}
+
+// Bytes that suffice for every bound up to max_kv_len. The best number of ranges goes up and down with the bound, a
+// limit of it does not go down: with a = items / pairs, n ranges of s steps in all take a s + 14 a n at the least, or
+// 7/8 a s + 109/8 a n - 1 where full rounds are weighed against ragged sequences, and the join. They are chosen only
+// where that is less than one round's ranges take, s / fill + 19 at the most, or, where a round does not hold one
+// range of each row tile, than one range each does, r (s + 14) in r rounds.
+int64_t enough_workspace(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
+  const int64_t items = static_cast<int64_t>(B) * ((N * H + kRows - 1) / kRows);
+  const double s = static_cast<double>(std::max<int64_t>(1, (max_kv_len + N + kKeys - 1) / kKeys));
+  const double a = static_cast<double>(items) / pairs, rounds = std::ceil(a);
+  const int64_t fill = std::max<int64_t>(1, pairs / items);
+  const double other = items <= pairs ? s / fill + 19 : rounds * (s + kRangeCost);
+  const double most = B > 1 ? (other - 0.875 * a * s - kJoinCost + 1) / (13.625 * a)
+                            : (other - a * s - kJoinCost) / (kRangeCost * a);
+  const double rounds_hold = static_cast<double>(kRounds * pairs / items);
+  const int64_t n = static_cast<int64_t>(
+      std::min({s, 2.0 * pairs, std::max(rounds_hold, 1.0), std::max(most, static_cast<double>(fill))}));
+  return n > 1 ? items * n * (kPartBytes + kPartSums) : 0;
 }
 
 bool sizes_ok(int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
@@ -1409,7 +1431,7 @@ extern "C" int ds4idx_tree_attention_workspace(int32_t B, int32_t n_nodes, int32
   if (!bytes || !sizes_ok(B, n_nodes, n_heads, max_kv_len)) return DS4IDX_ERR_INVALID_ARG;
   const int64_t pairs = pairs_at_once();
   if (pairs < 1) return DS4IDX_ERR_CUDA;
-  *bytes = B ? make_plan(pairs, B, n_nodes, n_heads, max_kv_len).bytes : 0;
+  *bytes = B ? enough_workspace(pairs, B, n_nodes, n_heads, max_kv_len) : 0;
   return DS4IDX_OK;
 }
 

@@ -641,7 +641,8 @@ def tree_attention(q, cache, kv_lens, mask, sm_scale: float, scale=None, kv_row0
 
 
 def tree_attention_workspace(B: int, N: int, H: int, max_kv_len: int) -> int:
-    """Bytes of a ``workspace`` that tree_attention calls of these sizes may share (on one stream)."""
+    """Bytes of a ``workspace`` that tree_attention calls of these sizes, and of any ``max_kv_len`` up to
+    this one, may share (on one stream)."""
     n = ctypes.c_int64()
     _check(load().ds4idx_tree_attention_workspace(B, N, H, int(max_kv_len), ctypes.addressof(n)),
            "ds4idx_tree_attention_workspace")

@@ -167,3 +167,24 @@ def test_a_loose_bound_leaves_the_work_spread(N, H, n):
     assert exact > 8
     for bound in (2 * n, 262144, 1 << 20):
         assert _parts_written(N, H, n, bound) >= 0.8 * exact, bound
+
+
+@pytest.mark.parametrize("B,N,H,bounds", [
+    (4, 64, 128, (11968, 12032, 16384, 100000)), (32, 4, 128, (2000, 37056, 37120, 50000)),
+    (1, 5, 128, (64, 640, 896, 960, 5000)), (8, 7, 128, (100, 5000, 30000, 262144)),
+    (1, 1, 16, (10, 4096, 70000, 1 << 20)), (2, 9, 64, (500, 3000, 20000, 20100))])
+def test_a_workspace_for_a_bound_serves_every_shorter_one(B, N, H, bounds):
+    lens = [70 + b % 3 for b in range(B)]
+    starts, R, rows = _contiguous(lens, N)
+    cache, scale, kv = _cache("fp8", R, 3)
+    masks = [[1] + [0] * (N - 2) + [1 << N - 1] if N > 1 else [1]] * B
+    masks = [[ref.signed(m) for m in row] for row in masks]
+    q = _q(B, N, H, 2)
+    need = [ds4idx.tree_attention_workspace(B, N, H, n) for n in bounds]
+    assert need == sorted(need)
+    ws = torch.empty(max(16, need[-1]), dtype=torch.uint8, device="cuda")
+    for n in bounds:
+        out, lse = ds4idx.tree_attention(q, cache, _i32(lens), _i64(masks), 0.04, scale=scale,
+                                         kv_row0=_i64(starts), max_kv_len=n, workspace=ws)
+        ds4idx.sparse_attention_status()
+        _check(q, kv, rows, lens, masks, 0.04, out, lse)
