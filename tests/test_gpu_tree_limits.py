@@ -1,4 +1,4 @@
-"""Tree attention and commit at the limits of their arguments.
+"""Tree attention and commit at the limits of their arguments, and the bounds that the choices in it give.
 Tolerances: those of test_gpu_tree_attention and test_gpu_tree_edges where nothing else is said."""
 import math
 
@@ -188,3 +188,67 @@ def test_a_workspace_for_a_bound_serves_every_shorter_one(B, N, H, bounds):
                                          kv_row0=_i64(starts), max_kv_len=n, workspace=ws)
         ds4idx.sparse_attention_status()
         _check(q, kv, rows, lens, masks, 0.04, out, lse)
+
+
+# The products are divided by the sum of the rounded terms: with e of a term its rounding, at most u = 2^-8, and
+# twice the error d of its score, out - o = sum p (1 + e) (v - o) / sum p (1 + e), which is at most
+# e / (1 - e) sum p |v - o|, and goes to 0 where one key outweighs the others. Besides: the output's own
+# rounding, t of sum p |v| for the sums in fp32, and the terms that are less than 2^-126 of the largest: there
+# exp2 gives 0 where the term is below the least normal number, and the maximum that terms are taken against is a
+# score of the row, so that what is lost of an output is less than 2^-126 |v| for each row seen. (It shows in 4-bit rows,
+# where a value of exactly 0 in the one row that counts leaves outputs of 1e-44.)
+
+# One key outweighs the rest (of one range: max_kv_len 0). Its term, 2^12 times 1.0037 above the maximum it is taken
+# against, loses 0.95 of half a bf16 step by its rounding. Divided by the exact sum the output would be 0.95 u off,
+# which rounds to the next bf16 number wherever the value's significand is above 1.06.
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [100, 1000])
+def test_a_key_that_outweighs_the_others_keeps_its_value(kind, n):
+    N, H, at = 1, 128, 90
+    cache, scale, kv = _cache(kind, n + N, 4)
+    rope = torch.zeros(n + N, 64, dtype=torch.bfloat16, device="cuda")
+    rope[at, 38] = 16
+    if kind == "bf16":
+        cache[:, 512:] = rope
+    else:
+        cache[:, -128:] = rope.view(torch.uint8)
+    kv[:, 512:] = rope.double()
+    q = torch.zeros(1, N, H, 576, dtype=torch.bfloat16, device="cuda")
+    q[..., 550] = 1
+    sm = float(np.float32(math.log(2) * (12 + math.log2(1.0037)) / 16))
+    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64([[1]]), sm, scale=scale, max_kv_len=0)
+    ds4idx.sparse_attention_status()
+    p = torch.softmax(sm * 16 * (torch.arange(n + N, device="cuda") == at).double(), 0)
+    v = kv[:, :512]
+    o = p @ v
+    u = 2.0 ** -8
+    spread = p @ (v - o).abs()
+    half = torch.exp2(torch.floor(torch.log2(o.abs())) - 8)
+    t = 2 * ((n + N) * 2.0 ** -23 + 2.0 ** -18) * (p @ v.abs())
+    assert bool(((out[0, 0].double() - o).abs() <= half + (u / (1 - u) + 2.0 ** -15) * spread + t).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,size", [(13, 2.0), (200, 2.0), (200, 12.0), (3000, 1.0), (3000, 30.0)])
+def test_outputs_divided_by_the_sum_of_the_rounded_terms(kind, n, size):
+    N, H, sm = 3, 128, 0.04
+    cache, scale, kv = _cache(kind, n + N, 9)
+    q, masks = _q(1, N, H, 5, scale=size), [[1, 3, 5]]
+    rows = [list(range(n + N))]
+    out, lse = ds4idx.tree_attention(q, cache, _i32([n]), _i64(masks), sm, scale=scale, max_kv_len=n // 4)
+    ds4idx.sparse_attention_status()
+    o, _, av, big, seen = ref.attention(q.double(), kv, rows, [n], masks, sm)
+    d = 37 * 2.0 ** -22 * big + 2.0 ** -20 * (1 + big)
+    if kind == "fp8":
+        d = d + 2.0 ** -21 * sm * q.double().abs().amax(dim=-1) * kv[:, :512].abs().sum(dim=1).max()
+    t = seen * 2.0 ** -23 + 2.0 ** -20
+    spread = torch.zeros_like(o)
+    for i in range(N):
+        at = torch.tensor(list(range(n)) + [n + j for j in range(N) if masks[0][i] >> j & 1], device="cuda")
+        p = torch.softmax(sm * q[0, i].double() @ kv[at].t(), dim=1)
+        for h in range(H):
+            spread[0, i, h] = p[h] @ (kv[at, :512] - o[0, i, h]).abs()
+    e = (2.0 ** -8 + 2 * d + 2.0 ** -15)[..., None]
+    bound = e / (1 - e) * spread + 2 * t[..., None] * av
+    bound = bound + 2.0 ** -8 * (o.abs() + bound) + seen[..., None] * 2.0 ** -126 * kv.abs().max()
+    assert bool(((out.double() - o).abs() <= bound).all())
