@@ -450,8 +450,8 @@ typedef enum {
  * Cache values are exact in bf16; products accumulate in fp32, softmax and sums are fp32, the
  * probabilities are rounded to bf16 for the value product and divided by the sum of the rounded ones.
  * Probabilities below 2^-126, beside 8-bit rows probabilities times the row's scale, lose bits or count as 0.
- * A term may be 2^32 (beside 8-bit and 4-bit rows 2^64) times the maximum that it is taken against, so
- * values of a bf16 cache stay finite in the sums below 2^96 / (rows of the sequence): below 2^64 always.
+ * A term may be 2^48 (beside 8-bit and 4-bit rows 2^64) times the maximum that it is taken against, so
+ * values of a bf16 cache stay finite in the sums below 2^80 / (rows of the sequence): below 2^49 always.
  * Beside an 8-bit cache the first 512 dims of a query are the sum of two 8-bit numbers: exact, or off by
  * at most 2^-21 of the query's largest value or of 2^-119, whichever is larger; rotary dims are finite
  * there and below 2^90, and a query that is not finite makes NaN of its output. What a row that is not seen holds (NaN included) does not reach the results. Scores that are

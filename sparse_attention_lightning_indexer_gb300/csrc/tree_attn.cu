@@ -99,13 +99,13 @@ constexpr uint32_t kColAside = 288;                // 224 columns that hold Q be
 constexpr float kNegInf = -__builtin_inff(), kMax = __FLT_MAX__;
 // log2 of what exp2(s - m) may be before m is raised. P and the sums are floating point with 2^127 of
 // range, so a stale m costs no precision, but it takes room from the values. Those of 8 and 4 bits are below 2^16,
-// which leaves 2^47 for their number. bf16 ones may be anything: 2^32 leaves room for values below 2^64 in
-// sequences of any length (2^31 of them), for 3% of the time of 13 nodes over 32768 rows (155 and 159 us). (With 2^8
-// some row of 128 raises m in most of the first hundred tiles, and a rescaling holds P V up for 4000 clocks:
+// which leaves 2^47 for their number. bf16 ones may be anything: 2^48 leaves room for values below 2^49 in
+// sequences of any length (2^31 of them) and costs nothing (13 nodes over 32768 rows 155.5 us, 160 with 2^32). (With
+// 2^8 some row of 128 raises m in most of the first hundred tiles, and a rescaling holds P V up for 4000 clocks:
 // one node over 262144 8-bit rows 150 us where it takes 98, 107 with 2^32; 4 sequences of 64 nodes over 16384
 // 1.78, 1.32 and 1.36 ms.)
 template <int kFormat>
-constexpr float kSlack = kFormat == DS4IDX_CACHE_BF16 ? 32.f : 64.f;
+constexpr float kSlack = kFormat == DS4IDX_CACHE_BF16 ? 48.f : 64.f;
 
 struct Params {
   const uint16_t* q;

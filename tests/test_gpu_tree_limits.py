@@ -107,18 +107,18 @@ def test_subnormal_scales_beside_large_8_bit_rows(sm):
     _check_ends(q, kv, [list(range(n + N))], [n], [[1, 3]], sm, out, lse, True)
 
 
-# log2 of the scores of the rows behind the first tile, by a rotary dim alone; values next to 2^64, of one sign in
-# a dim, so that a maximum left where it was would give sums past 2^128 (max_kv_len 0: one range)
-@pytest.mark.parametrize("above", [20.0, 31.0, 33.0, 60.0, 63.0, 66.0])
-def test_values_up_to_2_to_the_64(above):
+# log2 of the scores of the rows behind the first tile, by a rotary dim alone; values next to 2^80 / rows, of one sign
+# in a dim, so that a maximum left where it was would give sums past 2^128 (max_kv_len 0: one range)
+@pytest.mark.parametrize("above", [20.0, 47.0, 49.0, 60.0, 63.0, 66.0])
+def test_values_up_to_2_to_the_80_over_the_rows(above):
     n, N, H = 700, 1, 16
     g = torch.Generator().manual_seed(2)
     sign = torch.where(torch.rand(512, generator=g) < 0.5, -1.0, 1.0)
     x = torch.zeros(n + N, 576)
-    x[:, :512] = sign * (0.75 + 0.24 * torch.rand(n + N, 512, generator=g)) * 2.0 ** 64
+    x[:, :512] = sign * (0.75 + 0.24 * torch.rand(n + N, 512, generator=g)) * (2.0 ** 80 / (n + N))
     x[64:, 550] = above
     x = x.to(torch.bfloat16)
-    assert bool((x.abs() < 2.0 ** 64).all())
+    assert bool((x.abs() < 2.0 ** 80 / (n + N)).all())
     q = torch.zeros(1, N, H, 576, dtype=torch.bfloat16, device="cuda")
     q[..., 550] = 1
     sm = float(np.float32(math.log(2)))
