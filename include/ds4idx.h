@@ -444,9 +444,9 @@ typedef enum {
  *           sequence the results stay right and the call gets slower.
  *  out      [B, n_nodes, n_heads, 512] bf16, 32-byte aligned; lse [B, n_nodes, n_heads] fp32 or NULL.
  *           Of a node of mask 0, or that sees no row, out is 0 and lse -infinity.
- *  workspace  DEVICE, 16-byte aligned, at least the bytes that ds4idx_tree_attention_workspace
- *           gives for these sizes (may be 0, then NULL): partial sums of sequences
- *           whose keys are split. Calls that can overlap need one each.
+ *  workspace  DEVICE, 16-byte aligned, the bytes that ds4idx_tree_attention_workspace gives for these
+ *           sizes and this or a larger max_kv_len (may be 0, then NULL): partial sums of sequences whose
+ *           keys are split. Calls that can overlap need one each.
  * Cache values are exact in bf16; products accumulate in fp32, softmax and sums are fp32, the
  * probabilities are rounded to bf16 for the value product and divided by the sum of the rounded ones.
  * Probabilities below 2^-126, beside 8-bit rows probabilities times the row's scale, lose bits or count as 0.
@@ -454,10 +454,11 @@ typedef enum {
  * values of a bf16 cache stay finite in the sums below 2^80 / (rows of the sequence): below 2^49 always.
  * Beside an 8-bit cache the first 512 dims of a query are the sum of two 8-bit numbers: exact, or off by
  * at most 2^-21 of the query's largest value or of 2^-119, whichever is larger; rotary dims are finite
- * there and below 2^90, and a query that is not finite makes NaN of its output. What a row that is not seen holds (NaN included) does not reach the results. Scores that are
- * not finite follow the formulas, as in ds4idx_sparse_attention_q4; the values of a drafted row that
- * are not finite count as 0 (its scores still make NaN of the nodes that see it). Asynchronous on `stream`, allocates nothing. Bounded device waits that run
- * out are recorded for ds4idx_sparse_attention_status.
+ * there and below 2^90, and a query that is not finite makes NaN of its output. What a row that is not seen
+ * holds (NaN included) does not reach the results. Scores that are not finite follow the formulas, as in
+ * ds4idx_sparse_attention_q4; the values of a drafted row that are not finite count as 0 (its scores still
+ * make NaN of the nodes that see it). Asynchronous on `stream`, allocates nothing. Bounded device waits that
+ * run out are recorded for ds4idx_sparse_attention_status.
  * Errors: INVALID_ARG, UNSUPPORTED (d_qk != 576, d_v != 512), LAUNCH, CUDA. B = 0 is a no-op. */
 int ds4idx_tree_attention(const void* q, int32_t format, const void* cache, const float* scale,
                           int64_t kv_rows, const int32_t* kv_lens, const int64_t* mask,

@@ -195,8 +195,8 @@ def test_a_workspace_for_a_bound_serves_every_shorter_one(B, N, H, bounds):
 # e / (1 - e) sum p |v - o|, and goes to 0 where one key outweighs the others. Besides: the output's own
 # rounding, t of sum p |v| for the sums in fp32, and the terms that are less than 2^-126 of the largest: there
 # exp2 gives 0 where the term is below the least normal number, and the maximum that terms are taken against is a
-# score of the row, so that what is lost of an output is less than 2^-126 |v| for each row seen. (It shows in 4-bit rows,
-# where a value of exactly 0 in the one row that counts leaves outputs of 1e-44.)
+# score of the row, so that what is lost of an output is less than 2^-126 |v| for each row seen. (It shows in 4-bit
+# rows, where a value of exactly 0 in the one row that counts leaves outputs of 1e-44.)
 
 # One key outweighs the rest (of one range: max_kv_len 0). Its term, 2^12 times 1.0037 above the maximum it is taken
 # against, loses 0.95 of half a bf16 step by its rounding. Divided by the exact sum the output would be 0.95 u off,
