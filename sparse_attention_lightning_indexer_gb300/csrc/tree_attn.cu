@@ -791,7 +791,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     fence_mbar_init();
   }
   griddep_wait();
-  griddep_launch_dependents();
   const Range g = make_range(p, b, tile, split, lane);
   if (g.n == 0 && p.splits > 1) {  // nothing to do (with both barriers, whatever the other CTA finds)
     if (rank == 0 && tid < kRows) p.part_ml[static_cast<int64_t>(item) * 3 * kRows + tid] = kNegInf;
@@ -805,6 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   }
   tc_fence_before();
   __syncthreads();
+  // (Not before every CTA has its tensor memory: a dependent that took it first would wait for this grid.)
+  griddep_launch_dependents();
   cluster_sync();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
@@ -1389,7 +1390,7 @@ struct Plan {
 // above: one node over 8192 rows 28.4 and 29.3 us, 89 to 181 where a range was as long as the bound's; 8 ragged
 // sequences of 7 nodes, 800 to 5000 rows, 87 and 84, 128; 32 of 4 nodes over 4096 rows 198 and 225, 254; 64 of one
 // node over 1000 rows 37 and 65, 98: seven ranges a sequence, six of them without keys.)
-// At most eight rounds of pairs: more would save 0.6% at the most, and eight hold the workspace under 160 MB.
+// At most eight rounds of pairs: more would save 0.6% at the most, and eight hold the workspace under 161 MB.
 constexpr int64_t kRangeCost = 14, kJoinCost = 4, kRounds = 8;
 constexpr int64_t kPartBytes = 2 * 64 * kRows * 16, kPartSums = 3 * kRows * 4;  // of a range
 Plan make_plan(int64_t pairs, int32_t B, int32_t N, int32_t H, int64_t max_kv_len) {
